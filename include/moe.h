@@ -350,7 +350,8 @@ MOE_API moe_status moe_workspace_views(const moe_shape* shape, void* workspace, 
  * (MOE_ERR_TIMEOUT / MOE_ERR_DEVICE).  detail (may be NULL) receives the
  * four raw int32 words: the code, the id of the kernel that recorded it
  * (1 norm/router, 2 top-k, 3 align, 4 gather, 5 gate/up GEMM, 6 down GEMM,
- * 7 combine, 8 self-test), for the expert GEMMs a bit mask of the waits that
+ * 7 combine, 8 self-test, 9 grouped products' tables, 10 grouped GEMM), for
+ * the expert GEMMs a bit mask of the waits that
  * ran out (bit 1 producer: ring slot free; 2 MMA: accumulator free; 3 MMA:
  * ring slot loaded; 4 epilogue: accumulator complete; 5 epilogue: stream-K
  * partial sums; 6 epilogue: fused-combine rendezvous; 7 MMA: a stage's scales
@@ -515,6 +516,78 @@ MOE_API moe_status moe_forward_nvfp4(const moe_shape* shape, const moe_bf16* x, 
 MOE_API moe_status moe_qk_norm(int64_t T, int32_t Hq, int32_t Hk, int32_t D, moe_bf16* q, moe_bf16* k,
                                const moe_bf16* q_weight, const moe_bf16* k_weight, float weight_bias, float eps,
                                moe_stream_t stream);
+
+/* ---- Products grouped by expert, and their gradients ------------------
+ * The experts' matrix products on their own, for callers that bring their own
+ * routing or train the experts: rows of the token matrices belong to groups
+ * (experts), group g holding rows [offsets[g], offsets[g] + counts[g]), any
+ * number of them, none included; w is [groups, N, K] (K-major like W13 and W2).
+ *   forward          y[p, :]  = x[p, :] w_g^T                    (p in group g)
+ *   input gradient   dx[p, :] = dy[p, :] w_g
+ *   weight gradient  dw_g     = sum over the group's p of dy[p, :]^T x[p, :]
+ * The lists moe_route_debug and moe_views give (offsets with padding between
+ * the groups, counts) are such groups.  Products are summed in fp32 in one
+ * fixed order for a given shape and device, so calls repeat bit for bit; each
+ * output is rounded once.
+ *   offsets  [groups + 1] int32, device: offsets[g] + counts[g] <= offsets[g+1]
+ *            and offsets[groups] <= rows; or NULL: equal groups of
+ *            rows / groups rows (rows a multiple of groups, else
+ *            MOE_ERR_INVALID_ARG)
+ *   counts   [groups] int32, device, or NULL: offsets[g + 1] - offsets[g]
+ * Rows that belong to no group are not written, and what they hold (NaN
+ * included) reaches no output.  Offsets that break the rules above are found on the device:
+ * nothing is written then, and moe_device_status() returns MOE_ERR_DEVICE with
+ * kernel id 9 and the first such group's index (detail[2]).
+ *   type     of x, w, y, dy, dx: MOE_TYPE_BF16 or MOE_TYPE_FP16
+ *   ldx ...  row strides in elements: >= the row's width, multiples of 8
+ *   N, K     multiples of 8, <= 2^20; groups <= 1024; rows <= 2^31 - 512
+ *            (others: MOE_ERR_UNSUPPORTED)
+ *   workspace  moe_grouped_workspace_size() bytes, 256-byte aligned; contents
+ *            on entry do not matter; one call at a time uses it (two graphs
+ *            that share one are replayed one after the other).
+ * Matrices 16-byte aligned, outputs apart from the inputs.  Asynchronous on
+ * `stream`, capturable like every call.  rows = 0 is a no-op (the weight
+ * gradient still writes its zeros). */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_FP16 1
+#define MOE_TYPE_FP32 2
+
+typedef struct {
+  int32_t groups, N, K;
+  int32_t type;
+  int64_t rows; /* rows of the token matrices, those of no group included */
+} moe_grouped_shape;
+
+/* Host only; makes no CUDA call. */
+MOE_API moe_status moe_grouped_workspace_size(const moe_grouped_shape* shape, size_t* bytes);
+
+/* y [rows, N] from x [rows, K]. */
+MOE_API moe_status moe_grouped_gemm(const moe_grouped_shape* shape, const void* x, int64_t ldx, const void* w,
+                                    const int32_t* offsets, const int32_t* counts, void* y, int64_t ldy,
+                                    void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* dx [rows, K] from dy [rows, N]; w as in the forward (no transposed copy). */
+MOE_API moe_status moe_grouped_gemm_dgrad(const moe_grouped_shape* shape, const void* dy, int64_t lddy, const void* w,
+                                          const int32_t* offsets, const int32_t* counts, void* dx, int64_t lddx,
+                                          void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* dw [groups, N, K] of dw_type (the operands' type, or MOE_TYPE_FP32): written
+ * whole, zeros for an empty group; or, with accumulate != 0 (MOE_TYPE_FP32
+ * only, else MOE_ERR_INVALID_ARG), added to what dw holds. */
+MOE_API moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy, int64_t lddy, const void* x,
+                                          int64_t ldx, const int32_t* offsets, const int32_t* counts, void* dw,
+                                          int32_t dw_type, int32_t accumulate, void* workspace,
+                                          size_t workspace_bytes, moe_stream_t stream);
+
+/* SwiGLU of separate rows, between the gate/up and the down product: h
+ * [rows, 2I] holds gate in columns [0, I) and up in [I, 2I) (the order of a
+ * W13 product), act [rows, I] = SiLU(gate) * up; and its gradient,
+ * dh [rows, 2I] from dact [rows, I].  dh may be h itself.  type, strides,
+ * alignment and rows as above; I a multiple of 8, rows * I < 2^34. */
+MOE_API moe_status moe_swiglu(int32_t type, int64_t rows, int32_t I, const void* h, int64_t ldh, void* act,
+                              int64_t ldact, moe_stream_t stream);
+MOE_API moe_status moe_swiglu_grad(int32_t type, int64_t rows, int32_t I, const void* h, int64_t ldh,
+                                   const void* dact, int64_t lddact, void* dh, int64_t lddh, moe_stream_t stream);
 
 /* Self-test of the failure path of the library's bounded device waits (no
  * counterpart on the pages): enqueues one small kernel whose two waits -- on

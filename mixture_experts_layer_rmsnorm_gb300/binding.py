@@ -42,6 +42,11 @@ class MoeMxViews(ctypes.Structure):
                 ("x_gscale", ctypes.c_void_p), ("act_gscale", ctypes.c_void_p), ("nv_chunk_rows", ctypes.c_int32)]
 
 
+class MoeGroupedShape(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("rows", ctypes.c_int64)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {moe_status_string(status)} (status {status})")
@@ -92,6 +97,13 @@ def load(build: bool = True):
             lib.moe_forward_fused_front.argtypes = [sp, p, p, p, p, p, p, p, p, sz, p, p, i32]
             lib.moe_forward_fused_combine.argtypes = [sp, p, p, p, p, p, p, p, p, sz, p, p, i32]
             lib.moe_forward_fused_mlp.argtypes = [sp, p, p, p, p, p, p, p, p, sz, p, p, i32]
+            gp = ctypes.POINTER(MoeGroupedShape)
+            lib.moe_grouped_workspace_size.argtypes = [gp, psz]
+            lib.moe_grouped_gemm.argtypes = [gp, p, i64, p, p, p, p, i64, p, sz, p]
+            lib.moe_grouped_gemm_dgrad.argtypes = [gp, p, i64, p, p, p, p, i64, p, sz, p]
+            lib.moe_grouped_gemm_wgrad.argtypes = [gp, p, i64, p, i64, p, p, p, i32, i32, p, sz, p]
+            lib.moe_swiglu.argtypes = [i32, i64, i32, p, i64, p, i64, p]
+            lib.moe_swiglu_grad.argtypes = [i32, i64, i32, p, i64, p, i64, p, i64, p]
             lib.moe_status_string.argtypes = [ctypes.c_int]
             lib.moe_status_string.restype = ctypes.c_char_p
             for f in ("moe_workspace_size", "moe_forward", "moe_forward_events", "moe_route_debug",
@@ -103,7 +115,9 @@ def load(build: bool = True):
                       "moe_workspace_views_mx", "moe_forward_mx", "moe_forward_fused_combine",
                       "moe_mxfp4_weight_sizes", "moe_mxfp4_quantize_weights", "moe_forward_mxfp4",
                       "moe_forward_mxfp4a4", "moe_nvfp4_weight_sizes", "moe_nvfp4_quantize_weights",
-                      "moe_forward_nvfp4", "moe_forward_fused_mlp"):
+                      "moe_forward_nvfp4", "moe_forward_fused_mlp", "moe_grouped_workspace_size",
+                      "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_swiglu",
+                      "moe_swiglu_grad"):
                 getattr(lib, f).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -341,6 +355,188 @@ def moe_forward_nvfp4(s: MoeShape, x, g_norm, w_router, router_bias, w13_codes, 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+MOE_TYPE_BF16, MOE_TYPE_FP16, MOE_TYPE_FP32 = range(3)
+
+
+def grouped_shape(groups, N, K, rows, type=MOE_TYPE_BF16) -> MoeGroupedShape:
+    return MoeGroupedShape(int(groups), int(N), int(K), int(type), int(rows))
+
+
+def moe_grouped_workspace_size(s: MoeGroupedShape) -> tuple[int, int]:
+    n = ctypes.c_size_t(0)
+    st = load().moe_grouped_workspace_size(ctypes.byref(s), ctypes.byref(n))
+    return st, n.value
+
+
+def moe_grouped_gemm(s: MoeGroupedShape, x, ldx, w, offsets, counts, y, ldy, workspace, workspace_bytes,
+                     stream) -> int:
+    return load().moe_grouped_gemm(ctypes.byref(s), x, ldx, w, offsets, counts, y, ldy, workspace, workspace_bytes,
+                                   stream)
+
+
+def moe_grouped_gemm_dgrad(s: MoeGroupedShape, dy, lddy, w, offsets, counts, dx, lddx, workspace, workspace_bytes,
+                           stream) -> int:
+    return load().moe_grouped_gemm_dgrad(ctypes.byref(s), dy, lddy, w, offsets, counts, dx, lddx, workspace,
+                                         workspace_bytes, stream)
+
+
+def moe_grouped_gemm_wgrad(s: MoeGroupedShape, dy, lddy, x, ldx, offsets, counts, dw, dw_type, accumulate, workspace,
+                           workspace_bytes, stream) -> int:
+    return load().moe_grouped_gemm_wgrad(ctypes.byref(s), dy, lddy, x, ldx, offsets, counts, dw, int(dw_type),
+                                         int(bool(accumulate)), workspace, workspace_bytes, stream)
+
+
+def moe_swiglu(type, rows, I, h, ldh, act, ldact, stream) -> int:
+    return load().moe_swiglu(int(type), int(rows), int(I), h, ldh, act, ldact, stream)
+
+
+def moe_swiglu_grad(type, rows, I, h, ldh, dact, lddact, dh, lddh, stream) -> int:
+    return load().moe_swiglu_grad(int(type), int(rows), int(I), h, ldh, dact, lddact, dh, lddh, stream)
+
+
+def _type_of(dtype) -> int:
+    import torch
+    types = {torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_FP16, torch.float32: MOE_TYPE_FP32}
+    if dtype not in types:
+        raise TypeError(f"{dtype}: bfloat16, float16 or float32 wanted")
+    return types[dtype]
+
+
+def _check(what, t, device, dtype, shape_, rows=False):
+    """A tensor argument: its device, type and shape; contiguous, or (rows) rows of contiguous elements."""
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} is {t.dtype}, not {dtype}")
+    if tuple(t.shape) != tuple(shape_):
+        raise ValueError(f"{what} is {tuple(t.shape)}, not {tuple(shape_)}")
+    if not (t.stride(-1) == 1 or t.shape[-1] == 1) if rows else not t.is_contiguous():
+        raise ValueError(f"{what} is not contiguous" + (" along its rows" if rows else ""))
+    return t
+
+
+def _ld(t) -> int:
+    # (a single row's stride says nothing)
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def swiglu(h, act=None):
+    """SiLU(gate) * up of rows h = [gate | up] (moe_swiglu), on the current stream of h's device."""
+    import torch
+    rows, two_i = h.shape
+    _check("h", h, h.device, h.dtype, h.shape, rows=True)
+    with torch.cuda.device(h.device):
+        act = torch.empty((rows, two_i // 2), dtype=h.dtype, device=h.device) if act is None else \
+            _check("act", act, h.device, h.dtype, (rows, two_i // 2), rows=True)
+        st = moe_swiglu(_type_of(h.dtype), rows, two_i // 2, _ptr(h), _ld(h), _ptr(act), _ld(act),
+                        torch.cuda.current_stream().cuda_stream)
+    if st != MOE_OK:
+        raise MoeError(st, "moe_swiglu")
+    return act
+
+
+def swiglu_grad(h, dact, dh=None):
+    """d[gate | up] from dact (moe_swiglu_grad), on the current stream of h's device."""
+    import torch
+    rows, two_i = h.shape
+    _check("h", h, h.device, h.dtype, h.shape, rows=True)
+    _check("dact", dact, h.device, h.dtype, (rows, two_i // 2), rows=True)
+    with torch.cuda.device(h.device):
+        dh = torch.empty((rows, two_i), dtype=h.dtype, device=h.device) if dh is None else \
+            _check("dh", dh, h.device, h.dtype, (rows, two_i), rows=True)
+        st = moe_swiglu_grad(_type_of(h.dtype), rows, two_i // 2, _ptr(h), _ld(h), _ptr(dact), _ld(dact), _ptr(dh),
+                             _ld(dh), torch.cuda.current_stream().cuda_stream)
+    if st != MOE_OK:
+        raise MoeError(st, "moe_swiglu_grad")
+    return dh
+
+
+class GroupedProducts:
+    """The products of ``groups`` weight matrices [N, K] with the rows of their
+    groups, and the gradients (moe_grouped_gemm*), with a workspace of their
+    own.  Calls go to the current stream of the tensors' device; calls of one
+    object on several streams share its workspace and must not overlap.
+    offsets: int32 [groups + 1] on the device, or None (equal groups);
+    counts: int32 [groups] or None (offsets[g + 1] - offsets[g])."""
+
+    def __init__(self, groups, N, K, dtype, max_rows=0, device=None):
+        import torch
+        self.groups, self.N, self.K, self.dtype = int(groups), int(N), int(K), dtype
+        self.device = torch.empty(0, device=device or "cuda").device
+        st, n = moe_grouped_workspace_size(self.shape(max_rows))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_grouped_workspace_size")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def shape(self, rows) -> MoeGroupedShape:
+        return grouped_shape(self.groups, self.N, self.K, rows, _type_of(self.dtype))
+
+    def _lists(self, offsets, counts):
+        import torch
+        if offsets is not None:
+            _check("offsets", offsets, self.device, torch.int32, (self.groups + 1,))
+        if counts is not None:
+            _check("counts", counts, self.device, torch.int32, (self.groups,))
+        return _ptr(offsets), _ptr(counts)
+
+    def _rows(self, what, t, rows, width):
+        import torch
+        if t is None:
+            return torch.empty((rows, width), dtype=self.dtype, device=self.device)
+        return _check(what, t, self.device, self.dtype, (rows, width), rows=True)
+
+    def _call(self, name, fn, *args):
+        import torch
+        with torch.cuda.device(self.device):
+            st = fn(*args, _ptr(self.workspace), self.workspace.numel(), torch.cuda.current_stream().cuda_stream)
+        if st != MOE_OK:
+            raise MoeError(st, name)
+
+    def forward(self, x, w, offsets=None, counts=None, y=None):
+        """y[p] = x[p] w_g^T for the rows p of every group g; other rows of y stay as they are."""
+        rows = x.shape[0]
+        self._rows("x", x, rows, self.K)
+        _check("w", w, self.device, self.dtype, (self.groups, self.N, self.K))
+        y = self._rows("y", y, rows, self.N)
+        self._call("moe_grouped_gemm", moe_grouped_gemm, self.shape(rows), _ptr(x), _ld(x), _ptr(w),
+                   *self._lists(offsets, counts), _ptr(y), _ld(y))
+        return y
+
+    def dgrad(self, dy, w, offsets=None, counts=None, dx=None):
+        """dx[p] = dy[p] w_g."""
+        rows = dy.shape[0]
+        self._rows("dy", dy, rows, self.N)
+        _check("w", w, self.device, self.dtype, (self.groups, self.N, self.K))
+        dx = self._rows("dx", dx, rows, self.K)
+        self._call("moe_grouped_gemm_dgrad", moe_grouped_gemm_dgrad, self.shape(rows), _ptr(dy), _ld(dy), _ptr(w),
+                   *self._lists(offsets, counts), _ptr(dx), _ld(dx))
+        return dx
+
+    def wgrad(self, dy, x, offsets=None, counts=None, dw=None, dtype=None, accumulate=False):
+        """dw_g = sum over the group's rows of dy[p]^T x[p], in ``dtype`` (fp32 or the operands' type, the default)
+        or dw's type; accumulate (fp32): added to dw."""
+        import torch
+        rows = x.shape[0]
+        self._rows("dy", dy, rows, self.N)
+        self._rows("x", x, rows, self.K)
+        if dw is None:
+            if accumulate:
+                raise ValueError("accumulate adds to dw: pass it")
+            dw = torch.empty((self.groups, self.N, self.K), dtype=dtype or self.dtype, device=self.device)
+        else:
+            _check("dw", dw, self.device, dtype or dw.dtype, (self.groups, self.N, self.K))
+        self._call("moe_grouped_gemm_wgrad", moe_grouped_gemm_wgrad, self.shape(rows), _ptr(dy), _ld(dy), _ptr(x),
+                   _ld(x), *self._lists(offsets, counts), _ptr(dw), _type_of(dw.dtype), accumulate)
+        return dw
+
+    def device_status(self):
+        """(status, detail) of the last call, after waiting for the current stream (moe_device_status)."""
+        import torch
+        with torch.cuda.device(self.device):
+            return moe_device_status(_ptr(self.workspace), self.workspace.numel(),
+                                     torch.cuda.current_stream().cuda_stream)
 
 
 class MoeLayer:

@@ -1,0 +1,157 @@
+// grouped.cuh -- what the products grouped by expert share (internal): the
+// group tables a call's plan kernel writes into the workspace, the work units
+// made from them, and the launchers.
+//
+// Rows of the token matrices belong to groups: group g holds rows
+// [start_g, start_g + count_g).  Work units are numbered group by group; a
+// group's units are (its token chunks or column tiles) x (its feature tiles).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "moe_kernels.cuh"
+
+namespace moe {
+
+enum : int32_t { kKernGroupedPlan = 9, kKernGroupedGemm = 10, kKernFp4Gemm = 11 };
+
+constexpr int kGroupsMax = 1024;
+constexpr int kGroupsSmem = 256;  // the GEMM kernels keep unit_off in shared memory up to this many groups
+
+enum class GroupedOp : int { kForward = 0, kDgrad = 1, kWgrad = 2 };
+
+// Plan kernel (one CTA): checks offsets / counts, writes start[G], count[G]
+// and unit_off[G + 1], clears the error word and `n_flags` stream-K flags, and
+// for the weight gradient writes the groups' tensor maps.
+//   units of group g: ceil(count_g / bn) * tiles, or (bn = 0) `tiles`, none
+//   for an empty group if skip_empty.
+// A group that leaves [0, rows) or runs into the next one records
+// MOE_ERR_DEVICE, and the call then has no units at all.
+struct GroupedPlanArgs {
+  const int32_t* offsets;  // [G + 1], or null: G equal groups of rows / G rows
+  const int32_t* counts;   // [G], or null: offsets[g + 1] - offsets[g]
+  int G;
+  int64_t rows;
+  int bn, tiles, skip_empty;
+  int32_t* start;
+  int32_t* count;
+  int32_t* unit_off;
+  int32_t* err;
+  int32_t* flags;
+  int n_flags;
+  CUtensorMap* maps;  // weight gradient: [G][2] maps of dy and x whose rows end with the group, else null
+};
+cudaError_t launch_grouped_plan(const GroupedPlanArgs& a, const CUtensorMap& dy, const CUtensorMap& x,
+                                cudaStream_t stream);
+
+// One grouped 16-bit product.  F: features on the MMA's M side (N for the
+// forward and the weight gradient, K for the input gradient); R: reduction
+// length (forward K, input gradient N; unused by the weight gradient); C: the
+// weight gradient's columns (K).
+struct GroupedGemmArgs {
+  const int32_t* start;
+  const int32_t* count;
+  const int32_t* unit_off;
+  const CUtensorMap* maps;  // weight gradient: see GroupedPlanArgs
+  int32_t* err;
+  float* partials;  // stream-K partial sums: [kMaxGemmCtas][BN][128] fp32
+  int32_t* flags;   // [kMaxGemmCtas * 4], zero on entry
+  void* out;        // forward / input gradient: rows of ldo elements of the operand type
+  int64_t ldo;
+  int G, F, R, C;
+  int tiles;       // M tiles (of 128, or 256 for CTA pairs) per group
+  int tiles_n;     // weight gradient: column tiles of 256
+  int fp16;        // operands fp16, else bf16
+  int out_fp32;    // weight gradient: fp32, else the operand type
+  int accumulate;  // weight gradient (fp32): add to what dw holds
+};
+
+// Tile plans of the forward and the input gradient.
+enum class GroupedPlan : int { kSmall = 0, kLarge = 1 };
+int grouped_bn(GroupedPlan plan);         // token rows per unit
+int grouped_tile(GroupedPlan plan);       // features per unit
+int grouped_tok_box(GroupedPlan plan);    // token rows per TMA box
+size_t grouped_partial_bytes();           // stream-K partial sums
+constexpr int kWgradTile = 256;           // rows and columns of a unit of the weight gradient
+
+cudaError_t launch_grouped_gemm(GroupedOp op, GroupedPlan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
+                                const GroupedGemmArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_grouped_wgrad(const CUtensorMap& tm_dw, const GroupedGemmArgs& a, cudaStream_t stream);
+
+#ifdef __CUDACC__
+
+struct GroupedUnit {
+  int g, tile, tile_n, tok0, n;
+};
+
+// Unit u -> its group (binary search in unit_off), feature tile and token
+// chunk (chunk fastest: units that read the same weight tile are neighbours,
+// so the CTAs running side by side read it from DRAM once), or (bn = 0)
+// feature tile and column tile.
+__device__ __forceinline__ GroupedUnit grouped_unit(int u, const int32_t* unit_off, const int32_t* start,
+                                                    const int32_t* count, int G, int tiles, int tiles_n, int bn) {
+  int lo = 0, hi = G;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (unit_off[mid] <= u)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  GroupedUnit r;
+  r.g = lo;
+  const int local = u - unit_off[lo];
+  const int s = __ldcg(start + lo), c = __ldcg(count + lo);
+  if (bn > 0) {
+    const int chunks = (c + bn - 1) / bn;  // >= 1: u lies in this group's range
+    r.tile = local / chunks;
+    const int chunk = local - r.tile * chunks;
+    r.tile_n = 0;
+    r.tok0 = s + chunk * bn;
+    r.n = min(bn, c - chunk * bn);
+  } else {
+    r.tile = local / tiles_n;
+    r.tile_n = local - r.tile * tiles_n;
+    r.tok0 = s;
+    r.n = c;
+  }
+  return r;
+}
+
+// A worker's work, as segments: K-blocks [kb0, kb1) of unit u.  Stream-K: a
+// contiguous range of (unit, K-block) iterations of equal length for every
+// worker; otherwise whole units worker, worker + workers, ...
+struct GroupedRange {
+  int64_t it, end, W;
+  int kblocks, step;
+  bool stream_k;
+  __device__ GroupedRange(int units, int kb, int worker, int workers, bool sk)
+      : W(static_cast<int64_t>(units) * kb), kblocks(kb), step(workers), stream_k(sk) {
+    it = sk ? W * worker / workers : worker;
+    end = sk ? W * (worker + 1) / workers : units;
+  }
+  __device__ bool next(int& u, int& kb0, int& kb1) {
+    if (it >= end) return false;
+    if (!stream_k) {
+      u = static_cast<int>(it);
+      kb0 = 0;
+      kb1 = kblocks;
+      it += step;
+      return true;
+    }
+    u = static_cast<int>(it / kblocks);
+    kb0 = static_cast<int>(it - static_cast<int64_t>(u) * kblocks);
+    const int64_t stop = kb0 + (end - it);
+    kb1 = stop < kblocks ? static_cast<int>(stop) : kblocks;
+    it += kb1 - kb0;
+    return true;
+  }
+  // first iteration of a worker's range (stream-K)
+  __device__ int64_t begin_of(int worker) const { return W * worker / step; }
+};
+
+#endif  // __CUDACC__
+
+}  // namespace moe

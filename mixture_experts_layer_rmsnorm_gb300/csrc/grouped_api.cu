@@ -1,0 +1,305 @@
+// grouped_api.cu -- the C ABI of the grouped products and of SwiGLU on separate
+// rows: argument checks, workspace layout, tensor maps, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "../../include/moe.h"
+#include "grouped.cuh"
+#include "grouped_elementwise.cuh"
+#include "tensor_map.h"
+
+namespace {
+
+using moe::GroupedOp;
+using moe::GroupedPlan;
+
+constexpr int64_t kMaxDim = int64_t(1) << 20;         // N, K
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;  // 32-bit row coordinates, a token box past the end
+constexpr int64_t kMaxLd = int64_t(1) << 36;          // elements: row strides within the tensor maps' 2^40 bytes
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+struct Layout {
+  size_t start, count, unit_off, flags, maps, partials, total;
+};
+
+constexpr int kFlagInts = moe::kMaxGemmCtas * 4;
+
+Layout make_layout(int G) {
+  Layout L{};
+  size_t off = 64;  // the error word
+  auto take = [&](size_t bytes) {
+    off = align_up(off, 256);
+    const size_t r = off;
+    off += bytes;
+    return r;
+  };
+  L.start = take(static_cast<size_t>(G) * 4);
+  L.count = take(static_cast<size_t>(G) * 4);
+  L.unit_off = take(static_cast<size_t>(G + 1) * 4);
+  L.flags = take(static_cast<size_t>(kFlagInts) * 4);
+  L.maps = take(static_cast<size_t>(G) * 2 * sizeof(CUtensorMap));
+  L.partials = take(moe::grouped_partial_bytes());
+  L.total = align_up(off, 256);
+  return L;
+}
+
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+moe_status check_shape(const moe_grouped_shape* s) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->groups <= 0 || s->N <= 0 || s->K <= 0 || s->rows < 0) return MOE_ERR_INVALID_ARG;
+  if (s->type != MOE_TYPE_BF16 && s->type != MOE_TYPE_FP16) return MOE_ERR_INVALID_ARG;
+  if (s->groups > moe::kGroupsMax || s->N % 8 != 0 || s->K % 8 != 0 || s->N > kMaxDim || s->K > kMaxDim ||
+      s->rows > kMaxRows)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// A row matrix of `width` elements: null only without rows.
+moe_status check_rows(const void* p, int64_t rows, int64_t ld, int64_t width) {
+  if (ld < width) return MOE_ERR_INVALID_ARG;
+  if (ld % 8 != 0 || ld > kMaxLd) return MOE_ERR_UNSUPPORTED;
+  if (rows > 0 && (!p || !aligned(p, 16))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status check_call(const moe_grouped_shape* s, const int32_t* offsets, const int32_t* counts, void* ws,
+                      size_t ws_bytes) {
+  if (!offsets && s->rows % s->groups != 0) return MOE_ERR_INVALID_ARG;
+  if (!aligned(offsets, 4) || !aligned(counts, 4)) return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < make_layout(s->groups).total) return MOE_ERR_WORKSPACE;
+  return MOE_OK;
+}
+
+// Element types of the maps: 2-byte operands, or the weight gradient's output.
+CUtensorMapDataType map_type(int type) {
+  return type == MOE_TYPE_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+         : type == MOE_TYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+// Rows of a token matrix: boxes of 64 columns x box_rows, 128-byte swizzle.
+bool make_rows_map(CUtensorMap* m, int type, const void* base, int64_t width, int64_t rows, int64_t ld,
+                   uint32_t box_rows) {
+  auto fn = moe::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, map_type(type), 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [G, N, K] matrices: boxes of 128 bytes of K x box_rows of N.
+bool make_matrix_map(CUtensorMap* m, int type, const void* base, int64_t G, int64_t N, int64_t K, uint32_t box_rows) {
+  auto fn = moe::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t size = type == MOE_TYPE_FP32 ? 4 : 2;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(G)};
+  cuuint64_t strides[2] = {dims[0] * size, dims[0] * dims[1] * size};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, map_type(type), 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+moe::GroupedGemmArgs gemm_args(const moe_grouped_shape* s, const Layout& L, void* ws) {
+  moe::GroupedGemmArgs a{};
+  a.start = at<int32_t>(ws, L.start);
+  a.count = at<int32_t>(ws, L.count);
+  a.unit_off = at<int32_t>(ws, L.unit_off);
+  a.err = at<int32_t>(ws, 0);
+  a.partials = at<float>(ws, L.partials);
+  a.flags = at<int32_t>(ws, L.flags);
+  a.G = s->groups;
+  a.tiles_n = 1;
+  a.fp16 = s->type == MOE_TYPE_FP16;
+  return a;
+}
+
+moe::GroupedPlanArgs plan_args(const moe_grouped_shape* s, const Layout& L, void* ws, const int32_t* offsets,
+                               const int32_t* counts) {
+  moe::GroupedPlanArgs p{};
+  p.offsets = offsets;
+  p.counts = counts;
+  p.G = s->groups;
+  p.rows = s->rows;
+  p.start = at<int32_t>(ws, L.start);
+  p.count = at<int32_t>(ws, L.count);
+  p.unit_off = at<int32_t>(ws, L.unit_off);
+  p.err = at<int32_t>(ws, 0);
+  p.flags = at<int32_t>(ws, L.flags);
+  p.n_flags = kFlagInts;
+  return p;
+}
+
+// The tile plan follows the rows a group can be expected to hold: up to 16,
+// the product is bound by streaming the weights once (32-row units, stream-K),
+// above that by reuse of the weight tiles (256-row units on CTA pairs).
+GroupedPlan choose_plan(const moe_grouped_shape* s) {
+  return s->rows <= int64_t(16) * s->groups ? GroupedPlan::kSmall : GroupedPlan::kLarge;
+}
+
+// forward (F = N features, R = K) and input gradient (F = K, R = N)
+moe_status rows_product(GroupedOp op, const moe_grouped_shape* s, const void* in, int64_t ldin, const void* w,
+                        const int32_t* offsets, const int32_t* counts, void* out, int64_t ldout, void* ws,
+                        size_t ws_bytes, moe_stream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  const int F = op == GroupedOp::kForward ? s->N : s->K, R = op == GroupedOp::kForward ? s->K : s->N;
+  if ((st = check_rows(in, s->rows, ldin, R)) != MOE_OK) return st;
+  if ((st = check_rows(out, s->rows, ldout, F)) != MOE_OK) return st;
+  if (!w || !aligned(w, 16)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_call(s, offsets, counts, ws, ws_bytes)) != MOE_OK) return st;
+  const GroupedPlan plan = choose_plan(s);
+  const int bn = moe::grouped_bn(plan), tile = moe::grouped_tile(plan);
+  const int tiles = (F + tile - 1) / tile;
+  if ((s->rows / bn + s->groups) * tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (s->rows == 0) return MOE_OK;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  CUtensorMap tw, tx;
+  if (!make_matrix_map(&tw, s->type, w, s->groups, s->N, s->K, op == GroupedOp::kForward ? 128 : 64) ||
+      !make_rows_map(&tx, s->type, in, R, s->rows, ldin, static_cast<uint32_t>(moe::grouped_tok_box(plan))))
+    return MOE_ERR_CUDA;
+  const Layout L = make_layout(s->groups);
+  moe::GroupedPlanArgs p = plan_args(s, L, ws, offsets, counts);
+  p.bn = bn;
+  p.tiles = tiles;
+  moe::GroupedGemmArgs a = gemm_args(s, L, ws);
+  a.out = out;
+  a.ldo = ldout;
+  a.F = F;
+  a.R = R;
+  a.tiles = tiles;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (moe::launch_grouped_plan(p, tx, tx, cs) != cudaSuccess ||
+      moe::launch_grouped_gemm(op, plan, tw, tx, a, sms, cs) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+moe_status swiglu_check(int32_t type, int64_t rows, int32_t I) {
+  if ((type != MOE_TYPE_BF16 && type != MOE_TYPE_FP16) || rows < 0 || I <= 0) return MOE_ERR_INVALID_ARG;
+  if (I % 8 != 0 || I > kMaxDim || rows > kMaxRows || rows * (I / 8) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_workspace_size(const moe_grouped_shape* shape, size_t* bytes) {
+  const moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = make_layout(shape->groups).total;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm(const moe_grouped_shape* shape, const void* x, int64_t ldx, const void* w,
+                            const int32_t* offsets, const int32_t* counts, void* y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, moe_stream_t stream) {
+  return rows_product(GroupedOp::kForward, shape, x, ldx, w, offsets, counts, y, ldy, workspace, workspace_bytes,
+                      stream);
+}
+
+moe_status moe_grouped_gemm_dgrad(const moe_grouped_shape* shape, const void* dy, int64_t lddy, const void* w,
+                                  const int32_t* offsets, const int32_t* counts, void* dx, int64_t lddx,
+                                  void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  return rows_product(GroupedOp::kDgrad, shape, dy, lddy, w, offsets, counts, dx, lddx, workspace, workspace_bytes,
+                      stream);
+}
+
+moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy, int64_t lddy, const void* x,
+                                  int64_t ldx, const int32_t* offsets, const int32_t* counts, void* dw,
+                                  int32_t dw_type, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                  moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  const moe_grouped_shape* s = shape;
+  if ((st = check_rows(dy, s->rows, lddy, s->N)) != MOE_OK) return st;
+  if ((st = check_rows(x, s->rows, ldx, s->K)) != MOE_OK) return st;
+  if (!dw || !aligned(dw, 16)) return MOE_ERR_INVALID_ARG;
+  if (dw_type != s->type && dw_type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
+  if (accumulate && dw_type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
+  if ((st = check_call(s, offsets, counts, workspace, workspace_bytes)) != MOE_OK) return st;
+  const int tile = moe::kWgradTile;
+  const int64_t tiles_m = (s->N + tile - 1) / tile, tiles_n = (s->K + tile - 1) / tile;
+  if (tiles_m * tiles_n * s->groups >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (s->rows == 0 && accumulate) return MOE_OK;
+  // no rows: every group is empty and dw becomes zero; nothing is loaded through the row maps
+  const int64_t map_rows = s->rows > 0 ? s->rows : 1;
+  CUtensorMap tdy, tx, tdw;
+  if (!make_rows_map(&tdy, s->type, s->rows > 0 ? dy : dw, s->N, map_rows, lddy, 64) ||
+      !make_rows_map(&tx, s->type, s->rows > 0 ? x : dw, s->K, map_rows, ldx, 64) ||
+      !make_matrix_map(&tdw, dw_type, dw, s->groups, s->N, s->K, 32))
+    return MOE_ERR_CUDA;
+  const Layout L = make_layout(s->groups);
+  moe::GroupedPlanArgs p = plan_args(s, L, workspace, offsets, counts);
+  p.bn = 0;
+  p.tiles = static_cast<int>(tiles_m * tiles_n);
+  p.skip_empty = accumulate != 0;
+  p.n_flags = 0;
+  p.maps = at<CUtensorMap>(workspace, L.maps);
+  moe::GroupedGemmArgs a = gemm_args(s, L, workspace);
+  a.maps = p.maps;
+  a.F = s->N;
+  a.C = s->K;
+  a.tiles = p.tiles;
+  a.tiles_n = static_cast<int>(tiles_n);
+  a.out_fp32 = dw_type == MOE_TYPE_FP32;
+  a.accumulate = accumulate != 0;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (moe::launch_grouped_plan(p, tdy, tx, cs) != cudaSuccess || moe::launch_grouped_wgrad(tdw, a, cs) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+moe_status moe_swiglu(int32_t type, int64_t rows, int32_t I, const void* h, int64_t ldh, void* act, int64_t ldact,
+                      moe_stream_t stream) {
+  moe_status st = swiglu_check(type, rows, I);
+  if (st != MOE_OK) return st;
+  if ((st = check_rows(h, rows, ldh, 2 * static_cast<int64_t>(I))) != MOE_OK) return st;
+  if ((st = check_rows(act, rows, ldact, I)) != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  return moe::launch_swiglu(type == MOE_TYPE_FP16, h, ldh, act, ldact, rows, I,
+                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+moe_status moe_swiglu_grad(int32_t type, int64_t rows, int32_t I, const void* h, int64_t ldh, const void* dact,
+                           int64_t lddact, void* dh, int64_t lddh, moe_stream_t stream) {
+  moe_status st = swiglu_check(type, rows, I);
+  if (st != MOE_OK) return st;
+  if ((st = check_rows(h, rows, ldh, 2 * static_cast<int64_t>(I))) != MOE_OK) return st;
+  if ((st = check_rows(dact, rows, lddact, I)) != MOE_OK) return st;
+  if ((st = check_rows(dh, rows, lddh, 2 * static_cast<int64_t>(I))) != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  return moe::launch_swiglu_grad(type == MOE_TYPE_FP16, h, ldh, dact, lddact, dh, lddh, rows, I,
+                                 reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

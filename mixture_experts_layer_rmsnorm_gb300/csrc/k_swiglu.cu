@@ -1,0 +1,98 @@
+// k_swiglu.cu -- SwiGLU of separate rows and its gradient, the step between
+// the gate/up and the down product of an expert ("4 · La fusion de noyaux",
+// §4.2 "GEMM + GEMM"; inside the layer it is the gate/up GEMM's epilogue).
+// A row of h holds gate [0, I) and up [I, 2I).
+//   forward   a = g s u                       with s = sigmoid(g)
+//   gradient  dg = da u s (1 + g (1 - s)),  du = da g s
+// s and 1 - s come from e = exp(-|g|), which lies in (0, 1]: no overflow, no
+// cancellation of 1 - s for large g, and the divisor 1 + e is in [1, 2].
+// fp32 inside, one rounding per output.
+//
+// HBM-bound: 3 (forward) or 5 (gradient) elements moved per output feature.  A
+// thread takes 8 features (16-byte accesses) of two places far enough apart
+// that a warp's accesses stay contiguous, all loads before the first use.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "grouped_elementwise.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kPer = 2;
+
+struct Sig {
+  float s, t;  // sigmoid(g), 1 - sigmoid(g)
+};
+
+__device__ __forceinline__ Sig sigmoid(float g) {
+  const float e = __expf(-fabsf(g));
+  const float r = __fdividef(1.0f, 1.0f + e), er = e * r;
+  return g >= 0.0f ? Sig{r, er} : g < 0.0f ? Sig{er, r} : Sig{g + 0.5f, g + 0.5f};  // (NaN stays NaN)
+}
+
+template <bool FP16, bool GRAD>
+__global__ void __launch_bounds__(kThreads)
+    swiglu_kernel(const uint16_t* h, int64_t ldh, const uint16_t* da, int64_t ldda,
+                  uint16_t* out, int64_t ldo, uint32_t I, uint32_t n) {
+  const uint32_t per_row = I / 8, first = blockIdx.x * (kThreads * kPer) + threadIdx.x;
+  uint4 g[kPer], u[kPer], d[kPer];
+  uint32_t row[kPer], col[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const uint32_t at = first + i * kThreads;
+    if (at >= n) break;
+    row[i] = at / per_row;
+    col[i] = (at - row[i] * per_row) * 8;
+    const uint16_t* p = h + row[i] * ldh + col[i];
+    g[i] = __ldcs(reinterpret_cast<const uint4*>(p));
+    u[i] = __ldcs(reinterpret_cast<const uint4*>(p + I));
+    if (GRAD) d[i] = __ldcs(reinterpret_cast<const uint4*>(da + row[i] * ldda + col[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (first + i * kThreads >= n) break;
+    float gv[8], uv[8], dv[8], o[8], o2[8];
+    unpack8<FP16>(g[i], gv);
+    unpack8<FP16>(u[i], uv);
+    if (GRAD) unpack8<FP16>(d[i], dv);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const Sig s = sigmoid(gv[j]);
+      if (GRAD) {
+        o[j] = dv[j] * uv[j] * (s.s * (1.0f + gv[j] * s.t));
+        o2[j] = dv[j] * (gv[j] * s.s);
+      } else {
+        o[j] = gv[j] * s.s * uv[j];
+      }
+    }
+    uint16_t* p = out + row[i] * ldo + col[i];
+    *reinterpret_cast<uint4*>(p) = pack8<FP16>(o);
+    if (GRAD) *reinterpret_cast<uint4*>(p + I) = pack8<FP16>(o2);
+  }
+}
+
+template <bool GRAD>
+cudaError_t launch(bool fp16, const void* h, int64_t ldh, const void* da, int64_t ldda, void* out, int64_t ldo,
+                   int64_t rows, int I, cudaStream_t stream) {
+  const uint32_t n = static_cast<uint32_t>(rows * (I / 8));
+  const unsigned blocks = (n + kThreads * kPer - 1) / (kThreads * kPer);
+  auto kernel = fp16 ? swiglu_kernel<true, GRAD> : swiglu_kernel<false, GRAD>;
+  kernel<<<blocks, kThreads, 0, stream>>>(static_cast<const uint16_t*>(h), ldh, static_cast<const uint16_t*>(da), ldda,
+                                          static_cast<uint16_t*>(out), ldo, static_cast<uint32_t>(I), n);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu(bool fp16, const void* h, int64_t ldh, void* act, int64_t ldact, int64_t rows, int I,
+                          cudaStream_t stream) {
+  return launch<false>(fp16, h, ldh, nullptr, 0, act, ldact, rows, I, stream);
+}
+
+cudaError_t launch_swiglu_grad(bool fp16, const void* h, int64_t ldh, const void* dact, int64_t lddact, void* dh,
+                               int64_t lddh, int64_t rows, int I, cudaStream_t stream) {
+  return launch<true>(fp16, h, ldh, dact, lddact, dh, lddh, rows, I, stream);
+}
+
+}  // namespace moe

@@ -10,15 +10,14 @@
 // prefill tiles (128 / 256 tokens per unit).
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
 #include "../../include/moe.h"
 #include "moe_forward_impl.h"
 #include "moe_kernels.cuh"
+#include "tensor_map.h"
 
 namespace {
 
@@ -125,19 +124,7 @@ moe_status check_shape_mx(const moe_shape* s) {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
+using moe::encode_fn;
 
 // 2-D bf16 row-major [rows, inner] tensor, boxes of 64 x box_rows, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows) {

@@ -1,0 +1,330 @@
+"""The grouped products and their gradients, and SwiGLU, against their definitions in 64 bits.
+
+Tolerances.  A product of two 16-bit operands is exact in fp32 (bf16: 16 bits,
+fp16: 22 bits).  One tensor-core step adds 16 products to the fp32 accumulator
+and may cut each of the 17 terms after the last bit of the largest, which is at
+most S = sum |a||b|: an error of 17 ulps of S, 17 * 2^-23 S, per 16 terms of the
+reduction, R * 2^-23 * 17/16 * S in all (R rounded up to whole steps); stream-K
+adds one fp32 rounding for each of at most 256 partial sums.  The output is
+rounded once: half a step, eps/2 relative, or half a subnormal step (2^-25 for
+fp16).  So |err| <= eps/2 |y| + (17/16 (R + 16) + 256) 2^-23 S + 2^-25.
+"""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_rmsnorm_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def bound(want, s, r, dtype):
+    return half_step(dtype) * want.abs() + (17 / 16 * (r + 16) + 256) * 2.0 ** -23 * s + 2.0 ** -25
+
+
+def check(got, want, s, r):
+    err = (got.double() - want).abs()
+    lim = bound(want, s, r, got.dtype)
+    worst = (err - lim).max().item() if err.numel() else 0.0
+    assert worst <= 0, f"error above its bound by {worst:.3e} (largest error {err.max().item():.3e})"
+
+
+class Lists:
+    """Groups of the given counts; gap: rows left free behind every group (they hold NaN); tail: rows behind the last."""
+
+    def __init__(self, counts, gap=0, tail=0):
+        held = [c + gap for c in counts]
+        off = np.concatenate([[0], np.cumsum(held)])
+        self.spans = [(int(o), int(o + c)) for o, c in zip(off, counts)]
+        self.offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+        self.counts = torch.tensor(counts, dtype=torch.int32, device="cuda") if gap else None
+        self.rows = int(off[-1]) + tail
+        self.groups = len(counts)
+        self.free = torch.ones(self.rows, dtype=torch.bool, device="cuda")
+        for a, b in self.spans:
+            self.free[a:b] = False
+
+    def matrix(self, gen, width, dtype, pad=0, scale=1.0):
+        full = torch.randn((self.rows, width + pad), generator=gen, device="cuda").mul_(scale).to(dtype)
+        full[self.free] = float("nan")
+        return full[:, :width]
+
+    def blank(self, width, dtype, pad=0):
+        return torch.full((self.rows, width + pad), 7.0, dtype=dtype, device="cuda")[:, :width]
+
+
+# counts, N, K, dtype, gap, tail, pad: every tile plan, single rows, empty groups, chunk edges (32, 256), sizes that are no
+# multiple of a tile, strided matrices, more groups than the shared-memory table holds
+CASES = {
+    "one": ([1], 8, 8, BF16, 0, 0, 0),
+    "row_of_many": ([1], 1000, 4104, FP16, 0, 3, 0),
+    "small_edges": ([0, 1, 15, 16, 17, 31, 32, 33, 0, 1, 1, 0], 264, 200, BF16, 0, 0, 8),
+    "small_stream_k": ([3, 0, 5, 8, 0, 1, 2, 7], 1024, 2048, BF16, 3, 5, 0),
+    "small_fp16_gap": ([9, 12, 0, 0, 31, 2, 1], 392, 1032, FP16, 5, 1, 16),
+    "large_edges": ([255, 256, 257, 0, 1, 300, 511, 513], 520, 328, BF16, 0, 0, 0),
+    "large_fp16": ([100, 0, 700, 33], 1416, 640, FP16, 7, 9, 24),
+    "large_skewed": ([1500, 1, 0, 2, 40], 256, 128, BF16, 1, 0, 0),
+    "many_groups": ([(7 * i) % 5 for i in range(300)], 136, 72, BF16, 0, 2, 0),
+    "most_groups": ([(i * i) % 41 for i in range(1024)], 64, 64, FP16, 0, 0, 0),
+    "no_rows_at_all": ([0, 0, 0], 128, 64, BF16, 0, 4, 0),
+}
+
+
+def make(name):
+    counts, n, k, dtype, gap, tail, pad = CASES[name]
+    gen = torch.Generator(device="cuda").manual_seed(len(name))
+    lists = Lists(counts, gap, tail)
+    x = lists.matrix(gen, k, dtype, pad)
+    dy = lists.matrix(gen, n, dtype, pad, 0.25)
+    w = (torch.randn((lists.groups, n, k), generator=gen, device="cuda") * 0.05).to(dtype)
+    return lists, x, dy, w, binding.GroupedProducts(lists.groups, n, k, dtype), pad
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_forward(name):
+    lists, x, _, w, gp, pad = make(name)
+    y = lists.blank(gp.N, x.dtype, pad)
+    assert gp.forward(x, w, lists.offsets, lists.counts, y=y) is y
+    assert gp.device_status()[0] == binding.MOE_OK
+    for g, (a, b) in enumerate(lists.spans):
+        xd, wd = x[a:b].double(), w[g].double()
+        check(y[a:b], xd @ wd.T, xd.abs() @ wd.abs().T, gp.K)
+    assert torch.all(y[lists.free] == 7.0)
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_input_gradient(name):
+    lists, _, dy, w, gp, pad = make(name)
+    dx = lists.blank(gp.K, dy.dtype, pad)
+    gp.dgrad(dy, w, lists.offsets, lists.counts, dx=dx)
+    assert gp.device_status()[0] == binding.MOE_OK
+    for g, (a, b) in enumerate(lists.spans):
+        dd, wd = dy[a:b].double(), w[g].double()
+        check(dx[a:b], dd @ wd, dd.abs() @ wd.abs(), gp.N)
+    assert torch.all(dx[lists.free] == 7.0)
+
+
+@pytest.mark.parametrize("out", ["same", "fp32", "accumulate"])
+@pytest.mark.parametrize("name", CASES)
+def test_weight_gradient(name, out):
+    lists, x, dy, w, gp, pad = make(name)
+    if out == "accumulate":
+        start = torch.randn(w.shape, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+        dw = start.clone()
+        gp.wgrad(dy, x, lists.offsets, lists.counts, dw=dw, accumulate=True)
+    else:
+        dw = gp.wgrad(dy, x, lists.offsets, lists.counts, dtype=FP32 if out == "fp32" else None)
+    assert gp.device_status()[0] == binding.MOE_OK
+    for g, (a, b) in enumerate(lists.spans):
+        dd, xd = dy[a:b].double(), x[a:b].double()
+        want, s = dd.T @ xd, dd.abs().T @ xd.abs()
+        if out == "accumulate":  # one fp32 addition more
+            want, s = want + start[g].double(), s + start[g].abs().double()
+        check(dw[g], want, s, b - a)
+
+
+def test_equal_groups_without_lists():
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    gp = binding.GroupedProducts(3, 136, 264, BF16)
+    x = torch.randn((3 * 35, 264), generator=gen, device="cuda").to(BF16)
+    dy = torch.randn((3 * 35, 136), generator=gen, device="cuda").to(BF16)
+    w = (torch.randn((3, 136, 264), generator=gen, device="cuda") * 0.05).to(BF16)
+    y, dx, dw = gp.forward(x, w), gp.dgrad(dy, w), gp.wgrad(dy, x, dtype=FP32)
+    xd, dd, wd = x.double().view(3, 35, -1), dy.double().view(3, 35, -1), w.double()
+    check(y.view(3, 35, -1), xd @ wd.mT, xd.abs() @ wd.abs().mT, 264)
+    check(dx.view(3, 35, -1), dd @ wd, dd.abs() @ wd.abs(), 136)
+    check(dw, dd.mT @ xd, dd.abs().mT @ xd.abs(), 35)
+
+
+def test_nan_and_inf_stay_in_their_row_and_group():
+    lists = Lists([40, 21, 64])
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x, dy = lists.matrix(gen, 192, BF16), lists.matrix(gen, 136, BF16)
+    w = (torch.randn((3, 136, 192), generator=gen, device="cuda") * 0.05).to(BF16)
+    gp = binding.GroupedProducts(3, 136, 192, BF16)
+    clean = [t.clone() for t in (gp.forward(x, w, lists.offsets), gp.dgrad(dy, w, lists.offsets),
+                                 gp.wgrad(dy, x, lists.offsets))]
+    x[40, 3], x[60, 5], dy[60, 7], dy[40, 1] = float("nan"), float("inf"), float("nan"), float("-inf")
+    y, dx, dw = gp.forward(x, w, lists.offsets), gp.dgrad(dy, w, lists.offsets), gp.wgrad(dy, x, lists.offsets)
+    for got, ref in ((y, clean[0]), (dx, clean[1])):
+        hit = torch.zeros(lists.rows, dtype=torch.bool, device="cuda")
+        hit[[40, 60]] = True
+        assert torch.equal(got[~hit], ref[~hit])
+        assert not torch.isfinite(got[hit]).any()
+    assert torch.equal(dw[0], clean[2][0]) and torch.equal(dw[2], clean[2][2])
+    assert torch.isnan(dw[1, :, 3]).all() and torch.isnan(dw[1, 7]).all()
+
+
+@pytest.mark.parametrize("offsets,counts,group", [
+    ([0, 10, 8, 30], None, 1),            # decreasing
+    ([-1, 10, 20, 30], None, 0),          # negative
+    ([0, 10, 20, 41], None, 2),           # behind the last row
+    ([0, 10, 20, 30], [10, 11, 3], 1),    # into the next group
+    ([0, 10, 20, 30], [10, 10, -1], 2),   # a negative count
+])
+def test_bad_lists_write_nothing_and_are_reported(offsets, counts, group):
+    gp = binding.GroupedProducts(3, 64, 64, BF16)
+    x = torch.ones((40, 64), dtype=BF16, device="cuda")
+    w = torch.ones((3, 64, 64), dtype=BF16, device="cuda")
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    cnt = None if counts is None else torch.tensor(counts, dtype=torch.int32, device="cuda")
+    outs = [torch.full((40, 64), 7.0, dtype=BF16, device="cuda") for _ in range(2)] + [torch.full_like(w, 7.0)]
+    for call, out in ((lambda o: gp.forward(x, w, off, cnt, y=o), outs[0]),
+                      (lambda o: gp.dgrad(x, w, off, cnt, dx=o), outs[1]),
+                      (lambda o: gp.wgrad(x, x, off, cnt, dw=o), outs[2])):
+        call(out)
+        st, detail = gp.device_status()
+        assert st == binding.MOE_ERR_DEVICE and detail[1] == 9 and detail[2] == group
+        assert torch.all(out == 7.0)
+    good = torch.tensor([0, 10, 20, 30], dtype=torch.int32, device="cuda")
+    gp.forward(x, w, good, y=outs[0])  # the next call clears the error
+    assert gp.device_status()[0] == binding.MOE_OK and torch.all(outs[0][:30] == 64.0)
+
+
+def test_calls_repeat_bit_for_bit_and_replay_from_a_graph_on_new_lists():
+    lists = Lists([5, 0, 9, 2])
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x, dy = lists.matrix(gen, 1024, BF16), lists.matrix(gen, 512, BF16)
+    w = (torch.randn((4, 512, 1024), generator=gen, device="cuda") * 0.05).to(BF16)
+    gp = binding.GroupedProducts(4, 512, 1024, BF16)
+    off = lists.offsets.clone()
+    y, dx = torch.zeros_like(dy), torch.zeros_like(x)
+    dw = torch.zeros(w.shape, device="cuda")
+
+    def step():
+        gp.forward(x, w, off, y=y)
+        gp.dgrad(dy, w, off, dx=dx)
+        gp.wgrad(dy, x, off, dw=dw)
+
+    step()
+    first = [t.clone() for t in (y, dx, dw)]
+    step()
+    assert all(torch.equal(a, b) for a, b in zip(first, (y, dx, dw)))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    off.copy_(torch.tensor([0, 0, 12, 16, 16], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    replayed = [t.clone() for t in (y, dx, dw)]
+    step()
+    assert all(torch.equal(a, b) for a, b in zip(replayed, (y, dx, dw)))
+    with torch.cuda.stream(side):
+        side.wait_stream(torch.cuda.default_stream())
+        step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(replayed, (y, dx, dw)))
+
+
+# ------------------------------------------------------------------ SwiGLU
+
+
+@pytest.mark.parametrize("rows,i,dtype,pad", [(1, 8, BF16, 0), (7, 136, FP16, 8), (301, 1408, BF16, 16),
+                                              (64, 4096, FP16, 0), (5000, 24, BF16, 0)])
+def test_swiglu_and_its_gradient(rows, i, dtype, pad):
+    """fp32 inside.  exp(-|g|) is 2 ulps + |g| 2^-24 (its scaled argument is rounded), the quotient 2, each of at most six
+    further operations half: relative errors below (|g| + 16) 2^-23 of the terms, then one rounding of the output.  Below
+    fp32's smallest normal number the intermediate e may be cut: an absolute 2^-126 times the other factors."""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    h = (torch.randn((rows, 2 * i + pad), generator=gen, device="cuda") * 3).to(dtype)[:, :2 * i]
+    edge = torch.tensor([0.0, -0.0, 40.0, -40.0, 88.0, -88.0, 300.0, -300.0], device="cuda").to(dtype)
+    h[0, :8] = edge
+    da = torch.randn((rows, i), generator=gen, device="cuda").to(dtype)
+    g, u, d = h[:, :i].double(), h[:, i:].double(), da.double()
+    s, t = torch.special.expit(g), torch.special.expit(-g)
+    rel = (g.abs() + 16) * 2.0 ** -23
+    tiny = 2.0 ** -126 * 400 * (u.abs() + 1) * (d.abs() + 1) + 2.0 ** -25 * (dtype == FP16) + 2.0 ** -134
+
+    def within(got, want, size):
+        err = (got.double() - want).abs()
+        lim = half_step(dtype) * (want.abs() + rel * size) + rel * size + tiny
+        assert (err <= lim).all(), f"largest error {err.max().item():.3e}"
+
+    within(binding.swiglu(h), g * s * u, (g * s * u).abs())
+    for dh in (binding.swiglu_grad(h, da), binding.swiglu_grad(h.clone(), da)):
+        within(dh[:, :i], d * u * s * (1 + g * t), (d * u).abs() * s * (1 + g.abs() * t))
+        within(dh[:, i:], d * g * s, (d * g * s).abs())
+    inplace = h.clone()
+    assert torch.equal(binding.swiglu_grad(inplace, da, dh=inplace), dh)
+
+
+def test_swiglu_keeps_nan_and_infinities():
+    h = torch.tensor([[float("nan"), 1.0, float("inf"), 2.0, float("-inf"), 0.0, 1.0, 1.0] + [1.0] * 8], device="cuda")
+    h[0, 9] = float("nan")
+    a = binding.swiglu(h.to(BF16)).float()[0]
+    assert torch.isnan(a[0]) and torch.isnan(a[1]) and a[2] == float("inf") and torch.isnan(a[4])
+    assert torch.isfinite(a[[3, 5, 6, 7]]).all()
+
+
+# ------------------------------------------------------------------ a training step of the experts
+
+
+def test_training_step_of_the_experts():
+    """Gate/up product, SwiGLU, down product, and every gradient, over the router's own lists (16-row padding, counts);
+    against 64 bits with each stored tensor rounded as the chain rounds it, and the loss's slope against differences."""
+    T, H, I, E, top_k = 50, 256, 192, 6, 2
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    xs = torch.randn((T, H), generator=gen, device="cuda").to(BF16)
+    g_norm = torch.ones(H, dtype=BF16, device="cuda")
+    w_router = torch.randn((E, H), generator=gen, device="cuda") * 0.02
+    w13 = (torch.randn((E, 2 * I, H), generator=gen, device="cuda") * 0.05).to(BF16)
+    w2 = (torch.randn((E, H, I), generator=gen, device="cuda") * 0.05).to(BF16)
+    layer = binding.MoeLayer(g_norm, w_router, w13, w2, top_k, max_tokens=T)
+    layer.forward(xs)
+    h = layer.view_tensor(T, "h", BF16, (T, H)).clone()
+    counts = layer.view_tensor(T, "counts", torch.int32, (E,)).clone()
+    offsets = layer.view_tensor(T, "offsets", torch.int32, (E + 1,)).clone()
+    p_max = layer.views(T).P_max
+    ids = layer.view_tensor(T, "sorted_ids", torch.int32, (p_max,)).clone()
+    rows = torch.cat([torch.arange(o, o + c) for o, c in zip(offsets.tolist(), counts.tolist())]).cuda()
+    x = torch.full((p_max, H), float("nan"), dtype=BF16, device="cuda")
+    x[rows] = h[(ids[rows] // top_k).long()]
+
+    up, down = binding.GroupedProducts(E, 2 * I, H, BF16), binding.GroupedProducts(E, H, I, BF16)
+    hid = up.forward(x, w13, offsets, counts, y=torch.zeros((p_max, 2 * I), dtype=BF16, device="cuda"))
+    act = binding.swiglu(hid)
+    y = down.forward(act, w2, offsets, counts, y=torch.zeros((p_max, H), dtype=BF16, device="cuda"))
+    # the layer computes the same rows
+    out_rows = layer.view_tensor(T, "out_rows", BF16, (p_max, H))
+    ref = out_rows[rows].double()
+    assert (y[rows].double() - ref).norm() <= 2 * half_step(BF16) * ref.norm()
+
+    dy = torch.randn((p_max, H), generator=gen, device="cuda").to(BF16)
+    dact = down.dgrad(dy, w2, offsets, counts, dx=torch.zeros((p_max, I), dtype=BF16, device="cuda"))
+    dw2 = down.wgrad(dy, act, offsets, counts, dtype=FP32)
+    dhid = binding.swiglu_grad(hid, dact)
+    dx = up.dgrad(dhid, w13, offsets, counts, dx=torch.zeros((p_max, H), dtype=BF16, device="cuda"))
+    dw13 = up.wgrad(dhid, x, offsets, counts, dtype=FP32)
+
+    group = torch.repeat_interleave(torch.arange(E, device="cuda"), counts.long())
+    leaf = [t.double().requires_grad_() for t in (x[rows], w13, w2)]
+
+    def loss(xd, w13d, w2d):
+        hd = torch.einsum("ph,pnh->pn", xd, w13d[group])
+        ad = torch.nn.functional.silu(hd[:, :I]) * hd[:, I:]
+        return (torch.einsum("pi,phi->ph", ad, w2d[group]) * dy[rows].double()).sum()
+
+    loss(*leaf).backward()
+    # five roundings to bf16 at most lie between the inputs and a gradient (hid, act or dact, dhid, the output), each at
+    # most half a step of its tensor's norm; a product passes relative norms on with a factor of order one (here < 2)
+    for got, want in ((dx[rows], leaf[0].grad), (dw13, leaf[1].grad), (dw2, leaf[2].grad)):
+        rel = ((got.double() - want).norm() / want.norm()).item()
+        assert rel <= 5 * 2 * half_step(BF16), rel
+    # differences: the loss along the gradient's own direction
+    with torch.no_grad():
+        for at, got in ((0, dx[rows]), (1, dw13), (2, dw2)):
+            step = got.double() / got.double().norm()
+            args = [t.detach() for t in leaf]
+            eps = 1e-4
+            plus, minus = list(args), list(args)
+            plus[at], minus[at] = args[at] + eps * step, args[at] - eps * step
+            slope = ((loss(*plus) - loss(*minus)) / (2 * eps)).item()
+            assert abs(slope - got.double().norm().item()) <= 5 * 2 * half_step(BF16) * abs(slope) + 1e-5
