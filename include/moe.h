@@ -350,8 +350,8 @@ MOE_API moe_status moe_workspace_views(const moe_shape* shape, void* workspace, 
  * (MOE_ERR_TIMEOUT / MOE_ERR_DEVICE).  detail (may be NULL) receives the
  * four raw int32 words: the code, the id of the kernel that recorded it
  * (1 norm/router, 2 top-k, 3 align, 4 gather, 5 gate/up GEMM, 6 down GEMM,
- * 7 combine, 8 self-test, 9 grouped products' tables, 10 grouped GEMM), for
- * the expert GEMMs a bit mask of the waits that
+ * 7 combine, 8 self-test, 9 grouped products' tables, 10 grouped GEMM,
+ * 11 grouped 4-bit GEMM), for the expert GEMMs a bit mask of the waits that
  * ran out (bit 1 producer: ring slot free; 2 MMA: accumulator free; 3 MMA:
  * ring slot loaded; 4 epilogue: accumulator complete; 5 epilogue: stream-K
  * partial sums; 6 epilogue: fused-combine rendezvous; 7 MMA: a stage's scales
@@ -578,6 +578,63 @@ MOE_API moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const 
                                           int64_t ldx, const int32_t* offsets, const int32_t* counts, void* dw,
                                           int32_t dw_type, int32_t accumulate, void* workspace,
                                           size_t workspace_bytes, moe_stream_t stream);
+
+/* ---- Rows in 4 bits, and their grouped product -------------------------
+ * MXFP4 and NVFP4 of any rows (the formats of the layer's weights, above; here
+ * in plain row order), back, and the forward product of the grouped products
+ * on such operands (tcgen05.mma kind::mxf4 / kind::mxf4nvf4, fp32 accumulation).
+ *   codes   [rows, K / 2] bytes, two E2M1 codes each, element 2i in the low nibble
+ *   scales  512-byte tiles of 128 rows x 4 blocks of K (128 elements for MXFP4, 64
+ *           for NVFP4): byte r*16 + 4*j + b = the scale of row 32*j + r, block b;
+ *           the ceil(K / 128) (ceil(K / 64)) tiles of one tile row adjacent, blocks past K
+ *           zero.  A group's rows start a tile row of their own: for equal
+ *           groups of R rows (offsets NULL; weights [groups, N, K] are groups
+ *           of N rows) group g starts at tile row g * ceil(R / 128), for listed
+ *           ones at floor(offsets[g] / 128) + g.
+ *   gscale  NVFP4's fp32 scales: one per row (MOE_SCALE_PER_ROW, [rows]) or
+ *           one per group (MOE_SCALE_PER_GROUP, [groups]); unused (NULL) for MXFP4
+ * MXFP4: a block with a NaN or an infinity gets the NaN scale 255; NVFP4: a row
+ * (group) with one gets a NaN gscale; what they stand for is NaN.
+ * offsets, counts, rows, groups, strides and alignment as for the grouped
+ * products; K a multiple of 32 (else MOE_ERR_UNSUPPORTED); codes and scales
+ * 16-byte aligned.  Rows of no group are skipped; lists that break the rules
+ * are not reported by these two calls (rows they misplace are skipped), but by
+ * the product. */
+#define MOE_FORMAT_MXFP4 0
+#define MOE_FORMAT_NVFP4 1
+#define MOE_SCALE_PER_ROW 0
+#define MOE_SCALE_PER_GROUP 1
+
+typedef struct {
+  int32_t format;
+  int32_t groups;
+  int64_t rows;
+  int32_t K;
+} moe_fp4_shape;
+
+/* Byte sizes of codes and scales, enough for any lists.  Host only. */
+MOE_API moe_status moe_fp4_sizes(const moe_fp4_shape* shape, size_t* codes, size_t* scales);
+
+/* src [rows, K] of src_type (MOE_TYPE_*) -> codes, scales, gscale. */
+MOE_API moe_status moe_fp4_quantize(const moe_fp4_shape* shape, int32_t src_type, const void* src, int64_t ldsrc,
+                                    const int32_t* offsets, const int32_t* counts, uint8_t* codes, uint8_t* scales,
+                                    float* gscale, int32_t gscale_per, moe_stream_t stream);
+
+/* The values the codes stand for, rounded to dst_type, into dst [rows, K]. */
+MOE_API moe_status moe_fp4_dequantize(const moe_fp4_shape* shape, const uint8_t* codes, const uint8_t* scales,
+                                      const float* gscale, int32_t gscale_per, const int32_t* offsets,
+                                      const int32_t* counts, int32_t dst_type, void* dst, int64_t lddst,
+                                      moe_stream_t stream);
+
+/* y[p, :] = x[p, :] w_g^T as moe_grouped_gemm (lists, workspace of
+ * moe_grouped_workspace_size(), errors; GEMM kernel id 11), with x quantized
+ * for the same lists (NVFP4: x_gscale per row) and w as groups of N rows without
+ * lists (NVFP4: w_gscale per group).  shape->type: y's type. */
+MOE_API moe_status moe_fp4_gemm(const moe_grouped_shape* shape, int32_t format, const uint8_t* x_codes,
+                                const uint8_t* x_scales, const float* x_gscale, const uint8_t* w_codes,
+                                const uint8_t* w_scales, const float* w_gscale, const int32_t* offsets,
+                                const int32_t* counts, void* y, int64_t ldy, void* workspace,
+                                size_t workspace_bytes, moe_stream_t stream);
 
 /* SwiGLU of separate rows, between the gate/up and the down product: h
  * [rows, 2I] holds gate in columns [0, I) and up in [I, 2I) (the order of a

@@ -47,6 +47,11 @@ class MoeGroupedShape(ctypes.Structure):
                 ("rows", ctypes.c_int64)]
 
 
+class MoeFp4Shape(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("groups", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("K", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {moe_status_string(status)} (status {status})")
@@ -104,6 +109,11 @@ def load(build: bool = True):
             lib.moe_grouped_gemm_wgrad.argtypes = [gp, p, i64, p, i64, p, p, p, i32, i32, p, sz, p]
             lib.moe_swiglu.argtypes = [i32, i64, i32, p, i64, p, i64, p]
             lib.moe_swiglu_grad.argtypes = [i32, i64, i32, p, i64, p, i64, p, i64, p]
+            fp = ctypes.POINTER(MoeFp4Shape)
+            lib.moe_fp4_sizes.argtypes = [fp, psz, psz]
+            lib.moe_fp4_quantize.argtypes = [fp, i32, p, i64, p, p, p, p, p, i32, p]
+            lib.moe_fp4_dequantize.argtypes = [fp, p, p, p, i32, p, p, i32, p, i64, p]
+            lib.moe_fp4_gemm.argtypes = [gp, i32, p, p, p, p, p, p, p, p, p, i64, p, sz, p]
             lib.moe_status_string.argtypes = [ctypes.c_int]
             lib.moe_status_string.restype = ctypes.c_char_p
             for f in ("moe_workspace_size", "moe_forward", "moe_forward_events", "moe_route_debug",
@@ -117,7 +127,7 @@ def load(build: bool = True):
                       "moe_forward_mxfp4a4", "moe_nvfp4_weight_sizes", "moe_nvfp4_quantize_weights",
                       "moe_forward_nvfp4", "moe_forward_fused_mlp", "moe_grouped_workspace_size",
                       "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_swiglu",
-                      "moe_swiglu_grad"):
+                      "moe_swiglu_grad", "moe_fp4_sizes", "moe_fp4_quantize", "moe_fp4_dequantize", "moe_fp4_gemm"):
                 getattr(lib, f).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -396,6 +406,38 @@ def moe_swiglu_grad(type, rows, I, h, ldh, dact, lddact, dh, lddh, stream) -> in
     return load().moe_swiglu_grad(int(type), int(rows), int(I), h, ldh, dact, lddact, dh, lddh, stream)
 
 
+MOE_FORMAT_MXFP4, MOE_FORMAT_NVFP4 = range(2)
+MOE_SCALE_PER_ROW, MOE_SCALE_PER_GROUP = range(2)
+
+
+def fp4_shape(format, groups, rows, K) -> MoeFp4Shape:
+    return MoeFp4Shape(int(format), int(groups), int(rows), int(K))
+
+
+def moe_fp4_sizes(s: MoeFp4Shape) -> tuple[int, tuple[int, int]]:
+    v = [ctypes.c_size_t(0) for _ in range(2)]
+    st = load().moe_fp4_sizes(ctypes.byref(s), *[ctypes.byref(a) for a in v])
+    return st, tuple(a.value for a in v)
+
+
+def moe_fp4_quantize(s: MoeFp4Shape, src_type, src, ldsrc, offsets, counts, codes, scales, gscale, gscale_per,
+                     stream) -> int:
+    return load().moe_fp4_quantize(ctypes.byref(s), int(src_type), src, ldsrc, offsets, counts, codes, scales, gscale,
+                                   int(gscale_per), stream)
+
+
+def moe_fp4_dequantize(s: MoeFp4Shape, codes, scales, gscale, gscale_per, offsets, counts, dst_type, dst, lddst,
+                       stream) -> int:
+    return load().moe_fp4_dequantize(ctypes.byref(s), codes, scales, gscale, int(gscale_per), offsets, counts,
+                                     int(dst_type), dst, lddst, stream)
+
+
+def moe_fp4_gemm(s: MoeGroupedShape, format, x_codes, x_scales, x_gscale, w_codes, w_scales, w_gscale, offsets, counts,
+                 y, ldy, workspace, workspace_bytes, stream) -> int:
+    return load().moe_fp4_gemm(ctypes.byref(s), int(format), x_codes, x_scales, x_gscale, w_codes, w_scales, w_gscale,
+                               offsets, counts, y, ldy, workspace, workspace_bytes, stream)
+
+
 def _type_of(dtype) -> int:
     import torch
     types = {torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_FP16, torch.float32: MOE_TYPE_FP32}
@@ -415,6 +457,16 @@ def _check(what, t, device, dtype, shape_, rows=False):
     if not (t.stride(-1) == 1 or t.shape[-1] == 1) if rows else not t.is_contiguous():
         raise ValueError(f"{what} is not contiguous" + (" along its rows" if rows else ""))
     return t
+
+
+def _lists(of, offsets, counts):
+    """The row lists of an object with ``groups`` and ``device``, as pointers."""
+    import torch
+    if offsets is not None:
+        _check("offsets", offsets, of.device, torch.int32, (of.groups + 1,))
+    if counts is not None:
+        _check("counts", counts, of.device, torch.int32, (of.groups,))
+    return _ptr(offsets), _ptr(counts)
 
 
 def _ld(t) -> int:
@@ -473,14 +525,6 @@ class GroupedProducts:
     def shape(self, rows) -> MoeGroupedShape:
         return grouped_shape(self.groups, self.N, self.K, rows, _type_of(self.dtype))
 
-    def _lists(self, offsets, counts):
-        import torch
-        if offsets is not None:
-            _check("offsets", offsets, self.device, torch.int32, (self.groups + 1,))
-        if counts is not None:
-            _check("counts", counts, self.device, torch.int32, (self.groups,))
-        return _ptr(offsets), _ptr(counts)
-
     def _rows(self, what, t, rows, width):
         import torch
         if t is None:
@@ -501,7 +545,7 @@ class GroupedProducts:
         _check("w", w, self.device, self.dtype, (self.groups, self.N, self.K))
         y = self._rows("y", y, rows, self.N)
         self._call("moe_grouped_gemm", moe_grouped_gemm, self.shape(rows), _ptr(x), _ld(x), _ptr(w),
-                   *self._lists(offsets, counts), _ptr(y), _ld(y))
+                   *_lists(self, offsets, counts), _ptr(y), _ld(y))
         return y
 
     def dgrad(self, dy, w, offsets=None, counts=None, dx=None):
@@ -511,7 +555,7 @@ class GroupedProducts:
         _check("w", w, self.device, self.dtype, (self.groups, self.N, self.K))
         dx = self._rows("dx", dx, rows, self.K)
         self._call("moe_grouped_gemm_dgrad", moe_grouped_gemm_dgrad, self.shape(rows), _ptr(dy), _ld(dy), _ptr(w),
-                   *self._lists(offsets, counts), _ptr(dx), _ld(dx))
+                   *_lists(self, offsets, counts), _ptr(dx), _ld(dx))
         return dx
 
     def wgrad(self, dy, x, offsets=None, counts=None, dw=None, dtype=None, accumulate=False):
@@ -528,11 +572,168 @@ class GroupedProducts:
         else:
             _check("dw", dw, self.device, dtype or dw.dtype, (self.groups, self.N, self.K))
         self._call("moe_grouped_gemm_wgrad", moe_grouped_gemm_wgrad, self.shape(rows), _ptr(dy), _ld(dy), _ptr(x),
-                   _ld(x), *self._lists(offsets, counts), _ptr(dw), _type_of(dw.dtype), accumulate)
+                   _ld(x), *_lists(self, offsets, counts), _ptr(dw), _type_of(dw.dtype), accumulate)
         return dw
 
     def device_status(self):
         """(status, detail) of the last call, after waiting for the current stream (moe_device_status)."""
+        import torch
+        with torch.cuda.device(self.device):
+            return moe_device_status(_ptr(self.workspace), self.workspace.numel(),
+                                     torch.cuda.current_stream().cuda_stream)
+
+
+def _format_of(name) -> int:
+    formats = {"mx": MOE_FORMAT_MXFP4, "nv": MOE_FORMAT_NVFP4}
+    if name not in formats:
+        raise ValueError(f"format {name!r}: 'mx' (MXFP4) or 'nv' (NVFP4) wanted")
+    return formats[name]
+
+
+class Fp4Rows:
+    """Rows of groups in 4 bits (moe_fp4_quantize, moe_fp4_dequantize): buffers
+    for up to ``max_rows`` rows of K elements, filled by :meth:`quantize`.
+    format: "mx" (MXFP4) or "nv" (NVFP4, one fp32 scale per row).  offsets and
+    counts as for :class:`GroupedProducts`; pass the same ones to every call on
+    the same rows.  Calls go to the current stream of the device."""
+
+    def __init__(self, format, K, groups=1, max_rows=0, device=None):
+        import torch
+        self.format, self.K, self.groups = _format_of(format), int(K), int(groups)
+        self.device = torch.empty(0, device=device or "cuda").device
+        self.rows = self.max_rows = 0
+        self.ensure_capacity(max_rows)
+
+    def shape(self, rows) -> MoeFp4Shape:
+        return fp4_shape(self.format, self.groups, rows, self.K)
+
+    def ensure_capacity(self, rows):
+        import torch
+        if rows <= self.max_rows and self.max_rows > 0:
+            return
+        st, (n_codes, n_scales) = moe_fp4_sizes(self.shape(max(rows, 1)))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_fp4_sizes")
+        self.codes = torch.empty(n_codes, dtype=torch.uint8, device=self.device)
+        self.scales = torch.empty(n_scales, dtype=torch.uint8, device=self.device)
+        self.gscale = (torch.empty(max(rows, 1), dtype=torch.float32, device=self.device)
+                       if self.format == MOE_FORMAT_NVFP4 else None)
+        self.max_rows = max(rows, 1)
+
+    def quantize(self, x, offsets=None, counts=None):
+        """x [rows, K] (bf16, fp16 or fp32) to 4 bits; returns self."""
+        import torch
+        self.ensure_capacity(x.shape[0])
+        _check("x", x, self.device, x.dtype, (x.shape[0], self.K), rows=True)
+        lists = _lists(self, offsets, counts)
+        with torch.cuda.device(self.device):
+            st = moe_fp4_quantize(self.shape(x.shape[0]), _type_of(x.dtype), _ptr(x), _ld(x), *lists, _ptr(self.codes),
+                                  _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_ROW,
+                                  torch.cuda.current_stream().cuda_stream)
+        if st != MOE_OK:
+            raise MoeError(st, "moe_fp4_quantize")
+        self.rows = x.shape[0]
+        return self
+
+    def dequantize(self, offsets=None, counts=None, y=None, dtype=None):
+        """The values of the rows quantized last, in ``dtype`` (bf16 by default) or y's type."""
+        import torch
+        if y is None:
+            y = torch.empty((self.rows, self.K), dtype=dtype or torch.bfloat16, device=self.device)
+        else:
+            _check("y", y, self.device, dtype or y.dtype, (self.rows, self.K), rows=True)
+        lists = _lists(self, offsets, counts)
+        with torch.cuda.device(self.device):
+            st = moe_fp4_dequantize(self.shape(self.rows), _ptr(self.codes), _ptr(self.scales), _ptr(self.gscale),
+                                    MOE_SCALE_PER_ROW, *lists, _type_of(y.dtype), _ptr(y), _ld(y),
+                                    torch.cuda.current_stream().cuda_stream)
+        if st != MOE_OK:
+            raise MoeError(st, "moe_fp4_dequantize")
+        return y
+
+
+class Fp4Weights:
+    """Weights of ``groups`` matrices [N, K] in 4 bits and their product with 4-bit
+    rows (moe_fp4_gemm).  codes: uint8 [groups, N, K / 2]; scales: the tiles of
+    moe_fp4_quantize for equal groups of N rows; gscale: fp32 [groups] ("nv") or None."""
+
+    def __init__(self, format, codes, scales, gscale=None):
+        import torch
+        self.format = _format_of(format)
+        self.groups, self.N, half = codes.shape
+        self.K, self.device = 2 * half, codes.device
+        st, (_, n_scales) = moe_fp4_sizes(fp4_shape(self.format, self.groups, self.groups * self.N, self.K))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_fp4_sizes")
+        chunk = 128 if self.format == MOE_FORMAT_MXFP4 else 64
+        need = self.groups * -(-self.N // 128) * -(-self.K // chunk) * 512
+        _check("codes", codes, self.device, torch.uint8, codes.shape)
+        _check("scales", scales, self.device, torch.uint8, scales.shape)
+        if scales.numel() < need:
+            raise ValueError(f"scales hold {scales.numel()} bytes, {need} wanted")
+        if self.format == MOE_FORMAT_NVFP4:
+            if gscale is None:
+                raise ValueError("NVFP4 weights have an fp32 scale for each group")
+            _check("gscale", gscale, self.device, torch.float32, (self.groups,))
+        self.codes, self.scales, self.gscale = codes, scales, gscale
+        st, n = moe_grouped_workspace_size(grouped_shape(self.groups, self.N, self.K, 0))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_grouped_workspace_size")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    @classmethod
+    def quantize(cls, w, format):
+        """From w [groups, N, K] (bf16, fp16 or fp32)."""
+        import torch
+        groups, N, K = w.shape
+        _check("w", w, w.device, w.dtype, w.shape)
+        s = fp4_shape(_format_of(format), groups, groups * N, K)
+        st, (_, n_scales) = moe_fp4_sizes(s)
+        if st != MOE_OK:
+            raise MoeError(st, "moe_fp4_sizes")
+        codes = torch.empty((groups, N, K // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty(n_scales, dtype=torch.uint8, device=w.device)
+        gscale = torch.empty(groups, dtype=torch.float32, device=w.device) if format == "nv" else None
+        with torch.cuda.device(w.device):
+            st = moe_fp4_quantize(s, _type_of(w.dtype), _ptr(w), K, None, None, _ptr(codes), _ptr(scales),
+                                  _ptr(gscale), MOE_SCALE_PER_GROUP, torch.cuda.current_stream().cuda_stream)
+        if st != MOE_OK:
+            raise MoeError(st, "moe_fp4_quantize")
+        return cls(format, codes, scales, gscale)
+
+    def dequantize(self, dtype=None):
+        """The values the weights stand for, [groups, N, K] in ``dtype`` (bf16 by default)."""
+        import torch
+        w = torch.empty((self.groups, self.N, self.K), dtype=dtype or torch.bfloat16, device=self.device)
+        with torch.cuda.device(self.device):
+            st = moe_fp4_dequantize(fp4_shape(self.format, self.groups, self.groups * self.N, self.K),
+                                    _ptr(self.codes), _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_GROUP, None,
+                                    None, _type_of(w.dtype), _ptr(w), self.K, torch.cuda.current_stream().cuda_stream)
+        if st != MOE_OK:
+            raise MoeError(st, "moe_fp4_dequantize")
+        return w
+
+    def forward(self, rows: Fp4Rows, offsets=None, counts=None, y=None, dtype=None):
+        """y[p] = x[p] w_g^T in ``dtype`` (bf16 by default, or fp16) or y's type; rows: x quantized for the same lists."""
+        import torch
+        if rows.format != self.format or rows.K != self.K or rows.groups != self.groups or rows.device != self.device:
+            raise ValueError("rows of another format, K, number of groups or device")
+        if y is None:
+            y = torch.empty((rows.rows, self.N), dtype=dtype or torch.bfloat16, device=self.device)
+        else:
+            _check("y", y, self.device, dtype or y.dtype, (rows.rows, self.N), rows=True)
+        lists = _lists(self, offsets, counts)
+        with torch.cuda.device(self.device):
+            st = moe_fp4_gemm(grouped_shape(self.groups, self.N, self.K, rows.rows, _type_of(y.dtype)), self.format,
+                              _ptr(rows.codes), _ptr(rows.scales), _ptr(rows.gscale), _ptr(self.codes),
+                              _ptr(self.scales), _ptr(self.gscale), *lists, _ptr(y), _ld(y), _ptr(self.workspace),
+                              self.workspace.numel(), torch.cuda.current_stream().cuda_stream)
+        if st != MOE_OK:
+            raise MoeError(st, "moe_fp4_gemm")
+        return y
+
+    def device_status(self):
+        """(status, detail) of the last product, after waiting for the current stream (moe_device_status)."""
         import torch
         with torch.cuda.device(self.device):
             return moe_device_status(_ptr(self.workspace), self.workspace.numel(),

@@ -1,11 +1,13 @@
-// grouped_api.cu -- the C ABI of the grouped products and of SwiGLU on separate
-// rows: argument checks, workspace layout, tensor maps, launches.
+// grouped_api.cu -- the C ABI of the grouped products (16-bit and 4-bit), of
+// rows in 4 bits and of SwiGLU on separate rows: argument checks, workspace
+// layout, tensor maps, launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstring>
 
 #include "../../include/moe.h"
+#include "fp4.cuh"
 #include "grouped.cuh"
 #include "grouped_elementwise.cuh"
 #include "tensor_map.h"
@@ -204,6 +206,66 @@ moe_status swiglu_check(int32_t type, int64_t rows, int32_t I) {
   return MOE_OK;
 }
 
+// ---- 4 bits
+
+moe_status check_fp4(const moe_fp4_shape* s) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->format != MOE_FORMAT_MXFP4 && s->format != MOE_FORMAT_NVFP4) return MOE_ERR_INVALID_ARG;
+  if (s->groups <= 0 || s->K <= 0 || s->rows < 0) return MOE_ERR_INVALID_ARG;
+  // K: 16-byte rows of codes for TMA, whole blocks
+  if (s->groups > moe::kGroupsMax || s->K % 32 != 0 || s->K > kMaxDim || s->rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe::Fp4Format format_of(int32_t f) { return f == MOE_FORMAT_MXFP4 ? moe::Fp4Format::kMx : moe::Fp4Format::kNv; }
+
+size_t scale_bytes(moe::Fp4Format f, int64_t tile_rows, int64_t K) {
+  return static_cast<size_t>(tile_rows) * static_cast<size_t>((K + moe::fp4_chunk(f) - 1) / moe::fp4_chunk(f)) * 512;
+}
+
+moe_status fp4_rows(const moe_fp4_shape* s, int32_t type, const void* rows, int64_t ld, const int32_t* offsets,
+                    const int32_t* counts, const uint8_t* codes, const uint8_t* scales, const float* gscale,
+                    int32_t gscale_per, moe::Fp4RowsArgs* out) {
+  moe_status st = check_fp4(s);
+  if (st != MOE_OK) return st;
+  if (type != MOE_TYPE_BF16 && type != MOE_TYPE_FP16 && type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
+  if ((st = check_rows(rows, s->rows, ld, s->K)) != MOE_OK) return st;
+  if (!offsets && s->rows % s->groups != 0) return MOE_ERR_INVALID_ARG;
+  if (!aligned(offsets, 4) || !aligned(counts, 4)) return MOE_ERR_INVALID_ARG;
+  const bool nv = s->format == MOE_FORMAT_NVFP4;
+  if (gscale_per != MOE_SCALE_PER_ROW && gscale_per != MOE_SCALE_PER_GROUP) return MOE_ERR_INVALID_ARG;
+  if (s->rows > 0 && (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 16))) return MOE_ERR_INVALID_ARG;
+  if (s->rows > 0 && nv && (!gscale || !aligned(gscale, 4))) return MOE_ERR_INVALID_ARG;
+  moe::Fp4RowsArgs a{};
+  a.offsets = offsets;
+  a.counts = counts;
+  a.G = s->groups;
+  a.rows = s->rows;
+  a.K = s->K;
+  a.tile_rows = moe::fp4_tile_rows(s->rows, s->groups);
+  a.codes = const_cast<uint8_t*>(codes);
+  a.scales = const_cast<uint8_t*>(scales);
+  a.gscale = const_cast<float*>(gscale);
+  a.per_group = gscale_per == MOE_SCALE_PER_GROUP;
+  a.ld = ld;
+  a.type = type;
+  *out = a;
+  return MOE_OK;
+}
+
+// Code rows: boxes of 128 bytes x box_rows, 128-byte swizzle; matrices [G, N, K / 2] or rows (G = 0).
+bool make_codes_map(CUtensorMap* m, const void* base, int64_t K, int64_t N, int64_t G, uint32_t box_rows) {
+  auto fn = moe::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(G)};
+  cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
+  cuuint32_t box[3] = {128, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, G > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -300,6 +362,93 @@ moe_status moe_swiglu_grad(int32_t type, int64_t rows, int32_t I, const void* h,
                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
+}
+
+moe_status moe_fp4_sizes(const moe_fp4_shape* shape, size_t* codes, size_t* scales) {
+  const moe_status st = check_fp4(shape);
+  if (st != MOE_OK) return st;
+  if (!codes || !scales) return MOE_ERR_INVALID_ARG;
+  *codes = static_cast<size_t>(shape->rows) * (shape->K / 2);
+  *scales = scale_bytes(format_of(shape->format), moe::fp4_tile_rows(shape->rows, shape->groups), shape->K);
+  return MOE_OK;
+}
+
+moe_status moe_fp4_quantize(const moe_fp4_shape* shape, int32_t src_type, const void* src, int64_t ldsrc,
+                            const int32_t* offsets, const int32_t* counts, uint8_t* codes, uint8_t* scales,
+                            float* gscale, int32_t gscale_per, moe_stream_t stream) {
+  moe::Fp4RowsArgs a;
+  const moe_status st =
+      fp4_rows(shape, src_type, src, ldsrc, offsets, counts, codes, scales, gscale, gscale_per, &a);
+  if (st != MOE_OK || shape->rows == 0) return st;
+  a.src = src;
+  return moe::launch_fp4_quantize(format_of(shape->format), a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+moe_status moe_fp4_dequantize(const moe_fp4_shape* shape, const uint8_t* codes, const uint8_t* scales,
+                              const float* gscale, int32_t gscale_per, const int32_t* offsets, const int32_t* counts,
+                              int32_t dst_type, void* dst, int64_t lddst, moe_stream_t stream) {
+  moe::Fp4RowsArgs a;
+  const moe_status st =
+      fp4_rows(shape, dst_type, dst, lddst, offsets, counts, codes, scales, gscale, gscale_per, &a);
+  if (st != MOE_OK || shape->rows == 0) return st;
+  a.dst = dst;
+  return moe::launch_fp4_dequantize(format_of(shape->format), a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+moe_status moe_fp4_gemm(const moe_grouped_shape* shape, int32_t format, const uint8_t* x_codes,
+                        const uint8_t* x_scales, const float* x_gscale, const uint8_t* w_codes,
+                        const uint8_t* w_scales, const float* w_gscale, const int32_t* offsets, const int32_t* counts,
+                        void* y, int64_t ldy, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  const moe_grouped_shape* s = shape;
+  if (format != MOE_FORMAT_MXFP4 && format != MOE_FORMAT_NVFP4) return MOE_ERR_INVALID_ARG;
+  if (s->K % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if ((st = check_rows(y, s->rows, ldy, s->N)) != MOE_OK) return st;
+  const bool nv = format == MOE_FORMAT_NVFP4;
+  if (s->rows > 0 && (!x_codes || !aligned(x_codes, 16) || !x_scales || !aligned(x_scales, 16)))
+    return MOE_ERR_INVALID_ARG;
+  if (!w_codes || !aligned(w_codes, 16) || !w_scales || !aligned(w_scales, 16)) return MOE_ERR_INVALID_ARG;
+  if (nv && ((s->rows > 0 && (!x_gscale || !aligned(x_gscale, 4))) || !w_gscale || !aligned(w_gscale, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_call(s, offsets, counts, workspace, workspace_bytes)) != MOE_OK) return st;
+  const GroupedPlan plan = choose_plan(s);
+  const int bn = moe::fp4_bn(plan), tile = moe::fp4_tile(plan);
+  const int tiles = (s->N + tile - 1) / tile;
+  if ((s->rows / bn + s->groups) * tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (s->rows == 0) return MOE_OK;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  CUtensorMap tw, tx;
+  if (!make_codes_map(&tw, w_codes, s->K, s->N, s->groups, 128) ||
+      !make_codes_map(&tx, x_codes, s->K, s->rows, 0, static_cast<uint32_t>(moe::fp4_tok_box(plan))))
+    return MOE_ERR_CUDA;
+  const Layout L = make_layout(s->groups);
+  moe::GroupedPlanArgs p = plan_args(s, L, workspace, offsets, counts);
+  p.bn = bn;
+  p.tiles = tiles;
+  moe::Fp4GemmArgs a{};
+  a.g = gemm_args(s, L, workspace);
+  a.g.out = y;
+  a.g.ldo = ldy;
+  a.g.F = s->N;
+  a.g.R = s->K;
+  a.g.tiles = tiles;
+  a.w_scales = w_scales;
+  a.x_scales = x_scales;
+  a.w_gscale = w_gscale;
+  a.x_gscale = x_gscale;
+  a.w_tile_rows = (s->N + 127) / 128;
+  a.equal = offsets ? 0 : static_cast<int>(s->rows / s->groups);
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (moe::launch_grouped_plan(p, tx, tx, cs) != cudaSuccess ||
+      moe::launch_fp4_gemm(format_of(format), plan, tw, tx, a, sms, cs) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
 }
 
 }  // extern "C"

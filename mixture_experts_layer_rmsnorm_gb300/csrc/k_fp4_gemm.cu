@@ -1,0 +1,593 @@
+// k_fp4_gemm.cu -- the grouped product on 4-bit operands:
+//   y[p, :] = x[p, :] w_g^T    (p in group g)
+// with x and w as E2M1 codes under MXFP4's E8M0 scales per 32 elements
+// (tcgen05.mma kind::mxf4) or NVFP4's E4M3 scales per 16 (kind::mxf4nvf4) and
+// fp32 scales per row of x and per matrix, applied to the fp32 accumulators.
+//
+// Mapping, units and work split as in k_grouped_gemm.cu: the weights take the
+// MMA's M side, a group's rows its N side.  A stage holds 256 elements of K:
+// 128-byte rows of codes and, per operand, the scale tiles of its chunks (two
+// for MXFP4, four for NVFP4, 512 bytes per 128 rows).  K may end inside a
+// stage: TMA gives zero codes past it, the valid chunks' tiles alone are loaded
+// and the valid MMAs alone issued (the quantizer writes zero scales for the
+// blocks of a chunk past K, so that a last half MMA adds zeros).
+//
+// Scales.  The MMA reads them from TMEM: row 32 j + l of a tile in lane l of
+// every lane quarter, column j, four bytes = a chunk's four blocks.  Four scale
+// warps, one per lane quarter, write each stage's tiles there with tcgen05.st:
+// copies by the MMA thread (tcgen05.cp, six or twelve a stage) run in the tensor
+// pipe and cost the layer's NVFP4 GEMM a fifth of its rate.  In a CTA pair each
+// CTA needs the scales of its own 128 features and of all the unit's rows in its
+// own TMEM.  So a stage's scales are loaded on a barrier of their own in each
+// CTA, each CTA's scale warps write its TMEM, and all eight signal the even CTA,
+// whose thread issues the MMAs.
+//
+// TMEM of a pair: one accumulator of 256 columns beside 5 x 48 (NVFP4) or
+// 6 x 32 (MXFP4) scale columns.  With one accumulator the MMAs of the next unit
+// wait for the epilogue to read this one, so the epilogue reads all of its
+// columns into registers, rounded and packed in pairs, hands the accumulator back, and
+// stores after that.
+//
+// Bound by the fill of shared memory rather than by the FP4 rate: at the FP4
+// rate a pair's stage would need 38 KB per SM every 341 cycles.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "bounded_wait.cuh"
+#include "fp4.cuh"
+#include "launch_config.cuh"
+#include "pdl.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+constexpr int kABytes = 128 * 128;  // 128 features x 256 codes
+
+template <Fp4Format F, int BN, int STAGES, int TOKBOX, bool PAIR>
+struct Cfg {
+  static constexpr int kChunks = F == Fp4Format::kNv ? 4 : 2;  // scale tiles per 128 rows and stage
+  static constexpr int kBRows = PAIR ? BN / 2 : BN;
+  static constexpr int kBBytes = kBRows * 128;
+  static constexpr int kG = BN > 128 ? 2 : 1;  // 128-row scale tiles of a unit's rows
+  static constexpr int kSfW = 512 * kChunks, kSfX = 512 * kChunks * kG;
+  static constexpr int kStageBytes = (kABytes + kBBytes + kSfW + kSfX + 1023) / 1024 * 1024;
+  static constexpr int kAccBufs = PAIR ? 1 : 2;
+  static constexpr int kSfCols = 16 + (4 * kChunks * kG + 15) / 16 * 16;  // w scales from +0, x scales from +16
+  static constexpr int kTmemNeed = kAccBufs * BN + STAGES * kSfCols;
+  static constexpr uint32_t kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
+  static constexpr int kEpiWarps = PAIR ? 8 : 4;  // two per TMEM lane quarter for the pair's single accumulator
+  static constexpr int kThreads = 32 * (2 + kEpiWarps + 4);
+  static constexpr int kBarBytes = 512;
+  static constexpr int kTabBytes = (kGroupsSmem + 1) * 4;
+  static constexpr int kGxBytes = F == Fp4Format::kNv ? 4 * BN * 4 : 0;  // x's fp32 scales, per epilogue warp
+  static constexpr size_t kSmemBytes =
+      1024 + static_cast<size_t>(STAGES) * kStageBytes + kBarBytes + kTabBytes + kGxBytes + 16;
+  static_assert(kBRows % TOKBOX == 0 && BN >= 32 && BN <= 256, "token tile");
+  static_assert(4 * kChunks <= 16 && kTmemNeed <= 512, "TMEM columns");
+  static_assert((4 * STAGES + 5) * 8 + 8 <= kBarBytes, "barrier area");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+};
+
+enum : int {
+  kWaitSlotFree = 1,
+  kWaitAccFree = 2,
+  kWaitSlotFull = 3,
+  kWaitAccFull = 4,
+  kWaitPartials = 5,
+  kWaitScales = 7,
+  kWaitScaleLoads = 8
+};
+
+__device__ __forceinline__ uint16_t to16(float v, bool fp16) {
+  return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+template <Fp4Format F, int BN, int STAGES, int TOKBOX, bool PAIR>
+__global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                    const __grid_constant__ Fp4GemmArgs args) {
+  using C = Cfg<F, BN, STAGES, TOKBOX, PAIR>;
+  const GroupedGemmArgs& a = args.g;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStageBytes);
+  uint64_t* empty = full + STAGES;
+  uint64_t* sfld = empty + STAGES;   // a stage's scale tiles are in this CTA's shared memory
+  uint64_t* sfull = sfld + STAGES;   // ... and in TMEM (of both CTAs of a pair; the even CTA's barrier)
+  uint64_t* tfull = sfull + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* tab = reinterpret_cast<int32_t*>(smem + STAGES * C::kStageBytes + C::kBarBytes);
+  float* gx_buf = reinterpret_cast<float*>(
+      (reinterpret_cast<uintptr_t>(tab) + C::kTabBytes + 15) & ~uintptr_t(15));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int worker = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+  const int workers = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&sfld[s], 1);
+      mbar_init(&sfull[s], PAIR ? 8 : 4);  // the scale warps
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], (PAIR ? 2 : 1) * C::kEpiWarps);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_x);
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(tmem_slot, C::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::kTmemCols);
+      tmem_relinquish();
+    }
+  }
+  pdl_wait();  // the plan kernel's tables
+  const int32_t* t_unit = a.unit_off;
+  if (a.G <= kGroupsSmem) {
+    for (int i = threadIdx.x; i <= a.G; i += C::kThreads) tab[i] = __ldcg(a.unit_off + i);
+    t_unit = tab;
+  }
+  tc_fence_before();
+  if (PAIR)
+    cluster_sync();
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int total_units = t_unit[a.G];
+  const int kblocks = (a.R + 255) / 256;
+  const int chunks_k = (a.R + fp4_chunk(F) - 1) / fp4_chunk(F);  // scale tiles along K per tile row
+  constexpr bool kStreamK = !PAIR;
+  auto unit_of = [&](int u) { return grouped_unit(u, t_unit, a.start, a.count, a.G, a.tiles, 1, BN); };
+  auto valid_chunks = [&](int kb) { return min(C::kChunks, chunks_k - kb * C::kChunks); };
+  auto n_of = [](int n) { return PAIR ? (n + 31) / 32 * 32 : (n + 15) / 16 * 16; };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer
+      const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      const uint32_t full_cl = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
+      GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
+      int u, kb0, kb1;
+      while (ok && rg.next(u, kb0, kb1)) {
+        const GroupedUnit un = unit_of(u);
+        const int feat = PAIR ? un.tile * 256 + static_cast<int>(rank) * 128 : un.tile * 128;
+        const int n_mma = n_of(un.n);
+        const int half = PAIR ? n_mma / 2 : n_mma;
+        const int tok_first = un.tok0 + static_cast<int>(rank) * half;
+        const int tok_rows = (half + TOKBOX - 1) / TOKBOX * TOKBOX;
+        const uint32_t bytes = kABytes + tok_rows * 128;
+        const uint64_t pol_w = __ldcg(a.count + un.g) > BN ? pol_keep : pol_stream;
+        // scale tile rows: of this CTA's features (past N: a tile row of the
+        // same matrix, its products are dropped), of the unit's rows
+        const int64_t wt = static_cast<int64_t>(un.g) * args.w_tile_rows + min(feat / 128, args.w_tile_rows - 1);
+        const int start = __ldcg(a.start + un.g), within = un.tok0 - start;
+        const int64_t xt = (args.equal ? static_cast<int64_t>(un.g) * ((args.equal + 127) / 128) : start / 128 + un.g) +
+                           within / 128;
+        const int x_tiles = C::kG == 2 && un.n > 128 ? 2 : 1;
+        // a 32-row unit lies inside a tile: its rows are moved to row 0 by the scale warps
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, kWaitTimeoutNs, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * C::kStageBytes;
+          uint8_t* sb = sa + kABytes;
+          uint8_t* sf = sb + C::kBBytes;
+          uint64_t* bar = &full[stage];
+          const uint32_t bar_cl = full_cl + 8u * stage;
+          if (!PAIR)
+            mbar_arrive_expect_tx(bar, bytes);
+          else if (leader)
+            mbar_arrive_expect_tx(bar, 2 * bytes);
+          const uint32_t sf_bytes = 512u * valid_chunks(kb);
+          mbar_arrive_expect_tx(&sfld[stage], sf_bytes * (1 + x_tiles));
+          const int64_t chunk0 = static_cast<int64_t>(kb) * C::kChunks;
+          bulk_load(sf, args.w_scales + (wt * chunks_k + chunk0) * 512, sf_bytes, &sfld[stage], pol_w);
+          for (int h = 0; h < x_tiles; ++h)
+            bulk_load(sf + C::kSfW + h * C::kSfW, args.x_scales + ((xt + h) * chunks_k + chunk0) * 512, sf_bytes,
+                      &sfld[stage], pol_keep);
+          if (PAIR)
+            tma_load_3d_pair(sa, &tm_w, bar_cl, kb * 128, feat, un.g, pol_w);
+          else
+            tma_load_3d(sa, &tm_w, bar, kb * 128, feat, un.g, pol_w);
+          for (int r = 0; r < tok_rows; r += TOKBOX) {
+            if (PAIR)
+              tma_load_2d_pair(sb + r * 128, &tm_x, bar_cl, kb * 128, tok_first + r, pol_keep);
+            else
+              tma_load_2d(sb + r * 128, &tm_x, bar, kb * 128, tok_first + r, pol_keep);
+          }
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) raise_timeout(a.err, abort_flag, kKernFp4Gemm, kWaitSlotFree);
+      // every load this thread issued has landed before the CTA exits (the odd
+      // CTA of a pair sees its codes landed through the release of its stages)
+      for (int s = 0; s < STAGES; ++s) {
+        if (issued <= s) break;
+        const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
+        int dummy = 0;
+        mbar_wait(&sfld[s], par, kWaitTimeoutNs, &dummy);
+        mbar_wait(PAIR && !leader ? &empty[s] : &full[s], par, kWaitTimeoutNs, &dummy);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---------------- MMA issuer
+      int stage = 0, acc = 0, where = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
+      int u, kb0, kb1;
+      while (ok && rg.next(u, kb0, kb1)) {
+        const GroupedUnit un = unit_of(u);
+        const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag)
+                                   : mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag);
+        if (!free_acc) {
+          ok = false;
+          where = kWaitAccFree;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t n_mma = static_cast<uint32_t>(n_of(un.n));
+        const uint32_t d_acc = tmem_base + static_cast<uint32_t>(acc * BN);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&full[stage], phase, kWaitTimeoutNs, abort_flag)) {
+            ok = false;
+            where = kWaitSlotFull;
+            break;
+          }
+          const bool have_scales = PAIR ? mbar_wait_cluster(&sfull[stage], phase, kWaitTimeoutNs, abort_flag)
+                                        : mbar_wait(&sfull[stage], phase, kWaitTimeoutNs, abort_flag);
+          if (!have_scales) {
+            ok = false;
+            where = kWaitScales;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * C::kStageBytes), sb = sa + kABytes;
+          const uint32_t sf_w = tmem_base + static_cast<uint32_t>(C::kAccBufs * BN + stage * C::kSfCols);
+          const uint32_t sf_x = sf_w + 16;
+          const int n_k = min(4, (a.R - kb * 256 + 63) / 64);  // MMAs of K = 64
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k >= n_k) break;
+            const uint32_t accum = (kb > kb0 || k > 0) ? 1u : 0u;
+            const uint64_t ad = sdesc_kmajor_sw128(sa + k * 32), bd = sdesc_kmajor_sw128(sb + k * 32);
+            if constexpr (F == Fp4Format::kNv) {
+              const uint32_t id = idesc_nvf4(PAIR ? 256 : 128, n_mma);
+              if (PAIR)
+                mma_nvf4_ss_pair(d_acc, ad, bd, id, sf_w + 4 * k, sf_x + 4 * C::kG * k, accum);
+              else
+                mma_nvf4_ss(d_acc, ad, bd, id, sf_w + 4 * k, sf_x + 4 * C::kG * k, accum);
+            } else {
+              const uint32_t c = static_cast<uint32_t>(k >> 1), sid = 2u * static_cast<uint32_t>(k & 1);
+              const uint32_t id = idesc_mxf4(PAIR ? 256 : 128, n_mma, sid, sid);
+              if (PAIR)
+                mma_mxf4_ss_pair(d_acc, ad, bd, id, sf_w + 4 * c, sf_x + 4 * C::kG * c, accum);
+              else
+                mma_mxf4_ss(d_acc, ad, bd, id, sf_w + 4 * c, sf_x + 4 * C::kG * c, accum);
+            }
+          }
+          if (PAIR)
+            mma_commit_pair_mc(&empty[stage], 0x3);
+          else
+            mma_commit(&empty[stage]);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (PAIR)
+          mma_commit_pair_mc(&tfull[acc], 0x3);
+        else
+          mma_commit(&tfull[acc]);
+        if (++acc == C::kAccBufs) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (!ok) raise_timeout(a.err, abort_flag, kKernFp4Gemm, where);
+      if (PAIR)
+        mma_commit_pair(done);
+      else
+        mma_commit(done);
+      int dummy = 0;
+      mbar_wait(done, 0, kWaitTimeoutNs, &dummy);
+    }
+  } else if (warp >= 2 + C::kEpiWarps) {
+    // ---------------- scale warps: lane l of a quarter takes the 16 bytes of
+    // rows l, 32 + l, 64 + l, 96 + l of each tile (its four TMEM columns)
+    const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t sfull_cl = PAIR ? mapa_shared(smem_u32(sfull), 0) : 0u;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
+    int u, kb0, kb1;
+    while (ok && rg.next(u, kb0, kb1)) {
+      const GroupedUnit un = unit_of(u);
+      const int x_tiles = C::kG == 2 && un.n > 128 ? 2 : 1;
+      // a unit of 32 rows may start at row 32, 64 or 96 of its tile: column j
+      // of its words then belongs at column 0
+      const int j0 = BN < 128 ? ((un.tok0 - __ldcg(a.start + un.g)) & 127) >> 5 : 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const bool got = mbar_wait(&sfld[stage], phase, kWaitTimeoutNs, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, got)) {  // warp-uniform: tcgen05.st needs every lane
+          ok = false;
+          break;
+        }
+        const uint8_t* sf = smem + stage * C::kStageBytes + kABytes + C::kBBytes + lane * 16;
+        const uint32_t cols = tmem_base + static_cast<uint32_t>(C::kAccBufs * BN + stage * C::kSfCols) + quarter;
+        const int n_c = valid_chunks(kb);
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          if (c >= n_c) break;
+          tmem_st_32x32b_x4(cols + 4 * c, *reinterpret_cast<const uint4*>(sf + 512 * c));
+#pragma unroll
+          for (int h = 0; h < C::kG; ++h) {
+            if (h >= x_tiles) break;
+            uint4 w = *reinterpret_cast<const uint4*>(sf + C::kSfW + h * C::kSfW + 512 * c);
+            if (BN < 128) {
+              const uint32_t v = j0 == 0 ? w.x : j0 == 1 ? w.y : j0 == 2 ? w.z : w.w;
+              w = make_uint4(v, v, v, v);
+            }
+            tmem_st_32x32b_x4(cols + 16 + 4 * (c * C::kG + h), w);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(sfull_cl + 8u * stage);
+          else
+            mbar_arrive(&sfull[stage]);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && lane == 0) raise_timeout(a.err, abort_flag, kKernFp4Gemm, kWaitScaleLoads);
+  } else {
+    // ---------------- epilogue: warps 2.., TMEM lane quarter = warp % 4; two
+    // warps of a quarter take half of the columns each
+    const int q = warp & 3;
+    const int row = q * 32 + lane;
+    int acc = 0, where = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    const uint32_t tempty_cl = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
+    GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
+    int u, kb0, kb1;
+    constexpr int kCols = BN * 4 / C::kEpiWarps;  // columns per warp
+    const int col0 = (warp - 2) / 4 * kCols;
+    float* gx = gx_buf + (warp - 2) * kCols;
+    while (ok && rg.next(u, kb0, kb1)) {
+      const GroupedUnit un = unit_of(u);
+      const int feat0 = PAIR ? un.tile * 256 + static_cast<int>(rank) * 128 : un.tile * 128;
+      const bool fp16 = a.fp16 != 0, mine = feat0 + row < a.F;
+      uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(un.tok0) * a.ldo + feat0 + row;
+      if (F == Fp4Format::kNv) {  // the rows' fp32 scales times the matrix's, read while the MMAs run
+        const float gw = __ldg(args.w_gscale + un.g);
+        __syncwarp();
+        for (int c = lane; c < kCols; c += 32)
+          gx[c] = col0 + c < un.n ? __fmul_rn(gw, __ldcg(args.x_gscale + un.tok0 + col0 + c)) : 0.0f;
+        __syncwarp();
+      }
+      const bool got = mbar_wait(&tfull[acc], acc_phase, kWaitTimeoutNs, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        ok = false;
+        where = kWaitAccFull;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(tempty_cl + 8u * acc);
+          else
+            mbar_arrive(&tempty[acc]);
+        }
+      };
+      if constexpr (PAIR) {
+        uint32_t packed[kCols / 2];
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 32) {
+          if (col0 + c0 < un.n) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(t_row + col0 + c0, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float v0 = __uint_as_float(r[j]), v1 = __uint_as_float(r[j + 1]);
+              if (F == Fp4Format::kNv) {
+                v0 = __fmul_rn(v0, gx[c0 + j]);
+                v1 = __fmul_rn(v1, gx[c0 + j + 1]);
+              }
+              packed[(c0 + j) / 2] = static_cast<uint32_t>(to16(v0, fp16)) | (static_cast<uint32_t>(to16(v1, fp16)) << 16);
+            }
+          }
+        }
+        release();
+        if (mine) {
+          uint16_t* o = out + static_cast<int64_t>(col0) * a.ldo;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 2) {
+            if (col0 + c < un.n) o[static_cast<int64_t>(c) * a.ldo] = static_cast<uint16_t>(packed[c / 2]);
+            if (col0 + c + 1 < un.n) o[static_cast<int64_t>(c + 1) * a.ldo] = static_cast<uint16_t>(packed[c / 2] >> 16);
+          }
+        }
+      } else if (kb0 > 0) {
+        // a later part of a unit that an earlier CTA started: hand over the partial sums
+        float* slot = a.partials + static_cast<int64_t>(worker) * BN * 128;
+        for (int c0 = 0; c0 < un.n; c0 += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(t_row + c0, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) __stcg(slot + (c0 + j) * 128 + row, __uint_as_float(r[j]));
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) st_release(a.flags + worker * 4 + q, 1);
+        release();
+      } else {
+        int c_last = worker;
+        if (kb1 < kblocks) {
+          const int64_t unit_end = static_cast<int64_t>(u + 1) * kblocks;
+          while (c_last + 1 < workers && rg.begin_of(c_last + 1) < unit_end) ++c_last;
+        }
+        for (int c0 = 0; c0 < un.n; c0 += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(t_row + c0, r);
+          tmem_ld_wait();
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+          bool good = true;
+          for (int c = worker + 1; c <= c_last; ++c) {
+            if (rg.begin_of(c) == rg.begin_of(c + 1)) continue;  // empty range
+            if (c0 == 0 && !wait_flag(a.flags + c * 4 + q, abort_flag, kWaitTimeoutNs)) {
+              good = false;
+              break;
+            }
+            const float* slot = a.partials + static_cast<int64_t>(c) * BN * 128;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += __ldcg(slot + (c0 + j) * 128 + row);
+          }
+          if (!__all_sync(0xFFFFFFFFu, good)) {
+            ok = false;
+            where = kWaitPartials;
+            break;
+          }
+          if (mine) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c0 + j < un.n) {
+                if (F == Fp4Format::kNv) v[j] = __fmul_rn(v[j], gx[c0 + j]);
+                out[static_cast<int64_t>(c0 + j) * a.ldo] = to16(v[j], fp16);
+              }
+          }
+        }
+        if (ok) release();
+      }
+      if (!ok) break;
+      if (++acc == C::kAccBufs) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (!ok && lane == 0) raise_timeout(a.err, abort_flag, kKernFp4Gemm, where);
+  }
+
+  __syncthreads();
+  if (PAIR) cluster_sync();  // a pair keeps both CTAs until both are done
+  if (warp == 1) {
+    tc_fence_after();
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, C::kTmemCols);
+    else
+      tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+template <Fp4Format F, int BN, int STAGES, int TOKBOX, bool PAIR>
+cudaError_t launch_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a, int num_sms,
+                        cudaStream_t stream) {
+  using C = Cfg<F, BN, STAGES, TOKBOX, PAIR>;
+  auto kernel = fp4_gemm_kernel<F, BN, STAGES, TOKBOX, PAIR>;
+  static PerDevice config;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = PAIR ? 2 : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  int max_pairs = 0;
+  const cudaError_t e = config.get(
+      [&](int& pairs) -> cudaError_t {
+        cudaError_t ce =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytes));
+        if (ce != cudaSuccess || !PAIR) return ce;
+        cudaLaunchConfig_t q = cfg;
+        q.gridDim = dim3(2 * (kMaxGemmCtas / 2));
+        q.attrs = attr + 1;
+        q.numAttrs = 1;
+        int n = 0;
+        ce = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
+        if (ce != cudaSuccess) return ce;
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+        pairs = n;
+        return cudaSuccess;
+      },
+      &max_pairs);
+  if (e != cudaSuccess) return e;
+  const int most = PAIR ? kMaxGemmCtas / 2 : kMaxGemmCtas;
+  const int workers = PAIR ? max_pairs : num_sms;
+  cfg.gridDim = dim3((workers < most ? workers : most) * (PAIR ? 2 : 1));
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, a);
+}
+
+constexpr int kBn[2] = {32, 256}, kTile[2] = {128, 256}, kTokBox[2] = {16, 128};
+
+template <Fp4Format F>
+cudaError_t launch_plan(GroupedPlan plan, const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a,
+                        int num_sms, cudaStream_t stream) {
+  constexpr int small = F == Fp4Format::kNv ? 9 : 9, large = F == Fp4Format::kNv ? 5 : 6;  // stages
+  if (plan == GroupedPlan::kSmall) return launch_gemm<F, kBn[0], small, kTokBox[0], false>(tw, tx, a, num_sms, stream);
+  return launch_gemm<F, kBn[1], large, kTokBox[1], true>(tw, tx, a, num_sms, stream);
+}
+
+}  // namespace
+
+int fp4_bn(GroupedPlan plan) { return kBn[static_cast<int>(plan)]; }
+int fp4_tile(GroupedPlan plan) { return kTile[static_cast<int>(plan)]; }
+int fp4_tok_box(GroupedPlan plan) { return kTokBox[static_cast<int>(plan)]; }
+
+cudaError_t launch_fp4_gemm(Fp4Format f, GroupedPlan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
+                            const Fp4GemmArgs& a, int num_sms, cudaStream_t stream) {
+  return f == Fp4Format::kMx ? launch_plan<Fp4Format::kMx>(plan, tm_w, tm_x, a, num_sms, stream)
+                             : launch_plan<Fp4Format::kNv>(plan, tm_w, tm_x, a, num_sms, stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,314 @@
+"""Rows in 4 bits and their grouped product, against the formats' definitions.
+
+The quantizer and its inverse are whole-number decisions and single roundings of
+fp32 steps that numpy repeats (IEEE division and products): codes and scales are equal,
+the values differ by no more than their one rounding.  The product of two E2M1
+codes and two block scales is exact in fp32 (2 + 2 bits; NVFP4 4 + 4 more); sums
+as in the 16-bit grouped products: a step of K = 64 cuts at most 65 terms after
+the last bit of the largest, 65 * 2^-23 S per 64 terms with S = sum |a||b|, one
+rounding per stream-K partial sum, three for NVFP4's fp32 scales (their product,
+its product with the sum), and half a step of the output.
+"""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_rmsnorm_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+BLOCK = {"mx": 32, "nv": 16}
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6], np.float32)
+E4M3 = np.array([(m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10)) for e in range(16) for m in range(8)][:127],
+                np.float32)
+
+
+def nearest(table, v):
+    """Index of the nearest table entry, ties to the even index, the last beyond it (values >= 0)."""
+    hi = np.clip(np.searchsorted(table, v), 1, len(table) - 1)
+    lo = hi - 1
+    dl, dh = v.astype(np.float64) - table[lo], table[hi].astype(np.float64) - v
+    return np.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi)
+
+
+def quantise(x, fmt, per_group):
+    """Codes, scale bytes and (nv) fp32 scales of one group's rows, step by step in fp32; x: float32 [rows, K]."""
+    rows, k = x.shape
+    b = x.reshape(rows, k // BLOCK[fmt], BLOCK[fmt])
+    amax = np.abs(b).max(2)
+    with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+        if fmt == "mx":
+            e = np.where(amax > 0, np.frexp(amax)[1] - 3, -127).clip(-127, 127)
+            s, g = (e + 127).astype(np.uint8), None
+            q = np.ldexp(b.astype(np.float64), -e[..., None])
+        else:
+            top = np.full(rows, amax.max(initial=0.0), np.float32) if per_group else amax.max(1)
+            g = np.where(top > 0, top / np.float32(2688), np.float32(1)).astype(np.float32)
+            u = amax / (np.float32(6) * g)[:, None]
+            s = np.where(np.isnan(u), 0, nearest(E4M3, np.minimum(np.nan_to_num(u, posinf=448), 448))).astype(np.uint8)
+            d = (E4M3[s] * g[:, None]).astype(np.float32)[..., None]
+            q = np.where(d > 0, b / d, np.float32(0))
+    c = nearest(E2M1, np.abs(q)).astype(np.uint8) | (np.signbit(q).astype(np.uint8) << 3)
+    return c.reshape(rows, k), s, g
+
+
+def values(c, s, g, fmt):
+    """What codes stand for, in 64 bits."""
+    v = np.where(c & 8, -1.0, 1.0) * E2M1[c & 7].astype(np.float64)
+    f = np.ldexp(1.0, s.astype(int) - 127) if fmt == "mx" else E4M3[s].astype(np.float64) * g[:, None].astype(np.float64)
+    return v * np.repeat(f, BLOCK[fmt], axis=1)
+
+
+class Lists:
+    def __init__(self, counts, gap=0, tail=0, equal=False):
+        off = np.concatenate([[0], np.cumsum([c + gap for c in counts])])
+        self.spans = [(int(o), int(o + c)) for o, c in zip(off, counts)]
+        self.rows, self.groups, self.equal = int(off[-1]) + tail, len(counts), equal
+        self.offsets = None if equal else torch.tensor(off, dtype=torch.int32, device="cuda")
+        self.counts = torch.tensor(counts, dtype=torch.int32, device="cuda") if gap else None
+        self.free = np.ones(self.rows, bool)
+        for a, b in self.spans:
+            self.free[a:b] = False
+
+    def tile_row(self, g):
+        if self.equal:
+            return g * (-(-(self.rows // self.groups) // 128))
+        return self.spans[g][0] // 128 + g
+
+
+def unpack(codes, rows, k):
+    p = codes[:rows * k // 2].cpu().numpy().reshape(rows, k // 2)
+    return np.stack([p & 15, p >> 4], axis=2).reshape(rows, k)
+
+
+def scale_of(scales, lists, g, n, k, fmt):
+    """The scale bytes [n, blocks] of group g from the tiles; bytes of blocks past K in whole chunks must be zero."""
+    blocks, chunks = k // BLOCK[fmt], -(-k // (4 * BLOCK[fmt]))
+    tiles = -(-n // 128)
+    t0 = lists.tile_row(g)
+    raw = scales.cpu().numpy()[t0 * chunks * 512:(t0 + tiles) * chunks * 512].reshape(tiles, chunks, 32, 4, 4)
+    flat = raw.transpose(0, 3, 2, 1, 4).reshape(tiles * 128, chunks * 4)[:n]
+    assert not flat[:, blocks:].any()
+    return flat[:, :blocks]
+
+
+def hard_rows(rng, rows, k, dtype):
+    """Values over many binades, zeros, signed zeros, exact ties of every code, the type's extremes."""
+    x = rng.standard_normal((rows, k)) * np.exp2(rng.integers(-6, 7, (rows, k // 16)).repeat(16, axis=1))
+    x[rng.random((rows, k)) < 0.05] = 0.0
+    x = torch.tensor(x).to(dtype)
+    ties = torch.tensor([6.0, 0.25, -0.25, 0.75, 1.25, -1.75, 2.5, 3.5, 5.0, -5.0, 0.0, -0.0, 4.0, 1.0, 0.5, -6.0])
+    x[0, :16] = ties.to(dtype)
+    if k >= 64:
+        x[0, 32:64] = 0.0
+        x[-1, :16] = torch.finfo(dtype).tiny
+        x[-1, 16:32] = torch.finfo(dtype).smallest_normal * 8
+    if rows > 2:
+        x[1] = 0.0
+    return x
+
+
+CASES = {
+    "one_block": ([1], 32, 0, 0, False),
+    "lists": ([0, 5, 130, 1, 0, 128, 127], 352, 0, 0, False),
+    "gaps": ([33, 0, 256, 3], 1024, 13, 7, False),
+    "equal": ([72, 72, 72], 160, 0, 0, True),
+    "wide": ([3, 2], 8224, 0, 0, False),
+    "wider_than_held": ([2, 0, 1], 20512, 5, 1, False),
+    "many_groups": ([i % 4 for i in range(700)], 96, 1, 0, False),
+}
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("name", CASES)
+def test_quantise_and_back(name, fmt, dtype):
+    counts, k, gap, tail, equal = CASES[name]
+    lists = Lists(counts, gap, tail, equal)
+    rng = np.random.default_rng(len(name))
+    x = torch.full((lists.rows, k), float("nan"), dtype=dtype)
+    for a, b in lists.spans:
+        if b > a:
+            x[a:b] = hard_rows(rng, b - a, k, dtype)
+    wide = torch.zeros((lists.rows, k + 16), dtype=dtype, device="cuda")
+    wide[:, :k] = x.cuda()
+    r4 = binding.Fp4Rows(fmt, k, lists.groups, lists.rows)
+    r4.codes.fill_(0xAA)
+    r4.quantize(wide[:, :k], lists.offsets, lists.counts)
+    codes = unpack(r4.codes, lists.rows, k)
+    assert (codes[lists.free] == 0xA).all()  # rows of no group are left alone
+    back = {}
+    for out in (BF16, FP16, FP32):
+        y = torch.full((lists.rows, k + 8), 7.0, dtype=out, device="cuda")[:, :k]
+        r4.dequantize(lists.offsets, lists.counts, y=y)
+        back[out] = y
+        assert (y.cpu()[lists.free] == 7.0).all()
+    for g, (a, b) in enumerate(lists.spans):
+        if a == b:
+            continue
+        c, s, gs = quantise(x[a:b].float().numpy(), fmt, False)
+        assert np.array_equal(scale_of(r4.scales, lists, g, b - a, k, fmt), s)
+        if fmt == "nv":
+            assert np.array_equal(r4.gscale[a:b].cpu().numpy(), gs)
+            zero = np.repeat(E4M3[s] * gs[:, None] == 0, 16, axis=1)
+            c = np.where(zero, 0, c)
+        assert np.array_equal(codes[a:b], c)
+        want = torch.tensor(values(c, s, gs, fmt))
+        for out, y in back.items():
+            got = y[a:b].cpu().double()
+            over = want.abs() > torch.finfo(out).max  # beyond the type: infinity
+            tiny = torch.finfo(out).smallest_normal * torch.finfo(out).eps / 2
+            # (code * s) * g in fp32, then the type: two roundings for 16 bits, one for 32
+            rel = torch.finfo(out).eps / 2 + (2.0 ** -24 if out != FP32 else 0.0)
+            assert ((got - want).abs() <= want.abs() * rel * (1 + 2.0 ** -20) + tiny)[~over].all()
+            assert (got[over].abs() >= torch.finfo(out).max).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_weights_with_one_scale_per_matrix(fmt):
+    rng = np.random.default_rng(2)
+    w = torch.stack([hard_rows(rng, 200, 288, BF16) * 2.0 ** i for i in (0, -3, 5)]).to(BF16)
+    w[2] = 0.0
+    w4 = binding.Fp4Weights.quantize(w.cuda(), fmt)
+    lists = Lists([200] * 3, equal=True)
+    codes = unpack(w4.codes.view(-1), 600, 288).reshape(3, 200, 288)
+    for g in range(3):
+        c, s, gs = quantise(w[g].float().numpy(), fmt, True)
+        assert np.array_equal(scale_of(w4.scales, lists, g, 200, 288, fmt), s)
+        if fmt == "nv":
+            assert w4.gscale[g].item() == gs[0]
+            c = np.where(np.repeat(E4M3[s] * gs[:, None] == 0, 16, axis=1), 0, c)
+        assert np.array_equal(codes[g], c)
+        want = values(c, s, gs, fmt)
+        assert np.abs(w4.dequantize(FP32)[g].cpu().double().numpy() - want).max() <= 2.0 ** -24 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_division_near_the_borders_of_codes(fmt):
+    """Rows whose quotients lie on and next to the borders between codes, at many scales."""
+    rng = np.random.default_rng(9)
+    k = 4096
+    x = np.empty((64, k), np.float32)
+    for r in range(64):
+        big = np.float32(rng.uniform(1, 2) * 2.0 ** rng.integers(-20, 20))
+        x[r] = big
+        g = np.float32(big / np.float32(2688))
+        d = np.float32(448) * g if fmt == "nv" else np.float32(2.0 ** (np.frexp(big)[1] - 3))
+        border = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)[rng.integers(0, 7, k)]
+        at = (border * d).astype(np.float32)
+        for _ in range(3):
+            at = np.where(rng.random(k) < 0.5, np.nextafter(at, np.float32(np.inf)), np.nextafter(at, np.float32(0)))
+        x[r] = at * np.where(rng.random(k) < 0.5, -1, 1)
+        x[r, ::BLOCK[fmt]] = big
+    r4 = binding.Fp4Rows(fmt, k, 1, 64).quantize(torch.tensor(x).cuda())
+    c, s, gs = quantise(x, fmt, False)
+    assert np.array_equal(unpack(r4.codes, 64, k), c)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_nan_and_infinity_become_nan(fmt):
+    x = torch.ones((3, 64), device="cuda")
+    x[1, 5], x[2, 40] = float("nan"), float("-inf")
+    y = binding.Fp4Rows(fmt, 64, 1, 3).quantize(x).dequantize(dtype=FP32)
+    assert torch.equal(y[0], x[0])
+    if fmt == "nv":
+        assert torch.isnan(y[1:]).all()
+    else:
+        assert torch.isnan(y[1, :32]).all() and torch.isnan(y[2, 32:]).all()
+        assert torch.equal(y[1, 32:], x[1, 32:]) and torch.equal(y[2, :32], x[2, :32])
+
+
+GEMMS = {
+    # counts, N, K, gap, tail, equal
+    "one": ([1], 8, 32, 0, 0, False),
+    "small": ([0, 1, 15, 16, 17, 31, 32, 33, 0, 2], 264, 544, 0, 0, False),
+    "small_stream_k": ([3, 0, 9, 12], 1032, 4096, 5, 3, False),
+    "small_deep_group": ([300] + [0] * 30, 136, 320, 0, 0, False),
+    "large": ([255, 256, 257, 0, 1, 129, 511], 520, 288, 0, 0, False),
+    "large_gap": ([100, 700, 0, 33], 776, 1152, 9, 40, False),
+    "large_k64": ([300, 20], 256, 64, 0, 0, False),
+    "equal": ([130, 130, 130], 384, 416, 0, 0, True),
+    "many_groups": ([(5 * i) % 7 for i in range(300)], 72, 96, 0, 2, False),
+}
+
+
+@pytest.mark.parametrize("out", [BF16, FP16], ids=str)
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("name", GEMMS)
+def test_product(name, fmt, out):
+    counts, n, k, gap, tail, equal = GEMMS[name]
+    lists = Lists(counts, gap, tail, equal)
+    gen = torch.Generator(device="cuda").manual_seed(len(name))
+    x = torch.randn((lists.rows, k), generator=gen, device="cuda").to(BF16)
+    # the binade changes from block to block: a scale in the wrong place shows
+    x *= torch.exp2(torch.randint(-3, 4, (lists.rows, k // 16), generator=gen, device="cuda")).repeat_interleave(16, 1).to(BF16)
+    x[torch.tensor(lists.free, device="cuda")] = float("nan")
+    w = (torch.randn((lists.groups, n, k), generator=gen, device="cuda") * 0.05).to(BF16)
+    w *= torch.exp2(torch.randint(-3, 4, (lists.groups, n, k // 16), generator=gen, device="cuda")).repeat_interleave(16, 2).to(BF16)
+    r4 = binding.Fp4Rows(fmt, k, lists.groups, lists.rows)
+    r4.codes.fill_(0x77)
+    r4.scales.fill_(0xFF)  # what the quantizer leaves alone may hold anything
+    r4.quantize(x, lists.offsets, lists.counts)
+    w4 = binding.Fp4Weights.quantize(w, fmt)
+    y = torch.full((lists.rows, n + 8), 7.0, dtype=out, device="cuda")[:, :n]
+    w4.forward(r4, lists.offsets, lists.counts, y=y)
+    assert w4.device_status()[0] == binding.MOE_OK
+    xv = r4.dequantize(lists.offsets, lists.counts, dtype=FP32).double()
+    wv = w4.dequantize(FP32).double()
+    for g, (a, b) in enumerate(lists.spans):
+        if a == b:
+            continue
+        want, s = xv[a:b] @ wv[g].T, xv[a:b].abs() @ wv[g].abs().T
+        # (the dequantized values carry one fp32 rounding each: 2 * 2^-24 S)
+        lim = (torch.finfo(out).eps / 2 * want.abs() + (65 / 64 * (k + 64) + 256 + 8) * 2.0 ** -23 * s + 2.0 ** -25)
+        err = (y[a:b].double() - want).abs()
+        assert (err <= lim).all(), f"{(err - lim).max().item():.3e} above the bound"
+    assert (y.cpu()[lists.free] == 7.0).all()
+    again = y.clone()
+    w4.forward(r4, lists.offsets, lists.counts, y=y)
+    assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_nan_rows_stay_rows_and_bad_lists_write_nothing(fmt):
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((50, 128), generator=gen, device="cuda").to(BF16)
+    w = torch.randn((2, 136, 128), generator=gen, device="cuda").to(BF16)
+    off = torch.tensor([0, 20, 50], dtype=torch.int32, device="cuda")
+    w4 = binding.Fp4Weights.quantize(w, fmt)
+    clean = w4.forward(binding.Fp4Rows(fmt, 128, 2).quantize(x, off), off)
+    x[21, 100] = float("nan")
+    r4 = binding.Fp4Rows(fmt, 128, 2).quantize(x, off)
+    y = w4.forward(r4, off)
+    keep = torch.arange(50, device="cuda") != 21
+    assert torch.equal(y[keep], clean[keep]) and torch.isnan(y[21]).all()
+    bad = torch.tensor([0, 60, 50], dtype=torch.int32, device="cuda")
+    binding.Fp4Rows(fmt, 128, 2).quantize(x, bad)  # in bounds whatever the lists say
+    y.fill_(7.0)
+    w4.forward(r4, bad, y=y)
+    st, detail = w4.device_status()
+    assert st == binding.MOE_ERR_DEVICE and detail[1] == 9 and (y == 7.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_replay_from_a_graph_on_new_rows_and_lists(fmt):
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((40, 256), generator=gen, device="cuda").to(BF16)
+    w4 = binding.Fp4Weights.quantize(torch.randn((3, 200, 256), generator=gen, device="cuda").to(BF16), fmt)
+    off = torch.tensor([0, 9, 9, 40], dtype=torch.int32, device="cuda")
+    r4, y = binding.Fp4Rows(fmt, 256, 3, 40), torch.zeros((40, 200), dtype=BF16, device="cuda")
+
+    def step():
+        w4.forward(r4.quantize(x, off), off, y=y)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    x.copy_(torch.randn((40, 256), generator=gen, device="cuda"))
+    off.copy_(torch.tensor([0, 1, 30, 40], dtype=torch.int32))
+    graph.replay()
+    replayed = y.clone()
+    step()
+    assert torch.equal(replayed, y)

@@ -80,3 +80,48 @@ def test_swiglu_refuses(type_, rows, i, h, ldh, act, ldact, want):
     assert binding.moe_swiglu(type_, rows, i, h, ldh, act, ldact, None) == want
     if ldact == 64 and act == A:
         assert binding.moe_swiglu_grad(type_, rows, i, h, ldh, act, 64, A, 128, None) == want
+
+
+@pytest.mark.parametrize("fmt,groups,rows,k,want", [
+    (0, 1, 1, 32, OK), (1, 1024, 1 << 20, 1 << 20, OK), (2, 1, 1, 32, INV), (0, 0, 1, 32, INV), (0, 1, -1, 32, INV),
+    (0, 1, 1, 0, INV), (1, 1, 1, 16, UNS), (0, 1, 1, 48, UNS), (0, 1025, 1, 32, UNS), (0, 1, 1 << 31, 32, UNS),
+    (0, 1, 1, (1 << 20) + 32, UNS),
+])
+def test_fp4_sizes(fmt, groups, rows, k, want):
+    st, (codes, scales) = binding.moe_fp4_sizes(binding.fp4_shape(fmt, groups, rows, k))
+    assert st == want
+    if want == OK:
+        chunk = 128 if fmt == 0 else 64
+        assert codes == rows * k // 2 and scales == (rows // 128 + groups) * -(-k // chunk) * 512
+
+
+FP4_BAD = [(dict(src=None), INV), (dict(src=A + 8), INV), (dict(ld=60), INV), (dict(ld=68), UNS), (dict(type=3), INV),
+           (dict(codes=None), INV), (dict(codes=A + 8), INV), (dict(scales=None), INV), (dict(scales=A + 4), INV),
+           (dict(gscale=None), INV), (dict(gscale=A + 2), INV), (dict(per=2), INV), (dict(off=None), INV),
+           (dict(off=A + 2), INV), (dict(K=48), UNS), (dict(format=5), INV)]
+
+
+@pytest.mark.parametrize("over,want", FP4_BAD)
+def test_fp4_rows_refuse(over, want):
+    a = dict(format=1, groups=2, rows=7, K=64, type=0, src=A, ld=64, off=A, cnt=None, codes=A, scales=A, gscale=A, per=0)
+    a.update(over)
+    s = binding.fp4_shape(a["format"], a["groups"], a["rows"], a["K"])
+    assert binding.moe_fp4_quantize(s, a["type"], a["src"], a["ld"], a["off"], a["cnt"], a["codes"], a["scales"],
+                                    a["gscale"], a["per"], None) == want
+    assert binding.moe_fp4_dequantize(s, a["codes"], a["scales"], a["gscale"], a["per"], a["off"], a["cnt"], a["type"],
+                                      a["src"], a["ld"], None) == want
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(xc=None), INV), (dict(xs=A + 8), INV), (dict(xg=None), INV), (dict(wc=A + 8), INV), (dict(ws=None), INV),
+    (dict(wg=None), INV), (dict(off=None), INV), (dict(y=None), INV), (dict(ldy=56), INV), (dict(ldy=70), UNS),
+    (dict(space=A + 16), INV), (dict(space_bytes=64), WS), (dict(K=48), UNS), (dict(N=60), UNS), (dict(format=2), INV),
+    (dict(type=2), INV), (dict(rows=0, xc=None, xs=None, xg=None, y=None), OK),
+])
+def test_fp4_product_refuses(over, want):
+    a = dict(format=1, groups=2, rows=7, N=64, K=64, type=0, xc=A, xs=A, xg=A, wc=A, ws=A, wg=A, off=A, y=A, ldy=64,
+             space=A, space_bytes=BIG)
+    a.update(over)
+    s = binding.grouped_shape(a["groups"], a["N"], a["K"], a["rows"], a["type"])
+    assert binding.moe_fp4_gemm(s, a["format"], a["xc"], a["xs"], a["xg"], a["wc"], a["ws"], a["wg"], a["off"], None,
+                                a["y"], a["ldy"], a["space"], a["space_bytes"], None) == want
