@@ -65,6 +65,8 @@ def lib_path() -> str:
 def load(build: bool = True):
     """Load libmoe_gb300.so (compiling it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build() if build else _build.LIB

@@ -18,7 +18,9 @@ namespace moe {
 enum : int32_t { kKernGroupedPlan = 9, kKernGroupedGemm = 10, kKernFp4Gemm = 11 };
 
 constexpr int kGroupsMax = 1024;
-constexpr int kGroupsSmem = 256;  // the GEMM kernels keep unit_off in shared memory up to this many groups
+// the GEMM kernels keep the tables in shared memory up to this many groups
+// (single CTAs; CTA pairs, whose ring takes nearly all of it)
+constexpr int kGroupsSmem[2] = {256, 128};
 
 enum class GroupedOp : int { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
@@ -83,42 +85,77 @@ cudaError_t launch_grouped_wgrad(const CUtensorMap& tm_dw, const GroupedGemmArgs
 #ifdef __CUDACC__
 
 struct GroupedUnit {
-  int g, tile, tile_n, tok0, n;
+  int g, tile, tile_n, tok0, n, start, count;
 };
 
-// Unit u -> its group (binary search in unit_off), feature tile and token
-// chunk (chunk fastest: units that read the same weight tile are neighbours,
-// so the CTAs running side by side read it from DRAM once), or (bn = 0)
-// feature tile and column tile.
-__device__ __forceinline__ GroupedUnit grouped_unit(int u, const int32_t* unit_off, const int32_t* start,
-                                                    const int32_t* count, int G, int tiles, int tiles_n, int bn) {
-  int lo = 0, hi = G;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (unit_off[mid] <= u)
-      lo = mid;
-    else
-      hi = mid;
+// The group tables as a kernel's roles read them: copies in shared memory
+// (G <= the room it has), or the workspace's, through L1.
+struct GroupedTables {
+  const int32_t* unit_off;
+  const int32_t* start;
+  const int32_t* count;
+};
+
+// Copies the tables to `smem` ([3][room + 1]) with the block's threads (visible
+// after the next barrier) where they fit.
+__device__ __forceinline__ GroupedTables grouped_tables(const GroupedGemmArgs& a, int32_t* smem, int room,
+                                                        int threads) {
+  if (a.G > room) return GroupedTables{a.unit_off, a.start, a.count};
+  for (int i = threadIdx.x; i <= a.G; i += threads) {
+    smem[i] = __ldcg(a.unit_off + i);
+    if (i < a.G) {
+      smem[room + 1 + i] = __ldcg(a.start + i);
+      smem[2 * (room + 1) + i] = __ldcg(a.count + i);
+    }
   }
-  GroupedUnit r;
-  r.g = lo;
-  const int local = u - unit_off[lo];
-  const int s = __ldcg(start + lo), c = __ldcg(count + lo);
-  if (bn > 0) {
-    const int chunks = (c + bn - 1) / bn;  // >= 1: u lies in this group's range
-    r.tile = local / chunks;
-    const int chunk = local - r.tile * chunks;
-    r.tile_n = 0;
-    r.tok0 = s + chunk * bn;
-    r.n = min(bn, c - chunk * bn);
-  } else {
-    r.tile = local / tiles_n;
-    r.tile_n = local - r.tile * tiles_n;
-    r.tok0 = s;
-    r.n = c;
-  }
-  return r;
+  return GroupedTables{smem, smem + room + 1, smem + 2 * (room + 1)};
 }
+
+// Units -> groups for one role, which asks for ascending units: the group of
+// the last unit is kept, and searched for (binary, in unit_off) only when a
+// unit lies behind it.
+// A unit's feature tile and token chunk: chunk fastest (units that read the
+// same weight tile are neighbours, so the CTAs running side by side read it
+// from DRAM once), or (bn = 0) its feature tile and column tile.
+struct GroupedUnits {
+  GroupedTables t;
+  int G, tiles_n, bn;
+  int g, first, last;  // the kept group and its units [first, last)
+  int start, count, chunks;
+
+  __device__ GroupedUnits(const GroupedTables& tables, int groups, int tiles_n_, int bn_)
+      : t(tables), G(groups), tiles_n(tiles_n_), bn(bn_), g(0), first(0), last(0), start(0), count(0), chunks(1) {}
+
+  __device__ __forceinline__ GroupedUnit at(int u) {
+    if (u >= last) {
+      int lo = g, hi = G;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.unit_off[mid] <= u)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      g = lo;
+      first = t.unit_off[lo];
+      last = t.unit_off[lo + 1];
+      start = t.start[lo];
+      count = t.count[lo];
+      chunks = bn > 0 ? (count + bn - 1) / bn : tiles_n;  // >= 1: u lies in this group's range
+    }
+    GroupedUnit r;
+    r.g = g;
+    r.start = start;
+    r.count = count;
+    const int local = u - first;
+    r.tile = local / chunks;
+    const int fast = local - r.tile * chunks;
+    r.tile_n = bn > 0 ? 0 : fast;
+    r.tok0 = bn > 0 ? start + fast * bn : start;
+    r.n = bn > 0 ? min(bn, count - fast * bn) : count;
+    return r;
+  }
+};
 
 // A worker's work, as segments: K-blocks [kb0, kb1) of unit u.  Stream-K: a
 // contiguous range of (unit, K-block) iterations of equal length for every

@@ -61,7 +61,8 @@ struct Cfg {
   static constexpr int kEpiWarps = PAIR ? 8 : 4;  // two per TMEM lane quarter for the pair's single accumulator
   static constexpr int kThreads = 32 * (2 + kEpiWarps + 4);
   static constexpr int kBarBytes = 512;
-  static constexpr int kTabBytes = (kGroupsSmem + 1) * 4;
+  static constexpr int kTabGroups = kGroupsSmem[PAIR];
+  static constexpr int kTabBytes = 3 * (kTabGroups + 1) * 4;
   static constexpr int kGxBytes = F == Fp4Format::kNv ? 4 * BN * 4 : 0;  // x's fp32 scales, per epilogue warp
   static constexpr size_t kSmemBytes =
       1024 + static_cast<size_t>(STAGES) * kStageBytes + kBarBytes + kTabBytes + kGxBytes + 16;
@@ -80,6 +81,10 @@ enum : int {
   kWaitScales = 7,
   kWaitScaleLoads = 8
 };
+
+__device__ __forceinline__ void put4(uint32_t* d, const uint4& v) {
+  d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+}
 
 __device__ __forceinline__ uint16_t to16(float v, bool fp16) {
   return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
@@ -139,11 +144,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
     }
   }
   pdl_wait();  // the plan kernel's tables
-  const int32_t* t_unit = a.unit_off;
-  if (a.G <= kGroupsSmem) {
-    for (int i = threadIdx.x; i <= a.G; i += C::kThreads) tab[i] = __ldcg(a.unit_off + i);
-    t_unit = tab;
-  }
+  const GroupedTables tables = grouped_tables(a, tab, C::kTabGroups, C::kThreads);
   tc_fence_before();
   if (PAIR)
     cluster_sync();
@@ -152,11 +153,11 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  const int total_units = t_unit[a.G];
+  const int total_units = tables.unit_off[a.G];
   const int kblocks = (a.R + 255) / 256;
   const int chunks_k = (a.R + fp4_chunk(F) - 1) / fp4_chunk(F);  // scale tiles along K per tile row
   constexpr bool kStreamK = !PAIR;
-  auto unit_of = [&](int u) { return grouped_unit(u, t_unit, a.start, a.count, a.G, a.tiles, 1, BN); };
+  GroupedUnits units(tables, a.G, 1, BN);  // each thread walks its role's units
   auto valid_chunks = [&](int kb) { return min(C::kChunks, chunks_k - kb * C::kChunks); };
   auto n_of = [](int n) { return PAIR ? (n + 31) / 32 * 32 : (n + 15) / 16 * 16; };
 
@@ -172,19 +173,19 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
       int u, kb0, kb1;
       while (ok && rg.next(u, kb0, kb1)) {
-        const GroupedUnit un = unit_of(u);
+        const GroupedUnit un = units.at(u);
         const int feat = PAIR ? un.tile * 256 + static_cast<int>(rank) * 128 : un.tile * 128;
         const int n_mma = n_of(un.n);
         const int half = PAIR ? n_mma / 2 : n_mma;
         const int tok_first = un.tok0 + static_cast<int>(rank) * half;
         const int tok_rows = (half + TOKBOX - 1) / TOKBOX * TOKBOX;
         const uint32_t bytes = kABytes + tok_rows * 128;
-        const uint64_t pol_w = __ldcg(a.count + un.g) > BN ? pol_keep : pol_stream;
+        const uint64_t pol_w = un.count > BN ? pol_keep : pol_stream;
         // scale tile rows: of this CTA's features (past N: a tile row of the
         // same matrix, its products are dropped), of the unit's rows
         const int64_t wt = static_cast<int64_t>(un.g) * args.w_tile_rows + min(feat / 128, args.w_tile_rows - 1);
-        const int start = __ldcg(a.start + un.g), within = un.tok0 - start;
-        const int64_t xt = (args.equal ? static_cast<int64_t>(un.g) * ((args.equal + 127) / 128) : start / 128 + un.g) +
+        const int within = un.tok0 - un.start;
+        const int64_t xt = (args.equal ? static_cast<int64_t>(un.g) * ((args.equal + 127) / 128) : un.start / 128 + un.g) +
                            within / 128;
         const int x_tiles = C::kG == 2 && un.n > 128 ? 2 : 1;
         // a 32-row unit lies inside a tile: its rows are moved to row 0 by the scale warps
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
       int u, kb0, kb1;
       while (ok && rg.next(u, kb0, kb1)) {
-        const GroupedUnit un = unit_of(u);
+        const GroupedUnit un = units.at(u);
         const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag)
                                    : mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag);
         if (!free_acc) {
@@ -333,11 +334,10 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
     GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
     int u, kb0, kb1;
     while (ok && rg.next(u, kb0, kb1)) {
-      const GroupedUnit un = unit_of(u);
-      const int x_tiles = C::kG == 2 && un.n > 128 ? 2 : 1;
+      const GroupedUnit un = units.at(u);
       // a unit of 32 rows may start at row 32, 64 or 96 of its tile: column j
       // of its words then belongs at column 0
-      const int j0 = BN < 128 ? ((un.tok0 - __ldcg(a.start + un.g)) & 127) >> 5 : 0;
+      const int j0 = BN < 128 ? ((un.tok0 - un.start) & 127) >> 5 : 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         const bool got = mbar_wait(&sfld[stage], phase, kWaitTimeoutNs, abort_flag);
         if (!__all_sync(0xFFFFFFFFu, got)) {  // warp-uniform: tcgen05.st needs every lane
@@ -346,22 +346,23 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
         }
         const uint8_t* sf = smem + stage * C::kStageBytes + kABytes + C::kBBytes + lane * 16;
         const uint32_t cols = tmem_base + static_cast<uint32_t>(C::kAccBufs * BN + stage * C::kSfCols) + quarter;
-        const int n_c = valid_chunks(kb);
+        // all tiles of the stage (past K or the unit's rows: whatever the stage
+        // held, which no MMA reads) with one store per operand
+        uint32_t w[4 * C::kChunks], x[4 * C::kChunks * C::kG];
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c) {
-          if (c >= n_c) break;
-          tmem_st_32x32b_x4(cols + 4 * c, *reinterpret_cast<const uint4*>(sf + 512 * c));
+          put4(w + 4 * c, *reinterpret_cast<const uint4*>(sf + 512 * c));
 #pragma unroll
-          for (int h = 0; h < C::kG; ++h) {
-            if (h >= x_tiles) break;
-            uint4 w = *reinterpret_cast<const uint4*>(sf + C::kSfW + h * C::kSfW + 512 * c);
-            if (BN < 128) {
-              const uint32_t v = j0 == 0 ? w.x : j0 == 1 ? w.y : j0 == 2 ? w.z : w.w;
-              w = make_uint4(v, v, v, v);
-            }
-            tmem_st_32x32b_x4(cols + 16 + 4 * (c * C::kG + h), w);
-          }
+          for (int h = 0; h < C::kG; ++h)
+            put4(x + 4 * (c * C::kG + h), *reinterpret_cast<const uint4*>(sf + C::kSfW + h * C::kSfW + 512 * c));
         }
+        if (BN < 128) {
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            x[4 * c] = j0 == 0 ? x[4 * c] : j0 == 1 ? x[4 * c + 1] : j0 == 2 ? x[4 * c + 2] : x[4 * c + 3];
+        }
+        tmem_st_32x32b(cols, w);
+        tmem_st_32x32b(cols + 16, x);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
     const int col0 = (warp - 2) / 4 * kCols;
     float* gx = gx_buf + (warp - 2) * kCols;
     while (ok && rg.next(u, kb0, kb1)) {
-      const GroupedUnit un = unit_of(u);
+      const GroupedUnit un = units.at(u);
       const int feat0 = PAIR ? un.tile * 256 + static_cast<int>(rank) * 128 : un.tile * 128;
       const bool fp16 = a.fp16 != 0, mine = feat0 + row < a.F;
       uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(un.tok0) * a.ldo + feat0 + row;

@@ -146,7 +146,8 @@ struct Cfg {
   static constexpr uint32_t kTmemCols = 2 * BN <= 32 ? 32 : 2 * BN <= 64 ? 64 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;
   static constexpr int kStoreBytes = kWgrad ? 4 * 2 * 4096 : 0;  // two 32-row x 128-byte boxes per epilogue warp
   static constexpr int kBarBytes = 256;
-  static constexpr int kTabBytes = (kGroupsSmem + 1) * 4;
+  static constexpr int kTabGroups = kGroupsSmem[PAIR];
+  static constexpr int kTabBytes = 3 * (kTabGroups + 1) * 4;
   static constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(STAGES) * kStageBytes + kStoreBytes + kBarBytes + kTabBytes;
   static_assert(kBRows % TOKBOX == 0 && BN >= 32 && BN <= 256, "token tile");
   static_assert(!kWgrad || (PAIR && BN == 256), "weight gradient: 256 x 256 tiles of CTA pairs");
@@ -209,11 +210,7 @@ __global__ void __launch_bounds__(192, 1)
     }
   }
   pdl_wait();  // the plan kernel's tables
-  const int32_t* t_unit = a.unit_off;
-  if (a.G <= kGroupsSmem) {
-    for (int i = threadIdx.x; i <= a.G; i += C::kThreads) tab[i] = __ldcg(a.unit_off + i);
-    t_unit = tab;
-  }
+  const GroupedTables tables = grouped_tables(a, tab, C::kTabGroups, C::kThreads);
   tc_fence_before();
   if (PAIR)
     cluster_sync();  // the peer's barriers are initialised before any remote signal
@@ -222,11 +219,11 @@ __global__ void __launch_bounds__(192, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  const int total_units = t_unit[a.G];
+  const int total_units = tables.unit_off[a.G];
   const int kblocks = C::kWgrad ? 1 : (a.R + 63) / 64;
   constexpr bool kStreamK = !PAIR;
   constexpr int kUnitBn = C::kWgrad ? 0 : BN;
-  auto unit_of = [&](int u) { return grouped_unit(u, t_unit, a.start, a.count, a.G, a.tiles, a.tiles_n, kUnitBn); };
+  GroupedUnits units(tables, a.G, a.tiles_n, kUnitBn);  // each thread walks its role's units
 
   if (warp == 0) {
     if (lane == 0) {
@@ -241,7 +238,7 @@ __global__ void __launch_bounds__(192, 1)
       GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
       int u, kb0, kb1;
       while (ok && rg.next(u, kb0, kb1)) {
-        const GroupedUnit un = unit_of(u);
+        const GroupedUnit un = units.at(u);
         const int feat = PAIR ? un.tile * 256 + static_cast<int>(rank) * 128 : un.tile * 128;
         if (C::kWgrad) kb1 = (un.n + 63) / 64;
         const int n_mma = PAIR ? (un.n + 31) / 32 * 32 : (un.n + 15) / 16 * 16;
@@ -250,7 +247,7 @@ __global__ void __launch_bounds__(192, 1)
         const int tok_rows = (half + TOKBOX - 1) / TOKBOX * TOKBOX;  // whole boxes
         const uint32_t bytes = C::kWgrad ? C::kStageBytes : kABytes + tok_rows * 128;
         // a weight tile read by one token chunk only is streamed; by more, kept
-        const uint64_t pol_w = C::kWgrad || __ldcg(a.count + un.g) > BN ? pol_keep : pol_stream;
+        const uint64_t pol_w = C::kWgrad || un.count > BN ? pol_keep : pol_stream;
         const CUtensorMap* map_dy = a.maps + 2 * un.g;
         if (C::kWgrad && un.g != map_group) {
           tensormap_acquire(map_dy);
@@ -324,7 +321,7 @@ __global__ void __launch_bounds__(192, 1)
       GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
       int u, kb0, kb1;
       while (ok && rg.next(u, kb0, kb1)) {
-        const GroupedUnit un = unit_of(u);
+        const GroupedUnit un = units.at(u);
         if (C::kWgrad) {
           kb1 = (un.n + 63) / 64;
           if (kb1 == 0) continue;  // an empty group: the epilogue writes zeros
@@ -404,7 +401,7 @@ __global__ void __launch_bounds__(192, 1)
     uint8_t* my_store = store_buf + q * 8192;
     uint32_t buf = 0;
     while (ok && rg.next(u, kb0, kb1)) {
-      const GroupedUnit un = unit_of(u);
+      const GroupedUnit un = units.at(u);
       const int feat0 = PAIR ? un.tile * 256 + static_cast<int>(rank) * 128 : un.tile * 128;
       const bool has_acc = !C::kWgrad || un.n > 0;
       if (has_acc) {

@@ -104,6 +104,8 @@ def hard_rows(rng, rows, k, dtype):
         x[0, 32:64] = 0.0
         x[-1, :16] = torch.finfo(dtype).tiny
         x[-1, 16:32] = torch.finfo(dtype).smallest_normal * 8
+    if k >= 96:  # a block of subnormals alone
+        x[-1, 64:96] = torch.arange(32).to(dtype) * (torch.finfo(dtype).smallest_normal / 32)
     if rows > 2:
         x[1] = 0.0
     return x
