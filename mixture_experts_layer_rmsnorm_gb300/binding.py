@@ -440,12 +440,16 @@ def moe_fp4_gemm(s: MoeGroupedShape, format, x_codes, x_scales, x_gscale, w_code
                                offsets, counts, y, ldy, workspace, workspace_bytes, stream)
 
 
+_types = {}
+
+
 def _type_of(dtype) -> int:
-    import torch
-    types = {torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_FP16, torch.float32: MOE_TYPE_FP32}
-    if dtype not in types:
+    if not _types:
+        import torch
+        _types.update({torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_FP16, torch.float32: MOE_TYPE_FP32})
+    if dtype not in _types:
         raise TypeError(f"{dtype}: bfloat16, float16 or float32 wanted")
-    return types[dtype]
+    return _types[dtype]
 
 
 def _check(what, t, device, dtype, shape_, rows=False):
@@ -454,7 +458,7 @@ def _check(what, t, device, dtype, shape_, rows=False):
         raise ValueError(f"{what} is on {t.device}, not on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{what} is {t.dtype}, not {dtype}")
-    if tuple(t.shape) != tuple(shape_):
+    if t.shape != shape_:
         raise ValueError(f"{what} is {tuple(t.shape)}, not {tuple(shape_)}")
     if not (t.stride(-1) == 1 or t.shape[-1] == 1) if rows else not t.is_contiguous():
         raise ValueError(f"{what} is not contiguous" + (" along its rows" if rows else ""))
@@ -476,18 +480,29 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
 
 
+def _enqueue(name, device, fn, *args):
+    """fn(*args, stream) with ``device`` current, on its current stream; MoeError if it fails."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if st != MOE_OK:
+        raise MoeError(st, name)
+
+
 def swiglu(h, act=None):
     """SiLU(gate) * up of rows h = [gate | up] (moe_swiglu), on the current stream of h's device."""
     import torch
     rows, two_i = h.shape
     _check("h", h, h.device, h.dtype, h.shape, rows=True)
-    with torch.cuda.device(h.device):
-        act = torch.empty((rows, two_i // 2), dtype=h.dtype, device=h.device) if act is None else \
-            _check("act", act, h.device, h.dtype, (rows, two_i // 2), rows=True)
-        st = moe_swiglu(_type_of(h.dtype), rows, two_i // 2, _ptr(h), _ld(h), _ptr(act), _ld(act),
-                        torch.cuda.current_stream().cuda_stream)
-    if st != MOE_OK:
-        raise MoeError(st, "moe_swiglu")
+    if act is None:
+        act = torch.empty((rows, two_i // 2), dtype=h.dtype, device=h.device)
+    else:
+        _check("act", act, h.device, h.dtype, (rows, two_i // 2), rows=True)
+    _enqueue("moe_swiglu", h.device, moe_swiglu, _type_of(h.dtype), rows, two_i // 2, _ptr(h), _ld(h), _ptr(act),
+             _ld(act))
     return act
 
 
@@ -497,13 +512,12 @@ def swiglu_grad(h, dact, dh=None):
     rows, two_i = h.shape
     _check("h", h, h.device, h.dtype, h.shape, rows=True)
     _check("dact", dact, h.device, h.dtype, (rows, two_i // 2), rows=True)
-    with torch.cuda.device(h.device):
-        dh = torch.empty((rows, two_i), dtype=h.dtype, device=h.device) if dh is None else \
-            _check("dh", dh, h.device, h.dtype, (rows, two_i), rows=True)
-        st = moe_swiglu_grad(_type_of(h.dtype), rows, two_i // 2, _ptr(h), _ld(h), _ptr(dact), _ld(dact), _ptr(dh),
-                             _ld(dh), torch.cuda.current_stream().cuda_stream)
-    if st != MOE_OK:
-        raise MoeError(st, "moe_swiglu_grad")
+    if dh is None:
+        dh = torch.empty((rows, two_i), dtype=h.dtype, device=h.device)
+    else:
+        _check("dh", dh, h.device, h.dtype, (rows, two_i), rows=True)
+    _enqueue("moe_swiglu_grad", h.device, moe_swiglu_grad, _type_of(h.dtype), rows, two_i // 2, _ptr(h), _ld(h),
+             _ptr(dact), _ld(dact), _ptr(dh), _ld(dh))
     return dh
 
 
@@ -528,17 +542,13 @@ class GroupedProducts:
         return grouped_shape(self.groups, self.N, self.K, rows, _type_of(self.dtype))
 
     def _rows(self, what, t, rows, width):
-        import torch
         if t is None:
+            import torch
             return torch.empty((rows, width), dtype=self.dtype, device=self.device)
         return _check(what, t, self.device, self.dtype, (rows, width), rows=True)
 
     def _call(self, name, fn, *args):
-        import torch
-        with torch.cuda.device(self.device):
-            st = fn(*args, _ptr(self.workspace), self.workspace.numel(), torch.cuda.current_stream().cuda_stream)
-        if st != MOE_OK:
-            raise MoeError(st, name)
+        _enqueue(name, self.device, fn, *args, _ptr(self.workspace), self.workspace.numel())
 
     def forward(self, x, w, offsets=None, counts=None, y=None):
         """y[p] = x[p] w_g^T for the rows p of every group g; other rows of y stay as they are."""
@@ -628,12 +638,8 @@ class Fp4Rows:
         self.ensure_capacity(x.shape[0])
         _check("x", x, self.device, x.dtype, (x.shape[0], self.K), rows=True)
         lists = _lists(self, offsets, counts)
-        with torch.cuda.device(self.device):
-            st = moe_fp4_quantize(self.shape(x.shape[0]), _type_of(x.dtype), _ptr(x), _ld(x), *lists, _ptr(self.codes),
-                                  _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_ROW,
-                                  torch.cuda.current_stream().cuda_stream)
-        if st != MOE_OK:
-            raise MoeError(st, "moe_fp4_quantize")
+        _enqueue("moe_fp4_quantize", self.device, moe_fp4_quantize, self.shape(x.shape[0]), _type_of(x.dtype), _ptr(x),
+                 _ld(x), *lists, _ptr(self.codes), _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_ROW)
         self.rows = x.shape[0]
         return self
 
@@ -645,12 +651,8 @@ class Fp4Rows:
         else:
             _check("y", y, self.device, dtype or y.dtype, (self.rows, self.K), rows=True)
         lists = _lists(self, offsets, counts)
-        with torch.cuda.device(self.device):
-            st = moe_fp4_dequantize(self.shape(self.rows), _ptr(self.codes), _ptr(self.scales), _ptr(self.gscale),
-                                    MOE_SCALE_PER_ROW, *lists, _type_of(y.dtype), _ptr(y), _ld(y),
-                                    torch.cuda.current_stream().cuda_stream)
-        if st != MOE_OK:
-            raise MoeError(st, "moe_fp4_dequantize")
+        _enqueue("moe_fp4_dequantize", self.device, moe_fp4_dequantize, self.shape(self.rows), _ptr(self.codes),
+                 _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_ROW, *lists, _type_of(y.dtype), _ptr(y), _ld(y))
         return y
 
 
@@ -696,23 +698,18 @@ class Fp4Weights:
         codes = torch.empty((groups, N, K // 2), dtype=torch.uint8, device=w.device)
         scales = torch.empty(n_scales, dtype=torch.uint8, device=w.device)
         gscale = torch.empty(groups, dtype=torch.float32, device=w.device) if format == "nv" else None
-        with torch.cuda.device(w.device):
-            st = moe_fp4_quantize(s, _type_of(w.dtype), _ptr(w), K, None, None, _ptr(codes), _ptr(scales),
-                                  _ptr(gscale), MOE_SCALE_PER_GROUP, torch.cuda.current_stream().cuda_stream)
-        if st != MOE_OK:
-            raise MoeError(st, "moe_fp4_quantize")
+        _enqueue("moe_fp4_quantize", w.device, moe_fp4_quantize, s, _type_of(w.dtype), _ptr(w), K, None, None,
+                 _ptr(codes), _ptr(scales), _ptr(gscale), MOE_SCALE_PER_GROUP)
         return cls(format, codes, scales, gscale)
 
     def dequantize(self, dtype=None):
         """The values the weights stand for, [groups, N, K] in ``dtype`` (bf16 by default)."""
         import torch
         w = torch.empty((self.groups, self.N, self.K), dtype=dtype or torch.bfloat16, device=self.device)
-        with torch.cuda.device(self.device):
-            st = moe_fp4_dequantize(fp4_shape(self.format, self.groups, self.groups * self.N, self.K),
-                                    _ptr(self.codes), _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_GROUP, None,
-                                    None, _type_of(w.dtype), _ptr(w), self.K, torch.cuda.current_stream().cuda_stream)
-        if st != MOE_OK:
-            raise MoeError(st, "moe_fp4_dequantize")
+        _enqueue("moe_fp4_dequantize", self.device, moe_fp4_dequantize,
+                 fp4_shape(self.format, self.groups, self.groups * self.N, self.K), _ptr(self.codes),
+                 _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_GROUP, None, None, _type_of(w.dtype), _ptr(w),
+                 self.K)
         return w
 
     def forward(self, rows: Fp4Rows, offsets=None, counts=None, y=None, dtype=None):
@@ -725,13 +722,10 @@ class Fp4Weights:
         else:
             _check("y", y, self.device, dtype or y.dtype, (rows.rows, self.N), rows=True)
         lists = _lists(self, offsets, counts)
-        with torch.cuda.device(self.device):
-            st = moe_fp4_gemm(grouped_shape(self.groups, self.N, self.K, rows.rows, _type_of(y.dtype)), self.format,
-                              _ptr(rows.codes), _ptr(rows.scales), _ptr(rows.gscale), _ptr(self.codes),
-                              _ptr(self.scales), _ptr(self.gscale), *lists, _ptr(y), _ld(y), _ptr(self.workspace),
-                              self.workspace.numel(), torch.cuda.current_stream().cuda_stream)
-        if st != MOE_OK:
-            raise MoeError(st, "moe_fp4_gemm")
+        _enqueue("moe_fp4_gemm", self.device, moe_fp4_gemm,
+                 grouped_shape(self.groups, self.N, self.K, rows.rows, _type_of(y.dtype)), self.format,
+                 _ptr(rows.codes), _ptr(rows.scales), _ptr(rows.gscale), _ptr(self.codes), _ptr(self.scales),
+                 _ptr(self.gscale), *lists, _ptr(y), _ld(y), _ptr(self.workspace), self.workspace.numel())
         return y
 
     def device_status(self):
