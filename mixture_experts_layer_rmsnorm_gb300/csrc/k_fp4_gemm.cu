@@ -248,9 +248,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       int u, kb0, kb1;
       while (ok && rg.next(u, kb0, kb1)) {
         const GroupedUnit un = units.at(u);
-        const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag)
-                                   : mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag);
-        if (!free_acc) {
+        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag)) {
           ok = false;
           where = kWaitAccFree;
           break;
@@ -264,9 +262,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
             where = kWaitSlotFull;
             break;
           }
-          const bool have_scales = PAIR ? mbar_wait_cluster(&sfull[stage], phase, kWaitTimeoutNs, abort_flag)
-                                        : mbar_wait(&sfull[stage], phase, kWaitTimeoutNs, abort_flag);
-          if (!have_scales) {
+          if (!mbar_wait(&sfull[stage], phase, kWaitTimeoutNs, abort_flag)) {
             ok = false;
             where = kWaitScales;
             break;
@@ -368,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if (PAIR)
-            mbar_arrive_cluster(sfull_cl + 8u * stage);
+            mbar_arrive_remote(sfull_cl + 8u * stage);
           else
             mbar_arrive(&sfull[stage]);
         }
@@ -418,7 +414,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if (PAIR)
-            mbar_arrive_cluster(tempty_cl + 8u * acc);
+            mbar_arrive_remote(tempty_cl + 8u * acc);
           else
             mbar_arrive(&tempty[acc]);
         }

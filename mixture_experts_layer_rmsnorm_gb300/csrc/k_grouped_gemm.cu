@@ -326,9 +326,7 @@ __global__ void __launch_bounds__(192, 1)
           kb1 = (un.n + 63) / 64;
           if (kb1 == 0) continue;  // an empty group: the epilogue writes zeros
         }
-        const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag)
-                                   : mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag);
-        if (!free_acc) {
+        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag)) {
           ok = false;
           where = kWaitAccFree;
           break;
@@ -529,7 +527,7 @@ __global__ void __launch_bounds__(192, 1)
         __syncwarp();
         if (lane == 0) {
           if (PAIR)
-            mbar_arrive_cluster(tempty_cl + 8u * acc);
+            mbar_arrive_remote(tempty_cl + 8u * acc);
           else
             mbar_arrive(&tempty[acc]);
         }
