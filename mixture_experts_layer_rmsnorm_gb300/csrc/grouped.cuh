@@ -65,6 +65,7 @@ struct GroupedGemmArgs {
   int G, F, R, C;
   int tiles;       // M tiles (of 128, or 256 for CTA pairs) per group
   int tiles_n;     // weight gradient: column tiles of 256
+  int bn;          // rows per unit at most (CTA pairs; the single-CTA plan's is fixed)
   int fp16;        // operands fp16, else bf16
   int out_fp32;    // weight gradient: fp32, else the operand type
   int accumulate;  // weight gradient (fp32): add to what dw holds
@@ -78,8 +79,12 @@ int grouped_tok_box(GroupedPlan plan);    // token rows per TMA box
 size_t grouped_partial_bytes();           // stream-K partial sums
 constexpr int kWgradTile = 256;           // rows and columns of a unit of the weight gradient
 
+// tm_x: the token rows in boxes of kTokBox[plan] rows; tm_x32: of 32 (large plan)
 cudaError_t launch_grouped_gemm(GroupedOp op, GroupedPlan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
-                                const GroupedGemmArgs& a, int num_sms, cudaStream_t stream);
+                                const CUtensorMap& tm_x32, const GroupedGemmArgs& a, int num_sms,
+                                cudaStream_t stream);
+cudaError_t launch_grouped_pair(GroupedOp op, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
+                                const CUtensorMap& tm_x32, const GroupedGemmArgs& a, cudaStream_t stream);
 cudaError_t launch_grouped_wgrad(const CUtensorMap& tm_dw, const GroupedGemmArgs& a, cudaStream_t stream);
 
 #ifdef __CUDACC__
@@ -116,15 +121,23 @@ __device__ __forceinline__ GroupedTables grouped_tables(const GroupedGemmArgs& a
 // unit lies behind it.
 // A unit's feature tile and token chunk: chunk fastest (units that read the
 // same weight tile are neighbours, so the CTAs running side by side read it
-// from DRAM once), or (bn = 0) its feature tile and column tile.
+// from DRAM once), or (bn = 0) its feature tile and column tile.  Chunks are
+// bn rows each, or (balance) even: a group of c rows has m = ceil(c / bn) of
+// them, chunk i from row floor(i c / m) on.
 struct GroupedUnits {
   GroupedTables t;
   int G, tiles_n, bn;
+  bool balance;
   int g, first, last;  // the kept group and its units [first, last)
   int start, count, chunks;
 
-  __device__ GroupedUnits(const GroupedTables& tables, int groups, int tiles_n_, int bn_)
-      : t(tables), G(groups), tiles_n(tiles_n_), bn(bn_), g(0), first(0), last(0), start(0), count(0), chunks(1) {}
+  __device__ GroupedUnits(const GroupedTables& tables, int groups, int tiles_n_, int bn_, bool balance_ = false)
+      : t(tables), G(groups), tiles_n(tiles_n_), bn(bn_), balance(balance_), g(0), first(0), last(0), start(0),
+        count(0), chunks(1) {}
+
+  __device__ __forceinline__ int chunk_start(int i) const {
+    return balance ? static_cast<int>(static_cast<int64_t>(i) * count / chunks) : i * bn;
+  }
 
   __device__ __forceinline__ GroupedUnit at(int u) {
     if (u >= last) {
@@ -151,8 +164,14 @@ struct GroupedUnits {
     r.tile = local / chunks;
     const int fast = local - r.tile * chunks;
     r.tile_n = bn > 0 ? 0 : fast;
-    r.tok0 = bn > 0 ? start + fast * bn : start;
-    r.n = bn > 0 ? min(bn, count - fast * bn) : count;
+    if (bn > 0) {
+      const int from = chunks > 1 ? chunk_start(fast) : 0;
+      r.tok0 = start + from;
+      r.n = (fast + 1 < chunks ? chunk_start(fast + 1) : count) - from;
+    } else {
+      r.tok0 = start;
+      r.n = count;
+    }
     return r;
   }
 };

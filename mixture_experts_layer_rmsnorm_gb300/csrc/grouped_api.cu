@@ -179,9 +179,10 @@ moe_status rows_product(GroupedOp op, const moe_grouped_shape* s, const void* in
   if (s->rows == 0) return MOE_OK;
   const int sms = num_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
-  CUtensorMap tw, tx;
+  CUtensorMap tw, tx, tx32;
   if (!make_matrix_map(&tw, s->type, w, s->groups, s->N, s->K, op == GroupedOp::kForward ? 128 : 64) ||
-      !make_rows_map(&tx, s->type, in, R, s->rows, ldin, static_cast<uint32_t>(moe::grouped_tok_box(plan))))
+      !make_rows_map(&tx, s->type, in, R, s->rows, ldin, static_cast<uint32_t>(moe::grouped_tok_box(plan))) ||
+      (plan == GroupedPlan::kLarge && !make_rows_map(&tx32, s->type, in, R, s->rows, ldin, 32)))
     return MOE_ERR_CUDA;
   const Layout L = make_layout(s->groups);
   moe::GroupedPlanArgs p = plan_args(s, L, ws, offsets, counts);
@@ -193,9 +194,10 @@ moe_status rows_product(GroupedOp op, const moe_grouped_shape* s, const void* in
   a.F = F;
   a.R = R;
   a.tiles = tiles;
+  a.bn = bn;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (moe::launch_grouped_plan(p, tx, tx, cs) != cudaSuccess ||
-      moe::launch_grouped_gemm(op, plan, tw, tx, a, sms, cs) != cudaSuccess)
+      moe::launch_grouped_gemm(op, plan, tw, tx, plan == GroupedPlan::kLarge ? tx32 : tx, a, sms, cs) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
 }

@@ -239,8 +239,10 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ---------------- MMA issuer
+    if (leader) {
+      // ---------------- MMA issuer: the whole warp walks the units, one lane issues
+      const bool issue = elect_one();
+      const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(smem));
       int stage = 0, acc = 0, where = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -248,74 +250,84 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       int u, kb0, kb1;
       while (ok && rg.next(u, kb0, kb1)) {
         const GroupedUnit un = units.at(u);
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag)) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag))) {
           ok = false;
           where = kWaitAccFree;
           break;
         }
         tc_fence_after();
         const uint32_t n_mma = static_cast<uint32_t>(n_of(un.n));
+        // instruction descriptors: MXFP4's MMAs of a chunk take scale bytes 0, 1 and 2, 3
+        const uint32_t id0 = F == Fp4Format::kNv ? idesc_nvf4(PAIR ? 256 : 128, n_mma) : idesc_mxf4(PAIR ? 256 : 128, n_mma, 0, 0);
+        const uint32_t id2 = idesc_mxf4(PAIR ? 256 : 128, n_mma, 2, 2);
         const uint32_t d_acc = tmem_base + static_cast<uint32_t>(acc * BN);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&full[stage], phase, kWaitTimeoutNs, abort_flag)) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, kWaitTimeoutNs, abort_flag))) {
             ok = false;
             where = kWaitSlotFull;
             break;
           }
-          if (!mbar_wait(&sfull[stage], phase, kWaitTimeoutNs, abort_flag)) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sfull[stage], phase, kWaitTimeoutNs, abort_flag))) {
             ok = false;
             where = kWaitScales;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * C::kStageBytes), sb = sa + kABytes;
+          const uint64_t ad0 = a0 + static_cast<uint64_t>(stage * (C::kStageBytes >> 4)), bd0 = ad0 + (kABytes >> 4);
           const uint32_t sf_w = tmem_base + static_cast<uint32_t>(C::kAccBufs * BN + stage * C::kSfCols);
           const uint32_t sf_x = sf_w + 16;
           const int n_k = min(4, (a.R - kb * 256 + 63) / 64);  // MMAs of K = 64
+          if (issue) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= n_k) break;
-            const uint32_t accum = (kb > kb0 || k > 0) ? 1u : 0u;
-            const uint64_t ad = sdesc_kmajor_sw128(sa + k * 32), bd = sdesc_kmajor_sw128(sb + k * 32);
-            if constexpr (F == Fp4Format::kNv) {
-              const uint32_t id = idesc_nvf4(PAIR ? 256 : 128, n_mma);
-              if (PAIR)
-                mma_nvf4_ss_pair(d_acc, ad, bd, id, sf_w + 4 * k, sf_x + 4 * C::kG * k, accum);
-              else
-                mma_nvf4_ss(d_acc, ad, bd, id, sf_w + 4 * k, sf_x + 4 * C::kG * k, accum);
-            } else {
-              const uint32_t c = static_cast<uint32_t>(k >> 1), sid = 2u * static_cast<uint32_t>(k & 1);
-              const uint32_t id = idesc_mxf4(PAIR ? 256 : 128, n_mma, sid, sid);
-              if (PAIR)
-                mma_mxf4_ss_pair(d_acc, ad, bd, id, sf_w + 4 * c, sf_x + 4 * C::kG * c, accum);
-              else
-                mma_mxf4_ss(d_acc, ad, bd, id, sf_w + 4 * c, sf_x + 4 * C::kG * c, accum);
+            for (int k = 0; k < 4; ++k) {
+              if (k >= n_k) break;
+              const uint32_t accum = k > 0 ? 1u : kb > kb0;
+              const uint64_t ad = ad0 + 2 * k, bd = bd0 + 2 * k;  // 32 bytes further
+              if constexpr (F == Fp4Format::kNv) {
+                if (PAIR)
+                  mma_nvf4_ss_pair(d_acc, ad, bd, id0, sf_w + 4 * k, sf_x + 4 * C::kG * k, accum);
+                else
+                  mma_nvf4_ss(d_acc, ad, bd, id0, sf_w + 4 * k, sf_x + 4 * C::kG * k, accum);
+              } else {
+                const uint32_t c = static_cast<uint32_t>(k >> 1), id = (k & 1) ? id2 : id0;
+                if (PAIR)
+                  mma_mxf4_ss_pair(d_acc, ad, bd, id, sf_w + 4 * c, sf_x + 4 * C::kG * c, accum);
+                else
+                  mma_mxf4_ss(d_acc, ad, bd, id, sf_w + 4 * c, sf_x + 4 * C::kG * c, accum);
+              }
             }
+            if (PAIR)
+              mma_commit_pair_mc(&empty[stage], 0x3);
+            else
+              mma_commit(&empty[stage]);
           }
-          if (PAIR)
-            mma_commit_pair_mc(&empty[stage], 0x3);
-          else
-            mma_commit(&empty[stage]);
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (PAIR)
-          mma_commit_pair_mc(&tfull[acc], 0x3);
-        else
-          mma_commit(&tfull[acc]);
+        if (issue) {
+          if (PAIR)
+            mma_commit_pair_mc(&tfull[acc], 0x3);
+          else
+            mma_commit(&tfull[acc]);
+        }
+        __syncwarp();
         if (++acc == C::kAccBufs) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
-      if (!ok) raise_timeout(a.err, abort_flag, kKernFp4Gemm, where);
-      if (PAIR)
-        mma_commit_pair(done);
-      else
-        mma_commit(done);
+      if (!ok && issue) raise_timeout(a.err, abort_flag, kKernFp4Gemm, where);
+      if (issue) {
+        if (PAIR)
+          mma_commit_pair(done);
+        else
+          mma_commit(done);
+      }
+      __syncwarp();
       int dummy = 0;
       mbar_wait(done, 0, kWaitTimeoutNs, &dummy);
     }

@@ -24,9 +24,10 @@
 // add-reductions, each element added once, so the result does not depend on an
 // order).
 //
-// Work split.  Large plan and weight gradient: whole units round-robin over CTA
-// pairs (M = 256, 7 or 6 stages of 32 KB, two 256-column accumulators so that a
-// unit's epilogue runs under the next unit's MMAs).  Small plan (few rows per
+// Work split.  Weight gradient: whole units round-robin over CTA
+// pairs (M = 256, 6 stages of 32 KB, two 256-column accumulators so that a
+// unit's epilogue runs under the next unit's MMAs); forward and input gradient
+// of many rows: k_grouped_pair.cu.  Small plan (few rows per
 // group: the weights stream once, HBM-bound): 128 x 32-row units on single
 // CTAs, split stream-K so that every SM streams the same number of weight bytes;
 // partial sums meet in fp32 in a fixed order, so results repeat bit for bit.
@@ -313,8 +314,13 @@ __global__ void __launch_bounds__(192, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ---------------- MMA issuer
+    if (leader) {
+      // ---------------- MMA issuer: the whole warp walks the units, one lane issues
+      const bool issue = elect_one();
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t a0 = C::kWgrad || C::kDgrad ? sdesc_mnmajor_sw128(s0, kMnBox) : sdesc_kmajor_sw128(s0);
+      const uint64_t b0 = C::kWgrad ? sdesc_mnmajor_sw128(s0 + kABytes, kMnBox) : sdesc_kmajor_sw128(s0 + kABytes);
+      constexpr uint64_t kStepA = (C::kWgrad || C::kDgrad ? 2048 : 32) >> 4, kStepB = (C::kWgrad ? 2048 : 32) >> 4;
       int stage = 0, acc = 0, where = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(192, 1)
           kb1 = (un.n + 63) / 64;
           if (kb1 == 0) continue;  // an empty group: the epilogue writes zeros
         }
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag)) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag))) {
           ok = false;
           where = kWaitAccFree;
           break;
@@ -337,52 +343,58 @@ __global__ void __launch_bounds__(192, 1)
                                              C::kWgrad || C::kDgrad, C::kWgrad);
         const uint32_t d_acc = tmem_base + static_cast<uint32_t>(acc * BN);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&full[stage], phase, kWaitTimeoutNs, abort_flag)) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, kWaitTimeoutNs, abort_flag))) {
             ok = false;
             where = kWaitSlotFull;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * C::kStageBytes), sb = sa + kABytes;
+          const uint64_t at = static_cast<uint64_t>(stage * (C::kStageBytes >> 4));
           // MMAs of K = 16; a group's last block of rows ends with the group
           const int n_k = C::kWgrad ? min(4, (un.n - kb * 64 + 15) / 16) : 4;
+          if (issue) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (C::kWgrad && k >= n_k) break;
-            const uint64_t ad = C::kWgrad || C::kDgrad ? sdesc_mnmajor_sw128(sa + k * 2048, kMnBox)
-                                                       : sdesc_kmajor_sw128(sa + k * 32);
-            const uint64_t bd = C::kWgrad ? sdesc_mnmajor_sw128(sb + k * 2048, kMnBox) : sdesc_kmajor_sw128(sb + k * 32);
-            const uint32_t accum = (kb > kb0 || k > 0) ? 1u : 0u;
+            for (int k = 0; k < 4; ++k) {
+              if (C::kWgrad && k >= n_k) break;
+              const uint32_t accum = k > 0 ? 1u : kb > kb0;
+              if (PAIR)
+                mma_bf16_ss_pair(d_acc, a0 + at + k * kStepA, b0 + at + k * kStepB, idesc, accum);
+              else
+                mma_bf16_ss(d_acc, a0 + at + k * kStepA, b0 + at + k * kStepB, idesc, accum);
+            }
             if (PAIR)
-              mma_bf16_ss_pair(d_acc, ad, bd, idesc, accum);
+              mma_commit_pair_mc(&empty[stage], 0x3);
             else
-              mma_bf16_ss(d_acc, ad, bd, idesc, accum);
+              mma_commit(&empty[stage]);
           }
-          if (PAIR)
-            mma_commit_pair_mc(&empty[stage], 0x3);
-          else
-            mma_commit(&empty[stage]);
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (PAIR)
-          mma_commit_pair_mc(&tfull[acc], 0x3);
-        else
-          mma_commit(&tfull[acc]);
+        if (issue) {
+          if (PAIR)
+            mma_commit_pair_mc(&tfull[acc], 0x3);
+          else
+            mma_commit(&tfull[acc]);
+        }
+        __syncwarp();
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
-      if (!ok) raise_timeout(a.err, abort_flag, kKernGroupedGemm, where);
-      // all MMAs this thread issued have finished before TMEM is released
-      if (PAIR)
-        mma_commit_pair(done);
-      else
-        mma_commit(done);
+      if (!ok && issue) raise_timeout(a.err, abort_flag, kKernGroupedGemm, where);
+      // all MMAs issued have finished before TMEM is released
+      if (issue) {
+        if (PAIR)
+          mma_commit_pair(done);
+        else
+          mma_commit(done);
+      }
+      __syncwarp();
       int dummy = 0;
       mbar_wait(done, 0, kWaitTimeoutNs, &dummy);
     }
@@ -599,15 +611,7 @@ cudaError_t launch_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const Grou
 
 // rows per unit, stages, rows per token box: small (one CTA, 20 KB stages) and
 // large (CTA pairs, 32 KB stages per CTA)
-constexpr int kBn[2] = {32, 256}, kTile[2] = {128, 256}, kTokBox[2] = {16, 128};
-
-template <GroupedOp OP>
-cudaError_t launch_plan(GroupedPlan plan, const CUtensorMap& tw, const CUtensorMap& tx, const GroupedGemmArgs& a,
-                        int num_sms, cudaStream_t stream) {
-  constexpr int op = static_cast<int>(OP);
-  if (plan == GroupedPlan::kSmall) return launch_gemm<op, kBn[0], 10, kTokBox[0], false>(tw, tx, a, num_sms, stream);
-  return launch_gemm<op, kBn[1], 7, kTokBox[1], true>(tw, tx, a, num_sms, stream);
-}
+constexpr int kBn[2] = {32, 512}, kTile[2] = {128, 256}, kTokBox[2] = {16, 128};
 
 }  // namespace
 
@@ -624,9 +628,14 @@ cudaError_t launch_grouped_plan(const GroupedPlanArgs& a, const CUtensorMap& dy,
 }
 
 cudaError_t launch_grouped_gemm(GroupedOp op, GroupedPlan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
-                                const GroupedGemmArgs& a, int num_sms, cudaStream_t stream) {
-  return op == GroupedOp::kForward ? launch_plan<GroupedOp::kForward>(plan, tm_w, tm_x, a, num_sms, stream)
-                                   : launch_plan<GroupedOp::kDgrad>(plan, tm_w, tm_x, a, num_sms, stream);
+                                const CUtensorMap& tm_x32, const GroupedGemmArgs& a, int num_sms,
+                                cudaStream_t stream) {
+  if (plan == GroupedPlan::kLarge) return launch_grouped_pair(op, tm_w, tm_x, tm_x32, a, stream);
+  return op == GroupedOp::kForward
+             ? launch_gemm<static_cast<int>(GroupedOp::kForward), kBn[0], 10, kTokBox[0], false>(tm_w, tm_x, a, num_sms,
+                                                                                                  stream)
+             : launch_gemm<static_cast<int>(GroupedOp::kDgrad), kBn[0], 10, kTokBox[0], false>(tm_w, tm_x, a, num_sms,
+                                                                                                stream);
 }
 
 cudaError_t launch_grouped_wgrad(const CUtensorMap& tm_dw, const GroupedGemmArgs& a, cudaStream_t stream) {

@@ -1,0 +1,389 @@
+// k_grouped_pair.cu -- the forward and the input gradient of the grouped
+// products for groups of many rows, on CTA pairs (tcgen05.mma cta_group::2,
+// M = 256).  The mapping is k_grouped_gemm.cu's: the weights on the MMA's M
+// side, a group's rows on its N side.
+//
+// Groups are ragged, and a weight tile has to be filled into shared memory
+// once per unit whatever the unit's rows: with chunks of at most 256 rows a
+// group of 520 rows costs three passes over its weights for two passes' worth
+// of products (64 groups of 520 rows, N = 8192, K = 4096: 1612 us, of 512:
+// 1284 us).  So a unit takes up to 512 rows, even chunks, and neither shared
+// memory nor TMEM is divided into slots of the largest size:
+//   - The ring in shared memory is a ring of bytes.  A stage is the 16 KB weight
+//     tile plus half of the unit's rows (the pair's CTAs hold half each), so
+//     units of few rows have more stages in flight.  Producer and MMA thread
+//     compute the same places; the producer waits for the oldest stages until the
+//     new one fits.
+//   - TMEM's 512 columns are two accumulators of 256.  A unit of up to 256 rows
+//     takes one, so that its epilogue runs under the next unit's MMAs; one of more takes both, with two
+//     MMAs of about half its rows per step that share the stage's weight tile (an MMA of
+//     few columns costs far more than its share: 256 + 32 columns 1.3 times 144 + 144).
+// An MMA of N columns takes N / 2 rows from each CTA: its first N / 2 columns
+// are rows of the unit's first half, the others of the second.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "bounded_wait.cuh"
+#include "grouped.cuh"
+#include "launch_config.cuh"
+#include "pdl.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+constexpr int kABytes = 128 * 128;   // 128 features x 64 of the reduction, 16 bits
+constexpr int kMnBox = 64 * 128;     // an MN-major box: 64 features x 64 of the reduction
+constexpr int kRing = 224 * 1024;    // bytes: 7 stages of 256 rows, 4 of 512
+constexpr int kStages = 11;          // stages in flight at most (the smallest are 20 KB)
+constexpr int kAccCols = 256;
+constexpr int kEpiWarps = 8;         // two per TMEM lane quarter, alternate groups of 32 columns
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kBarBytes = 256;
+constexpr int kTabBytes = 3 * (kGroupsSmem[1] + 1) * 4;
+constexpr size_t kSmemBytes = 1024 + kRing + kBarBytes + kTabBytes;
+static_assert((2 * kStages + 5) * 8 + 8 <= kBarBytes, "barrier area");
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+
+enum : int { kWaitSlotFree = 1, kWaitAccFree = 2, kWaitSlotFull = 3, kWaitAccFull = 4 };
+
+__device__ __forceinline__ uint16_t to16(float v, bool fp16) {
+  return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// A unit's size: MMA columns in all and of its first MMA, rows per CTA, rows
+// loaded (boxes of 128 and of 32), bytes of a stage.
+struct Size {
+  int cols, cols0, half, rows, bytes;
+  __device__ explicit Size(int n) {
+    cols = (n + 15) & ~15;
+    cols0 = cols <= kAccCols ? cols : (cols / 2 + 15) & ~15;
+    half = cols / 2;
+    const int rest = half & 127;
+    rows = (half & ~127) + (rest > 96 ? 128 : (rest + 31) & ~31);
+    bytes = kABytes + rows * 128;
+  }
+};
+
+// Places in the byte ring, in the order of the stages: a stage lies whole, so
+// the end of the ring is skipped where the next one does not fit.
+struct BytePlace {
+  int at = 0;
+  int64_t virt = 0;  // bytes given out so far, skipped ones included
+  __device__ __forceinline__ int take(int bytes) {
+    if (at + bytes > kRing) {
+      virt += kRing - at;
+      at = 0;
+    }
+    const int r = at;
+    at += bytes;
+    virt += bytes;
+    return r;
+  }
+};
+
+template <bool DGRAD>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ CUtensorMap tm_x32, const __grid_constant__ GroupedGemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;  // an accumulator's MMAs are complete
+  uint64_t* tempty = tfull + 2;       // it is read, by the epilogue of both CTAs
+  uint64_t* done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* tab = reinterpret_cast<int32_t*>(smem + kRing + kBarBytes);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kEpiWarps);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_x);
+    prefetch_tensormap(&tm_x32);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 2 * kAccCols);
+    tmem_relinquish_pair();
+  }
+  pdl_wait();  // the plan kernel's tables
+  const GroupedTables tables = grouped_tables(a, tab, kGroupsSmem[1], kThreads);
+  tc_fence_before();
+  cluster_sync();  // the peer's barriers are initialised before any remote signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int total_units = tables.unit_off[a.G];
+  const int kblocks = (a.R + 63) / 64;
+  GroupedUnits units(tables, a.G, 1, a.bn, true);  // each thread walks its role's units
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer
+      const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_last();
+      const uint32_t full_cl = mapa_shared(smem_u32(full), 0);  // both CTAs signal the even one
+      bool ok = true;
+      BytePlace place;
+      int64_t ends[kStages];  // virtual end of each stage in flight
+      int64_t issued = 0, freed = 0;
+      int64_t freed_to = 0;  // virtual bytes below it are free
+      int stage = 0, oldest = 0;
+      uint32_t oldest_phase = 0;
+      for (int u = worker; ok && u < total_units; u += workers) {
+        const GroupedUnit un = units.at(u);
+        const Size z(un.n);
+        const int feat = un.tile * 256 + static_cast<int>(rank) * 128;
+        const int tok = un.tok0 + static_cast<int>(rank) * z.half;
+        // a weight tile read by one chunk only is streamed; by more, kept
+        const uint64_t pol_w = units.chunks > 1 ? pol_keep : pol_stream;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          const int at = place.take(z.bytes);
+          while (place.virt - freed_to > kRing || issued - freed == kStages) {
+            if (!mbar_wait(&empty[oldest], oldest_phase, kWaitTimeoutNs, abort_flag)) {
+              ok = false;
+              break;
+            }
+            freed_to = ends[oldest];
+            ++freed;
+            if (++oldest == kStages) {
+              oldest = 0;
+              oldest_phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          ends[stage] = place.virt;
+          uint8_t* sa = smem + at;
+          uint8_t* sb = sa + kABytes;
+          const uint32_t bar = full_cl + 8u * stage;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * z.bytes);
+          if constexpr (DGRAD) {  // [64 rows of w][64 columns] boxes: the columns are the features
+            tma_load_3d_pair(sa, &tm_w, bar, feat, kb * 64, un.g, pol_w);
+            tma_load_3d_pair(sa + kMnBox, &tm_w, bar, feat + 64, kb * 64, un.g, pol_w);
+          } else {
+            tma_load_3d_pair(sa, &tm_w, bar, kb * 64, feat, un.g, pol_w);
+          }
+          int r = 0;
+          for (; r + 128 <= z.rows; r += 128) tma_load_2d_pair(sb + r * 128, &tm_x, bar, kb * 64, tok + r, pol_keep);
+          for (; r < z.rows; r += 32) tma_load_2d_pair(sb + r * 128, &tm_x32, bar, kb * 64, tok + r, pol_keep);
+          ++issued;
+          if (++stage == kStages) stage = 0;
+        }
+      }
+      if (!ok) raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitSlotFree);
+      // every load this thread issued has been used (or given up) before the CTA exits
+      while (freed < issued) {
+        int dummy = 0;
+        mbar_wait(&empty[oldest], oldest_phase, ok ? kWaitTimeoutNs : kWaitTimeoutNs / 16, &dummy);
+        ++freed;
+        if (++oldest == kStages) {
+          oldest = 0;
+          oldest_phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // ---------------- MMA issuer for both CTAs: the whole warp walks the
+      // units, one lane issues (a stage of narrow MMAs is bound by the issuing
+      // thread's instructions: the descriptors advance by additions alone)
+      const bool issue = elect_one();
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t a0 = DGRAD ? sdesc_mnmajor_sw128(s0, kMnBox) : sdesc_kmajor_sw128(s0);
+      const uint64_t b0 = sdesc_kmajor_sw128(s0 + kABytes);
+      constexpr uint64_t kStepA = (DGRAD ? 2048 : 32) >> 4, kStepB = 32 >> 4;  // K = 16
+      bool ok = true;
+      int where = 0;
+      BytePlace place;
+      int stage = 0;
+      uint32_t phase = 0, uses = 0;  // accumulators taken so far: the next is uses & 1
+      for (int u = worker; ok && u < total_units; u += workers) {
+        const GroupedUnit un = units.at(u);
+        const Size z(un.n);
+        const int parts = z.cols > z.cols0 ? 2 : 1;
+        for (int j = 0; j < parts; ++j)
+          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(&tempty[(uses + j) & 1], (((uses + j) >> 1) & 1u) ^ 1u,
+                                                      kWaitTimeoutNs, abort_flag));
+        if (!ok) {
+          where = kWaitAccFree;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d0 = tmem_base + (uses & 1) * kAccCols, d1 = tmem_base + ((uses & 1) ^ 1) * kAccCols;
+        const uint64_t b1 = static_cast<uint64_t>(z.cols0 / 2 * 128) >> 4;  // the second MMA's rows
+        const uint32_t idesc0 = idesc_f16_f32(256, static_cast<uint32_t>(z.cols0), a.fp16, DGRAD, 0);
+        const uint32_t idesc1 = idesc_f16_f32(256, static_cast<uint32_t>(z.cols - z.cols0), a.fp16, DGRAD, 0);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          const int at = place.take(z.bytes);
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, kWaitTimeoutNs, abort_flag))) {
+            ok = false;
+            where = kWaitSlotFull;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = a0 + static_cast<uint64_t>(at >> 4), bd = b0 + static_cast<uint64_t>(at >> 4);
+          if (issue) {
+            mma_bf16_ss_pair(d0, ad, bd, idesc0, kb > 0);
+#pragma unroll
+            for (int k = 1; k < 4; ++k) mma_bf16_ss_pair(d0, ad + k * kStepA, bd + k * kStepB, idesc0, 1u);
+            if (parts == 2) {
+              const uint64_t bd1 = bd + b1;
+              mma_bf16_ss_pair(d1, ad, bd1, idesc1, kb > 0);
+#pragma unroll
+              for (int k = 1; k < 4; ++k) mma_bf16_ss_pair(d1, ad + k * kStepA, bd1 + k * kStepB, idesc1, 1u);
+            }
+            mma_commit_pair_mc(&empty[stage], 0x3);
+          }
+          __syncwarp();
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (issue)
+          for (int j = 0; j < parts; ++j) mma_commit_pair_mc(&tfull[(uses + j) & 1], 0x3);
+        __syncwarp();
+        uses += parts;
+      }
+      if (!ok && issue) raise_timeout(a.err, abort_flag, kKernGroupedGemm, where);
+      // all MMAs issued have finished before TMEM is released
+      if (issue) mma_commit_pair(done);
+      __syncwarp();
+      int dummy = 0;
+      mbar_wait(done, 0, kWaitTimeoutNs, &dummy);
+    }
+  } else {
+    // ---------------- epilogue: TMEM lane quarter = warp % 4; a quarter's two
+    // warps take alternate groups of 32 columns
+    const int q = warp & 3, turn = (warp - 2) >> 2;
+    const int row = q * 32 + lane;  // feature of this CTA's 128
+    const bool fp16 = a.fp16 != 0;
+    const uint32_t tempty_cl = mapa_shared(smem_u32(tempty), 0);
+    bool ok = true;
+    uint32_t uses = 0;
+    for (int u = worker; ok && u < total_units; u += workers) {
+      const GroupedUnit un = units.at(u);
+      const Size z(un.n);
+      const int feat = un.tile * 256 + static_cast<int>(rank) * 128 + row;
+      const bool mine = feat < a.F;
+      uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(un.tok0) * a.ldo + feat;
+      const int parts = z.cols > z.cols0 ? 2 : 1;
+      for (int j = 0; j < parts; ++j) {
+        const uint32_t buf = uses & 1;
+        // warp-uniform outcome: tcgen05.ld below is executed by all 32 lanes
+        const bool got = mbar_wait(&tfull[buf], (uses >> 1) & 1u, kWaitTimeoutNs, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        ++uses;
+        const int cols = j ? z.cols - z.cols0 : z.cols0, before = j ? z.cols0 / 2 : 0;
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
+        for (int c0 = 32 * turn; c0 < cols; c0 += 64) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t_row + c0, r);
+          tmem_ld_wait();
+          if (mine) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {  // 8 columns: rows of one half
+              const int c = c0 + 8 * h;
+              const int t = c < cols / 2 ? before + c : z.half + before + c - cols / 2;
+              uint16_t* o = out + static_cast<int64_t>(t) * a.ldo;
+              const int left = c < cols ? un.n - t : 0;
+              if (left >= 8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[static_cast<int64_t>(i) * a.ldo] = to16(__uint_as_float(r[8 * h + i]), fp16);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (i < left) o[static_cast<int64_t>(i) * a.ldo] = to16(__uint_as_float(r[8 * h + i]), fp16);
+              }
+            }
+          }
+        }
+        // hand the accumulator back to the MMA thread
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_cl + 8u * buf);
+      }
+    }
+    if (!ok && lane == 0) raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitAccFull);
+  }
+
+  __syncthreads();
+  cluster_sync();  // both CTAs keep their shared memory, barriers and TMEM until both are done
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * kAccCols);
+  }
+}
+
+template <bool DGRAD>
+cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx32, const GroupedGemmArgs& a,
+                   cudaStream_t stream) {
+  auto kernel = grouped_pair_kernel<DGRAD>;
+  static PerDevice config;  // the smem attribute, and the CTA pairs that fit on the device at once
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  int max_pairs = 0;
+  const cudaError_t e = config.get(
+      [&](int& pairs) -> cudaError_t {
+        cudaError_t ce =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+        if (ce != cudaSuccess) return ce;
+        cudaLaunchConfig_t q = cfg;
+        q.gridDim = dim3(2 * (kMaxGemmCtas / 2));
+        q.attrs = attr + 1;
+        q.numAttrs = 1;
+        int n = 0;
+        ce = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
+        if (ce != cudaSuccess) return ce;
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+        pairs = n;
+        return cudaSuccess;
+      },
+      &max_pairs);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(2 * (max_pairs < kMaxGemmCtas / 2 ? max_pairs : kMaxGemmCtas / 2));
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, tx32, a);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_pair(GroupedOp op, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
+                                const CUtensorMap& tm_x32, const GroupedGemmArgs& a, cudaStream_t stream) {
+  return op == GroupedOp::kForward ? launch<false>(tm_w, tm_x, tm_x32, a, stream)
+                                   : launch<true>(tm_w, tm_x, tm_x32, a, stream);
+}
+
+}  // namespace moe

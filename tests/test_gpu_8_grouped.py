@@ -328,3 +328,22 @@ def test_training_step_of_the_experts():
             plus[at], minus[at] = args[at] + eps * step, args[at] - eps * step
             slope = ((loss(*plus) - loss(*minus)) / (2 * eps)).item()
             assert abs(slope - got.double().norm().item()) <= 5 * 2 * half_step(BF16) * abs(slope) + 1e-5
+
+
+@pytest.mark.parametrize("counts", [[513, 512, 1, 1024, 31, 1023, 545], [96, 480, 130, 290, 272, 33], [2000, 17, 17, 17, 17],
+                                    [64 + 32 * (i % 15) for i in range(90)]], ids=lambda c: f"{len(c)}_groups")
+@pytest.mark.parametrize("op", ["forward", "dgrad"])
+def test_units_of_every_width_follow_one_another(op, counts):
+    """Units of 32 to 512 rows in one call: shared memory and TMEM are handed on between units of different sizes,
+    over several units per CTA pair."""
+    lists = Lists(counts)
+    gen = torch.Generator(device="cuda").manual_seed(len(counts))
+    n, k = (2560, 320) if op == "forward" else (320, 2560)
+    gp = binding.GroupedProducts(lists.groups, n, k, BF16)
+    w = (torch.randn((lists.groups, n, k), generator=gen, device="cuda") * 0.05).to(BF16)
+    a = lists.matrix(gen, k if op == "forward" else n, BF16)
+    out = gp.forward(a, w, lists.offsets) if op == "forward" else gp.dgrad(a, w, lists.offsets)
+    assert gp.device_status()[0] == binding.MOE_OK
+    for g, (lo, hi) in enumerate(lists.spans):
+        ad, wd = a[lo:hi].double(), w[g].double().T if op == "forward" else w[g].double()
+        check(out[lo:hi], ad @ wd, ad.abs() @ wd.abs(), 320)
