@@ -40,7 +40,7 @@ constexpr int kRing = 224 * 1024;    // bytes: 7 stages of 256 rows, 4 of 512
 constexpr int kStages = 11;          // stages in flight at most (the smallest are 20 KB)
 constexpr int kAccCols = 256;
 constexpr int kEpiWarps = 8;         // two per TMEM lane quarter, alternate groups of 32 columns
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kThreads = 32 * (3 + kEpiWarps);  // + the weights' producer, the MMA warp, the rows' producer
 constexpr int kBarBytes = 256;
 constexpr int kTabBytes = 3 * (kGroupsSmem[1] + 1) * 4;
 constexpr size_t kSmemBytes = 1024 + kRing + kBarBytes + kTabBytes;
@@ -71,7 +71,7 @@ struct Size {
 // the end of the ring is skipped where the next one does not fit.
 struct BytePlace {
   int at = 0;
-  int64_t virt = 0;  // bytes given out so far, skipped ones included
+  uint32_t virt = 0;  // bytes given out so far, skipped ones included (mod 2^32)
   __device__ __forceinline__ int take(int bytes) {
     if (at + bytes > kRing) {
       virt += kRing - at;
@@ -81,6 +81,48 @@ struct BytePlace {
     at += bytes;
     virt += bytes;
     return r;
+  }
+};
+
+// A producer's walk along the ring (a whole warp): the place of the next stage,
+// once the oldest stages have left room for it.  Lane s keeps the virtual end
+// of stage s.
+struct Producer {
+  BytePlace place;
+  uint64_t* empty;
+  const volatile int* abort_flag;
+  uint32_t freed_to = 0, my_end = 0, oldest_phase = 0;
+  int stage = 0, oldest = 0, in_flight = 0;
+  const int lane;
+  __device__ Producer(uint64_t* e, const volatile int* f, int l) : empty(e), abort_flag(f), lane(l) {}
+
+  __device__ __forceinline__ bool free_oldest(uint64_t timeout_ns, const volatile int* flag) {
+    const bool got = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[oldest], oldest_phase, timeout_ns, flag));
+    freed_to = __shfl_sync(0xFFFFFFFFu, my_end, oldest);
+    --in_flight;
+    if (++oldest == kStages) {
+      oldest = 0;
+      oldest_phase ^= 1u;
+    }
+    return got;
+  }
+  // byte offset of the next stage (its index: stage, until advance()), or -1
+  __device__ __forceinline__ int next(int bytes) {
+    const int at = place.take(bytes);
+    while (place.virt - freed_to > kRing || in_flight == kStages)
+      if (!free_oldest(kWaitTimeoutNs, abort_flag)) return -1;
+    if (lane == stage) my_end = place.virt;
+    return at;
+  }
+  __device__ __forceinline__ void advance() {
+    ++in_flight;
+    if (++stage == kStages) stage = 0;
+  }
+  // every load issued has been used before the CTA exits
+  __device__ __forceinline__ void drain() {
+    const int never = 0;
+    bool got = true;
+    while (in_flight > 0 && got) got = free_oldest(kWaitTimeoutNs, &never);
   }
 };
 
@@ -135,70 +177,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kblocks = (a.R + 63) / 64;
   GroupedUnits units(tables, a.G, 1, a.bn, true);  // each thread walks its role's units
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer
-      const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_last();
-      const uint32_t full_cl = mapa_shared(smem_u32(full), 0);  // both CTAs signal the even one
-      bool ok = true;
-      BytePlace place;
-      int64_t ends[kStages];  // virtual end of each stage in flight
-      int64_t issued = 0, freed = 0;
-      int64_t freed_to = 0;  // virtual bytes below it are free
-      int stage = 0, oldest = 0;
-      uint32_t oldest_phase = 0;
-      for (int u = worker; ok && u < total_units; u += workers) {
-        const GroupedUnit un = units.at(u);
-        const Size z(un.n);
-        const int feat = un.tile * 256 + static_cast<int>(rank) * 128;
-        const int tok = un.tok0 + static_cast<int>(rank) * z.half;
-        // a weight tile read by one chunk only is streamed; by more, kept
-        const uint64_t pol_w = units.chunks > 1 ? pol_keep : pol_stream;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          const int at = place.take(z.bytes);
-          while (place.virt - freed_to > kRing || issued - freed == kStages) {
-            if (!mbar_wait(&empty[oldest], oldest_phase, kWaitTimeoutNs, abort_flag)) {
-              ok = false;
-              break;
-            }
-            freed_to = ends[oldest];
-            ++freed;
-            if (++oldest == kStages) {
-              oldest = 0;
-              oldest_phase ^= 1u;
-            }
-          }
-          if (!ok) break;
-          ends[stage] = place.virt;
+  if (warp == 0 || warp == 2 + kEpiWarps) {
+    // ---------------- TMA producers: one warp for the weight tiles, one for the
+    // rows (one thread that issues both, three to five copies a stage, is
+    // slower than the copies); one lane issues
+    const bool weights = warp == 0, issue = elect_one();
+    const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_last();
+    const uint32_t full_cl = mapa_shared(smem_u32(full), 0);  // both CTAs signal the even one
+    Producer ring(empty, abort_flag, lane);
+    bool ok = true;
+    for (int u = worker; ok && u < total_units; u += workers) {
+      const GroupedUnit un = units.at(u);
+      const Size z(un.n);
+      const int feat = un.tile * 256 + static_cast<int>(rank) * 128;
+      const int tok = un.tok0 + static_cast<int>(rank) * z.half;
+      // a weight tile read by one chunk only is streamed; by more, kept
+      const uint64_t pol_w = units.chunks > 1 ? pol_keep : pol_stream;
+      for (int kb = 0; kb < kblocks; ++kb) {
+        const int at = ring.next(z.bytes);
+        if (at < 0) {
+          ok = false;
+          break;
+        }
+        if (issue) {
           uint8_t* sa = smem + at;
-          uint8_t* sb = sa + kABytes;
-          const uint32_t bar = full_cl + 8u * stage;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * z.bytes);
-          if constexpr (DGRAD) {  // [64 rows of w][64 columns] boxes: the columns are the features
-            tma_load_3d_pair(sa, &tm_w, bar, feat, kb * 64, un.g, pol_w);
-            tma_load_3d_pair(sa + kMnBox, &tm_w, bar, feat + 64, kb * 64, un.g, pol_w);
+          const uint32_t bar = full_cl + 8u * ring.stage;
+          if (weights) {
+            if (leader) mbar_arrive_expect_tx(&full[ring.stage], 2 * z.bytes);
+            if constexpr (DGRAD) {  // [64 rows of w][64 columns] boxes: the columns are the features
+              tma_load_3d_pair(sa, &tm_w, bar, feat, kb * 64, un.g, pol_w);
+              tma_load_3d_pair(sa + kMnBox, &tm_w, bar, feat + 64, kb * 64, un.g, pol_w);
+            } else {
+              tma_load_3d_pair(sa, &tm_w, bar, kb * 64, feat, un.g, pol_w);
+            }
           } else {
-            tma_load_3d_pair(sa, &tm_w, bar, kb * 64, feat, un.g, pol_w);
+            uint8_t* sb = sa + kABytes;
+            int r = 0;
+            for (; r + 128 <= z.rows; r += 128) tma_load_2d_pair(sb + r * 128, &tm_x, bar, kb * 64, tok + r, pol_keep);
+            for (; r < z.rows; r += 32) tma_load_2d_pair(sb + r * 128, &tm_x32, bar, kb * 64, tok + r, pol_keep);
           }
-          int r = 0;
-          for (; r + 128 <= z.rows; r += 128) tma_load_2d_pair(sb + r * 128, &tm_x, bar, kb * 64, tok + r, pol_keep);
-          for (; r < z.rows; r += 32) tma_load_2d_pair(sb + r * 128, &tm_x32, bar, kb * 64, tok + r, pol_keep);
-          ++issued;
-          if (++stage == kStages) stage = 0;
         }
-      }
-      if (!ok) raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitSlotFree);
-      // every load this thread issued has been used (or given up) before the CTA exits
-      while (freed < issued) {
-        int dummy = 0;
-        mbar_wait(&empty[oldest], oldest_phase, ok ? kWaitTimeoutNs : kWaitTimeoutNs / 16, &dummy);
-        ++freed;
-        if (++oldest == kStages) {
-          oldest = 0;
-          oldest_phase ^= 1u;
-        }
+        __syncwarp();
+        ring.advance();
       }
     }
+    if (!ok && issue) raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitSlotFree);
+    ring.drain();
   } else if (warp == 1) {
     if (leader) {
       // ---------------- MMA issuer for both CTAs: the whole warp walks the
