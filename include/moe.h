@@ -355,7 +355,7 @@ MOE_API moe_status moe_workspace_views(const moe_shape* shape, void* workspace, 
  * ran out (bit 1 producer: ring slot free; 2 MMA: accumulator free; 3 MMA:
  * ring slot loaded; 4 epilogue: accumulator complete; 5 epilogue: stream-K
  * partial sums; 6 epilogue: fused-combine rendezvous; 7 MMA: a stage's scales
- * written to TMEM; 8 scale warps: ring slot loaded), and the index of the CTA
+ * written to TMEM; 8 scale warps: ring slot loaded; 10 a CTA pair's next unit), and the index of the CTA
  * that recorded the timeout. */
 MOE_API moe_status moe_device_status(const void* workspace, size_t workspace_bytes, moe_stream_t stream,
                              int32_t* detail);

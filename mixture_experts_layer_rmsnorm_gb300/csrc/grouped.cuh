@@ -60,6 +60,7 @@ struct GroupedGemmArgs {
   int32_t* err;
   float* partials;  // stream-K partial sums: [kMaxGemmCtas][BN][128] fp32
   int32_t* flags;   // [kMaxGemmCtas * 4], zero on entry
+  int32_t* next_unit;  // CTA pairs: the next unit to hand out, zero on entry
   void* out;        // forward / input gradient: rows of ldo elements of the operand type
   int64_t ldo;
   int G, F, R, C;
@@ -73,7 +74,8 @@ struct GroupedGemmArgs {
 
 // Tile plans of the forward and the input gradient.
 enum class GroupedPlan : int { kSmall = 0, kLarge = 1 };
-int grouped_bn(GroupedPlan plan);         // token rows per unit
+// token rows per unit at most: 32, or what the expected rows per group make the fastest
+int grouped_bn(GroupedPlan plan, int64_t rows, int64_t groups, int64_t tiles, int num_sms);
 int grouped_tile(GroupedPlan plan);       // features per unit
 int grouped_tok_box(GroupedPlan plan);    // token rows per TMA box
 size_t grouped_partial_bytes();           // stream-K partial sums
@@ -122,21 +124,20 @@ __device__ __forceinline__ GroupedTables grouped_tables(const GroupedGemmArgs& a
 // A unit's feature tile and token chunk: chunk fastest (units that read the
 // same weight tile are neighbours, so the CTAs running side by side read it
 // from DRAM once), or (bn = 0) its feature tile and column tile.  Chunks are
-// bn rows each, or (balance) even: a group of c rows has m = ceil(c / bn) of
-// them, chunk i from row floor(i c / m) on.
+// bn rows each and a rest, or (even) as equal as rows go.
 struct GroupedUnits {
   GroupedTables t;
   int G, tiles_n, bn;
-  bool balance;
+  bool even;
   int g, first, last;  // the kept group and its units [first, last)
   int start, count, chunks;
 
-  __device__ GroupedUnits(const GroupedTables& tables, int groups, int tiles_n_, int bn_, bool balance_ = false)
-      : t(tables), G(groups), tiles_n(tiles_n_), bn(bn_), balance(balance_), g(0), first(0), last(0), start(0),
-        count(0), chunks(1) {}
+  __device__ GroupedUnits(const GroupedTables& tables, int groups, int tiles_n_, int bn_, bool even_ = false)
+      : t(tables), G(groups), tiles_n(tiles_n_), bn(bn_), even(even_), g(0), first(0), last(0), start(0), count(0),
+        chunks(1) {}
 
   __device__ __forceinline__ int chunk_start(int i) const {
-    return balance ? static_cast<int>(static_cast<int64_t>(i) * count / chunks) : i * bn;
+    return even ? static_cast<int>(static_cast<int64_t>(i) * count / chunks) : i * bn;
   }
 
   __device__ __forceinline__ GroupedUnit at(int u) {
@@ -176,27 +177,21 @@ struct GroupedUnits {
   }
 };
 
-// A worker's work, as segments: K-blocks [kb0, kb1) of unit u.  Stream-K: a
-// contiguous range of (unit, K-block) iterations of equal length for every
-// worker; otherwise whole units worker, worker + workers, ...
+// A worker's share of a stream-K split, as segments: K-blocks [kb0, kb1) of
+// unit u.  The (unit, K-block) iterations form one list; every worker takes a
+// contiguous range of equal length.
 struct GroupedRange {
   int64_t it, end, W;
-  int kblocks, step;
-  bool stream_k;
-  __device__ GroupedRange(int units, int kb, int worker, int workers, bool sk)
-      : W(static_cast<int64_t>(units) * kb), kblocks(kb), step(workers), stream_k(sk) {
-    it = sk ? W * worker / workers : worker;
-    end = sk ? W * (worker + 1) / workers : units;
+  int kblocks, workers;
+  __device__ GroupedRange(int units, int kb, int worker, int workers_)
+      : W(static_cast<int64_t>(units) * kb), kblocks(kb), workers(workers_) {
+    it = begin_of(worker);
+    end = begin_of(worker + 1);
   }
+  // first iteration of a worker's range
+  __device__ int64_t begin_of(int worker) const { return W * worker / workers; }
   __device__ bool next(int& u, int& kb0, int& kb1) {
     if (it >= end) return false;
-    if (!stream_k) {
-      u = static_cast<int>(it);
-      kb0 = 0;
-      kb1 = kblocks;
-      it += step;
-      return true;
-    }
     u = static_cast<int>(it / kblocks);
     kb0 = static_cast<int>(it - static_cast<int64_t>(u) * kblocks);
     const int64_t stop = kb0 + (end - it);
@@ -204,8 +199,6 @@ struct GroupedRange {
     it += kb1 - kb0;
     return true;
   }
-  // first iteration of a worker's range (stream-K)
-  __device__ int64_t begin_of(int worker) const { return W * worker / step; }
 };
 
 #endif  // __CUDACC__

@@ -132,6 +132,7 @@ moe::GroupedGemmArgs gemm_args(const moe_grouped_shape* s, const Layout& L, void
   a.err = at<int32_t>(ws, 0);
   a.partials = at<float>(ws, L.partials);
   a.flags = at<int32_t>(ws, L.flags);
+  a.next_unit = a.flags;  // (a plan uses one or the other)
   a.G = s->groups;
   a.tiles_n = 1;
   a.fp16 = s->type == MOE_TYPE_FP16;
@@ -173,12 +174,12 @@ moe_status rows_product(GroupedOp op, const moe_grouped_shape* s, const void* in
   if (!w || !aligned(w, 16)) return MOE_ERR_INVALID_ARG;
   if ((st = check_call(s, offsets, counts, ws, ws_bytes)) != MOE_OK) return st;
   const GroupedPlan plan = choose_plan(s);
-  const int bn = moe::grouped_bn(plan), tile = moe::grouped_tile(plan);
-  const int tiles = (F + tile - 1) / tile;
-  if ((s->rows / bn + s->groups) * tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  const int tile = moe::grouped_tile(plan), tiles = (F + tile - 1) / tile;
+  if ((s->rows / 32 + s->groups) * tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   if (s->rows == 0) return MOE_OK;
   const int sms = num_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
+  const int bn = moe::grouped_bn(plan, s->rows, s->groups, tiles, sms);
   CUtensorMap tw, tx, tx32;
   if (!make_matrix_map(&tw, s->type, w, s->groups, s->N, s->K, op == GroupedOp::kForward ? 128 : 64) ||
       !make_rows_map(&tx, s->type, in, R, s->rows, ldin, static_cast<uint32_t>(moe::grouped_tok_box(plan))) ||
@@ -323,7 +324,7 @@ moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy
   p.bn = 0;
   p.tiles = static_cast<int>(tiles_m * tiles_n);
   p.skip_empty = accumulate != 0;
-  p.n_flags = 0;
+  p.n_flags = 1;
   p.maps = at<CUtensorMap>(workspace, L.maps);
   moe::GroupedGemmArgs a = gemm_args(s, L, workspace);
   a.maps = p.maps;

@@ -36,6 +36,7 @@
 #include "bounded_wait.cuh"
 #include "fp4.cuh"
 #include "launch_config.cuh"
+#include "pair_sched.cuh"
 #include "pdl.cuh"
 #include "tc_ptx.cuh"
 
@@ -59,13 +60,14 @@ struct Cfg {
   static constexpr int kTmemNeed = kAccBufs * BN + STAGES * kSfCols;
   static constexpr uint32_t kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
   static constexpr int kEpiWarps = PAIR ? 8 : 4;  // two per TMEM lane quarter for the pair's single accumulator
-  static constexpr int kThreads = 32 * (2 + kEpiWarps + 4);
+  static constexpr int kThreads = 32 * (3 + kEpiWarps + 4);  // + the weights' producer, the MMA warp, the rows' producer; 4 scale warps
+  static constexpr int kReaders = 2 * (2 + kEpiWarps + 4) + 1;  // warps of a pair that walk the units
   static constexpr int kBarBytes = 512;
   static constexpr int kTabGroups = kGroupsSmem[PAIR];
   static constexpr int kTabBytes = 3 * (kTabGroups + 1) * 4;
   static constexpr int kGxBytes = F == Fp4Format::kNv ? 4 * BN * 4 : 0;  // x's fp32 scales, per epilogue warp
   static constexpr size_t kSmemBytes =
-      1024 + static_cast<size_t>(STAGES) * kStageBytes + kBarBytes + kTabBytes + kGxBytes + 16;
+      1024 + static_cast<size_t>(STAGES) * kStageBytes + kBarBytes + kSchedBytes + kTabBytes + kGxBytes + 16;
   static_assert(kBRows % TOKBOX == 0 && BN >= 32 && BN <= 256, "token tile");
   static_assert(4 * kChunks <= 16 && kTmemNeed <= 512, "TMEM columns");
   static_assert((4 * STAGES + 5) * 8 + 8 <= kBarBytes, "barrier area");
@@ -79,8 +81,23 @@ enum : int {
   kWaitAccFull = 4,
   kWaitPartials = 5,
   kWaitScales = 7,
-  kWaitScaleLoads = 8
+  kWaitScaleLoads = 8,
+  kWaitUnit = 10
 };
+
+// A pair's walk in the form of a stream-K range: whole units.
+struct PairWalk {
+  PairUnits units;
+  int kblocks;
+  __device__ __forceinline__ bool next(int& u, int& kb0, int& kb1) {
+    u = units.next();
+    kb0 = 0;
+    kb1 = kblocks;
+    return u >= 0;
+  }
+};
+__device__ __forceinline__ bool walk_ok(const PairWalk& w) { return w.units.ok; }
+__device__ __forceinline__ bool walk_ok(const GroupedRange&) { return true; }
 
 __device__ __forceinline__ void put4(uint32_t* d, const uint4& v) {
   d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
@@ -107,15 +124,15 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* tab = reinterpret_cast<int32_t*>(smem + STAGES * C::kStageBytes + C::kBarBytes);
+  const PairSched sched(smem + STAGES * C::kStageBytes + C::kBarBytes);
+  int32_t* tab = reinterpret_cast<int32_t*>(smem + STAGES * C::kStageBytes + C::kBarBytes + kSchedBytes);
   float* gx_buf = reinterpret_cast<float*>(
       (reinterpret_cast<uintptr_t>(tab) + C::kTabBytes + 15) & ~uintptr_t(15));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
-  const int worker = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
-  const int workers = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+  const int worker = static_cast<int>(blockIdx.x), workers = static_cast<int>(gridDim.x);  // (single CTAs)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -129,6 +146,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       mbar_init(&tempty[b], (PAIR ? 2 : 1) * C::kEpiWarps);
     }
     mbar_init(done, 1);
+    if (PAIR) sched.init(C::kReaders);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tm_w);
@@ -156,87 +174,93 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
   const int total_units = tables.unit_off[a.G];
   const int kblocks = (a.R + 255) / 256;
   const int chunks_k = (a.R + fp4_chunk(F) - 1) / fp4_chunk(F);  // scale tiles along K per tile row
-  constexpr bool kStreamK = !PAIR;
-  GroupedUnits units(tables, a.G, 1, BN);  // each thread walks its role's units
+  GroupedUnits units(tables, a.G, 1, BN);  // each warp walks its role's units
+  // single CTAs: a stream-K range; pairs: whole units as they are handed out
+  auto rg = [&] {
+    if constexpr (PAIR)
+      return PairWalk{PairUnits(sched, total_units, kWaitTimeoutNs, abort_flag), kblocks};
+    else
+      return GroupedRange(total_units, kblocks, worker, workers);
+  }();
+  int u, kb0, kb1;
   auto valid_chunks = [&](int kb) { return min(C::kChunks, chunks_k - kb * C::kChunks); };
   auto n_of = [](int n) { return PAIR ? (n + 31) / 32 * 32 : (n + 15) / 16 * 16; };
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer
-      const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_last();
-      int stage = 0;
-      uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      const uint32_t full_cl = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
-      GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
-      int u, kb0, kb1;
-      while (ok && rg.next(u, kb0, kb1)) {
-        const GroupedUnit un = units.at(u);
-        const int feat = PAIR ? un.tile * 256 + static_cast<int>(rank) * 128 : un.tile * 128;
-        const int n_mma = n_of(un.n);
-        const int half = PAIR ? n_mma / 2 : n_mma;
-        const int tok_first = un.tok0 + static_cast<int>(rank) * half;
-        const int tok_rows = (half + TOKBOX - 1) / TOKBOX * TOKBOX;
-        const uint32_t bytes = kABytes + tok_rows * 128;
-        const uint64_t pol_w = un.count > BN ? pol_keep : pol_stream;
-        // scale tile rows: of this CTA's features (past N: a tile row of the
-        // same matrix, its products are dropped), of the unit's rows
-        const int64_t wt = static_cast<int64_t>(un.g) * args.w_tile_rows + min(feat / 128, args.w_tile_rows - 1);
-        const int within = un.tok0 - un.start;
-        const int64_t xt = (args.equal ? static_cast<int64_t>(un.g) * ((args.equal + 127) / 128) : un.start / 128 + un.g) +
-                           within / 128;
-        const int x_tiles = C::kG == 2 && un.n > 128 ? 2 : 1;
-        // a 32-row unit lies inside a tile: its rows are moved to row 0 by the scale warps
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, kWaitTimeoutNs, abort_flag)) {
-            ok = false;
-            break;
-          }
+  if (warp == 0 || warp == C::kThreads / 32 - 1) {
+    // ---------------- TMA producers, one warp for the weights and their scales,
+    // one for the rows and theirs; one lane issues
+    const bool weights = warp == 0, issue = elect_one();
+    const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_last();
+    const uint32_t full_cl = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    while (ok && rg.next(u, kb0, kb1)) {
+      const GroupedUnit un = units.at(u);
+      const int feat = PAIR ? un.tile * 256 + static_cast<int>(rank) * 128 : un.tile * 128;
+      const int n_mma = n_of(un.n);
+      const int half = PAIR ? n_mma / 2 : n_mma;
+      const int tok_first = un.tok0 + static_cast<int>(rank) * half;
+      const int tok_rows = (half + TOKBOX - 1) / TOKBOX * TOKBOX;
+      const uint64_t pol_w = units.chunks > 1 ? pol_keep : pol_stream;
+      // scale tile rows: of this CTA's features (past N: a tile row of the
+      // same matrix, its products are dropped), of the unit's rows
+      const int64_t wt = static_cast<int64_t>(un.g) * args.w_tile_rows + min(feat / 128, args.w_tile_rows - 1);
+      const int64_t xt = (args.equal ? static_cast<int64_t>(un.g) * ((args.equal + 127) / 128) : un.start / 128 + un.g) +
+                         (un.tok0 - un.start) / 128;
+      const int x_tiles = C::kG == 2 && un.n > 128 ? 2 : 1;
+      const uint8_t* w_sf = args.w_scales + wt * chunks_k * 512;
+      const uint8_t* x_sf = args.x_scales + xt * chunks_k * 512;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase ^ 1u, kWaitTimeoutNs, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (issue) {
           uint8_t* sa = smem + stage * C::kStageBytes;
           uint8_t* sb = sa + kABytes;
           uint8_t* sf = sb + C::kBBytes;
           uint64_t* bar = &full[stage];
           const uint32_t bar_cl = full_cl + 8u * stage;
-          if (!PAIR)
-            mbar_arrive_expect_tx(bar, bytes);
-          else if (leader)
-            mbar_arrive_expect_tx(bar, 2 * bytes);
           const uint32_t sf_bytes = 512u * valid_chunks(kb);
-          mbar_arrive_expect_tx(&sfld[stage], sf_bytes * (1 + x_tiles));
-          const int64_t chunk0 = static_cast<int64_t>(kb) * C::kChunks;
-          bulk_load(sf, args.w_scales + (wt * chunks_k + chunk0) * 512, sf_bytes, &sfld[stage], pol_w);
-          for (int h = 0; h < x_tiles; ++h)
-            bulk_load(sf + C::kSfW + h * C::kSfW, args.x_scales + ((xt + h) * chunks_k + chunk0) * 512, sf_bytes,
-                      &sfld[stage], pol_keep);
-          if (PAIR)
-            tma_load_3d_pair(sa, &tm_w, bar_cl, kb * 128, feat, un.g, pol_w);
-          else
-            tma_load_3d(sa, &tm_w, bar, kb * 128, feat, un.g, pol_w);
-          for (int r = 0; r < tok_rows; r += TOKBOX) {
+          const int sf_at = kb * C::kChunks * 512;
+          if (weights) {
+            if (leader) mbar_arrive_expect_tx(bar, (PAIR ? 2 : 1) * (kABytes + tok_rows * 128));
+            mbar_arrive_expect_tx(&sfld[stage], sf_bytes * (1 + x_tiles));
+            bulk_load(sf, w_sf + sf_at, sf_bytes, &sfld[stage], pol_w);
             if (PAIR)
-              tma_load_2d_pair(sb + r * 128, &tm_x, bar_cl, kb * 128, tok_first + r, pol_keep);
+              tma_load_3d_pair(sa, &tm_w, bar_cl, kb * 128, feat, un.g, pol_w);
             else
-              tma_load_2d(sb + r * 128, &tm_x, bar, kb * 128, tok_first + r, pol_keep);
-          }
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+              tma_load_3d(sa, &tm_w, bar, kb * 128, feat, un.g, pol_w);
+          } else {
+            for (int h = 0; h < x_tiles; ++h)
+              bulk_load(sf + (1 + h) * C::kSfW, x_sf + static_cast<int64_t>(h) * chunks_k * 512 + sf_at, sf_bytes,
+                        &sfld[stage], pol_keep);
+            for (int r = 0; r < tok_rows; r += TOKBOX) {
+              if (PAIR)
+                tma_load_2d_pair(sb + r * 128, &tm_x, bar_cl, kb * 128, tok_first + r, pol_keep);
+              else
+                tma_load_2d(sb + r * 128, &tm_x, bar, kb * 128, tok_first + r, pol_keep);
+            }
           }
         }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      if (!ok) raise_timeout(a.err, abort_flag, kKernFp4Gemm, kWaitSlotFree);
-      // every load this thread issued has landed before the CTA exits (the odd
-      // CTA of a pair sees its codes landed through the release of its stages)
-      for (int s = 0; s < STAGES; ++s) {
-        if (issued <= s) break;
-        const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
-        int dummy = 0;
-        mbar_wait(&sfld[s], par, kWaitTimeoutNs, &dummy);
-        mbar_wait(PAIR && !leader ? &empty[s] : &full[s], par, kWaitTimeoutNs, &dummy);
-      }
+    }
+    ok = ok && walk_ok(rg);
+    if (!ok && issue) raise_timeout(a.err, abort_flag, kKernFp4Gemm, walk_ok(rg) ? kWaitSlotFree : kWaitUnit);
+    // every load issued has been used before the CTA exits
+    for (int s = 0; s < STAGES; ++s) {
+      if (issued <= s) break;
+      const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
+      const int never = 0;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], par, kWaitTimeoutNs, &never))) break;
     }
   } else if (warp == 1) {
     if (leader) {
@@ -246,8 +270,6 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       int stage = 0, acc = 0, where = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
-      int u, kb0, kb1;
       while (ok && rg.next(u, kb0, kb1)) {
         const GroupedUnit un = units.at(u);
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag))) {
@@ -320,6 +342,8 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
           acc_phase ^= 1u;
         }
       }
+      if (!walk_ok(rg)) where = kWaitUnit;
+      ok = ok && walk_ok(rg);
       if (!ok && issue) raise_timeout(a.err, abort_flag, kKernFp4Gemm, where);
       if (issue) {
         if (PAIR)
@@ -330,6 +354,9 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       __syncwarp();
       int dummy = 0;
       mbar_wait(done, 0, kWaitTimeoutNs, &dummy);
+    } else if (lane == 0) {
+      if (!sched.schedule(a.next_unit, total_units, kWaitTimeoutNs, abort_flag))
+        raise_timeout(a.err, abort_flag, kKernFp4Gemm, kWaitUnit);
     }
   } else if (warp >= 2 + C::kEpiWarps) {
     // ---------------- scale warps: lane l of a quarter takes the 16 bytes of
@@ -339,8 +366,6 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
-    int u, kb0, kb1;
     while (ok && rg.next(u, kb0, kb1)) {
       const GroupedUnit un = units.at(u);
       // a unit of 32 rows may start at row 32, 64 or 96 of its tile: column j
@@ -386,7 +411,8 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
         }
       }
     }
-    if (!ok && lane == 0) raise_timeout(a.err, abort_flag, kKernFp4Gemm, kWaitScaleLoads);
+    ok = ok && walk_ok(rg);
+    if (!ok && lane == 0) raise_timeout(a.err, abort_flag, kKernFp4Gemm, walk_ok(rg) ? kWaitScaleLoads : kWaitUnit);
   } else {
     // ---------------- epilogue: warps 2.., TMEM lane quarter = warp % 4; two
     // warps of a quarter take half of the columns each
@@ -396,8 +422,6 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     const uint32_t tempty_cl = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
-    GroupedRange rg(total_units, kblocks, worker, workers, kStreamK);
-    int u, kb0, kb1;
     constexpr int kCols = BN * 4 / C::kEpiWarps;  // columns per warp
     const int col0 = (warp - 2) / 4 * kCols;
     float* gx = gx_buf + (warp - 2) * kCols;
@@ -437,6 +461,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
         for (int c0 = 0; c0 < kCols; c0 += 32) {
           if (col0 + c0 < un.n) {
             uint32_t r[32];
+            __syncwarp();  // tcgen05.ld is warp-aligned
             tmem_ld_32x32b_x32(t_row + col0 + c0, r);
             tmem_ld_wait();
 #pragma unroll
@@ -464,6 +489,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
         float* slot = a.partials + static_cast<int64_t>(worker) * BN * 128;
         for (int c0 = 0; c0 < un.n; c0 += 16) {
           uint32_t r[16];
+          __syncwarp();  // tcgen05.ld is warp-aligned
           tmem_ld_32x32b_x16(t_row + c0, r);
           tmem_ld_wait();
 #pragma unroll
@@ -481,6 +507,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
         }
         for (int c0 = 0; c0 < un.n; c0 += 16) {
           uint32_t r[16];
+          __syncwarp();  // tcgen05.ld is warp-aligned
           tmem_ld_32x32b_x16(t_row + c0, r);
           tmem_ld_wait();
           float v[16];
@@ -519,12 +546,15 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
         acc_phase ^= 1u;
       }
     }
+    if (!walk_ok(rg)) where = kWaitUnit;
+    ok = ok && walk_ok(rg);
     if (!ok && lane == 0) raise_timeout(a.err, abort_flag, kKernFp4Gemm, where);
   }
 
   __syncthreads();
   if (PAIR) cluster_sync();  // a pair keeps both CTAs until both are done
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
     if (PAIR)
       tmem_dealloc_pair(tmem_base, C::kTmemCols);
@@ -537,44 +567,11 @@ template <Fp4Format F, int BN, int STAGES, int TOKBOX, bool PAIR>
 cudaError_t launch_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArgs& a, int num_sms,
                         cudaStream_t stream) {
   using C = Cfg<F, BN, STAGES, TOKBOX, PAIR>;
-  auto kernel = fp4_gemm_kernel<F, BN, STAGES, TOKBOX, PAIR>;
   static PerDevice config;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = PAIR ? 2 : 1;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  int max_pairs = 0;
-  const cudaError_t e = config.get(
-      [&](int& pairs) -> cudaError_t {
-        cudaError_t ce =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytes));
-        if (ce != cudaSuccess || !PAIR) return ce;
-        cudaLaunchConfig_t q = cfg;
-        q.gridDim = dim3(2 * (kMaxGemmCtas / 2));
-        q.attrs = attr + 1;
-        q.numAttrs = 1;
-        int n = 0;
-        ce = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
-        if (ce != cudaSuccess) return ce;
-        if (n <= 0) return cudaErrorInvalidConfiguration;
-        pairs = n;
-        return cudaSuccess;
-      },
-      &max_pairs);
-  if (e != cudaSuccess) return e;
-  const int most = PAIR ? kMaxGemmCtas / 2 : kMaxGemmCtas;
-  const int workers = PAIR ? max_pairs : num_sms;
-  cfg.gridDim = dim3((workers < most ? workers : most) * (PAIR ? 2 : 1));
-  cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, a);
+  auto kernel = fp4_gemm_kernel<F, BN, STAGES, TOKBOX, PAIR>;
+  if constexpr (PAIR) return launch_pairs(kernel, config, C::kThreads, C::kSmemBytes, stream, tw, tx, a);
+  return launch_ctas(kernel, config, num_sms < kMaxGemmCtas ? num_sms : kMaxGemmCtas, C::kThreads, C::kSmemBytes, stream,
+                     tw, tx, a);
 }
 
 constexpr int kBn[2] = {32, 256}, kTile[2] = {128, 256}, kTokBox[2] = {16, 128};

@@ -18,14 +18,19 @@
 //     takes one, so that its epilogue runs under the next unit's MMAs; one of more takes both, with two
 //     MMAs of about half its rows per step that share the stage's weight tile (an MMA of
 //     few columns costs far more than its share: 256 + 32 columns 1.3 times 144 + 144).
-// An MMA of N columns takes N / 2 rows from each CTA: its first N / 2 columns
-// are rows of the unit's first half, the others of the second.
+// A group's rows are cut into units of up to bn rows, evenly (full units and a
+// rest, 512 + 8 for 2 x 260 rows, measured 1.2 times as long), and units are handed out as
+// pairs ask for them (pair_sched.cuh; dealt round-robin 1.14 times as long).
+// Measured, 64 groups, N = 8192, K = 4096: 512 rows 1179 us (1.87 PFLOP/s, 0.96 of the burst
+// rate), 520 rows 1362 us, 256 rows 709 us (0.95 of HBM: the weights alone);
+// one group of 8192 rows, N = K = 8192: 571 us (1.93 PFLOP/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "bounded_wait.cuh"
 #include "grouped.cuh"
 #include "launch_config.cuh"
+#include "pair_sched.cuh"
 #include "pdl.cuh"
 #include "tc_ptx.cuh"
 
@@ -43,11 +48,11 @@ constexpr int kEpiWarps = 8;         // two per TMEM lane quarter, alternate gro
 constexpr int kThreads = 32 * (3 + kEpiWarps);  // + the weights' producer, the MMA warp, the rows' producer
 constexpr int kBarBytes = 256;
 constexpr int kTabBytes = 3 * (kGroupsSmem[1] + 1) * 4;
-constexpr size_t kSmemBytes = 1024 + kRing + kBarBytes + kTabBytes;
+constexpr size_t kSmemBytes = 1024 + kRing + kBarBytes + kSchedBytes + kTabBytes;
 static_assert((2 * kStages + 5) * 8 + 8 <= kBarBytes, "barrier area");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
-enum : int { kWaitSlotFree = 1, kWaitAccFree = 2, kWaitSlotFull = 3, kWaitAccFull = 4 };
+enum : int { kWaitSlotFree = 1, kWaitAccFree = 2, kWaitSlotFull = 3, kWaitAccFull = 4, kWaitUnit = 10 };
 
 __device__ __forceinline__ uint16_t to16(float v, bool fp16) {
   return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
@@ -139,12 +144,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* tab = reinterpret_cast<int32_t*>(smem + kRing + kBarBytes);
+  const PairSched sched(smem + kRing + kBarBytes);
+  int32_t* tab = reinterpret_cast<int32_t*>(smem + kRing + kBarBytes + kSchedBytes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -156,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tempty[b], 2 * kEpiWarps);
     }
     mbar_init(done, 1);
+    sched.init(2 * (2 + kEpiWarps) + 1);  // producers and epilogue of both CTAs, the MMA warp
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tm_w);
@@ -175,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int total_units = tables.unit_off[a.G];
   const int kblocks = (a.R + 63) / 64;
-  GroupedUnits units(tables, a.G, 1, a.bn, true);  // each thread walks its role's units
+  GroupedUnits units(tables, a.G, 1, a.bn, true);  // each warp walks its role's units
+  PairUnits walk(sched, total_units, kWaitTimeoutNs, abort_flag);
 
   if (warp == 0 || warp == 2 + kEpiWarps) {
     // ---------------- TMA producers: one warp for the weight tiles, one for the
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t full_cl = mapa_shared(smem_u32(full), 0);  // both CTAs signal the even one
     Producer ring(empty, abort_flag, lane);
     bool ok = true;
-    for (int u = worker; ok && u < total_units; u += workers) {
+    for (int u; ok && (u = walk.next()) >= 0;) {
       const GroupedUnit un = units.at(u);
       const Size z(un.n);
       const int feat = un.tile * 256 + static_cast<int>(rank) * 128;
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring.advance();
       }
     }
-    if (!ok && issue) raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitSlotFree);
+    if (!(ok && walk.ok) && issue) raise_timeout(a.err, abort_flag, kKernGroupedGemm, walk.ok ? kWaitSlotFree : kWaitUnit);
     ring.drain();
   } else if (warp == 1) {
     if (leader) {
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       BytePlace place;
       int stage = 0;
       uint32_t phase = 0, uses = 0;  // accumulators taken so far: the next is uses & 1
-      for (int u = worker; ok && u < total_units; u += workers) {
+      for (int u; ok && (u = walk.next()) >= 0;) {
         const GroupedUnit un = units.at(u);
         const Size z(un.n);
         const int parts = z.cols > z.cols0 ? 2 : 1;
@@ -287,12 +294,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         uses += parts;
       }
-      if (!ok && issue) raise_timeout(a.err, abort_flag, kKernGroupedGemm, where);
+      if (!walk.ok) where = kWaitUnit;
+      if (!(ok && walk.ok) && issue) raise_timeout(a.err, abort_flag, kKernGroupedGemm, where);
       // all MMAs issued have finished before TMEM is released
       if (issue) mma_commit_pair(done);
       __syncwarp();
       int dummy = 0;
       mbar_wait(done, 0, kWaitTimeoutNs, &dummy);
+    } else if (lane == 0) {
+      if (!sched.schedule(a.next_unit, total_units, kWaitTimeoutNs, abort_flag))
+        raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitUnit);
     }
   } else {
     // ---------------- epilogue: TMEM lane quarter = warp % 4; a quarter's two
@@ -303,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty_cl = mapa_shared(smem_u32(tempty), 0);
     bool ok = true;
     uint32_t uses = 0;
-    for (int u = worker; ok && u < total_units; u += workers) {
+    for (int u; ok && (u = walk.next()) >= 0;) {
       const GroupedUnit un = units.at(u);
       const Size z(un.n);
       const int feat = un.tile * 256 + static_cast<int>(rank) * 128 + row;
@@ -324,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
         for (int c0 = 32 * turn; c0 < cols; c0 += 64) {
           uint32_t r[32];
+          __syncwarp();  // tcgen05.ld is warp-aligned: the stores before it are not
           tmem_ld_32x32b_x32(t_row + c0, r);
           tmem_ld_wait();
           if (mine) {
@@ -350,12 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_remote(tempty_cl + 8u * buf);
       }
     }
-    if (!ok && lane == 0) raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitAccFull);
+    if (!(ok && walk.ok) && lane == 0)
+      raise_timeout(a.err, abort_flag, kKernGroupedGemm, walk.ok ? kWaitAccFull : kWaitUnit);
   }
 
   __syncthreads();
   cluster_sync();  // both CTAs keep their shared memory, barriers and TMEM until both are done
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 2 * kAccCols);
   }
@@ -364,42 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool DGRAD>
 cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx32, const GroupedGemmArgs& a,
                    cudaStream_t stream) {
-  auto kernel = grouped_pair_kernel<DGRAD>;
-  static PerDevice config;  // the smem attribute, and the CTA pairs that fit on the device at once
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  int max_pairs = 0;
-  const cudaError_t e = config.get(
-      [&](int& pairs) -> cudaError_t {
-        cudaError_t ce =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
-        if (ce != cudaSuccess) return ce;
-        cudaLaunchConfig_t q = cfg;
-        q.gridDim = dim3(2 * (kMaxGemmCtas / 2));
-        q.attrs = attr + 1;
-        q.numAttrs = 1;
-        int n = 0;
-        ce = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
-        if (ce != cudaSuccess) return ce;
-        if (n <= 0) return cudaErrorInvalidConfiguration;
-        pairs = n;
-        return cudaSuccess;
-      },
-      &max_pairs);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(2 * (max_pairs < kMaxGemmCtas / 2 ? max_pairs : kMaxGemmCtas / 2));
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, tx32, a);
+  static PerDevice config;
+  return launch_pairs(grouped_pair_kernel<DGRAD>, config, kThreads, kSmemBytes, stream, tw, tx, tx32, a);
 }
 
 }  // namespace

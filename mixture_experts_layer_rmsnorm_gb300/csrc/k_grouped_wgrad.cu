@@ -1,0 +1,308 @@
+// k_grouped_wgrad.cu -- the weight gradient of the products grouped by expert,
+//   dw_g = sum over the group's rows p of dy[p, :]^T x[p, :]
+// on CTA pairs (tcgen05.mma cta_group::2, 256 x 256 tiles of dw_g, fp32
+// accumulation in TMEM).
+//
+// The reduction runs over the group's rows, the slow index of both operands:
+// both are MN-major (the descriptors' transpose bits), read as stored.  A
+// group's last block of 64 rows holds rows of the next group, which must not
+// enter the sum (as zeros times a NaN would): the plan kernel writes per group
+// copies of the host's two tensor maps whose row extent ends with the group, so
+// TMA fills the rows past it with zeros, and MMAs past it are not issued.
+//
+// Two accumulators of 256 columns: a tile's epilogue runs under the next tile's
+// MMAs.  The epilogue's four warps (one per TMEM lane quarter) move 32 x 128-byte
+// boxes through shared memory, two each, to TMA stores, which clip at the matrix's
+// edges; fp32 accumulation into dw is a TMA add, each element added once, so no
+// order changes a result.  An empty group's tile is stored as zeros, without MMAs.
+// Tiles go round-robin to the CTA pairs (a group's tiles are equally long).
+//
+// Bound: by writing dw where groups are short (a tile of fp32 moves 128 KB per
+// CTA for 64 KB of operands per 64 rows), else by the tensor cores; in between by shared memory, which
+// the operands cross twice and the tile too.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "bounded_wait.cuh"
+#include "grouped.cuh"
+#include "launch_config.cuh"
+#include "pdl.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+constexpr int kMnBox = 64 * 128;                // 64 columns x 64 rows, 16 bits
+constexpr int kOperand = 2 * kMnBox;            // this CTA's 128 columns of dy, or of x
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 4;
+constexpr int kBox = 32 * 128;                  // an epilogue warp has two boxes of 32 rows x 128 bytes
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kBarBytes = 256;
+constexpr int kTabBytes = 3 * (kGroupsSmem[1] + 1) * 4;
+constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + 2 * kEpiWarps * kBox + kBarBytes + kTabBytes;
+static_assert((2 * kStages + 5) * 8 + 8 <= kBarBytes, "barrier area");
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+
+enum : int { kWaitSlotFree = 1, kWaitAccFree = 2, kWaitSlotFull = 3, kWaitAccFull = 4 };
+
+__device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi, bool fp16) {
+  const float a = __uint_as_float(lo), b = __uint_as_float(hi);
+  if (fp16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tm_dw, const __grid_constant__ GroupedGemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* boxes = smem + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 2 * kEpiWarps * kBox);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* tab = reinterpret_cast<int32_t*>(boxes + 2 * kEpiWarps * kBox + kBarBytes);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kEpiWarps);  // of both CTAs
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tm_dw);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  pdl_wait();  // the plan kernel's tables and maps
+  const GroupedTables tables = grouped_tables(a, tab, kGroupsSmem[1], kThreads);
+  tc_fence_before();
+  cluster_sync();  // the peer's barriers are initialised before any remote signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int total_units = tables.unit_off[a.G];
+  GroupedUnits units(tables, a.G, a.tiles_n, 0);  // each thread walks its role's units
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer
+      const uint64_t policy = policy_evict_last();  // both operands are read by every tile of their group
+      const uint32_t full_cl = mapa_shared(smem_u32(full), 0);  // both CTAs signal the even one
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      int map_group = -1;
+      for (int u = worker; ok && u < total_units; u += workers) {
+        const GroupedUnit un = units.at(u);
+        const int row = un.tile * 256 + static_cast<int>(rank) * 128, col = un.tile_n * 256 + static_cast<int>(rank) * 128;
+        const CUtensorMap* map = a.maps + 2 * un.g;
+        if (un.g != map_group) {
+          tensormap_acquire(map);
+          tensormap_acquire(map + 1);
+          map_group = un.g;
+        }
+        for (int p = 0; p < un.n; p += 64) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, kWaitTimeoutNs, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * kStageBytes;
+          const uint32_t bar = full_cl + 8u * stage;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tma_load_2d_pair(sa + j * kMnBox, map, bar, row + 64 * j, un.tok0 + p, policy);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            tma_load_2d_pair(sa + kOperand + j * kMnBox, map + 1, bar, col + 64 * j, un.tok0 + p, policy);
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitSlotFree);
+      // every load this thread issued has landed before the CTA exits (the odd
+      // CTA of a pair sees that through the release of its stages)
+      for (int s = 0; s < kStages; ++s) {
+        if (issued <= s) break;
+        const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
+        int dummy = 0;
+        mbar_wait(leader ? &full[s] : &empty[s], par, kWaitTimeoutNs, &dummy);
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      // ---------------- MMA issuer for both CTAs: the whole warp walks the units, one lane issues
+      const bool issue = elect_one();
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t a0 = sdesc_mnmajor_sw128(s0, kMnBox), b0 = sdesc_mnmajor_sw128(s0 + kOperand, kMnBox);
+      const uint32_t idesc = idesc_f16_f32(256, 256, a.fp16, 1, 1);
+      int stage = 0, acc = 0, where = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int u = worker; ok && u < total_units; u += workers) {
+        const GroupedUnit un = units.at(u);
+        if (un.n == 0) continue;  // the epilogue writes zeros
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag))) {
+          ok = false;
+          where = kWaitAccFree;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_acc = tmem_base + static_cast<uint32_t>(acc * 256);
+        for (int row = 0; row < un.n; row += 64) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, kWaitTimeoutNs, abort_flag))) {
+            ok = false;
+            where = kWaitSlotFull;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t at = static_cast<uint64_t>(stage * (kStageBytes >> 4));
+          const int n_k = min(4, (un.n - row + 15) / 16);  // MMAs of 16 rows
+          if (issue) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k >= n_k) break;
+              mma_bf16_ss_pair(d_acc, a0 + at + k * (2048 >> 4), b0 + at + k * (2048 >> 4), idesc, k > 0 ? 1u : row > 0);
+            }
+            mma_commit_pair_mc(&empty[stage], 0x3);
+          }
+          __syncwarp();
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (issue) mma_commit_pair_mc(&tfull[acc], 0x3);
+        __syncwarp();
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (!ok && issue) raise_timeout(a.err, abort_flag, kKernGroupedGemm, where);
+      // all MMAs issued have finished before TMEM is released
+      if (issue) mma_commit_pair(done);
+      __syncwarp();
+      int dummy = 0;
+      mbar_wait(done, 0, kWaitTimeoutNs, &dummy);
+    }
+  } else {
+    // ---------------- epilogue: TMEM lane quarter = warp % 4
+    const int q = warp & 3;
+    uint8_t* my_boxes = boxes + q * 2 * kBox;
+    uint32_t buf = 0;
+    const uint32_t tempty_cl = mapa_shared(smem_u32(tempty), 0);
+    const int span = a.out_fp32 ? 32 : 64;  // columns of a box
+    const bool fp16 = a.fp16 != 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int u = worker; ok && u < total_units; u += workers) {
+      const GroupedUnit un = units.at(u);
+      const int row0 = un.tile * 256 + static_cast<int>(rank) * 128 + q * 32;
+      const bool has_acc = un.n > 0;
+      if (has_acc) {
+        // warp-uniform outcome: tcgen05.ld below is executed by all 32 lanes
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_phase, kWaitTimeoutNs, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      for (int c0 = 0; c0 < 256 && row0 < a.F; c0 += span) {
+        const int col = un.tile_n * 256 + c0;
+        if (col >= a.C) break;
+        uint8_t* box = my_boxes + buf * kBox;
+        buf ^= 1u;
+        if (lane == 0) bulk_wait_read<1>();  // the box's last store has read it
+        __syncwarp();    // (tcgen05.ld is warp-aligned: lane 0 comes from its store)
+        uint32_t w[32];  // the lane's 128 bytes
+        if (!has_acc) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) w[j] = 0u;
+        } else if (a.out_fp32) {
+          tmem_ld_32x32b_x32(t_row + c0, w);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(t_row + c0 + 32 * h, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[16 * h + j] = pack16(r[2 * j], r[2 * j + 1], fp16);
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < 8; ++p)  // the 128-byte swizzle of the store's map
+          *reinterpret_cast<uint4*>(box + lane * 128 + ((p ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (a.accumulate)
+            tma_add_3d(&tm_dw, box, col, row0, un.g);
+          else
+            tma_store_3d(&tm_dw, box, col, row0, un.g);
+          bulk_commit();
+        }
+      }
+      if (has_acc) {  // hand the accumulator back to the MMA warp
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_cl + 8u * acc);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    if (!ok && lane == 0) raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitAccFull);
+  }
+
+  __syncthreads();
+  cluster_sync();  // both CTAs keep their shared memory, barriers and TMEM until both are done
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_wgrad(const CUtensorMap& tm_dw, const GroupedGemmArgs& a, cudaStream_t stream) {
+  static PerDevice config;
+  return launch_pairs(grouped_wgrad_kernel, config, kThreads, kSmemBytes, stream, tm_dw, a);
+}
+
+}  // namespace moe
