@@ -11,16 +11,18 @@
 // scale, so the values it stands for are NaN.
 //
 // Bound: HBM asks for 2.56 bytes per 16-bit element, 14 instruction slots of an SM at the
-// measured copy rate, so the instructions per element decide.  A thread takes 8
-// elements (16 bytes of 16-bit input) at a time and kHold such vectors at once,
-// all loads first; TPR threads share a row.
+// measured copy rate, so the instructions per element decide.  A thread takes 16
+// elements at a time (a whole NVFP4 block, half an MXFP4 one: the scale is computed once for
+// them) and hold_of(type) such vectors at once, all loads first; TPR threads share a row.
 //   - The block maximum is taken on the packed 16-bit magnitudes, whose order
 //     is that of their bits (NaN and infinities above all numbers).
-//   - NVFP4's two quotients decide codes, so they have to be the rounded
-//     quotients, but only their side of a code's border matters.  x times a
-//     reciprocal lowered and raised by 2^-21 (more than all roundings of that product,
-//     2^-22) brackets the quotient: if both ends get the same code, so does the quotient; else the
-//     division is done.  Two products and conversions instead of a division.
+//   - NVFP4's quotients decide codes, so they have to be the rounded quotients.
+//     One rounded reciprocal y = 1 / d serves 16 of them by Markstein's correction
+//     ("Computation of elementary functions on the IBM RISC System/6000", 1990):
+//     q = x y, r = x - q d (exact in a fused multiply-add), x / d = q + r y rounded, on two elements an
+//     instruction.  (Products with a lowered and a raised reciprocal, whose codes agree unless the
+//     quotient lies at a border, cost a second conversion, the slowest
+//     instruction here: 105 us for 134 M elements.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,7 +33,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHold = 4;  // vectors of 8 elements a thread holds
+// vectors of 16 elements a thread holds: 32 registers
+__host__ __device__ constexpr int hold_of(int type) { return type == 2 ? 2 : 4; }
 
 struct RowPlace {
   int group, tile_row, in_tile;
@@ -80,32 +83,36 @@ __device__ __forceinline__ uint8_t* row_scales(const Fp4RowsArgs& a, const RowPl
   return a.scales + static_cast<size_t>(r.tile_row) * chunks * 512 + (r.in_tile & 31) * 16 + (r.in_tile >> 5) * 4;
 }
 
+constexpr int kElems = 16;  // of a vector
+
 template <int TYPE>
-struct Vec {  // 8 elements
-  uint4 raw[TYPE == 2 ? 2 : 1];
+struct Vec {
+  static constexpr int kQuads = TYPE == 2 ? 4 : 2;
+  uint4 raw[kQuads];
 };
 
 template <int TYPE>
-__device__ __forceinline__ void load8(const void* row, int v, Vec<TYPE>& x) {
-  const uint4* p = static_cast<const uint4*>(row) + static_cast<int64_t>(v) * (TYPE == 2 ? 2 : 1);
-  x.raw[0] = __ldg(p);
-  if constexpr (TYPE == 2) x.raw[1] = __ldg(p + 1);
+__device__ __forceinline__ void load_vec(const void* row, int v, Vec<TYPE>& x) {
+  const uint4* p = static_cast<const uint4*>(row) + static_cast<int64_t>(v) * Vec<TYPE>::kQuads;
+#pragma unroll
+  for (int i = 0; i < Vec<TYPE>::kQuads; ++i) x.raw[i] = __ldg(p + i);
 }
 
 template <int TYPE>
-__device__ __forceinline__ void zero8(Vec<TYPE>& x) {
-  x.raw[0] = make_uint4(0, 0, 0, 0);
-  if constexpr (TYPE == 2) x.raw[1] = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void zero_vec(Vec<TYPE>& x) {
+#pragma unroll
+  for (int i = 0; i < Vec<TYPE>::kQuads; ++i) x.raw[i] = make_uint4(0, 0, 0, 0);
 }
 
+// Elements 8 h .. 8 h + 7 as fp32.
 template <int TYPE>
-__device__ __forceinline__ void values8(const Vec<TYPE>& x, float (&f)[8]) {
+__device__ __forceinline__ void values8(const Vec<TYPE>& x, int h, float (&f)[8]) {
   if constexpr (TYPE == 2) {
-    f[0] = __uint_as_float(x.raw[0].x), f[1] = __uint_as_float(x.raw[0].y), f[2] = __uint_as_float(x.raw[0].z);
-    f[3] = __uint_as_float(x.raw[0].w), f[4] = __uint_as_float(x.raw[1].x), f[5] = __uint_as_float(x.raw[1].y);
-    f[6] = __uint_as_float(x.raw[1].z), f[7] = __uint_as_float(x.raw[1].w);
+    const uint4 &a = x.raw[2 * h], &b = x.raw[2 * h + 1];
+    f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
+    f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
   } else {
-    unpack8<TYPE == 1>(x.raw[0], f);
+    unpack8<TYPE == 1>(x.raw[h], f);
   }
 }
 
@@ -115,16 +122,15 @@ __device__ __forceinline__ uint32_t max_mag(uint32_t a, uint32_t b) {
   return TYPE == 2 ? max(a, b) : __vmaxu2(a, b);
 }
 template <int TYPE>
-__device__ __forceinline__ uint32_t mag8(const Vec<TYPE>& x) {
-  if constexpr (TYPE == 2) {
-    const uint4 &a = x.raw[0], &b = x.raw[1];
-    constexpr uint32_t m = 0x7FFFFFFFu;
-    return max(max(max(a.x & m, a.y & m), max(a.z & m, a.w & m)), max(max(b.x & m, b.y & m), max(b.z & m, b.w & m)));
-  } else {
-    const uint4& a = x.raw[0];
-    constexpr uint32_t m = 0x7FFF7FFFu;
-    return __vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m));
+__device__ __forceinline__ uint32_t mag_vec(const Vec<TYPE>& x) {
+  constexpr uint32_t m = TYPE == 2 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < Vec<TYPE>::kQuads; ++i) {
+    const uint4& a = x.raw[i];
+    r = max_mag<TYPE>(r, max_mag<TYPE>(max_mag<TYPE>(a.x & m, a.y & m), max_mag<TYPE>(a.z & m, a.w & m)));
   }
+  return r;
 }
 template <int TYPE>
 __device__ __forceinline__ uint32_t mag_bits(uint32_t m) {  // of fp32
@@ -154,9 +160,9 @@ __device__ __forceinline__ float nv_global(uint32_t amax) {
   return amax ? __fdiv_rn(__uint_as_float(amax), 2688.0f) : 1.0f;
 }
 
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+__device__ __forceinline__ uint32_t e4m3_of(float u) {  // u >= 0
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(u));
   return r;
 }
 __device__ __forceinline__ float e4m3_to(uint32_t c) {  // 0x7F is NaN
@@ -165,31 +171,60 @@ __device__ __forceinline__ float e4m3_to(uint32_t c) {  // 0x7F is NaN
   return __low2float(*reinterpret_cast<const __half2*>(&h));
 }
 
-// What a row's NVFP4 codes need: g and 1 / (6 g) lowered and raised, or (far
-// from 1, or no number) the sign that quotients are divided out.
+// What a row's NVFP4 codes need: g and the reciprocal of 6 g.  `plain`: g is so
+// near 1 that no step below leaves fp32's normal range where it matters (else,
+// or with no number, quotients are divided out).
 struct NvRow {
-  float g, six_g, r_lo, r_hi;
+  float g, six_g, inv_six_g;
   bool plain;
 };
-constexpr float kLo = 1.0f - 0x1p-21f, kHi = 1.0f + 0x1p-21f;
-
-__device__ __forceinline__ bool mid_range(float v) { return v > 0x1p-100f && v < 0x1p100f; }
 
 __device__ __forceinline__ NvRow nv_row(float g) {
   NvRow r;
   r.g = g;
   r.six_g = __fmul_rn(6.0f, g);
-  const float inv = __frcp_rn(r.six_g);
-  r.r_lo = inv * kLo;
-  r.r_hi = inv * kHi;
-  r.plain = mid_range(r.six_g);
+  r.inv_six_g = __frcp_rn(r.six_g);
+  r.plain = g > 0x1p-80f && g < 0x1p80f;
   return r;
 }
 
-// Codes and scale byte of 8 elements of a block whose largest magnitude has
+// a / d by Markstein's correction, y = the rounded 1 / d
+__device__ __forceinline__ float quotient(float a, float d, float y) {
+  const float q = __fmul_rn(a, y);
+  return __fmaf_rn(__fmaf_rn(-q, d, a), y, q);
+}
+
+// The same for eight, negated: x becomes -(x / d), ny the negated reciprocal.
+// (With x = -0 the residual is +0, so q + r y would lose the zero's sign; here
+// every product of the last step has the sign of -0.)
+__device__ __forceinline__ void negated_quotients8(float (&x)[8], float d, float ny) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("{\n\t.reg .b64 x, d, n, q;\n\t"
+        "mov.b64 x, {%0, %1};\n\t"
+        "mov.b64 d, {%2, %2};\n\t"
+        "mov.b64 n, {%3, %3};\n\t"
+        "mul.rn.f32x2 q, x, n;\n\t"
+        "fma.rn.f32x2 x, q, d, x;\n\t"
+        "fma.rn.f32x2 x, x, n, q;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(x[i]), "+f"(x[i + 1])
+        : "f"(d), "f"(ny));
+}
+
+// The rare way: divisions.
+__device__ __noinline__ uint32_t divided_codes(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+                                               float x7, float d) {
+  const float x[8] = {__fdiv_rn(x0, d), __fdiv_rn(x1, d), __fdiv_rn(x2, d), __fdiv_rn(x3, d),
+                      __fdiv_rn(x4, d), __fdiv_rn(x5, d), __fdiv_rn(x6, d), __fdiv_rn(x7, d)};
+  return codes8(x);
+}
+
+// Codes and scale byte of 16 elements of a block whose largest magnitude has
 // the fp32 bits `amax`.
 template <Fp4Format F, int TYPE>
-__device__ __forceinline__ uint32_t encode8(const Vec<TYPE>& v, uint32_t amax, const NvRow& nv, uint32_t& scale) {
+__device__ __forceinline__ uint2 encode(const Vec<TYPE>& v, uint32_t amax, const NvRow& nv, uint32_t& scale) {
+  uint32_t w[2];
   float x[8];
   if constexpr (F == Fp4Format::kMx) {
     int e = static_cast<int>(amax >> 23) - 127 - 2;  // (a subnormal maximum clamps too)
@@ -197,52 +232,55 @@ __device__ __forceinline__ uint32_t encode8(const Vec<TYPE>& v, uint32_t amax, c
     scale = amax >= kInfBits ? 255u : static_cast<uint32_t>(e + 127);
     // 2^-e; x 2^-e is exact down to magnitudes whose code is 0 either way
     const uint32_t inv = static_cast<uint32_t>(127 - e) << 23;
-    if constexpr (TYPE == 0) {
-      const uint32_t w[4] = {v.raw[0].x, v.raw[0].y, v.raw[0].z, v.raw[0].w};
-      const uint32_t s2 = inv | (inv >> 16);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&s2));
-        const uint32_t b = *reinterpret_cast<const uint32_t*>(&p);
-        x[2 * i] = __uint_as_float(b << 16);
-        x[2 * i + 1] = __uint_as_float(b & 0xFFFF0000u);
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (TYPE == 0) {
+        const uint32_t q[4] = {v.raw[h].x, v.raw[h].y, v.raw[h].z, v.raw[h].w};
+        const uint32_t s2 = inv | (inv >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&q[i]),
+                                           *reinterpret_cast<const __nv_bfloat162*>(&s2));
+          const uint32_t b = *reinterpret_cast<const uint32_t*>(&p);
+          x[2 * i] = __uint_as_float(b << 16);
+          x[2 * i + 1] = __uint_as_float(b & 0xFFFF0000u);
+        }
+      } else {
+        values8<TYPE>(v, h, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= __uint_as_float(inv);
       }
-    } else {
-      values8<TYPE>(v, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= __uint_as_float(inv);
+      w[h] = codes8(x);
     }
-    return codes8(x);
+    return make_uint2(w[0], w[1]);
   }
   const float top = __uint_as_float(amax);
-  const uint32_t both = e4m3_pair(top * nv.r_lo, top * nv.r_hi);
-  scale = both & 0xFFu;
-  if (scale != both >> 8 || !nv.plain) scale = nv.g == nv.g ? e4m3_pair(__fdiv_rn(top, nv.six_g), 0.0f) & 0xFFu : 0x7Fu;
-  const float d = __fmul_rn(e4m3_to(scale), nv.g);
-  float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
-  values8<TYPE>(v, x);
-  float lo[8], hi[8];
+  if (!nv.plain) {  // (whole rows)
+    scale = nv.g == nv.g ? e4m3_of(__fdiv_rn(top, nv.six_g)) : 0x7Fu;
+    const float d = __fmul_rn(e4m3_to(scale), nv.g);
+    if (!(d > 0.0f)) return make_uint2(0u, 0u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = x[i] * (inv * kLo);
-    hi[i] = x[i] * (inv * kHi);
+    for (int h = 0; h < 2; ++h) {
+      values8<TYPE>(v, h, x);
+      w[h] = divided_codes(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], d);
+    }
+    return make_uint2(w[0], w[1]);
   }
-  uint32_t w = codes8(lo);
-  if (w != codes8(hi) || !mid_range(d)) {
-    if (!(d > 0.0f)) return 0u;
+  scale = e4m3_of(quotient(top, nv.six_g, nv.inv_six_g));
+  const float d = __fmul_rn(e4m3_to(scale), nv.g), ny = -__frcp_rn(d);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], d);
-    w = codes8(x);
+  for (int h = 0; h < 2; ++h) {
+    values8<TYPE>(v, h, x);
+    negated_quotients8(x, d, ny);
+    w[h] = codes8(x) ^ 0x88888888u;
   }
-  return w;
+  return scale ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
 }
 
 // TPR threads per row.  NVFP4 per row: the row's maximum first; per group: from
 // gscale, which then holds the maxima's bits.
 template <Fp4Format F, int TYPE, int TPR>
-__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_constant__ Fp4RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_constant__ Fp4RowsArgs a) {
   constexpr int kRows = kThreads / TPR, kWarpsPerRow = TPR / 32;
   __shared__ uint32_t warp_max[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -250,16 +288,17 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_con
   const int64_t p64 = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
   const bool in = p64 < a.rows;
   const int p = in ? static_cast<int>(p64) : 0;
-  const int vecs = a.K / 8;
+  const int vecs = a.K / kElems;
   const char* src = static_cast<const char*>(a.src) + p * a.ld * (TYPE == 2 ? 4 : 2);
+  constexpr int kHold = hold_of(TYPE);
   Vec<TYPE> held[kHold];
   // (a row of no group is read in vain: its place is looked up meanwhile)
 #pragma unroll
   for (int i = 0; i < kHold; ++i) {
     if (t + i * TPR < vecs)
-      load8<TYPE>(src, t + i * TPR, held[i]);
+      load_vec<TYPE>(src, t + i * TPR, held[i]);
     else
-      zero8<TYPE>(held[i]);
+      zero_vec<TYPE>(held[i]);
   }
   const RowPlace r = place_of(a, p, lane);
   const bool row_on = in && r.on;
@@ -269,11 +308,18 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_con
     if (!a.per_group) {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) m = max_mag<TYPE>(m, mag8<TYPE>(held[i]));
-      for (int v = t + kHold * TPR; v < vecs; v += TPR) {
-        Vec<TYPE> x;
-        load8<TYPE>(src, v, x);
-        m = max_mag<TYPE>(m, mag8<TYPE>(x));
+      for (int i = 0; i < kHold; ++i) m = max_mag<TYPE>(m, mag_vec<TYPE>(held[i]));
+      for (int v0 = kHold * TPR + t; v0 < vecs; v0 += kHold * TPR) {
+        Vec<TYPE> x[kHold];
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+          if (v0 + i * TPR < vecs)
+            load_vec<TYPE>(src, v0 + i * TPR, x[i]);
+          else
+            zero_vec<TYPE>(x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) m = max_mag<TYPE>(m, mag_vec<TYPE>(x[i]));
       }
       m = __reduce_max_sync(0xFFFFFFFFu, mag_bits<TYPE>(m));
       if (kWarpsPerRow > 1) {
@@ -292,36 +338,43 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_con
   }
   if (!row_on) return;  // (whole warps)
   const int chunks = (a.K + fp4_chunk(F) - 1) / fp4_chunk(F);
-  constexpr int kLanesPerBlock = fp4_block(F) / 8;
+  constexpr int kLanesPerBlock = fp4_block(F) / kElems;
   uint8_t* codes = a.codes + static_cast<size_t>(p) * (a.K / 2);
   uint8_t* scales = row_scales(a, r, chunks);
-  auto emit = [&](int v, const Vec<TYPE>& x) {  // whole warps; a block's lanes are all below `vecs` or all not
-    uint32_t m = mag8<TYPE>(x);
+  // this lane's places of vector t; one of TPR vectors further is whole chunks further
+  constexpr int kScaleStep = TPR / kLanesPerBlock / 4 * 512;
+  const int block = t / kLanesPerBlock;
+  codes += t * 8;
+  uint8_t* scale_at = scales + (block >> 2) * 512 + (block & 3);
+  const bool scale_lane = lane % kLanesPerBlock == 0;
+  auto emit = [&](int i, const Vec<TYPE>& x, bool on) {  // whole warps; a block's lanes are all on or all off
+    uint32_t m = mag_vec<TYPE>(x);
 #pragma unroll
     for (int o = 1; o < kLanesPerBlock; o <<= 1) m = max_mag<TYPE>(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     uint32_t sc;
-    const uint32_t w = encode8<F, TYPE>(x, mag_bits<TYPE>(m), nv, sc);
-    if (v < vecs) {
-      *reinterpret_cast<uint32_t*>(codes + v * 4) = w;
-      const int block = v / kLanesPerBlock;
-      if (lane % kLanesPerBlock == 0) scales[(block >> 2) * 512 + (block & 3)] = static_cast<uint8_t>(sc);
+    const uint2 w = encode<F, TYPE>(x, mag_bits<TYPE>(m), nv, sc);
+    if (on) {
+      *reinterpret_cast<uint2*>(codes + i * (TPR * 8)) = w;
+      if (scale_lane) scale_at[i * kScaleStep] = static_cast<uint8_t>(sc);
     }
   };
   const int w0 = t & ~31;  // the warp's first vector of a round
 #pragma unroll
   for (int i = 0; i < kHold; ++i)
-    if (i * TPR + w0 < vecs) emit(t + i * TPR, held[i]);
+    if (i * TPR + w0 < vecs) emit(i, held[i], t + i * TPR < vecs);
   for (int v0 = kHold * TPR; v0 + w0 < vecs; v0 += kHold * TPR) {
+    codes += kHold * TPR * 8;
+    scale_at += kHold * kScaleStep;
 #pragma unroll
     for (int i = 0; i < kHold; ++i) {
       if (v0 + t + i * TPR < vecs)
-        load8<TYPE>(src, v0 + t + i * TPR, held[i]);
+        load_vec<TYPE>(src, v0 + t + i * TPR, held[i]);
       else
-        zero8<TYPE>(held[i]);
+        zero_vec<TYPE>(held[i]);
     }
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
-      if (v0 + i * TPR + w0 < vecs) emit(v0 + t + i * TPR, held[i]);
+      if (v0 + i * TPR + w0 < vecs) emit(i, held[i], v0 + t + i * TPR < vecs);
   }
   // blocks of the last chunk past K: zero scales
   const int blocks = a.K / fp4_block(F);
@@ -334,20 +387,21 @@ __global__ void __launch_bounds__(kThreads) fp4_group_amax_kernel(const __grid_c
   const int lane = threadIdx.x & 31;
   const int64_t p64 = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   if (p64 >= a.rows) return;
-  const int p = static_cast<int>(p64), vecs = a.K / 8;
+  const int p = static_cast<int>(p64), vecs = a.K / kElems;
   const char* src = static_cast<const char*>(a.src) + p * a.ld * (TYPE == 2 ? 4 : 2);
+  constexpr int kHold = hold_of(TYPE);
   uint32_t m = 0;
   for (int v0 = 0; v0 < vecs; v0 += kHold * 32) {
     Vec<TYPE> held[kHold];
 #pragma unroll
     for (int i = 0; i < kHold; ++i) {
       if (v0 + i * 32 + lane < vecs)
-        load8<TYPE>(src, v0 + i * 32 + lane, held[i]);
+        load_vec<TYPE>(src, v0 + i * 32 + lane, held[i]);
       else
-        zero8<TYPE>(held[i]);
+        zero_vec<TYPE>(held[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) m = max_mag<TYPE>(m, mag8<TYPE>(held[i]));
+    for (int i = 0; i < kHold; ++i) m = max_mag<TYPE>(m, mag_vec<TYPE>(held[i]));
   }
   m = __reduce_max_sync(0xFFFFFFFFu, mag_bits<TYPE>(m));
   const RowPlace r = place_of(a, p, lane);
@@ -360,73 +414,78 @@ __global__ void fp4_group_scale_kernel(float* gscale, int n) {
   if (i < n) gscale[i] = nv_global(__float_as_uint(gscale[i]));
 }
 
-// eight codes -> their values
-__device__ __forceinline__ void decode8(uint32_t w, float (&f)[8]) {
-  uint32_t h[4];
+// four codes (16 bits) -> their values
+__device__ __forceinline__ void decode4(uint32_t w, float* f) {
+  uint32_t h[2];
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %2;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t}"
+      : "=r"(h[0]), "=r"(h[1])
       : "r"(w));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
     f[2 * i] = v.x;
     f[2 * i + 1] = v.y;
   }
 }
 
+// A thread writes 16 bytes at a time (8 elements of 16 bits or 4 of 32), so a
+// warp's stores are contiguous; kAhead of them per round, their loads first.
 template <Fp4Format F, int TYPE, int TPR>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const __grid_constant__ Fp4RowsArgs a) {
+  constexpr int kVec = TYPE == 2 ? 4 : 8, kAhead = 8;
   const int lane = threadIdx.x & 31, t = threadIdx.x % TPR;
   const int64_t p64 = static_cast<int64_t>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
   if (p64 >= a.rows) return;
   const int p = static_cast<int>(p64);
-  const int vecs = a.K / 8, chunks = (a.K + fp4_chunk(F) - 1) / fp4_chunk(F);
-  const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes + static_cast<size_t>(p) * (a.K / 2));
-  uint32_t w[kHold];
+  const int vecs = a.K / kVec, chunks = (a.K + fp4_chunk(F) - 1) / fp4_chunk(F);
+  const uint8_t* codes = a.codes + static_cast<size_t>(p) * (a.K / 2);
+  auto load = [&](int v) -> uint32_t {
+    if (v >= vecs) return 0u;
+    return kVec == 8 ? __ldcs(reinterpret_cast<const uint32_t*>(codes) + v)
+                     : static_cast<uint32_t>(__ldcs(reinterpret_cast<const unsigned short*>(codes) + v));
+  };
+  uint32_t w[kAhead];
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) w[i] = t + i * TPR < vecs ? __ldcs(codes + t + i * TPR) : 0u;
+  for (int i = 0; i < kAhead; ++i) w[i] = load(t + i * TPR);
   const RowPlace r = place_of(a, p, lane);
   if (!r.on) return;
   const uint8_t* scales = row_scales(a, r, chunks);
-  char* dst = static_cast<char*>(a.dst) + p * a.ld * (TYPE == 2 ? 4 : 2);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(a.dst) + p * a.ld * (TYPE == 2 ? 4 : 2));
   const float g = F == Fp4Format::kNv ? __ldg(a.gscale + (a.per_group ? r.group : p)) : 1.0f;
-  for (int v0 = 0; v0 < vecs; v0 += kHold * TPR) {
-    uint32_t sc[kHold];
+  for (int v0 = 0; v0 < vecs; v0 += kAhead * TPR) {
+    uint32_t sc[kAhead];
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      const int v = v0 + t + i * TPR, block = v / (fp4_block(F) / 8);
-      if (v0 > 0) w[i] = v < vecs ? __ldcs(codes + v) : 0u;
+    for (int i = 0; i < kAhead; ++i) {
+      const int v = v0 + t + i * TPR, block = v / (fp4_block(F) / kVec);
+      if (v0 > 0) w[i] = load(v);
       sc[i] = v < vecs ? __ldg(scales + (block >> 2) * 512 + (block & 3)) : 0u;
     }
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       const int v = v0 + t + i * TPR;
       if (v >= vecs) break;
       float f[8];
-      decode8(w[i], f);
+      decode4(w[i], f);
+      if (kVec == 8) decode4(w[i] >> 16, f + 4);
       if constexpr (F == Fp4Format::kMx) {
         // 2^(sc - 127); the smallest is subnormal, 255 stands for NaN
         const float s =
             sc[i] == 255u ? __uint_as_float(0x7FC00000u) : sc[i] ? __uint_as_float(sc[i] << 23) : 0x1p-127f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], s);
+        for (int j = 0; j < kVec; ++j) f[j] = __fmul_rn(f[j], s);
       } else {
         const float s = e4m3_to(sc[i]);  // times a code: exact
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], s), g);
+        for (int j = 0; j < kVec; ++j) f[j] = __fmul_rn(__fmul_rn(f[j], s), g);
       }
-      if constexpr (TYPE == 2) {
-        float4* o = reinterpret_cast<float4*>(dst) + 2 * v;
-        __stcs(o, make_float4(f[0], f[1], f[2], f[3]));
-        __stcs(o + 1, make_float4(f[4], f[5], f[6], f[7]));
-      } else {
-        __stcs(reinterpret_cast<uint4*>(dst) + v, pack8<TYPE == 1>(f));
-      }
+      if constexpr (TYPE == 2)
+        __stcs(dst + v, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                   __float_as_uint(f[3])));
+      else
+        __stcs(dst + v, pack8<TYPE == 1>(f));
     }
   }
 }
@@ -438,10 +497,9 @@ cudaError_t quantize_t(const Fp4RowsArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Threads per row.  Where a row's vectors have to be held at once (NVFP4's
-// scale per row), as many as hold them, up to 8192 elements.  Else a warp per row, whose look-up of the
-// row's place then serves most elements, unless there are too few rows to fill
-// the GPU with warps.
+// Threads per row.  Few rows: as many as spread a row over the GPU's warps best.
+// Many: as few as hold a row's vectors at once where they have to (NVFP4's scale
+// per row), else a warp, so that the look-up of the row's place serves most elements.
 template <Fp4Format F, int TYPE>
 cudaError_t quantize(const Fp4RowsArgs& a, cudaStream_t stream) {
   const bool whole = F == Fp4Format::kNv && !a.per_group;
@@ -451,11 +509,15 @@ cudaError_t quantize(const Fp4RowsArgs& a, cudaStream_t stream) {
     fp4_group_amax_kernel<TYPE><<<static_cast<unsigned>((a.rows + 7) / 8), kThreads, 0, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const int vecs = a.K / 8;
-  const cudaError_t e = vecs <= 32 * kHold || (!whole && a.rows >= 8192) ? quantize_t<F, TYPE, 32>(a, stream)
-                        : vecs <= 64 * kHold                             ? quantize_t<F, TYPE, 64>(a, stream)
-                        : vecs <= 128 * kHold                            ? quantize_t<F, TYPE, 128>(a, stream)
-                                                                         : quantize_t<F, TYPE, 256>(a, stream);
+  const int vecs = a.K / kElems;
+  constexpr int kHold = hold_of(TYPE);
+  const bool many = a.rows >= 8192;
+  // vectors a thread is to hold: all of kHold, or two
+  const int per = many ? kHold : 1;
+  const cudaError_t e = vecs <= 32 * per || (!whole && many) ? quantize_t<F, TYPE, 32>(a, stream)
+                        : vecs <= 64 * per                   ? quantize_t<F, TYPE, 64>(a, stream)
+                        : vecs <= 128 * per                  ? quantize_t<F, TYPE, 128>(a, stream)
+                                                             : quantize_t<F, TYPE, 256>(a, stream);
   if (e != cudaSuccess || F != Fp4Format::kNv || !a.per_group) return e;
   fp4_group_scale_kernel<<<(a.G + 127) / 128, 128, 0, stream>>>(a.gscale, a.G);
   return cudaGetLastError();
@@ -470,8 +532,9 @@ cudaError_t dequantize_t(const Fp4RowsArgs& a, cudaStream_t stream) {
 
 template <Fp4Format F, int TYPE>
 cudaError_t dequantize(const Fp4RowsArgs& a, cudaStream_t stream) {
-  if (a.K <= 32 * 8 * kHold || a.rows >= 8192) return dequantize_t<F, TYPE, 32>(a, stream);
-  return a.K <= 128 * 8 * kHold ? dequantize_t<F, TYPE, 128>(a, stream) : dequantize_t<F, TYPE, 256>(a, stream);
+  const int vecs = a.K / (TYPE == 2 ? 4 : 8), per = a.rows >= 8192 ? 8 : 2;
+  if (vecs <= 32 * per || a.rows >= 8192) return dequantize_t<F, TYPE, 32>(a, stream);
+  return vecs <= 128 * per ? dequantize_t<F, TYPE, 128>(a, stream) : dequantize_t<F, TYPE, 256>(a, stream);
 }
 
 }  // namespace
