@@ -454,25 +454,26 @@ def _type_of(dtype) -> int:
 
 def _check(what, t, device, dtype, shape_, rows=False):
     """A tensor argument: its device, type and shape; contiguous, or (rows) rows of contiguous elements."""
+    if t.dtype == dtype and t.shape == shape_ and t.device == device and (
+            t.is_contiguous() or (rows and (t.stride(-1) == 1 or t.shape[-1] == 1))):
+        return t
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, not on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{what} is {t.dtype}, not {dtype}")
     if t.shape != shape_:
         raise ValueError(f"{what} is {tuple(t.shape)}, not {tuple(shape_)}")
-    if not (t.stride(-1) == 1 or t.shape[-1] == 1) if rows else not t.is_contiguous():
-        raise ValueError(f"{what} is not contiguous" + (" along its rows" if rows else ""))
-    return t
+    raise ValueError(f"{what} is not contiguous" + (" along its rows" if rows else ""))
 
 
 def _lists(of, offsets, counts):
     """The row lists of an object with ``groups`` and ``device``, as pointers."""
     import torch
     if offsets is not None:
-        _check("offsets", offsets, of.device, torch.int32, (of.groups + 1,))
+        offsets = _check("offsets", offsets, of.device, torch.int32, (of.groups + 1,)).data_ptr()
     if counts is not None:
-        _check("counts", counts, of.device, torch.int32, (of.groups,))
-    return _ptr(offsets), _ptr(counts)
+        counts = _check("counts", counts, of.device, torch.int32, (of.groups,)).data_ptr()
+    return offsets, counts
 
 
 def _ld(t) -> int:
@@ -482,12 +483,13 @@ def _ld(t) -> int:
 
 def _enqueue(name, device, fn, *args):
     """fn(*args, stream) with ``device`` current, on its current stream; MoeError if it fails."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    from torch import _C, cuda
+    index = device.index
+    if _C._cuda_getDevice() == index:  # (the tensors exist: CUDA is initialised)
+        st = fn(*args, _C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+        with cuda.device(device):
+            st = fn(*args, _C._cuda_getCurrentRawStream(index))
     if st != MOE_OK:
         raise MoeError(st, name)
 
@@ -533,13 +535,17 @@ class GroupedProducts:
         import torch
         self.groups, self.N, self.K, self.dtype = int(groups), int(N), int(K), dtype
         self.device = torch.empty(0, device=device or "cuda").device
+        self._shape = None
         st, n = moe_grouped_workspace_size(self.shape(max_rows))
         if st != MOE_OK:
             raise MoeError(st, "moe_grouped_workspace_size")
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def shape(self, rows) -> MoeGroupedShape:
-        return grouped_shape(self.groups, self.N, self.K, rows, _type_of(self.dtype))
+        s = self._shape  # (kept by one assignment: other host threads may ask too)
+        if s is None or s.rows != rows:
+            s = self._shape = grouped_shape(self.groups, self.N, self.K, rows, _type_of(self.dtype))
+        return s
 
     def _rows(self, what, t, rows, width):
         if t is None:
@@ -548,7 +554,7 @@ class GroupedProducts:
         return _check(what, t, self.device, self.dtype, (rows, width), rows=True)
 
     def _call(self, name, fn, *args):
-        _enqueue(name, self.device, fn, *args, _ptr(self.workspace), self.workspace.numel())
+        _enqueue(name, self.device, fn, *args, self.workspace.data_ptr(), self.workspace.numel())
 
     def forward(self, x, w, offsets=None, counts=None, y=None):
         """y[p] = x[p] w_g^T for the rows p of every group g; other rows of y stay as they are."""
