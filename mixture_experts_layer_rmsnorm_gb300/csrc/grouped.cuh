@@ -8,6 +8,8 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -90,6 +92,24 @@ cudaError_t launch_grouped_pair(GroupedOp op, const CUtensorMap& tm_w, const CUt
 cudaError_t launch_grouped_wgrad(const CUtensorMap& tm_dw, const GroupedGemmArgs& a, cudaStream_t stream);
 
 #ifdef __CUDACC__
+
+// Two fp32 values rounded to 16 bits, `lo` in the low half.
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
+  if (fp16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A lane's word holds one feature (its lane's) of rows c and c + 1.  Neighbouring
+// lanes trade halves: the even lane gets both features of row c, the odd
+// one those of row c + 1, so that each stores 4 bytes of one row (whole warp).
+__device__ __forceinline__ uint32_t trade_rows(uint32_t word) {
+  const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, word, 1);
+  return __byte_perm(word, other, (threadIdx.x & 1) ? 0x3276 : 0x5410);
+}
 
 struct GroupedUnit {
   int g, tile, tile_n, tok0, n, start, count;

@@ -456,6 +456,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
         }
       };
       if constexpr (PAIR) {
+        const int odd = lane & 1;
         uint32_t packed[kCols / 2];
 #pragma unroll
         for (int c0 = 0; c0 < kCols; c0 += 32) {
@@ -471,18 +472,17 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
                 v0 = __fmul_rn(v0, gx[c0 + j]);
                 v1 = __fmul_rn(v1, gx[c0 + j + 1]);
               }
-              packed[(c0 + j) / 2] = static_cast<uint32_t>(to16(v0, fp16)) | (static_cast<uint32_t>(to16(v1, fp16)) << 16);
+              packed[(c0 + j) / 2] = pack16(v0, v1, fp16);
             }
           }
         }
         release();
-        if (mine) {
-          uint16_t* o = out + static_cast<int64_t>(col0) * a.ldo;
+        // this lane's two features, of its row of each pair of rows (F is even: a pair of lanes alike)
+        uint16_t* o = out + static_cast<int64_t>(col0 + odd) * a.ldo - odd;
 #pragma unroll
-          for (int c = 0; c < kCols; c += 2) {
-            if (col0 + c < un.n) o[static_cast<int64_t>(c) * a.ldo] = static_cast<uint16_t>(packed[c / 2]);
-            if (col0 + c + 1 < un.n) o[static_cast<int64_t>(c + 1) * a.ldo] = static_cast<uint16_t>(packed[c / 2] >> 16);
-          }
+        for (int c = 0; c < kCols; c += 2) {
+          const uint32_t v = trade_rows(packed[c / 2]);
+          if (mine && col0 + c + odd < un.n) *reinterpret_cast<uint32_t*>(o + static_cast<int64_t>(c) * a.ldo) = v;
         }
       } else if (kb0 > 0) {
         // a later part of a unit that an earlier CTA started: hand over the partial sums

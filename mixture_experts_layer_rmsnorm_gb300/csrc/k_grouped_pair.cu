@@ -54,10 +54,6 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
 enum : int { kWaitSlotFree = 1, kWaitAccFree = 2, kWaitSlotFull = 3, kWaitAccFull = 4, kWaitUnit = 10 };
 
-__device__ __forceinline__ uint16_t to16(float v, bool fp16) {
-  return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
 // A unit's size: MMA columns in all and of its first MMA, rows per CTA, rows
 // loaded (boxes of 128 and of 32), bytes of a stage.
 struct Size {
@@ -311,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, turn = (warp - 2) >> 2;
     const int row = q * 32 + lane;  // feature of this CTA's 128
     const bool fp16 = a.fp16 != 0;
+    const int odd = lane & 1;
     const uint32_t tempty_cl = mapa_shared(smem_u32(tempty), 0);
     bool ok = true;
     uint32_t uses = 0;
@@ -318,8 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const GroupedUnit un = units.at(u);
       const Size z(un.n);
       const int feat = un.tile * 256 + static_cast<int>(rank) * 128 + row;
-      const bool mine = feat < a.F;
-      uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(un.tok0) * a.ldo + feat;
+      const bool mine = feat < a.F;  // (F is even: a pair of lanes alike)
+      // this lane's two features, of its row of each pair of rows
+      uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(un.tok0 + odd) * a.ldo + (feat & ~1);
       const int parts = z.cols > z.cols0 ? 2 : 1;
       for (int j = 0; j < parts; ++j) {
         const uint32_t buf = uses & 1;
@@ -338,21 +336,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();  // tcgen05.ld is warp-aligned: the stores before it are not
           tmem_ld_32x32b_x32(t_row + c0, r);
           tmem_ld_wait();
-          if (mine) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {  // 8 columns: rows of one half
-              const int c = c0 + 8 * h;
-              const int t = c < cols / 2 ? before + c : z.half + before + c - cols / 2;
-              uint16_t* o = out + static_cast<int64_t>(t) * a.ldo;
-              const int left = c < cols ? un.n - t : 0;
-              if (left >= 8) {
+          for (int h = 0; h < 4; ++h) {  // 8 columns: rows of one half
+            const int c = c0 + 8 * h;
+            const int t = c < cols / 2 ? before + c : z.half + before + c - cols / 2;
+            const int left = c < cols ? un.n - t : 0;
+            uint16_t* o = out + static_cast<int64_t>(t) * a.ldo;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[static_cast<int64_t>(i) * a.ldo] = to16(__uint_as_float(r[8 * h + i]), fp16);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (i < left) o[static_cast<int64_t>(i) * a.ldo] = to16(__uint_as_float(r[8 * h + i]), fp16);
-              }
+            for (int i = 0; i < 8; i += 2) {
+              const uint32_t v = trade_rows(pack16(__uint_as_float(r[8 * h + i]), __uint_as_float(r[8 * h + i + 1]), fp16));
+              if (mine && i + odd < left) *reinterpret_cast<uint32_t*>(o + static_cast<int64_t>(i) * a.ldo) = v;
             }
           }
         }

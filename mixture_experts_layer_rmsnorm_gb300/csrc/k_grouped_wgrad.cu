@@ -49,16 +49,6 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
 enum : int { kWaitSlotFree = 1, kWaitAccFree = 2, kWaitSlotFull = 3, kWaitAccFull = 4 };
 
-__device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi, bool fp16) {
-  const float a = __uint_as_float(lo), b = __uint_as_float(hi);
-  if (fp16) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tm_dw, const __grid_constant__ GroupedGemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -258,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_32x32b_x32(t_row + c0 + 32 * h, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[16 * h + j] = pack16(r[2 * j], r[2 * j + 1], fp16);
+            for (int j = 0; j < 16; ++j) w[16 * h + j] = pack16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), fp16);
           }
         }
 #pragma unroll
