@@ -466,13 +466,15 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
             tmem_ld_32x32b_x32(t_row + col0 + c0, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              float v0 = __uint_as_float(r[j]), v1 = __uint_as_float(r[j + 1]);
+            for (int j = 0; j < 32; j += 4) {
+              float4 v = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
+                                     __uint_as_float(r[j + 3]));
               if (F == Fp4Format::kNv) {
-                v0 = __fmul_rn(v0, gx[c0 + j]);
-                v1 = __fmul_rn(v1, gx[c0 + j + 1]);
+                const float4 s = *reinterpret_cast<const float4*>(gx + c0 + j);
+                v = make_float4(__fmul_rn(v.x, s.x), __fmul_rn(v.y, s.y), __fmul_rn(v.z, s.z), __fmul_rn(v.w, s.w));
               }
-              packed[(c0 + j) / 2] = pack16(v0, v1, fp16);
+              packed[(c0 + j) / 2] = pack16(v.x, v.y, fp16);
+              packed[(c0 + j) / 2 + 1] = pack16(v.z, v.w, fp16);
             }
           }
         }
