@@ -72,6 +72,7 @@ CASES = {
     "large_skewed": ([1500, 1, 0, 2, 40], 256, 128, BF16, 1, 0, 0),
     "many_groups": ([(7 * i) % 5 for i in range(300)], 136, 72, BF16, 0, 2, 0),
     "most_groups": ([(i * i) % 41 for i in range(1024)], 64, 64, FP16, 0, 0, 0),
+    "long_groups": ([2500, 0, 769, 768, 1537], 264, 136, BF16, 0, 1, 0),
     "no_rows_at_all": ([0, 0, 0], 128, 64, BF16, 0, 4, 0),
 }
 
@@ -126,7 +127,22 @@ def test_weight_gradient(name, out):
         want, s = dd.T @ xd, dd.abs().T @ xd.abs()
         if out == "accumulate":  # one fp32 addition more
             want, s = want + start[g].double(), s + start[g].abs().double()
-        check(dw[g], want, s, b - a)
+        # into fp32 at most 768 rows are accumulated by the tensor core, then added in fp32 (one of the 256 roundings each)
+        check(dw[g], want, s, b - a if out == "same" else min(b - a, 768))
+
+
+def test_long_sums_into_fp32_keep_their_precision():
+    """The tensor core cuts towards zero once a step: unsplit, 16384 rows of one sign lose some 1e-4.  Split, a segment of
+    768 rows takes 48 steps, each cutting less than a unit in the last place of the accumulator, 2^-23 of it, by its own
+    sum and, on average over the 16 products' random bits below it, half a unit for each product: 48 (1 + 16 / 2) 2^-23
+    = 5.2e-5 of the sum at most, and the segments' own additions 22 2^-24."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.rand((16384, 136), generator=gen, device="cuda").to(BF16)
+    dy = torch.rand((16384, 264), generator=gen, device="cuda").to(BF16)
+    gp = binding.GroupedProducts(1, 264, 136, BF16)
+    want = dy.double().T @ x.double()
+    rel = ((gp.wgrad(dy, x, dtype=FP32)[0].double() - want) / want).abs().max().item()
+    assert rel <= 48 * 9 * 2.0 ** -23 + 22 * 2.0 ** -24, rel
 
 
 def test_equal_groups_without_lists():
