@@ -468,11 +468,10 @@ def _check(what, t, device, dtype, shape_, rows=False):
 
 def _lists(of, offsets, counts):
     """The row lists of an object with ``groups`` and ``device``, as pointers."""
-    import torch
     if offsets is not None:
-        offsets = _check("offsets", offsets, of.device, torch.int32, (of.groups + 1,)).data_ptr()
+        offsets = _check("offsets", offsets, of.device, of.int32, (of.groups + 1,)).data_ptr()
     if counts is not None:
-        counts = _check("counts", counts, of.device, torch.int32, (of.groups,)).data_ptr()
+        counts = _check("counts", counts, of.device, of.int32, (of.groups,)).data_ptr()
     return offsets, counts
 
 
@@ -481,13 +480,20 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
 
 
+_C = None  # torch's native module, once it is needed
+
+
 def _enqueue(name, device, fn, *args):
     """fn(*args, stream) with ``device`` current, on its current stream; MoeError if it fails."""
-    from torch import _C, cuda
+    global _C
+    if _C is None:
+        from torch import _C as native
+        _C = native
     index = device.index
     if _C._cuda_getDevice() == index:  # (the tensors exist: CUDA is initialised)
         st = fn(*args, _C._cuda_getCurrentRawStream(index))
     else:
+        from torch import cuda
         with cuda.device(device):
             st = fn(*args, _C._cuda_getCurrentRawStream(index))
     if st != MOE_OK:
@@ -496,10 +502,10 @@ def _enqueue(name, device, fn, *args):
 
 def swiglu(h, act=None):
     """SiLU(gate) * up of rows h = [gate | up] (moe_swiglu), on the current stream of h's device."""
-    import torch
     rows, two_i = h.shape
     _check("h", h, h.device, h.dtype, h.shape, rows=True)
     if act is None:
+        import torch
         act = torch.empty((rows, two_i // 2), dtype=h.dtype, device=h.device)
     else:
         _check("act", act, h.device, h.dtype, (rows, two_i // 2), rows=True)
@@ -510,11 +516,11 @@ def swiglu(h, act=None):
 
 def swiglu_grad(h, dact, dh=None):
     """d[gate | up] from dact (moe_swiglu_grad), on the current stream of h's device."""
-    import torch
     rows, two_i = h.shape
     _check("h", h, h.device, h.dtype, h.shape, rows=True)
     _check("dact", dact, h.device, h.dtype, (rows, two_i // 2), rows=True)
     if dh is None:
+        import torch
         dh = torch.empty((rows, two_i), dtype=h.dtype, device=h.device)
     else:
         _check("dh", dh, h.device, h.dtype, (rows, two_i), rows=True)
@@ -535,7 +541,7 @@ class GroupedProducts:
         import torch
         self.groups, self.N, self.K, self.dtype = int(groups), int(N), int(K), dtype
         self.device = torch.empty(0, device=device or "cuda").device
-        self._shape = None
+        self._shape, self.int32 = None, torch.int32
         st, n = moe_grouped_workspace_size(self.shape(max_rows))
         if st != MOE_OK:
             raise MoeError(st, "moe_grouped_workspace_size")
@@ -579,13 +585,13 @@ class GroupedProducts:
     def wgrad(self, dy, x, offsets=None, counts=None, dw=None, dtype=None, accumulate=False):
         """dw_g = sum over the group's rows of dy[p]^T x[p], in ``dtype`` (fp32 or the operands' type, the default)
         or dw's type; accumulate (fp32): added to dw."""
-        import torch
         rows = x.shape[0]
         self._rows("dy", dy, rows, self.N)
         self._rows("x", x, rows, self.K)
         if dw is None:
             if accumulate:
                 raise ValueError("accumulate adds to dw: pass it")
+            import torch
             dw = torch.empty((self.groups, self.N, self.K), dtype=dtype or self.dtype, device=self.device)
         else:
             _check("dw", dw, self.device, dtype or dw.dtype, (self.groups, self.N, self.K))
@@ -618,17 +624,21 @@ class Fp4Rows:
     def __init__(self, format, K, groups=1, max_rows=0, device=None):
         import torch
         self.format, self.K, self.groups = _format_of(format), int(K), int(groups)
-        self.device = torch.empty(0, device=device or "cuda").device
+        self.device, self.int32 = torch.empty(0, device=device or "cuda").device, torch.int32
         self.rows = self.max_rows = 0
+        self._shape = None
         self.ensure_capacity(max_rows)
 
     def shape(self, rows) -> MoeFp4Shape:
-        return fp4_shape(self.format, self.groups, rows, self.K)
+        s = self._shape  # (kept by one assignment: other host threads may ask too)
+        if s is None or s.rows != rows:
+            s = self._shape = fp4_shape(self.format, self.groups, rows, self.K)
+        return s
 
     def ensure_capacity(self, rows):
-        import torch
         if rows <= self.max_rows and self.max_rows > 0:
             return
+        import torch
         st, (n_codes, n_scales) = moe_fp4_sizes(self.shape(max(rows, 1)))
         if st != MOE_OK:
             raise MoeError(st, "moe_fp4_sizes")
@@ -640,7 +650,6 @@ class Fp4Rows:
 
     def quantize(self, x, offsets=None, counts=None):
         """x [rows, K] (bf16, fp16 or fp32) to 4 bits; returns self."""
-        import torch
         self.ensure_capacity(x.shape[0])
         _check("x", x, self.device, x.dtype, (x.shape[0], self.K), rows=True)
         lists = _lists(self, offsets, counts)
@@ -651,8 +660,8 @@ class Fp4Rows:
 
     def dequantize(self, offsets=None, counts=None, y=None, dtype=None):
         """The values of the rows quantized last, in ``dtype`` (bf16 by default) or y's type."""
-        import torch
         if y is None:
+            import torch
             y = torch.empty((self.rows, self.K), dtype=dtype or torch.bfloat16, device=self.device)
         else:
             _check("y", y, self.device, dtype or y.dtype, (self.rows, self.K), rows=True)
@@ -671,7 +680,7 @@ class Fp4Weights:
         import torch
         self.format = _format_of(format)
         self.groups, self.N, half = codes.shape
-        self.K, self.device = 2 * half, codes.device
+        self.K, self.device, self.int32 = 2 * half, codes.device, torch.int32
         st, (_, n_scales) = moe_fp4_sizes(fp4_shape(self.format, self.groups, self.groups * self.N, self.K))
         if st != MOE_OK:
             raise MoeError(st, "moe_fp4_sizes")
@@ -720,10 +729,10 @@ class Fp4Weights:
 
     def forward(self, rows: Fp4Rows, offsets=None, counts=None, y=None, dtype=None):
         """y[p] = x[p] w_g^T in ``dtype`` (bf16 by default, or fp16) or y's type; rows: x quantized for the same lists."""
-        import torch
         if rows.format != self.format or rows.K != self.K or rows.groups != self.groups or rows.device != self.device:
             raise ValueError("rows of another format, K, number of groups or device")
         if y is None:
+            import torch
             y = torch.empty((rows.rows, self.N), dtype=dtype or torch.bfloat16, device=self.device)
         else:
             _check("y", y, self.device, dtype or y.dtype, (rows.rows, self.N), rows=True)

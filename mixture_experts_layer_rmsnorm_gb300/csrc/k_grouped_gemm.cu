@@ -40,36 +40,50 @@ using namespace ptx;
 
 // ------------------------------------------------------------------ plan
 
+// Latency alone counts here (the GEMM waits for the tables): every load first,
+// what does not depend on them next, two barriers.
 __global__ void __launch_bounds__(kGroupsMax, 1)
     grouped_plan_kernel(const __grid_constant__ GroupedPlanArgs a, const __grid_constant__ CUtensorMap tm_dy,
                         const __grid_constant__ CUtensorMap tm_x) {
   __shared__ int warp_sum[32];
-  __shared__ int bad;
+  __shared__ int first_bad;
   pdl_launch_dependents();  // the GEMM sets up its barriers and TMEM meanwhile
   const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
-  if (g == 0) bad = 0;
-  for (int i = g; i < a.n_flags; i += blockDim.x) a.flags[i] = 0;
-  __syncthreads();
-  int64_t s = 0, c = 0;
+  int64_t s = 0, c = 0, end = 0;  // end: where the next group may begin
   if (g < a.G) {
-    int64_t end;  // where the next group may begin
     if (a.offsets) {
-      s = a.offsets[g];
-      end = a.offsets[g + 1];
-      c = a.counts ? a.counts[g] : end - s;
+      s = __ldg(a.offsets + g);
+      end = __ldg(a.offsets + g + 1);
     } else {
       c = a.rows / a.G;
       s = g * c;
       end = s + c;
-      if (a.counts) c = a.counts[g];
     }
-    if (s < 0 || c < 0 || s + c > end || end > a.rows) atomicMax(&bad, g + 1);
+    c = a.counts ? __ldg(a.counts + g) : end - s;
   }
-  __syncthreads();
-  const int bad_group = bad;
-  if (bad_group) s = c = 0;
+  for (int i = g; i < a.n_flags; i += blockDim.x) a.flags[i] = 0;
+  if (g == 0) first_bad = kGroupsMax;
+  const bool bad = s < 0 || c < 0 || s + c > end || end > a.rows;
+  const bool any_bad = __syncthreads_or(bad) != 0;
+  if (any_bad) {  // (uniform) no group has rows or units then
+    if (bad) atomicMin(&first_bad, g);
+    __syncthreads();
+    s = c = 0;
+  }
+  if (a.maps && g < a.G) {
+    const uint32_t rows_end = s + c > 0 ? static_cast<uint32_t>(s + c) : 1u;  // (an empty group loads nothing)
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      uint4* dst = reinterpret_cast<uint4*>(a.maps + 2 * g + m);
+      const uint4* src = reinterpret_cast<const uint4*>(m ? &tm_x : &tm_dy);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dst[i] = src[i];
+      tensormap_set_dim1(dst, rows_end);
+    }
+    tensormap_release();
+  }
   int units = 0;
-  if (g < a.G && !bad_group) {
+  if (g < a.G && !any_bad) {
     if (a.bn > 0)
       units = static_cast<int>((c + a.bn - 1) / a.bn) * a.tiles;
     else
@@ -83,39 +97,21 @@ __global__ void __launch_bounds__(kGroupsMax, 1)
   }
   if (lane == 31) warp_sum[warp] = sum;
   __syncthreads();
-  if (warp == 0) {
-    int v = lane < static_cast<int>(blockDim.x >> 5) ? warp_sum[lane] : 0;
+  // the sum of the warps before this one
+  int before = lane < warp ? warp_sum[lane] : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-      if (lane >= d) v += o;
-    }
-    warp_sum[lane] = v;
-  }
-  __syncthreads();
-  if (warp > 0) sum += warp_sum[warp - 1];
+  for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
+  sum += before;
   if (g < a.G) {
     a.start[g] = static_cast<int32_t>(s);
     a.count[g] = static_cast<int32_t>(c);
     a.unit_off[g] = sum - units;
     if (g == a.G - 1) a.unit_off[a.G] = sum;
-    if (a.maps) {
-      const uint32_t end = s + c > 0 ? static_cast<uint32_t>(s + c) : 1u;  // (an empty group loads nothing)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint4* dst = reinterpret_cast<uint4*>(a.maps + 2 * g + m);
-        const uint4* src = reinterpret_cast<const uint4*>(m ? &tm_x : &tm_dy);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = src[i];
-        tensormap_set_dim1(dst, end);
-      }
-      tensormap_release();
-    }
   }
   if (g == 0) {
-    a.err[0] = bad_group ? kErrDevice : 0;
-    a.err[1] = bad_group ? kKernGroupedPlan : 0;
-    a.err[2] = bad_group ? bad_group - 1 : 0;
+    a.err[0] = any_bad ? kErrDevice : 0;
+    a.err[1] = any_bad ? kKernGroupedPlan : 0;
+    a.err[2] = any_bad ? first_bad : 0;
     a.err[3] = 0;
   }
 }
