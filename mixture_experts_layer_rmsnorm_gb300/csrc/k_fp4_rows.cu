@@ -28,6 +28,7 @@
 
 #include "fp4.cuh"
 #include "grouped_elementwise.cuh"
+#include "pdl.cuh"
 
 namespace moe {
 namespace {
@@ -282,6 +283,8 @@ __device__ __forceinline__ uint2 encode(const Vec<TYPE>& v, uint32_t amax, const
 template <Fp4Format F, int TYPE, int TPR>
 __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_constant__ Fp4RowsArgs a) {
   constexpr int kRows = kThreads / TPR, kWarpsPerRow = TPR / 32;
+  pdl_wait();
+  pdl_launch_dependents();
   __shared__ uint32_t warp_max[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = threadIdx.x % TPR;
@@ -384,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_
 // Largest magnitude of every group's rows into gscale's bits (zero before).
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads) fp4_group_amax_kernel(const __grid_constant__ Fp4RowsArgs a) {
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t p64 = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   if (p64 >= a.rows) return;
@@ -410,6 +414,8 @@ __global__ void __launch_bounds__(kThreads) fp4_group_amax_kernel(const __grid_c
 
 // maxima -> scales, in place
 __global__ void fp4_group_scale_kernel(float* gscale, int n) {
+  pdl_wait();
+  pdl_launch_dependents();
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i < n) gscale[i] = nv_global(__float_as_uint(gscale[i]));
 }
@@ -436,6 +442,8 @@ __device__ __forceinline__ void decode4(uint32_t w, float* f) {
 template <Fp4Format F, int TYPE, int TPR>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const __grid_constant__ Fp4RowsArgs a) {
   constexpr int kVec = TYPE == 2 ? 4 : 8, kAhead = 8;
+  pdl_wait();
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31, t = threadIdx.x % TPR;
   const int64_t p64 = static_cast<int64_t>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
   if (p64 >= a.rows) return;
@@ -493,8 +501,8 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const __grid_c
 template <Fp4Format F, int TYPE, int TPR>
 cudaError_t quantize_t(const Fp4RowsArgs& a, cudaStream_t stream) {
   constexpr int rows = kThreads / TPR;
-  fp4_quantize_kernel<F, TYPE, TPR><<<static_cast<unsigned>((a.rows + rows - 1) / rows), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(fp4_quantize_kernel<F, TYPE, TPR>, dim3(static_cast<unsigned>((a.rows + rows - 1) / rows)),
+                    dim3(kThreads), 0, stream, a);
 }
 
 // Threads per row.  Few rows: as many as spread a row over the GPU's warps best.
@@ -519,15 +527,14 @@ cudaError_t quantize(const Fp4RowsArgs& a, cudaStream_t stream) {
                         : vecs <= 128 * per                  ? quantize_t<F, TYPE, 128>(a, stream)
                                                              : quantize_t<F, TYPE, 256>(a, stream);
   if (e != cudaSuccess || F != Fp4Format::kNv || !a.per_group) return e;
-  fp4_group_scale_kernel<<<(a.G + 127) / 128, 128, 0, stream>>>(a.gscale, a.G);
-  return cudaGetLastError();
+  return launch_pdl(fp4_group_scale_kernel, dim3((a.G + 127) / 128), dim3(128), 0, stream, a.gscale, a.G);
 }
 
 template <Fp4Format F, int TYPE, int TPR>
 cudaError_t dequantize_t(const Fp4RowsArgs& a, cudaStream_t stream) {
   constexpr int rows = kThreads / TPR;
-  fp4_dequantize_kernel<F, TYPE, TPR><<<static_cast<unsigned>((a.rows + rows - 1) / rows), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(fp4_dequantize_kernel<F, TYPE, TPR>, dim3(static_cast<unsigned>((a.rows + rows - 1) / rows)),
+                    dim3(kThreads), 0, stream, a);
 }
 
 template <Fp4Format F, int TYPE>

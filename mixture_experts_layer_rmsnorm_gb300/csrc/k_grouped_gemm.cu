@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(kGroupsMax, 1)
                         const __grid_constant__ CUtensorMap tm_x) {
   __shared__ int warp_sum[32];
   __shared__ int first_bad;
+  pdl_wait();
   pdl_launch_dependents();  // the GEMM sets up its barriers and TMEM meanwhile
   const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
   int64_t s = 0, c = 0, end = 0;  // end: where the next group may begin
@@ -425,8 +426,7 @@ size_t grouped_partial_bytes() { return static_cast<size_t>(kMaxGemmCtas) * kBn[
 cudaError_t launch_grouped_plan(const GroupedPlanArgs& a, const CUtensorMap& dy, const CUtensorMap& x,
                                 cudaStream_t stream) {
   const int threads = (a.G + 31) / 32 * 32 < 256 ? 256 : (a.G + 31) / 32 * 32;
-  grouped_plan_kernel<<<1, threads, 0, stream>>>(a, dy, x);
-  return cudaGetLastError();
+  return launch_pdl(grouped_plan_kernel, dim3(1), dim3(threads), 0, stream, a, dy, x);
 }
 
 cudaError_t launch_grouped_gemm(GroupedOp op, GroupedPlan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,

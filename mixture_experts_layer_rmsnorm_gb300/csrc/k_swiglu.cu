@@ -15,6 +15,8 @@
 #include <cuda_fp16.h>
 
 #include "grouped_elementwise.cuh"
+#include "moe_kernels.cuh"
+#include "pdl.cuh"
 
 namespace moe {
 namespace {
@@ -35,6 +37,8 @@ template <bool FP16, bool GRAD>
 __global__ void __launch_bounds__(kThreads)
     swiglu_kernel(const uint16_t* h, int64_t ldh, const uint16_t* da, int64_t ldda,
                   uint16_t* out, int64_t ldo, uint32_t I, uint32_t n) {
+  pdl_wait();
+  pdl_launch_dependents();
   const uint32_t per_row = I / 8, first = blockIdx.x * (kThreads * kPer) + threadIdx.x;
   uint4 g[kPer], u[kPer], d[kPer];
   uint32_t row[kPer], col[kPer];
@@ -78,9 +82,8 @@ cudaError_t launch(bool fp16, const void* h, int64_t ldh, const void* da, int64_
   const uint32_t n = static_cast<uint32_t>(rows * (I / 8));
   const unsigned blocks = (n + kThreads * kPer - 1) / (kThreads * kPer);
   auto kernel = fp16 ? swiglu_kernel<true, GRAD> : swiglu_kernel<false, GRAD>;
-  kernel<<<blocks, kThreads, 0, stream>>>(static_cast<const uint16_t*>(h), ldh, static_cast<const uint16_t*>(da), ldda,
-                                          static_cast<uint16_t*>(out), ldo, static_cast<uint32_t>(I), n);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, stream, static_cast<const uint16_t*>(h), ldh,
+                    static_cast<const uint16_t*>(da), ldda, static_cast<uint16_t*>(out), ldo, static_cast<uint32_t>(I), n);
 }
 
 }  // namespace
