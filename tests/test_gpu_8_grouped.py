@@ -363,3 +363,68 @@ def test_units_of_every_width_follow_one_another(op, counts):
     for g, (lo, hi) in enumerate(lists.spans):
         ad, wd = a[lo:hi].double(), w[g].double().T if op == "forward" else w[g].double()
         check(out[lo:hi], ad @ wd, ad.abs() @ wd.abs(), 320)
+
+
+def test_two_host_threads_on_their_own_streams():
+    """Objects, workspaces and streams of their own, calls at once: the bits of calls alone.  (The host side's
+    once-per-device configuration and the shape an object keeps are shared state.)"""
+    import threading
+
+    def work(seed):
+        lists = Lists([9 * seed, 0, 300, 17 + seed])
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        x, dy = lists.matrix(gen, 512, BF16), lists.matrix(gen, 384, BF16)
+        w = (torch.randn((4, 384, 512), generator=gen, device="cuda") * 0.05).to(BF16)
+        few = Lists([1, 0, 2, 1])
+        xf = few.matrix(gen, 512, BF16)
+        return lists, x, dy, w, few, xf
+
+    def run(gp, lists, x, dy, w, few, xf):
+        r4 = binding.Fp4Rows("nv", 512, 4).quantize(x, lists.offsets)
+        return [gp.forward(x, w, lists.offsets), gp.dgrad(dy, w, lists.offsets), gp.wgrad(dy, x, lists.offsets, dtype=FP32),
+                gp.forward(xf, w, few.offsets), binding.swiglu(x), r4.dequantize(lists.offsets),
+                binding.Fp4Weights.quantize(w, "mx").forward(binding.Fp4Rows("mx", 512, 4).quantize(x, lists.offsets),
+                                                             lists.offsets)]
+
+    data = [work(1), work(2)]
+    alone = [run(binding.GroupedProducts(4, 384, 512, BF16), *d) for d in data]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def thread(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                gp = binding.GroupedProducts(4, 384, 512, BF16)
+                for _ in range(20):
+                    out = run(gp, *data[i])
+                torch.cuda.current_stream().synchronize()
+                got[i] = out
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors, errors
+    for a, b in zip(alone, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_the_objects_refuse_wrong_tensors():
+    gp = binding.GroupedProducts(2, 64, 128, BF16)
+    x, w = torch.zeros((6, 128), dtype=BF16, device="cuda"), torch.zeros((2, 64, 128), dtype=BF16, device="cuda")
+    off = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    gp.forward(x, w, off)
+    for bad in (lambda: gp.forward(x.cpu(), w, off), lambda: gp.forward(x[:, :64], w, off),
+                lambda: gp.forward(x.t().contiguous().t(), w, off), lambda: gp.forward(x, w[:1], off),
+                lambda: gp.forward(x, w, off[:2]), lambda: gp.forward(x, w, off, y=torch.zeros((6, 64), device="cuda").cpu()),
+                lambda: gp.wgrad(x[:, :64], x, off, accumulate=True), lambda: gp.wgrad(x[:5, :64], x, off)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: gp.forward(x.half(), w, off), lambda: gp.forward(x, w, off.long()), lambda: binding.swiglu(x.double())):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(binding.MoeError):
+        gp.forward(x[:5], w)  # no lists, and 5 rows do not make 2 equal groups
+    with pytest.raises(binding.MoeError):
+        gp.wgrad(x[:, :64], x, off, dw=torch.zeros((2, 64, 128), dtype=BF16, device="cuda"), accumulate=True)

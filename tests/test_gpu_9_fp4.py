@@ -314,3 +314,53 @@ def test_replay_from_a_graph_on_new_rows_and_lists(fmt):
     replayed = y.clone()
     step()
     assert torch.equal(replayed, y)
+
+
+def test_group_scales_over_listed_groups_and_fp16_rows():
+    """One NVFP4 scale per listed group through the C entry point: empty groups get 1, rows of no group take no part."""
+    lists = Lists([3, 0, 40], gap=2, tail=1)
+    k = 96
+    rng = np.random.default_rng(5)
+    x = torch.full((lists.rows, k), float("inf"), dtype=FP16)
+    for a, b in lists.spans:
+        if b > a:
+            x[a:b] = hard_rows(rng, b - a, k, FP16)
+    xd = x.cuda()
+    s = binding.fp4_shape(binding.MOE_FORMAT_NVFP4, 3, lists.rows, k)
+    _, (n_codes, n_scales) = binding.moe_fp4_sizes(s)
+    codes, scales = (torch.zeros(n, dtype=torch.uint8, device="cuda") for n in (n_codes, n_scales))
+    gscale = torch.zeros(3, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    args = (lists.offsets.data_ptr(), lists.counts.data_ptr())
+    assert binding.moe_fp4_quantize(s, binding.MOE_TYPE_FP16, xd.data_ptr(), k, *args, codes.data_ptr(), scales.data_ptr(),
+                                    gscale.data_ptr(), binding.MOE_SCALE_PER_GROUP, stream) == binding.MOE_OK
+    y = torch.zeros((lists.rows, k), device="cuda")
+    assert binding.moe_fp4_dequantize(s, codes.data_ptr(), scales.data_ptr(), gscale.data_ptr(),
+                                      binding.MOE_SCALE_PER_GROUP, *args, binding.MOE_TYPE_FP32, y.data_ptr(), k,
+                                      stream) == binding.MOE_OK
+    assert gscale[1].item() == 1.0
+    for g, (a, b) in enumerate(lists.spans):
+        if b > a:
+            c, sc, gs = quantise(x[a:b].float().numpy(), "nv", True)
+            assert gscale[g].item() == gs[0]
+            c = np.where(np.repeat(E4M3[sc] * gs[:, None] == 0, 16, axis=1), 0, c)
+            assert np.array_equal(unpack(codes, lists.rows, k)[a:b], c)
+            want = values(c, sc, gs, "nv")
+            assert np.abs(y[a:b].cpu().double().numpy() - want).max() <= 2.0 ** -24 * np.abs(want).max()
+
+
+def test_rows_are_as_the_layers_weight_quantizer_makes_them():
+    """w2 of the layer and the same matrix as groups of rows: the same codes and scale bytes (K a multiple of 128)."""
+    E, H, I = 3, 256, 384
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    w2 = (torch.randn((E, H, I), generator=gen, device="cuda") * 0.02).to(BF16)
+    w13 = (torch.randn((E, 2 * I, H), generator=gen, device="cuda") * 0.02).to(BF16)
+    layer = binding.MoeLayer(torch.ones(H, dtype=BF16, device="cuda"), torch.zeros((E, H), device="cuda"), w13, w2, 1)
+    layer.quantize_mxfp4()
+    layer.quantize_nvfp4()
+    mx, nv = binding.Fp4Weights.quantize(w2, "mx"), binding.Fp4Weights.quantize(w2, "nv")
+    assert torch.equal(mx.codes.view(-1), layer.w2_codes4) and torch.equal(nv.codes.view(-1), layer.w2_codes_nv)
+    n = layer.w2_scales4.numel()
+    assert torch.equal(mx.scales[:n], layer.w2_scales4) and torch.equal(nv.gscale, layer.w2_gscale_nv)
+    n = layer.w2_scales_nv.numel()
+    assert torch.equal(nv.scales[:n], layer.w2_scales_nv)
