@@ -23,6 +23,8 @@
 //     instruction.  (Products with a lowered and a raised reciprocal, whose codes agree unless the
 //     quotient lies at a border, cost a second conversion, the slowest
 //     instruction here: 105 us for 134 M elements.)
+// Measured, 134 M bf16 elements: NVFP4 68 to 71 us (0.71 to 0.74 of the copy rate), MXFP4 50 to
+// 52 us (0.96 to 1.01); NVFP4 back to 16 bits 61 us, to fp32 96 us.  1.07 G elements to MXFP4 and back 818 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -11,6 +11,8 @@
 // HBM-bound: 3 (forward) or 5 (gradient) elements moved per output feature.  A
 // thread takes 8 features (16-byte accesses) of two places far enough apart
 // that a warp's accesses stay contiguous, all loads before the first use.
+// Measured: forward of 32768 x 4096 in bf16 116 us (1.02 of the measured copy rate);
+// gradient of 6141 x 1408 in fp16, which fits the L2, 14.5 to 16 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
