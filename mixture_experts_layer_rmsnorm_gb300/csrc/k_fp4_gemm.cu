@@ -32,9 +32,10 @@
 // MXFP4: 117 us with the rows' quantizer, 0.92 of the measured rate).  Many: at the FP4 rate a pair
 // would take a stage of 38 KB per SM every 341 cycles, more than its five (NVFP4) or six (MXFP4)
 // stages cover of the load latency, and the single accumulator is idle between units.  Measured,
-// 64 groups of 512 rows, N = K = 4096: NVFP4 224 us (4.9 PFLOP/s; four stages 237, three 269),
-// MXFP4 188 us (five stages 193); with K = 16384 and 16 groups, a quarter of the hand-overs, NVFP4
-// takes 195 us for the same products.  One group of 8192 rows, N = K = 8192: 184 us (6.0 PFLOP/s).
+// 64 groups of 512 rows, N = K = 4096: NVFP4 230 us (4.8 PFLOP/s), MXFP4 191 us.  In one comparison
+// five, four and three stages took 224, 237 and 269 us (NVFP4; MXFP4's six and five 188 and 193), and K =
+// 16384 with 16 groups, the same products with a quarter of the hand-overs, 195 us; one group of 8192
+// rows, N = K = 8192, 184 us (6.0 PFLOP/s).  The row scales' second factor (scale_parts) costs 4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -70,7 +71,7 @@ struct Cfg {
   static constexpr int kBarBytes = 512;
   static constexpr int kTabGroups = kGroupsSmem[PAIR];
   static constexpr int kTabBytes = 3 * (kTabGroups + 1) * 4;
-  static constexpr int kGxBytes = F == Fp4Format::kNv ? 4 * BN * 4 : 0;  // x's fp32 scales, per epilogue warp
+  static constexpr int kGxBytes = F == Fp4Format::kNv ? 2 * 4 * BN * 4 : 0;  // rows' scales and exponents, per epilogue warp
   static constexpr size_t kSmemBytes =
       1024 + static_cast<size_t>(STAGES) * kStageBytes + kBarBytes + kSchedBytes + kTabBytes + kGxBytes + 16;
   static_assert(kBRows % TOKBOX == 0 && BN >= 32 && BN <= 256, "token tile");
@@ -106,6 +107,23 @@ __device__ __forceinline__ bool walk_ok(const GroupedRange&) { return true; }
 
 __device__ __forceinline__ void put4(uint32_t* d, const uint4& v) {
   d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+}
+
+// gw gx = s p, s returned with p = 1, or where their product lies outside [2^-100, 2^100]
+// (it might not be an fp32 value although the result is) p = 2^-120 or 2^120, taken out of the
+// factor that is farther from 1: s then lies in fp32's range, or the result is zero.
+__device__ __forceinline__ float scale_parts(float gw, float gx, float& p) {
+  p = 1.0f;
+  const float s = __fmul_rn(gw, gx), big = fmaxf(fabsf(gw), fabsf(gx)), small = fminf(fabsf(gw), fabsf(gx));
+  if (fabsf(s) < 0x1p-100f) {
+    p = 0x1p-120f;
+    return copysignf(__fmul_rn(big, __fmul_rn(small, 0x1p120f)), s);
+  }
+  if (fabsf(s) > 0x1p100f) {
+    p = 0x1p120f;
+    return copysignf(__fmul_rn(small, __fmul_rn(big, 0x1p-120f)), s);
+  }
+  return s;
 }
 
 __device__ __forceinline__ uint16_t to16(float v, bool fp16) {
@@ -429,7 +447,8 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
     const uint32_t tempty_cl = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
     constexpr int kCols = BN * 4 / C::kEpiWarps;  // columns per warp
     const int col0 = (warp - 2) / 4 * kCols;
-    float* gx = gx_buf + (warp - 2) * kCols;
+    float *gx = gx_buf + (warp - 2) * kCols, *gp = gx + 4 * BN;  // columns' scales, in two factors
+    bool wide = false;  // (warp-uniform) some column's second factor is not 1
     while (ok && rg.next(u, kb0, kb1)) {
       const GroupedUnit un = units.at(u);
       const int feat0 = PAIR ? un.tile * 256 + static_cast<int>(rank) * 128 : un.tile * 128;
@@ -437,9 +456,15 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(un.tok0) * a.ldo + feat0 + row;
       if (F == Fp4Format::kNv) {  // the rows' fp32 scales times the matrix's, read while the MMAs run
         const float gw = __ldg(args.w_gscale + un.g);
+        bool other = false;
         __syncwarp();
-        for (int c = lane; c < kCols; c += 32)
-          gx[c] = col0 + c < un.n ? __fmul_rn(gw, __ldcg(args.x_gscale + un.tok0 + col0 + c)) : 0.0f;
+        for (int c = lane; c < kCols; c += 32) {
+          float p = 1.0f;
+          gx[c] = col0 + c < un.n ? scale_parts(gw, __ldcg(args.x_gscale + un.tok0 + col0 + c), p) : 0.0f;
+          gp[c] = p;
+          other |= p != 1.0f;
+        }
+        wide = __any_sync(0xFFFFFFFFu, other);
         __syncwarp();
       }
       const bool got = mbar_wait(&tfull[acc], acc_phase, kWaitTimeoutNs, abort_flag);
@@ -477,6 +502,10 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
               if (F == Fp4Format::kNv) {
                 const float4 s = *reinterpret_cast<const float4*>(gx + c0 + j);
                 v = make_float4(__fmul_rn(v.x, s.x), __fmul_rn(v.y, s.y), __fmul_rn(v.z, s.z), __fmul_rn(v.w, s.w));
+                if (wide) {
+                  const float4 p = *reinterpret_cast<const float4*>(gp + c0 + j);
+                  v = make_float4(__fmul_rn(v.x, p.x), __fmul_rn(v.y, p.y), __fmul_rn(v.z, p.z), __fmul_rn(v.w, p.w));
+                }
               }
               packed[(c0 + j) / 2] = pack16(v.x, v.y, fp16);
               packed[(c0 + j) / 2 + 1] = pack16(v.z, v.w, fp16);
@@ -540,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               if (c0 + j < un.n) {
-                if (F == Fp4Format::kNv) v[j] = __fmul_rn(v[j], gx[c0 + j]);
+                if (F == Fp4Format::kNv) v[j] = __fmul_rn(__fmul_rn(v[j], gx[c0 + j]), gp[c0 + j]);
                 out[static_cast<int64_t>(c0 + j) * a.ldo] = to16(v[j], fp16);
               }
           }

@@ -364,3 +364,30 @@ def test_rows_are_as_the_layers_weight_quantizer_makes_them():
     assert torch.equal(mx.scales[:n], layer.w2_scales4) and torch.equal(nv.gscale, layer.w2_gscale_nv)
     n = layer.w2_scales_nv.numel()
     assert torch.equal(nv.scales[:n], layer.w2_scales_nv)
+
+
+@pytest.mark.parametrize("counts", [[5, 0, 7], [300, 20, 0]], ids=["few", "many"])
+@pytest.mark.parametrize("ex,ew", [(-63, -60), (-80, -38), (-113, 43), (66, 63), (113, -100), (83, 80)])
+def test_scales_whose_product_leaves_the_range(ex, ew, counts):
+    """NVFP4's two fp32 scales may multiply to less or more than fp32 holds where the results do not.  Inputs shifted by
+    powers of two (normal ones: 2^-113 times randn's values above 2^-13; smaller ones have the code 0) have the same
+    codes and block scales, and every scale and rounding of the product shifts with them: equal results, but for a
+    step of the subnormal ones (half for each of the two roundings)."""
+    n, k = 72, 128
+    lists = Lists(counts)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x, w = (torch.randn(s, generator=gen, device="cuda").to(BF16) for s in ((lists.rows, k), (3, n, k)))
+    x[0] = 0.0
+    x[1, :64], x[1, 64:], w[:, 0, :64], w[:, 0, 64:] = 0.0, 1.0, 1.0, 0.0  # a sum of zeros
+
+    def run(a, b):
+        return binding.Fp4Weights.quantize(b, "nv").forward(binding.Fp4Rows("nv", k, 3).quantize(a, lists.offsets),
+                                                            lists.offsets)
+
+    want = run(x, w).double() * 2.0 ** (ex + ew)
+    got = run((x.float() * 2.0 ** ex).to(BF16), (w.float() * 2.0 ** ew).to(BF16)).double()
+    top = torch.finfo(BF16).max
+    assert (got[0] == 0).all() and got[1, 0] == 0
+    inside, over = want.abs() <= top, want.abs() > top * (1 + 2.0 ** -8)
+    assert ((got - want).abs()[inside] <= 2.0 ** -133).all()
+    assert torch.isinf(got[over]).all()
