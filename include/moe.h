@@ -639,7 +639,7 @@ MOE_API moe_status moe_fp4_gemm(const moe_grouped_shape* shape, int32_t format, 
 /* SwiGLU of separate rows, between the gate/up and the down product: h
  * [rows, 2I] holds gate in columns [0, I) and up in [I, 2I) (the order of a
  * W13 product), act [rows, I] = SiLU(gate) * up; and its gradient,
- * dh [rows, 2I] from dact [rows, I].  dh may be h itself.  type, strides,
+ * dh [rows, 2I] from dact [rows, I].  dh may be h itself (lddh = ldh).  type, strides,
  * alignment and rows as above; I a multiple of 8, rows * I < 2^34. */
 MOE_API moe_status moe_swiglu(int32_t type, int64_t rows, int32_t I, const void* h, int64_t ldh, void* act,
                               int64_t ldact, moe_stream_t stream);

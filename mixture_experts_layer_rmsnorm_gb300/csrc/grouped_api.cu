@@ -360,6 +360,7 @@ moe_status moe_swiglu_grad(int32_t type, int64_t rows, int32_t I, const void* h,
   if ((st = check_rows(h, rows, ldh, 2 * static_cast<int64_t>(I))) != MOE_OK) return st;
   if ((st = check_rows(dact, rows, lddact, I)) != MOE_OK) return st;
   if ((st = check_rows(dh, rows, lddh, 2 * static_cast<int64_t>(I))) != MOE_OK) return st;
+  if (rows > 1 && dh == h && lddh != ldh) return MOE_ERR_INVALID_ARG;  // rows of one over rows of the other
   if (rows == 0) return MOE_OK;
   return moe::launch_swiglu_grad(type == MOE_TYPE_FP16, h, ldh, dact, lddact, dh, lddh, rows, I,
                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess

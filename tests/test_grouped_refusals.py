@@ -125,3 +125,7 @@ def test_fp4_product_refuses(over, want):
     s = binding.grouped_shape(a["groups"], a["N"], a["K"], a["rows"], a["type"])
     assert binding.moe_fp4_gemm(s, a["format"], a["xc"], a["xs"], a["xg"], a["wc"], a["ws"], a["wg"], a["off"], None,
                                 a["y"], a["ldy"], a["space"], a["space_bytes"], None) == want
+
+
+def test_swiglu_gradient_in_place_has_one_stride():
+    assert binding.moe_swiglu_grad(0, 4, 64, A, 128, 2 * A, 64, A, 136, None) == INV
