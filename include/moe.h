@@ -573,7 +573,11 @@ MOE_API moe_status moe_grouped_gemm_dgrad(const moe_grouped_shape* shape, const 
 
 /* dw [groups, N, K] of dw_type (the operands' type, or MOE_TYPE_FP32): written
  * whole, zeros for an empty group; or, with accumulate != 0 (MOE_TYPE_FP32
- * only, else MOE_ERR_INVALID_ARG), added to what dw holds. */
+ * only, else MOE_ERR_INVALID_ARG), added to what dw holds.  The tensor core cuts
+ * its fp32 sums towards zero: up to rows * 2^-28 of the sum of |dy x|.  Into fp32 that
+ * is 768 rows at most, the rest is added rounded to nearest; into 16 bits it is all
+ * rows of the group (2^20 rows: half a bf16 step), rows <= 2^26 (else
+ * MOE_ERR_UNSUPPORTED). */
 MOE_API moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy, int64_t lddy, const void* x,
                                           int64_t ldx, const int32_t* offsets, const int32_t* counts, void* dw,
                                           int32_t dw_type, int32_t accumulate, void* workspace,

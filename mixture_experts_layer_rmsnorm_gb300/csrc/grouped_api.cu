@@ -19,6 +19,9 @@ using moe::GroupedPlan;
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;         // N, K
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;  // 32-bit row coordinates, a token box past the end
+// Weight gradient into 16 bits: one accumulation per group, which a wait of the epilogue (two
+// seconds at most) spans: 2^20 blocks of 64 rows at 500 to 1000 cycles take up to half a second.
+constexpr int64_t kMaxRows16 = int64_t(1) << 26;
 constexpr int64_t kMaxLd = int64_t(1) << 36;          // elements: row strides within the tensor maps' 2^40 bytes
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -157,7 +160,7 @@ moe::GroupedPlanArgs plan_args(const moe_grouped_shape* s, const Layout& L, void
 
 // The tile plan follows the rows a group can be expected to hold: up to 16,
 // the product is bound by streaming the weights once (32-row units, stream-K),
-// above that by reuse of the weight tiles (256-row units on CTA pairs).
+// above that by reuse of the weight tiles (units of up to 512 rows on CTA pairs; 4 bits: 256).
 GroupedPlan choose_plan(const moe_grouped_shape* s) {
   return s->rows <= int64_t(16) * s->groups ? GroupedPlan::kSmall : GroupedPlan::kLarge;
 }
@@ -311,6 +314,7 @@ moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy
   const int tile = moe::kWgradTile;
   const int64_t tiles_m = (s->N + tile - 1) / tile, tiles_n = (s->K + tile - 1) / tile;
   if (tiles_m * tiles_n * s->groups >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (dw_type != MOE_TYPE_FP32 && s->rows > kMaxRows16) return MOE_ERR_UNSUPPORTED;
   if (s->rows == 0 && accumulate) return MOE_OK;
   // no rows: every group is empty and dw becomes zero; nothing is loaded through the row maps
   const int64_t map_rows = s->rows > 0 ? s->rows : 1;

@@ -129,3 +129,10 @@ def test_fp4_product_refuses(over, want):
 
 def test_swiglu_gradient_in_place_has_one_stride():
     assert binding.moe_swiglu_grad(0, 4, 64, A, 128, 2 * A, 64, A, 136, None) == INV
+
+
+def test_weight_gradient_into_16_bits_of_too_many_rows():
+    for rows, want in (((1 << 26) + 1, UNS), (1 << 26, WS)):  # (the second is refused for its workspace alone)
+        s = binding.grouped_shape(4, 64, 128, rows)
+        ws = 64 if want == WS else BIG
+        assert binding.moe_grouped_gemm_wgrad(s, A, 64, A, 128, A, None, A, 0, 0, A, ws, None) == want
