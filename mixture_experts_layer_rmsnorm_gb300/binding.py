@@ -503,7 +503,7 @@ def _enqueue(name, device, fn, *args):
 def swiglu(h, act=None):
     """SiLU(gate) * up of rows h = [gate | up] (moe_swiglu), on the current stream of h's device."""
     rows, two_i = h.shape
-    _check("h", h, h.device, h.dtype, h.shape, rows=True)
+    _check("h", h, h.device, h.dtype, (rows, two_i // 2 * 2), rows=True)
     if act is None:
         import torch
         act = torch.empty((rows, two_i // 2), dtype=h.dtype, device=h.device)
@@ -517,7 +517,7 @@ def swiglu(h, act=None):
 def swiglu_grad(h, dact, dh=None):
     """d[gate | up] from dact (moe_swiglu_grad), on the current stream of h's device."""
     rows, two_i = h.shape
-    _check("h", h, h.device, h.dtype, h.shape, rows=True)
+    _check("h", h, h.device, h.dtype, (rows, two_i // 2 * 2), rows=True)
     _check("dact", dact, h.device, h.dtype, (rows, two_i // 2), rows=True)
     if dh is None:
         import torch
@@ -529,7 +529,28 @@ def swiglu_grad(h, dact, dh=None):
     return dh
 
 
-class GroupedProducts:
+class _Workspace:
+    """A workspace of the grouped calls, for an object with ``device`` and ``workspace``."""
+
+    called = False
+
+    def _entered(self, rows):
+        # a call without rows enqueues nothing: what a call before it reported is not its own
+        self.called = True
+        if rows == 0:
+            self.workspace[:16].zero_()
+
+    def device_status(self):
+        """(status, detail) of the last call, after waiting for the current stream (moe_device_status)."""
+        if not self.called:  # (what the workspace holds means nothing yet)
+            return MOE_OK, [0] * 4
+        import torch
+        with torch.cuda.device(self.device):
+            return moe_device_status(_ptr(self.workspace), self.workspace.numel(),
+                                     torch.cuda.current_stream().cuda_stream)
+
+
+class GroupedProducts(_Workspace):
     """The products of ``groups`` weight matrices [N, K] with the rows of their
     groups, and the gradients (moe_grouped_gemm*), with a workspace of their
     own.  Calls go to the current stream of the tensors' device; calls of one
@@ -559,8 +580,9 @@ class GroupedProducts:
             return torch.empty((rows, width), dtype=self.dtype, device=self.device)
         return _check(what, t, self.device, self.dtype, (rows, width), rows=True)
 
-    def _call(self, name, fn, *args):
-        _enqueue(name, self.device, fn, *args, self.workspace.data_ptr(), self.workspace.numel())
+    def _call(self, name, fn, shape_, *args):
+        self._entered(shape_.rows)
+        _enqueue(name, self.device, fn, shape_, *args, self.workspace.data_ptr(), self.workspace.numel())
 
     def forward(self, x, w, offsets=None, counts=None, y=None):
         """y[p] = x[p] w_g^T for the rows p of every group g; other rows of y stay as they are."""
@@ -599,13 +621,6 @@ class GroupedProducts:
                    _ld(x), *_lists(self, offsets, counts), _ptr(dw), _type_of(dw.dtype), accumulate)
         return dw
 
-    def device_status(self):
-        """(status, detail) of the last call, after waiting for the current stream (moe_device_status)."""
-        import torch
-        with torch.cuda.device(self.device):
-            return moe_device_status(_ptr(self.workspace), self.workspace.numel(),
-                                     torch.cuda.current_stream().cuda_stream)
-
 
 def _format_of(name) -> int:
     formats = {"mx": MOE_FORMAT_MXFP4, "nv": MOE_FORMAT_NVFP4}
@@ -619,7 +634,9 @@ class Fp4Rows:
     for up to ``max_rows`` rows of K elements, filled by :meth:`quantize`.
     format: "mx" (MXFP4) or "nv" (NVFP4, one fp32 scale per row).  offsets and
     counts as for :class:`GroupedProducts`; pass the same ones to every call on
-    the same rows.  Calls go to the current stream of the device."""
+    the same rows.  Calls go to the current stream of the device.  More rows than
+    ``max_rows`` get larger buffers; the outgrown ones live as long as the object,
+    for graphs that were captured with them and work still queued on other streams."""
 
     def __init__(self, format, K, groups=1, max_rows=0, device=None):
         import torch
@@ -627,6 +644,7 @@ class Fp4Rows:
         self.device, self.int32 = torch.empty(0, device=device or "cuda").device, torch.int32
         self.rows = self.max_rows = 0
         self._shape = None
+        self._outgrown, self._listed = [], None
         self.ensure_capacity(max_rows)
 
     def shape(self, rows) -> MoeFp4Shape:
@@ -639,14 +657,18 @@ class Fp4Rows:
         if rows <= self.max_rows and self.max_rows > 0:
             return
         import torch
-        st, (n_codes, n_scales) = moe_fp4_sizes(self.shape(max(rows, 1)))
+        # (by half at least: what outgrown buffers hold stays below twice the last ones)
+        rows = max(rows, min(self.max_rows * 3 // 2, 2 ** 31 - 512), 1)
+        st, (n_codes, n_scales) = moe_fp4_sizes(fp4_shape(self.format, self.groups, rows, self.K))
         if st != MOE_OK:
             raise MoeError(st, "moe_fp4_sizes")
+        if self.max_rows > 0:
+            self._outgrown.append((self.codes, self.scales, self.gscale))
         self.codes = torch.empty(n_codes, dtype=torch.uint8, device=self.device)
         self.scales = torch.empty(n_scales, dtype=torch.uint8, device=self.device)
-        self.gscale = (torch.empty(max(rows, 1), dtype=torch.float32, device=self.device)
+        self.gscale = (torch.empty(rows, dtype=torch.float32, device=self.device)
                        if self.format == MOE_FORMAT_NVFP4 else None)
-        self.max_rows = max(rows, 1)
+        self.max_rows = rows
 
     def quantize(self, x, offsets=None, counts=None):
         """x [rows, K] (bf16, fp16 or fp32) to 4 bits; returns self."""
@@ -655,11 +677,17 @@ class Fp4Rows:
         lists = _lists(self, offsets, counts)
         _enqueue("moe_fp4_quantize", self.device, moe_fp4_quantize, self.shape(x.shape[0]), _type_of(x.dtype), _ptr(x),
                  _ld(x), *lists, _ptr(self.codes), _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_ROW)
-        self.rows = x.shape[0]
+        self.rows, self._listed = x.shape[0], offsets is not None
         return self
+
+    def check_lists(self, offsets):
+        # (listed groups' scales lie elsewhere than equal groups')
+        if self._listed is not None and self._listed != (offsets is not None):
+            raise ValueError(f"the rows were quantized {'with' if self._listed else 'without'} offsets")
 
     def dequantize(self, offsets=None, counts=None, y=None, dtype=None):
         """The values of the rows quantized last, in ``dtype`` (bf16 by default) or y's type."""
+        self.check_lists(offsets)
         if y is None:
             import torch
             y = torch.empty((self.rows, self.K), dtype=dtype or torch.bfloat16, device=self.device)
@@ -671,7 +699,7 @@ class Fp4Rows:
         return y
 
 
-class Fp4Weights:
+class Fp4Weights(_Workspace):
     """Weights of ``groups`` matrices [N, K] in 4 bits and their product with 4-bit
     rows (moe_fp4_gemm).  codes: uint8 [groups, N, K / 2]; scales: the tiles of
     moe_fp4_quantize for equal groups of N rows; gscale: fp32 [groups] ("nv") or None."""
@@ -731,24 +759,19 @@ class Fp4Weights:
         """y[p] = x[p] w_g^T in ``dtype`` (bf16 by default, or fp16) or y's type; rows: x quantized for the same lists."""
         if rows.format != self.format or rows.K != self.K or rows.groups != self.groups or rows.device != self.device:
             raise ValueError("rows of another format, K, number of groups or device")
+        rows.check_lists(offsets)
         if y is None:
             import torch
             y = torch.empty((rows.rows, self.N), dtype=dtype or torch.bfloat16, device=self.device)
         else:
             _check("y", y, self.device, dtype or y.dtype, (rows.rows, self.N), rows=True)
         lists = _lists(self, offsets, counts)
+        self._entered(rows.rows)
         _enqueue("moe_fp4_gemm", self.device, moe_fp4_gemm,
                  grouped_shape(self.groups, self.N, self.K, rows.rows, _type_of(y.dtype)), self.format,
                  _ptr(rows.codes), _ptr(rows.scales), _ptr(rows.gscale), _ptr(self.codes), _ptr(self.scales),
                  _ptr(self.gscale), *lists, _ptr(y), _ld(y), _ptr(self.workspace), self.workspace.numel())
         return y
-
-    def device_status(self):
-        """(status, detail) of the last product, after waiting for the current stream (moe_device_status)."""
-        import torch
-        with torch.cuda.device(self.device):
-            return moe_device_status(_ptr(self.workspace), self.workspace.numel(),
-                                     torch.cuda.current_stream().cuda_stream)
 
 
 class MoeLayer:

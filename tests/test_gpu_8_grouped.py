@@ -428,3 +428,27 @@ def test_the_objects_refuse_wrong_tensors():
         gp.forward(x[:5], w)  # no lists, and 5 rows do not make 2 equal groups
     with pytest.raises(binding.MoeError):
         gp.wgrad(x[:, :64], x, off, dw=torch.zeros((2, 64, 128), dtype=BF16, device="cuda"), accumulate=True)
+
+
+def test_swiglu_refuses_an_odd_width():
+    h, a = torch.zeros((4, 17), dtype=BF16, device="cuda"), torch.zeros((4, 8), dtype=BF16, device="cuda")
+    for bad in (lambda: binding.swiglu(h), lambda: binding.swiglu_grad(h, a)):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_calls_without_rows_report_nothing_of_earlier_calls():
+    gp = binding.GroupedProducts(2, 8, 64, BF16)
+    gp.workspace.fill_(0xFF)
+    assert gp.device_status()[0] == binding.MOE_OK  # no call yet
+    x, w = torch.ones((6, 64), dtype=BF16, device="cuda"), torch.ones((2, 8, 64), dtype=BF16, device="cuda")
+    dy, dw = torch.ones((6, 8), dtype=BF16, device="cuda"), torch.ones((2, 8, 64), device="cuda")
+    bad = torch.tensor([0, 9, 6], dtype=torch.int32, device="cuda")
+    empty = (lambda: gp.forward(x[:0], w, bad), lambda: gp.dgrad(dy[:0], w, bad),
+             lambda: gp.wgrad(dy[:0], x[:0], dw=dw, accumulate=True))
+    for call in empty:
+        gp.forward(x, w, bad)
+        assert gp.device_status()[0] == binding.MOE_ERR_DEVICE
+        call()
+        assert gp.device_status()[0] == binding.MOE_OK
+    assert (dw == 1).all()

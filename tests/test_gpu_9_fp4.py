@@ -391,3 +391,51 @@ def test_scales_whose_product_leaves_the_range(ex, ew, counts):
     inside, over = want.abs() <= top, want.abs() > top * (1 + 2.0 ** -8)
     assert ((got - want).abs()[inside] <= 2.0 ** -133).all()
     assert torch.isinf(got[over]).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_a_captured_graph_outlives_larger_buffers(fmt):
+    """The buffers a graph was captured with are nobody else's after the object has grown."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn((100, 256), generator=gen, device="cuda").to(BF16)
+    w4 = binding.Fp4Weights.quantize(torch.randn((2, 64, 256), generator=gen, device="cuda").to(BF16), fmt)
+    off = torch.tensor([0, 40, 100], dtype=torch.int32, device="cuda")
+    r4, y = binding.Fp4Rows(fmt, 256, 2, 100), torch.zeros((100, 64), dtype=BF16, device="cuda")
+    w4.forward(r4.quantize(x, off), off, y=y)
+    want = y.clone()
+    held = {t.data_ptr(): t.numel() for t in (r4.codes, r4.scales)}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w4.forward(r4.quantize(x, off), off, y=y)
+    more = torch.randn((1000, 256), generator=gen, device="cuda").to(BF16)
+    off_more = torch.tensor([0, 900, 1000], dtype=torch.int32, device="cuda")
+    w4.forward(r4.quantize(more, off_more), off_more)
+    others = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in held.values() for _ in range(8)]
+    assert not any(t.data_ptr() in held for t in others)
+    y.zero_()
+    graph.replay()
+    assert torch.equal(y, want) and not any(t.any() for t in others)
+
+
+def test_rows_and_product_take_the_same_kind_of_lists():
+    off = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    x, w = torch.ones((6, 64), dtype=BF16, device="cuda"), torch.ones((2, 8, 64), dtype=BF16, device="cuda")
+    w4 = binding.Fp4Weights.quantize(w, "nv")
+    listed, equal = (binding.Fp4Rows("nv", 64, 2).quantize(x, o) for o in (off, None))
+    assert (w4.forward(listed, off) == 64).all() and (w4.forward(equal) == 64).all()
+    for bad in (lambda: w4.forward(listed), lambda: w4.forward(equal, off), lambda: listed.dequantize(),
+                lambda: equal.dequantize(off)):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_a_product_without_rows_reports_nothing_of_earlier_calls():
+    x, w = torch.ones((6, 64), dtype=BF16, device="cuda"), torch.ones((2, 8, 64), dtype=BF16, device="cuda")
+    bad = torch.tensor([0, 9, 6], dtype=torch.int32, device="cuda")
+    w4 = binding.Fp4Weights.quantize(w, "mx")
+    w4.workspace.fill_(0xFF)
+    assert w4.device_status()[0] == binding.MOE_OK
+    w4.forward(binding.Fp4Rows("mx", 64, 2).quantize(x, bad), bad)
+    assert w4.device_status()[0] == binding.MOE_ERR_DEVICE
+    assert w4.forward(binding.Fp4Rows("mx", 64, 2).quantize(x[:0], bad), bad).shape == (0, 8)
+    assert w4.device_status()[0] == binding.MOE_OK
