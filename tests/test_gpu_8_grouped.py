@@ -452,3 +452,62 @@ def test_calls_without_rows_report_nothing_of_earlier_calls():
         call()
         assert gp.device_status()[0] == binding.MOE_OK
     assert (dw == 1).all()
+
+
+@pytest.mark.parametrize("rows_per_group", [12, 200], ids=["few", "many"])
+def test_equal_groups_filled_in_part(rows_per_group):
+    """counts without offsets: group g holds the first counts[g] of its rows / groups rows."""
+    counts = [rows_per_group, 0, 1, rows_per_group // 2]
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    rows, n, k = 4 * rows_per_group, 136, 200
+    x, dy = (torch.full((rows, c), float("nan"), dtype=BF16, device="cuda") for c in (k, n))
+    w = (torch.randn((4, n, k), generator=gen, device="cuda") * 0.05).to(BF16)
+    free = torch.ones(rows, dtype=torch.bool, device="cuda")
+    spans = [(g * rows_per_group, g * rows_per_group + c) for g, c in enumerate(counts)]
+    for a, b in spans:
+        x[a:b] = torch.randn((b - a, k), generator=gen, device="cuda").to(BF16)
+        dy[a:b] = torch.randn((b - a, n), generator=gen, device="cuda").to(BF16)
+        free[a:b] = False
+    gp, cnt = binding.GroupedProducts(4, n, k, BF16), torch.tensor(counts, dtype=torch.int32, device="cuda")
+    y, dx = (torch.full((rows, c), 7.0, dtype=BF16, device="cuda") for c in (n, k))
+    gp.forward(x, w, None, cnt, y=y)
+    gp.dgrad(dy, w, None, cnt, dx=dx)
+    dw = gp.wgrad(dy, x, None, cnt, dtype=FP32)
+    assert gp.device_status()[0] == binding.MOE_OK and (y[free] == 7.0).all() and (dx[free] == 7.0).all()
+    for g, (a, b) in enumerate(spans):
+        xd, dd, wd = x[a:b].double(), dy[a:b].double(), w[g].double()
+        check(y[a:b], xd @ wd.T, xd.abs() @ wd.abs().T, k)
+        check(dx[a:b], dd @ wd, dd.abs() @ wd.abs(), n)
+        check(dw[g], dd.T @ xd, dd.abs().T @ xd.abs(), b - a)
+    gp.forward(x, w, None, cnt + (torch.arange(4, device="cuda") == 2).int() * rows_per_group, y=y)  # one row too many
+    status, detail = gp.device_status()
+    assert status == binding.MOE_ERR_DEVICE and detail[2] == 2
+
+
+def test_rows_behind_2_to_the_32_elements():
+    """Matrices whose last rows start more than 2^32 elements behind the first."""
+    rows, ld, n, k = 66000, 65600, 72, 64
+    x = torch.empty(rows * ld, dtype=BF16, device="cuda").view(rows, ld)[:, :k]
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    x.copy_(torch.randn((rows, k), generator=gen, device="cuda"))
+    packed = x.contiguous()
+    off = torch.tensor([0, 7, 65700, rows], dtype=torch.int32, device="cuda")
+    w = (torch.randn((3, n, k), generator=gen, device="cuda") * 0.05).to(BF16)
+    gp = binding.GroupedProducts(3, n, k, BF16)
+    y = gp.forward(x, w, off)
+    assert torch.equal(y, gp.forward(packed, w, off))
+    assert torch.equal(gp.wgrad(y, x, off, dtype=FP32), gp.wgrad(y, packed, off, dtype=FP32))
+    assert torch.equal(binding.swiglu(x), binding.swiglu(packed))
+    for fmt in ("mx", "nv"):
+        a, b = (binding.Fp4Rows(fmt, k, 3).quantize(t, off) for t in (x, packed))
+        assert torch.equal(a.codes, b.codes)
+        values = b.dequantize(off)
+        a.dequantize(off, y=x)
+        assert torch.equal(x, values)
+        x.copy_(packed)
+    want = gp.dgrad(y, w, off)
+    assert torch.equal(gp.dgrad(y, w, off, dx=x), want)
+    x.copy_(packed)
+    act = torch.ones((rows, k // 2), dtype=BF16, device="cuda")
+    want = binding.swiglu_grad(packed, act)
+    assert torch.equal(binding.swiglu_grad(x, act, dh=x), want)  # in place

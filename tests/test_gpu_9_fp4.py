@@ -439,3 +439,19 @@ def test_a_product_without_rows_reports_nothing_of_earlier_calls():
     assert w4.device_status()[0] == binding.MOE_ERR_DEVICE
     assert w4.forward(binding.Fp4Rows("mx", 64, 2).quantize(x[:0], bad), bad).shape == (0, 8)
     assert w4.device_status()[0] == binding.MOE_OK
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_equal_groups_filled_in_part(fmt):
+    """counts without offsets: the rows behind a group's count are skipped, their NaN reach nothing."""
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    x = torch.randn((4 * 150, 96), generator=gen, device="cuda").to(BF16)
+    w4 = binding.Fp4Weights.quantize(torch.randn((4, 72, 96), generator=gen, device="cuda").to(BF16), fmt)
+    full = w4.forward(binding.Fp4Rows(fmt, 96, 4).quantize(x))
+    cnt = torch.tensor([150, 0, 1, 131], dtype=torch.int32, device="cuda")
+    on = (torch.arange(150, device="cuda")[None, :] < cnt[:, None]).reshape(-1)
+    x[~on] = float("nan")
+    y = torch.full((600, 72), 7.0, dtype=BF16, device="cuda")
+    w4.forward(binding.Fp4Rows(fmt, 96, 4).quantize(x, None, cnt), None, cnt, y=y)
+    assert w4.device_status()[0] == binding.MOE_OK
+    assert torch.equal(y[on], full[on]) and (y[~on] == 7.0).all()
