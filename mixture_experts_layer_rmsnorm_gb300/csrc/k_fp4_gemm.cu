@@ -29,13 +29,15 @@
 // stores after that.
 //
 // Few rows a group: bound by HBM (64 rows in 41 of 64 groups, N = 8192, K = 4096,
-// MXFP4: 117 us with the rows' quantizer, 0.92 of the measured rate).  Many: at the FP4 rate a pair
-// would take a stage of 38 KB per SM every 341 cycles, more than its five (NVFP4) or six (MXFP4)
-// stages cover of the load latency, and the single accumulator is idle between units.  Measured,
-// 64 groups of 512 rows, N = K = 4096: NVFP4 230 us (4.8 PFLOP/s), MXFP4 191 us.  In one comparison
-// five, four and three stages took 224, 237 and 269 us (NVFP4; MXFP4's six and five 188 and 193), and K =
-// 16384 with 16 groups, the same products with a quarter of the hand-overs, 195 us; one group of 8192
-// rows, N = K = 8192, 184 us (6.0 PFLOP/s).  The row scales' second factor (scale_parts) costs 4 us.
+// MXFP4: 117 us with the rows' quantizer, 0.92 of the measured rate).  Many: bound by the fill of
+// shared memory; at the FP4 rate a pair would take a stage of 38 KB per SM every 341 cycles, 111
+// bytes a cycle, where the 16-bit kernel's loads alone reach 68 and this one takes 48.  Measured,
+// 64 groups of 512 rows, N = K = 4096: NVFP4 230 us (4.8 PFLOP/s), MXFP4 191 us; one group of
+// 8192 rows, N = K = 8192: NVFP4 184 to 191 us (5.7 to 6.0 PFLOP/s).  In one comparison five,
+// four and three stages took 224, 237 and 269 us (NVFP4; MXFP4's six and five 188 and 193).  The hand-over
+// of the single accumulator is not what costs: all columns read into registers before any
+// arithmetic (176 registers a thread) 229 us, MXFP4 199; nor is HBM's latency: weights prefetched into L2
+// 4, 8 or 15 stages ahead 235, 237, 244 us.  The row scales' second factor (scale_parts) costs 4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
