@@ -516,8 +516,11 @@ cudaError_t quantize(const Fp4RowsArgs& a, cudaStream_t stream) {
   if (F == Fp4Format::kNv && a.per_group) {
     cudaError_t e = cudaMemsetAsync(a.gscale, 0, sizeof(float) * a.G, stream);
     if (e != cudaSuccess) return e;
-    fp4_group_amax_kernel<TYPE><<<static_cast<unsigned>((a.rows + 7) / 8), kThreads, 0, stream>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};  // (after a memset: no programmatic dependency)
+    cfg.gridDim = dim3(static_cast<unsigned>((a.rows + 7) / 8));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    if ((e = cudaLaunchKernelEx(&cfg, fp4_group_amax_kernel<TYPE>, a)) != cudaSuccess) return e;
   }
   const int vecs = a.K / kElems;
   constexpr int kHold = hold_of(TYPE);

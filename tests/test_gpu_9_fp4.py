@@ -455,3 +455,18 @@ def test_equal_groups_filled_in_part(fmt):
     w4.forward(binding.Fp4Rows(fmt, 96, 4).quantize(x, None, cnt), None, cnt, y=y)
     assert w4.device_status()[0] == binding.MOE_OK
     assert torch.equal(y[on], full[on]) and (y[~on] == 7.0).all()
+
+
+def test_weights_quantized_in_a_graph():
+    """The group maxima (a memset, three kernels) replayed on new weights."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    w = torch.randn((3, 72, 160), generator=gen, device="cuda").to(BF16)
+    binding.Fp4Weights.quantize(w, "nv")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = binding.Fp4Weights.quantize(w, "nv")
+    w.copy_(torch.randn(w.shape, generator=gen, device="cuda") * 3)
+    graph.replay()
+    eager = binding.Fp4Weights.quantize(w, "nv")
+    assert torch.equal(captured.codes, eager.codes) and torch.equal(captured.gscale, eager.gscale)
+    assert torch.equal(captured.dequantize(), eager.dequantize())
