@@ -24,9 +24,11 @@
 //     quotient lies at a border, cost a second conversion, the slowest
 //     instruction here: 105 us for 134 M elements.)
 // Measured, 134 M bf16 elements: NVFP4 68 to 71 us (0.71 to 0.74 of the copy rate), MXFP4 50 to
-// 52 us (0.96 to 1.01); NVFP4 back to 16 bits 61 us, to fp32 96 us.  1.07 G elements to MXFP4 and back 818 us.
+// 52 us (0.96 to 1.01); back to 16 bits 52 us, to fp32 93 us.  1.07 G elements to MXFP4 and back 771 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "grouped_elementwise.cuh"
@@ -44,13 +46,51 @@ struct RowPlace {
   bool on;
 };
 
-// The group and scale place of row p (warp-collective, the same p in a warp):
-// two rounds of 32 comparisons find the group among up to 1024.  Rows of no
-// group, and places that lists out of order could lead to, are off.
-__device__ __forceinline__ RowPlace place_of(const Fp4RowsArgs& a, int p, int lane) {
+// The offsets of up to kOneRound groups, entry 32 i + lane in [i], for a kernel that reads
+// them ahead of its row: the inverse with a warp per row (134 M elements 58 -> 52 us; with
+// more warps per row, 1021 rows of 7168, 4.7 -> 5.0; the quantizer, whose registers are full,
+// gains nothing).
+constexpr int kOneRound = 256;
+struct Offsets {
+  int at[kOneRound / 32 + 1];
+  __device__ __forceinline__ Offsets(const Fp4RowsArgs& a, int lane) {
+#pragma unroll
+    for (int i = 0; i <= kOneRound / 32; ++i)
+      at[i] = a.offsets && a.G <= kOneRound && 32 * i + lane <= a.G ? __ldg(a.offsets + 32 * i + lane) : 0x7FFFFFFF;
+  }
+};
+struct NoOffsets {
+  __device__ __forceinline__ NoOffsets(const Fp4RowsArgs&, int) {}
+};
+
+// The group and scale place of row p (warp-collective, the same p in a warp): the
+// last group that starts at p or before, from `off`, or in two rounds of 32
+// comparisons among up to 1024.  Rows of no group, and places that lists out of order
+// could lead to, are off.
+template <typename Ahead>
+__device__ __forceinline__ RowPlace place_of(const Fp4RowsArgs& a, const Ahead& off, int p, int lane) {
+  constexpr bool kAhead = std::is_same_v<Ahead, Offsets>;
   RowPlace r{0, 0, 0, false};
   int start, count;
-  if (a.offsets) {
+  if (kAhead && a.offsets && a.G <= kOneRound) {
+    if constexpr (kAhead) {
+      int n = 0, from = -1, to = 0x7FFFFFFF;
+#pragma unroll
+      for (int i = 0; i <= kOneRound / 32; ++i) {
+        const bool before = off.at[i] <= p;
+        n += before && 32 * i + lane < a.G;
+        from = before ? max(from, off.at[i]) : from;
+        to = before ? to : min(to, off.at[i]);
+      }
+      const int g = __reduce_add_sync(0xFFFFFFFFu, n) - 1;
+      start = __reduce_max_sync(0xFFFFFFFFu, from);
+      to = __reduce_min_sync(0xFFFFFFFFu, to);  // the next group's start
+      if (g < 0 || start < 0 || to == 0x7FFFFFFF) return r;
+      count = a.counts ? __ldg(a.counts + g) : to - start;
+      r.group = g;
+      r.tile_row = start / 128 + g;
+    }
+  } else if (a.offsets) {
     const int step = (a.G + 31) / 32;
     int at = lane * step;
     const unsigned m1 = __ballot_sync(0xFFFFFFFFu, at < a.G && __ldg(a.offsets + at) <= p);
@@ -305,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const __grid_
     else
       zero_vec<TYPE>(held[i]);
   }
-  const RowPlace r = place_of(a, p, lane);
+  const RowPlace r = place_of(a, NoOffsets(a, lane), p, lane);
   const bool row_on = in && r.on;
   NvRow nv{};
   if constexpr (F == Fp4Format::kNv) {
@@ -410,7 +450,7 @@ __global__ void __launch_bounds__(kThreads) fp4_group_amax_kernel(const __grid_c
     for (int i = 0; i < kHold; ++i) m = max_mag<TYPE>(m, mag_vec<TYPE>(held[i]));
   }
   m = __reduce_max_sync(0xFFFFFFFFu, mag_bits<TYPE>(m));
-  const RowPlace r = place_of(a, p, lane);
+  const RowPlace r = place_of(a, NoOffsets(a, lane), p, lane);
   if (r.on && lane == 0) atomicMax(reinterpret_cast<unsigned int*>(a.gscale) + r.group, m);
 }
 
@@ -457,10 +497,11 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const __grid_c
     return kVec == 8 ? __ldcs(reinterpret_cast<const uint32_t*>(codes) + v)
                      : static_cast<uint32_t>(__ldcs(reinterpret_cast<const unsigned short*>(codes) + v));
   };
+  const std::conditional_t<TPR == 32, Offsets, NoOffsets> off(a, lane);
   uint32_t w[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) w[i] = load(t + i * TPR);
-  const RowPlace r = place_of(a, p, lane);
+  const RowPlace r = place_of(a, off, p, lane);
   if (!r.on) return;
   const uint8_t* scales = row_scales(a, r, chunks);
   uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(a.dst) + p * a.ld * (TYPE == 2 ? 4 : 2));

@@ -470,3 +470,23 @@ def test_weights_quantized_in_a_graph():
     eager = binding.Fp4Weights.quantize(w, "nv")
     assert torch.equal(captured.codes, eager.codes) and torch.equal(captured.gscale, eager.gscale)
     assert torch.equal(captured.dequantize(), eager.dequantize())
+
+
+@pytest.mark.parametrize("offsets", [[0, 60, 50], [40, 20, 50], [-5, 10, 50], [0, 10, 1 << 30], [0, 0, 0], [60, 70, 80]])
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_rows_in_wrong_lists_stay_in_bounds(fmt, offsets):
+    """Whatever the lists say, only the call's own buffers are written (guards around them), and no scale is read elsewhere."""
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    x = torch.randn((50, 128), device="cuda").to(BF16)
+    r4 = binding.Fp4Rows(fmt, 128, 2, 50)
+    guarded = {}
+    for name in ("codes", "scales") + (("gscale",) if fmt == "nv" else ()):
+        t = getattr(r4, name)
+        wide = torch.full((t.numel() + 64,), 99, dtype=t.dtype, device="cuda")
+        guarded[name] = wide
+        setattr(r4, name, wide[32:-32])
+    r4.quantize(x, off)
+    y = torch.full((52, 128), 7.0, dtype=BF16, device="cuda")
+    r4.dequantize(off, y=y[1:-1])
+    assert all((t[:32] == 99).all() and (t[-32:] == 99).all() for t in guarded.values())
+    assert (y[0] == 7.0).all() and (y[-1] == 7.0).all()
