@@ -475,21 +475,37 @@ def _lists(of, offsets, counts):
     return offsets, counts
 
 
-def _ld(t) -> int:
-    # (a single row's stride says nothing)
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+def _matrix(what, t, device, dtype, shape_):
+    """A matrix argument, rows of contiguous elements: its pointer and row stride."""
+    if t.dtype == dtype and t.shape == shape_ and t.device == device:  # (the common way, in few calls)
+        ld, one = t.stride()
+        if one == 1 and shape_[0] > 1:
+            return t.data_ptr(), ld
+    _check(what, t, device, dtype, shape_, rows=True)
+    return t.data_ptr(), t.stride(0) if shape_[0] > 1 else (shape_[1] + 7) // 8 * 8  # (one row's stride says nothing)
+
+
+_torch = None
+
+
+def _empty(shape_, dtype, device):
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.empty(shape_, dtype=dtype, device=device)
 
 
 _C = None  # torch's native module, once it is needed
 
 
-def _enqueue(name, device, fn, *args):
-    """fn(*args, stream) with ``device`` current, on its current stream; MoeError if it fails."""
+def _enqueue(name, device, *args):
+    """name(*args, stream) of the library with ``device`` current, on its current stream; MoeError if it fails."""
     global _C
     if _C is None:
         from torch import _C as native
         _C = native
-    index = device.index
+    index, fn = device.index, getattr(_lib or load(), name)
     if _C._cuda_getDevice() == index:  # (the tensors exist: CUDA is initialised)
         st = fn(*args, _C._cuda_getCurrentRawStream(index))
     else:
@@ -503,29 +519,25 @@ def _enqueue(name, device, fn, *args):
 def swiglu(h, act=None):
     """SiLU(gate) * up of rows h = [gate | up] (moe_swiglu), on the current stream of h's device."""
     rows, two_i = h.shape
-    _check("h", h, h.device, h.dtype, (rows, two_i // 2 * 2), rows=True)
+    i, device, dtype = two_i // 2, h.device, h.dtype
+    hp, ldh = _matrix("h", h, device, dtype, (rows, 2 * i))
     if act is None:
-        import torch
-        act = torch.empty((rows, two_i // 2), dtype=h.dtype, device=h.device)
-    else:
-        _check("act", act, h.device, h.dtype, (rows, two_i // 2), rows=True)
-    _enqueue("moe_swiglu", h.device, moe_swiglu, _type_of(h.dtype), rows, two_i // 2, _ptr(h), _ld(h), _ptr(act),
-             _ld(act))
+        act = _empty((rows, i), dtype, device)
+    ap, lda = _matrix("act", act, device, dtype, (rows, i))
+    _enqueue("moe_swiglu", device, _type_of(dtype), rows, i, hp, ldh, ap, lda)
     return act
 
 
 def swiglu_grad(h, dact, dh=None):
     """d[gate | up] from dact (moe_swiglu_grad), on the current stream of h's device."""
     rows, two_i = h.shape
-    _check("h", h, h.device, h.dtype, (rows, two_i // 2 * 2), rows=True)
-    _check("dact", dact, h.device, h.dtype, (rows, two_i // 2), rows=True)
+    i, device, dtype = two_i // 2, h.device, h.dtype
+    hp, ldh = _matrix("h", h, device, dtype, (rows, 2 * i))
+    ap, lda = _matrix("dact", dact, device, dtype, (rows, i))
     if dh is None:
-        import torch
-        dh = torch.empty((rows, two_i), dtype=h.dtype, device=h.device)
-    else:
-        _check("dh", dh, h.device, h.dtype, (rows, two_i), rows=True)
-    _enqueue("moe_swiglu_grad", h.device, moe_swiglu_grad, _type_of(h.dtype), rows, two_i // 2, _ptr(h), _ld(h),
-             _ptr(dact), _ld(dact), _ptr(dh), _ld(dh))
+        dh = _empty((rows, 2 * i), dtype, device)
+    dp, ldd = _matrix("dh", dh, device, dtype, (rows, 2 * i))
+    _enqueue("moe_swiglu_grad", device, _type_of(dtype), rows, i, hp, ldh, ap, lda, dp, ldd)
     return dh
 
 
@@ -534,11 +546,11 @@ class _Workspace:
 
     called = False
 
-    def _entered(self, rows):
-        # a call without rows enqueues nothing: what a call before it reported is not its own
+    def _call(self, name, shape_, *args):
         self.called = True
-        if rows == 0:
+        if shape_.rows == 0:  # nothing is enqueued: what a call before it reported is not its own
             self.workspace[:16].zero_()
+        _enqueue(name, self.device, ctypes.byref(shape_), *args, self.workspace.data_ptr(), self.workspace.numel())
 
     def device_status(self):
         """(status, detail) of the last call, after waiting for the current stream (moe_device_status)."""
@@ -574,51 +586,45 @@ class GroupedProducts(_Workspace):
             s = self._shape = grouped_shape(self.groups, self.N, self.K, rows, _type_of(self.dtype))
         return s
 
-    def _rows(self, what, t, rows, width):
-        if t is None:
-            import torch
-            return torch.empty((rows, width), dtype=self.dtype, device=self.device)
-        return _check(what, t, self.device, self.dtype, (rows, width), rows=True)
-
-    def _call(self, name, fn, shape_, *args):
-        self._entered(shape_.rows)
-        _enqueue(name, self.device, fn, shape_, *args, self.workspace.data_ptr(), self.workspace.numel())
+    def _weights(self, w):
+        return _check("w", w, self.device, self.dtype, (self.groups, self.N, self.K)).data_ptr()
 
     def forward(self, x, w, offsets=None, counts=None, y=None):
         """y[p] = x[p] w_g^T for the rows p of every group g; other rows of y stay as they are."""
         rows = x.shape[0]
-        self._rows("x", x, rows, self.K)
-        _check("w", w, self.device, self.dtype, (self.groups, self.N, self.K))
-        y = self._rows("y", y, rows, self.N)
-        self._call("moe_grouped_gemm", moe_grouped_gemm, self.shape(rows), _ptr(x), _ld(x), _ptr(w),
-                   *_lists(self, offsets, counts), _ptr(y), _ld(y))
+        xp, ldx = _matrix("x", x, self.device, self.dtype, (rows, self.K))
+        if y is None:
+            y = _empty((rows, self.N), self.dtype, self.device)
+        yp, ldy = _matrix("y", y, self.device, self.dtype, (rows, self.N))
+        self._call("moe_grouped_gemm", self.shape(rows), xp, ldx, self._weights(w), *_lists(self, offsets, counts), yp,
+                   ldy)
         return y
 
     def dgrad(self, dy, w, offsets=None, counts=None, dx=None):
         """dx[p] = dy[p] w_g."""
         rows = dy.shape[0]
-        self._rows("dy", dy, rows, self.N)
-        _check("w", w, self.device, self.dtype, (self.groups, self.N, self.K))
-        dx = self._rows("dx", dx, rows, self.K)
-        self._call("moe_grouped_gemm_dgrad", moe_grouped_gemm_dgrad, self.shape(rows), _ptr(dy), _ld(dy), _ptr(w),
-                   *_lists(self, offsets, counts), _ptr(dx), _ld(dx))
+        yp, ldy = _matrix("dy", dy, self.device, self.dtype, (rows, self.N))
+        if dx is None:
+            dx = _empty((rows, self.K), self.dtype, self.device)
+        xp, ldx = _matrix("dx", dx, self.device, self.dtype, (rows, self.K))
+        self._call("moe_grouped_gemm_dgrad", self.shape(rows), yp, ldy, self._weights(w),
+                   *_lists(self, offsets, counts), xp, ldx)
         return dx
 
     def wgrad(self, dy, x, offsets=None, counts=None, dw=None, dtype=None, accumulate=False):
         """dw_g = sum over the group's rows of dy[p]^T x[p], in ``dtype`` (fp32 or the operands' type, the default)
         or dw's type; accumulate (fp32): added to dw."""
         rows = x.shape[0]
-        self._rows("dy", dy, rows, self.N)
-        self._rows("x", x, rows, self.K)
+        yp, ldy = _matrix("dy", dy, self.device, self.dtype, (rows, self.N))
+        xp, ldx = _matrix("x", x, self.device, self.dtype, (rows, self.K))
         if dw is None:
             if accumulate:
                 raise ValueError("accumulate adds to dw: pass it")
-            import torch
-            dw = torch.empty((self.groups, self.N, self.K), dtype=dtype or self.dtype, device=self.device)
+            dw = _empty((self.groups, self.N, self.K), dtype or self.dtype, self.device)
         else:
             _check("dw", dw, self.device, dtype or dw.dtype, (self.groups, self.N, self.K))
-        self._call("moe_grouped_gemm_wgrad", moe_grouped_gemm_wgrad, self.shape(rows), _ptr(dy), _ld(dy), _ptr(x),
-                   _ld(x), *_lists(self, offsets, counts), _ptr(dw), _type_of(dw.dtype), accumulate)
+        self._call("moe_grouped_gemm_wgrad", self.shape(rows), yp, ldy, xp, ldx, *_lists(self, offsets, counts),
+                   dw.data_ptr(), _type_of(dw.dtype), 1 if accumulate else 0)
         return dw
 
 
@@ -672,12 +678,14 @@ class Fp4Rows:
 
     def quantize(self, x, offsets=None, counts=None):
         """x [rows, K] (bf16, fp16 or fp32) to 4 bits; returns self."""
-        self.ensure_capacity(x.shape[0])
-        _check("x", x, self.device, x.dtype, (x.shape[0], self.K), rows=True)
-        lists = _lists(self, offsets, counts)
-        _enqueue("moe_fp4_quantize", self.device, moe_fp4_quantize, self.shape(x.shape[0]), _type_of(x.dtype), _ptr(x),
-                 _ld(x), *lists, _ptr(self.codes), _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_ROW)
-        self.rows, self._listed = x.shape[0], offsets is not None
+        rows = x.shape[0]
+        xp, ldx = _matrix("x", x, self.device, x.dtype, (rows, self.K))
+        lists, type_ = _lists(self, offsets, counts), _type_of(x.dtype)
+        self.ensure_capacity(rows)
+        self.rows = 0  # (until they are on their way)
+        _enqueue("moe_fp4_quantize", self.device, ctypes.byref(self.shape(rows)), type_, xp, ldx, *lists,
+                 self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.gscale), MOE_SCALE_PER_ROW)
+        self.rows, self._listed = rows, offsets is not None
         return self
 
     def check_lists(self, offsets):
@@ -691,11 +699,10 @@ class Fp4Rows:
         if y is None:
             import torch
             y = torch.empty((self.rows, self.K), dtype=dtype or torch.bfloat16, device=self.device)
-        else:
-            _check("y", y, self.device, dtype or y.dtype, (self.rows, self.K), rows=True)
-        lists = _lists(self, offsets, counts)
-        _enqueue("moe_fp4_dequantize", self.device, moe_fp4_dequantize, self.shape(self.rows), _ptr(self.codes),
-                 _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_ROW, *lists, _type_of(y.dtype), _ptr(y), _ld(y))
+        yp, ldy = _matrix("y", y, self.device, dtype or y.dtype, (self.rows, self.K))
+        _enqueue("moe_fp4_dequantize", self.device, ctypes.byref(self.shape(self.rows)), self.codes.data_ptr(),
+                 self.scales.data_ptr(), _ptr(self.gscale), MOE_SCALE_PER_ROW, *_lists(self, offsets, counts),
+                 _type_of(y.dtype), yp, ldy)
         return y
 
 
@@ -741,7 +748,7 @@ class Fp4Weights(_Workspace):
         codes = torch.empty((groups, N, K // 2), dtype=torch.uint8, device=w.device)
         scales = torch.empty(n_scales, dtype=torch.uint8, device=w.device)
         gscale = torch.empty(groups, dtype=torch.float32, device=w.device) if format == "nv" else None
-        _enqueue("moe_fp4_quantize", w.device, moe_fp4_quantize, s, _type_of(w.dtype), _ptr(w), K, None, None,
+        _enqueue("moe_fp4_quantize", w.device, ctypes.byref(s), _type_of(w.dtype), _ptr(w), K, None, None,
                  _ptr(codes), _ptr(scales), _ptr(gscale), MOE_SCALE_PER_GROUP)
         return cls(format, codes, scales, gscale)
 
@@ -749,8 +756,8 @@ class Fp4Weights(_Workspace):
         """The values the weights stand for, [groups, N, K] in ``dtype`` (bf16 by default)."""
         import torch
         w = torch.empty((self.groups, self.N, self.K), dtype=dtype or torch.bfloat16, device=self.device)
-        _enqueue("moe_fp4_dequantize", self.device, moe_fp4_dequantize,
-                 fp4_shape(self.format, self.groups, self.groups * self.N, self.K), _ptr(self.codes),
+        _enqueue("moe_fp4_dequantize", self.device,
+                 ctypes.byref(fp4_shape(self.format, self.groups, self.groups * self.N, self.K)), _ptr(self.codes),
                  _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_GROUP, None, None, _type_of(w.dtype), _ptr(w),
                  self.K)
         return w
@@ -763,14 +770,11 @@ class Fp4Weights(_Workspace):
         if y is None:
             import torch
             y = torch.empty((rows.rows, self.N), dtype=dtype or torch.bfloat16, device=self.device)
-        else:
-            _check("y", y, self.device, dtype or y.dtype, (rows.rows, self.N), rows=True)
-        lists = _lists(self, offsets, counts)
-        self._entered(rows.rows)
-        _enqueue("moe_fp4_gemm", self.device, moe_fp4_gemm,
-                 grouped_shape(self.groups, self.N, self.K, rows.rows, _type_of(y.dtype)), self.format,
-                 _ptr(rows.codes), _ptr(rows.scales), _ptr(rows.gscale), _ptr(self.codes), _ptr(self.scales),
-                 _ptr(self.gscale), *lists, _ptr(y), _ld(y), _ptr(self.workspace), self.workspace.numel())
+        yp, ldy = _matrix("y", y, self.device, dtype or y.dtype, (rows.rows, self.N))
+        self._call("moe_fp4_gemm", grouped_shape(self.groups, self.N, self.K, rows.rows, _type_of(y.dtype)),
+                   self.format, rows.codes.data_ptr(), rows.scales.data_ptr(), _ptr(rows.gscale),
+                   self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.gscale), *_lists(self, offsets, counts),
+                   yp, ldy)
         return y
 
 

@@ -490,3 +490,12 @@ def test_rows_in_wrong_lists_stay_in_bounds(fmt, offsets):
     r4.dequantize(off, y=y[1:-1])
     assert all((t[:32] == 99).all() and (t[-32:] == 99).all() for t in guarded.values())
     assert (y[0] == 7.0).all() and (y[-1] == 7.0).all()
+
+
+def test_a_refused_quantize_leaves_the_rows_before():
+    x = torch.randn((10, 64), device="cuda").to(BF16)
+    r4 = binding.Fp4Rows("nv", 64, 1, 10).quantize(x)
+    want = r4.dequantize()
+    with pytest.raises(TypeError):
+        r4.quantize(torch.zeros((500, 64), device="cuda").double())
+    assert torch.equal(r4.dequantize(), want)
