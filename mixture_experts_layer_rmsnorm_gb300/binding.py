@@ -729,11 +729,17 @@ class Fp4Weights(_Workspace):
             if gscale is None:
                 raise ValueError("NVFP4 weights have an fp32 scale for each group")
             _check("gscale", gscale, self.device, torch.float32, (self.groups,))
-        self.codes, self.scales, self.gscale = codes, scales, gscale
+        self.codes, self.scales, self.gscale, self._shape = codes, scales, gscale, None
         st, n = moe_grouped_workspace_size(grouped_shape(self.groups, self.N, self.K, 0))
         if st != MOE_OK:
             raise MoeError(st, "moe_grouped_workspace_size")
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def shape(self, rows, type) -> MoeGroupedShape:
+        s = self._shape  # (kept by one assignment: other host threads may ask too)
+        if s is None or s.rows != rows or s.type != type:
+            s = self._shape = grouped_shape(self.groups, self.N, self.K, rows, type)
+        return s
 
     @classmethod
     def quantize(cls, w, format):
@@ -771,8 +777,7 @@ class Fp4Weights(_Workspace):
             import torch
             y = torch.empty((rows.rows, self.N), dtype=dtype or torch.bfloat16, device=self.device)
         yp, ldy = _matrix("y", y, self.device, dtype or y.dtype, (rows.rows, self.N))
-        self._call("moe_fp4_gemm", grouped_shape(self.groups, self.N, self.K, rows.rows, _type_of(y.dtype)),
-                   self.format, rows.codes.data_ptr(), rows.scales.data_ptr(), _ptr(rows.gscale),
+        self._call("moe_fp4_gemm", self.shape(rows.rows, _type_of(y.dtype)), self.format, rows.codes.data_ptr(), rows.scales.data_ptr(), _ptr(rows.gscale),
                    self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.gscale), *_lists(self, offsets, counts),
                    yp, ldy)
         return y

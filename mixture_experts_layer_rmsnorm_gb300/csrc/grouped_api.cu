@@ -158,11 +158,27 @@ moe::GroupedPlanArgs plan_args(const moe_grouped_shape* s, const Layout& L, void
   return p;
 }
 
-// The tile plan follows the rows a group can be expected to hold: up to 16,
-// the product is bound by streaming the weights once (32-row units, stream-K),
-// above that by reuse of the weight tiles (units of up to 512 rows on CTA pairs; 4 bits: 256).
-GroupedPlan choose_plan(const moe_grouped_shape* s) {
-  return s->rows <= int64_t(16) * s->groups ? GroupedPlan::kSmall : GroupedPlan::kLarge;
+// More work units than an int counts, in the smallest ones.
+bool too_many_units(const moe_grouped_shape* s, int F) {
+  return (s->rows / 32 + s->groups) * ((F + 127) / 128) >= (int64_t(1) << 31);
+}
+
+// The tile plan follows the rows a group can be expected to hold: few, the product is
+// bound by streaming the weights once (32-row units on single CTAs, stream-K), else by reuse of
+// the weight tiles (units of up to 512 rows, 4 bits 256, on CTA pairs).  Up to 16 rows: single CTAs, also because
+// fewer groups than all may hold them.  Up to 24 (of ragged groups few are longer than
+// 32 rows then): single CTAs where whole units leave pairs idle for over 5% of their waves, or where a
+// 4-bit unit is short (K <= 2048).  Measured (us, pairs / single CTAs), 16 bits forward: 16 groups, N = K = 4096 (3.4
+// waves), 16 rows: 91 / 83, 24: 102 / 85; 64 groups, N = 8192, K = 4096 (26.9 waves), 16 rows: 616 / 628, 24: 627 / 647,
+// 64: 649 / 1438.  NVFP4 of these: 37 / 32, 37 / 34; 187 / 187, 189 / 197, 207 / 308; 256 groups, N = 1536, K = 2048, 16
+// rows: 106 / 78, 24: 107 / 81, 64: 125 / 137.
+GroupedPlan choose_plan(const moe_grouped_shape* s, int F, int sms, bool fp4) {
+  if (s->rows <= int64_t(16) * s->groups) return GroupedPlan::kSmall;
+  if (s->rows > int64_t(24) * s->groups) return GroupedPlan::kLarge;
+  const int tile = moe::grouped_tile(GroupedPlan::kLarge);
+  const int64_t units = int64_t(s->groups) * ((F + tile - 1) / tile), pairs = sms / 2 > 0 ? sms / 2 : 1;
+  const bool idle = (units + pairs - 1) / pairs * pairs * 20 > units * 21;
+  return idle || (fp4 && s->K <= 2048) ? GroupedPlan::kSmall : GroupedPlan::kLarge;
 }
 
 // forward (F = N features, R = K) and input gradient (F = K, R = N)
@@ -176,12 +192,12 @@ moe_status rows_product(GroupedOp op, const moe_grouped_shape* s, const void* in
   if ((st = check_rows(out, s->rows, ldout, F)) != MOE_OK) return st;
   if (!w || !aligned(w, 16)) return MOE_ERR_INVALID_ARG;
   if ((st = check_call(s, offsets, counts, ws, ws_bytes)) != MOE_OK) return st;
-  const GroupedPlan plan = choose_plan(s);
-  const int tile = moe::grouped_tile(plan), tiles = (F + tile - 1) / tile;
-  if ((s->rows / 32 + s->groups) * tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (too_many_units(s, F)) return MOE_ERR_UNSUPPORTED;
   if (s->rows == 0) return MOE_OK;
   const int sms = num_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
+  const GroupedPlan plan = choose_plan(s, F, sms, false);
+  const int tile = moe::grouped_tile(plan), tiles = (F + tile - 1) / tile;
   const int bn = moe::grouped_bn(plan, s->rows, s->groups, tiles, sms);
   CUtensorMap tw, tx, tx32;
   if (!make_matrix_map(&tw, s->type, w, s->groups, s->N, s->K, op == GroupedOp::kForward ? 128 : 64) ||
@@ -424,13 +440,13 @@ moe_status moe_fp4_gemm(const moe_grouped_shape* shape, int32_t format, const ui
   if (nv && ((s->rows > 0 && (!x_gscale || !aligned(x_gscale, 4))) || !w_gscale || !aligned(w_gscale, 4)))
     return MOE_ERR_INVALID_ARG;
   if ((st = check_call(s, offsets, counts, workspace, workspace_bytes)) != MOE_OK) return st;
-  const GroupedPlan plan = choose_plan(s);
-  const int bn = moe::fp4_bn(plan), tile = moe::fp4_tile(plan);
-  const int tiles = (s->N + tile - 1) / tile;
-  if ((s->rows / bn + s->groups) * tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (too_many_units(s, s->N)) return MOE_ERR_UNSUPPORTED;
   if (s->rows == 0) return MOE_OK;
   const int sms = num_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
+  const GroupedPlan plan = choose_plan(s, s->N, sms, true);
+  const int bn = moe::fp4_bn(plan), tile = moe::fp4_tile(plan);
+  const int tiles = (s->N + tile - 1) / tile;
   CUtensorMap tw, tx;
   if (!make_codes_map(&tw, w_codes, s->K, s->N, s->groups, 128) ||
       !make_codes_map(&tx, x_codes, s->K, s->rows, 0, static_cast<uint32_t>(moe::fp4_tok_box(plan))))

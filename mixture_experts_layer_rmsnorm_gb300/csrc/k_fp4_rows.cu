@@ -24,7 +24,7 @@
 //     quotient lies at a border, cost a second conversion, the slowest
 //     instruction here: 105 us for 134 M elements.)
 // Measured, 134 M bf16 elements: NVFP4 65 us (0.78 of the copy rate), MXFP4 48 to
-// 50 us (1.0); back to 16 bits 52 us, to fp32 93 us.  1.07 G elements to MXFP4 and back 771 us.
+// 50 us (1.0); back to 16 bits 50 us, to fp32 88 us.  1.07 G elements to MXFP4 and back 755 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -69,11 +69,11 @@ struct NoOffsets {
 // could lead to, are off.
 template <typename Ahead>
 __device__ __forceinline__ RowPlace place_of(const Fp4RowsArgs& a, const Ahead& off, int p, int lane) {
-  constexpr bool kAhead = std::is_same_v<Ahead, Offsets>;
+  constexpr bool kRead = std::is_same_v<Ahead, Offsets>;
   RowPlace r{0, 0, 0, false};
   int start, count;
-  if (kAhead && a.offsets && a.G <= kOneRound) {
-    if constexpr (kAhead) {
+  if (kRead && a.offsets && a.G <= kOneRound) {
+    if constexpr (kRead) {
       int n = 0, from = -1, to = 0x7FFFFFFF;
 #pragma unroll
       for (int i = 0; i <= kOneRound / 32; ++i) {
@@ -480,11 +480,13 @@ __device__ __forceinline__ void decode4(uint32_t w, float* f) {
   }
 }
 
+constexpr int kAhead = 8;
+
 // A thread writes 16 bytes at a time (8 elements of 16 bits or 4 of 32), so a
 // warp's stores are contiguous; kAhead of them per round, their loads first.
 template <Fp4Format F, int TYPE, int TPR>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const __grid_constant__ Fp4RowsArgs a) {
-  constexpr int kVec = TYPE == 2 ? 4 : 8, kAhead = 8;
+  constexpr int kVec = TYPE == 2 ? 4 : 8;
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, t = threadIdx.x % TPR;
@@ -549,9 +551,16 @@ cudaError_t quantize_t(const Fp4RowsArgs& a, cudaStream_t stream) {
                     dim3(kThreads), 0, stream, a);
 }
 
-// Threads per row.  Few rows: as many as spread a row over the GPU's warps best.
-// Many: as few as hold a row's vectors at once where they have to (NVFP4's scale
-// per row), else a warp, so that the look-up of the row's place serves most elements.
+// Threads per row: as few as hold its vectors at once, `hold` each; more where there are
+// few rows, up to `most` threads in all.
+int threads_per_row(int vecs, int hold, int64_t rows, int64_t most) {
+  int tpr = 32;
+  while (tpr < 256 && vecs > tpr * hold) tpr *= 2;
+  while (tpr < 256 && tpr < vecs && rows * tpr * 2 <= most) tpr *= 2;
+  return tpr;
+}
+constexpr int64_t kResident = 152 * 1024;  // threads of the quantizer that run at once
+
 template <Fp4Format F, int TYPE>
 cudaError_t quantize(const Fp4RowsArgs& a, cudaStream_t stream) {
   const bool whole = F == Fp4Format::kNv && !a.per_group;
@@ -565,14 +574,18 @@ cudaError_t quantize(const Fp4RowsArgs& a, cudaStream_t stream) {
     if ((e = cudaLaunchKernelEx(&cfg, fp4_group_amax_kernel<TYPE>, a)) != cudaSuccess) return e;
   }
   const int vecs = a.K / kElems;
-  constexpr int kHold = hold_of(TYPE);
-  const bool many = a.rows >= 8192;
-  // vectors a thread is to hold: all of kHold, or two
-  const int per = many ? kHold : 1;
-  const cudaError_t e = vecs <= 32 * per || (!whole && many) ? quantize_t<F, TYPE, 32>(a, stream)
-                        : vecs <= 64 * per                   ? quantize_t<F, TYPE, 64>(a, stream)
-                        : vecs <= 128 * per                  ? quantize_t<F, TYPE, 128>(a, stream)
-                                                             : quantize_t<F, TYPE, 256>(a, stream);
+  // A scale per row asks for the row's maximum before any code, so all of its vectors are to be
+  // held; else a warp, whose look-up of the place then serves most elements.  Measured (us, bf16,
+  // 32 / 64 / 128 / 256 threads): NVFP4, 64 x 4096: 5.0 / 3.2 / 2.7 / 2.3, 1021 x 7168: 7.7 / 6.3 / 6.4 / 6.9,
+  // 2048 x 4096: 6.6 / 6.4 / 7.7 / 9.6, 32768 x 4096: 71 / 65 / 93 / 127, 8192 x 8192: 44 / 42 / 35 / 45;
+  // MXFP4, 64 x 4096: 3.1 / 2.2 / 1.9 / 1.8, 2048 x 4096: 4.3 / 4.2 / 4.4 / 5.7, 32768 x 4096: 48 / 49 / 55 / 79.
+  cudaError_t e;
+  switch (threads_per_row(vecs, whole ? hold_of(TYPE) : vecs, a.rows, kResident)) {
+    case 32: e = quantize_t<F, TYPE, 32>(a, stream); break;
+    case 64: e = quantize_t<F, TYPE, 64>(a, stream); break;
+    case 128: e = quantize_t<F, TYPE, 128>(a, stream); break;
+    default: e = quantize_t<F, TYPE, 256>(a, stream);
+  }
   if (e != cudaSuccess || F != Fp4Format::kNv || !a.per_group) return e;
   return launch_pdl(fp4_group_scale_kernel, dim3((a.G + 127) / 128), dim3(128), 0, stream, a.gscale, a.G);
 }
@@ -586,9 +599,16 @@ cudaError_t dequantize_t(const Fp4RowsArgs& a, cudaStream_t stream) {
 
 template <Fp4Format F, int TYPE>
 cudaError_t dequantize(const Fp4RowsArgs& a, cudaStream_t stream) {
-  const int vecs = a.K / (TYPE == 2 ? 4 : 8), per = a.rows >= 8192 ? 8 : 2;
-  if (vecs <= 32 * per || a.rows >= 8192) return dequantize_t<F, TYPE, 32>(a, stream);
-  return vecs <= 128 * per ? dequantize_t<F, TYPE, 128>(a, stream) : dequantize_t<F, TYPE, 256>(a, stream);
+  // (its loads are in flight kAhead at a time.)  Measured (us, 32 / 64 / 128 / 256 threads): to fp32, 1021 x
+  // 7168: 9.9 / 7.6 / 8.7 / 6.7, 32768 x 4096: 93 / 91 / 88 / 87, 8192 x 8192: 62 / 52 / 48 / 46; to 16 bits, 64 x 4096:
+  // 3.4 / 2.6 / 2.2 / 2.2, 2048 x 4096: 4.7 / 5.7 / 4.6 / 6.3, 32768 x 4096: 52 / 50 / 52 / 78, 8192 x 8192: 30 / 33 / 26 /
+  // 28, 32768 x 1408: 20 / 24 / 37 / 65.
+  switch (threads_per_row(a.K / (TYPE == 2 ? 4 : 8), kAhead, a.rows, 2 * kResident)) {
+    case 32: return dequantize_t<F, TYPE, 32>(a, stream);
+    case 64: return dequantize_t<F, TYPE, 64>(a, stream);
+    case 128: return dequantize_t<F, TYPE, 128>(a, stream);
+    default: return dequantize_t<F, TYPE, 256>(a, stream);
+  }
 }
 
 }  // namespace

@@ -73,6 +73,8 @@ CASES = {
     "many_groups": ([(7 * i) % 5 for i in range(300)], 136, 72, BF16, 0, 2, 0),
     "most_groups": ([(i * i) % 41 for i in range(1024)], 64, 64, FP16, 0, 0, 0),
     "long_groups": ([2500, 0, 769, 768, 1537], 264, 136, BF16, 0, 1, 0),
+    "some_rows": ([20, 40, 0, 17, 24, 21, 19], 264, 200, BF16, 0, 3, 0),
+    "some_rows_whole_wave": ([19 + i % 5 for i in range(76)], 256, 72, FP16, 0, 0, 8),
     "no_rows_at_all": ([0, 0, 0], 128, 64, BF16, 0, 4, 0),
 }
 

@@ -227,6 +227,8 @@ GEMMS = {
     "small": ([0, 1, 15, 16, 17, 31, 32, 33, 0, 2], 264, 544, 0, 0, False),
     "small_stream_k": ([3, 0, 9, 12], 1032, 4096, 5, 3, False),
     "small_deep_group": ([300] + [0] * 30, 136, 320, 0, 0, False),
+    "some_rows": ([20, 40, 0, 17, 24, 21, 19], 264, 544, 0, 0, False),
+    "some_rows_whole_wave": ([19 + i % 5 for i in range(76)], 72, 2080, 0, 3, False),
     "large": ([255, 256, 257, 0, 1, 129, 511], 520, 288, 0, 0, False),
     "large_gap": ([100, 700, 0, 33], 776, 1152, 9, 40, False),
     "large_k64": ([300, 20], 256, 64, 0, 0, False),
