@@ -34,6 +34,17 @@ __device__ __forceinline__ void st_release(int32_t* p, int v) {
   asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// Bounded wait of one thread for a flag another CTA sets (non-zero).
+__device__ __forceinline__ bool wait_flag_thread(const int32_t* flag, const volatile int* abort_flag,
+                                                 uint64_t timeout_ns) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (ld_acquire(flag) == 0) {
+    if (*abort_flag || ptx::globaltimer_ns() - t0 > timeout_ns) return false;
+    __nanosleep(64);
+  }
+  return true;
+}
+
 // Bounded wait of one warp for a flag another CTA sets (non-zero); the result
 // is warp-uniform.  Gives up after timeout_ns or once *abort_flag is set.
 __device__ __forceinline__ bool wait_flag(const int32_t* flag, const volatile int* abort_flag, uint64_t timeout_ns) {

@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
   // single CTAs: a stream-K range; pairs: whole units as they are handed out
   auto rg = [&] {
     if constexpr (PAIR)
-      return PairWalk{PairUnits(sched, total_units, kWaitTimeoutNs, abort_flag), kblocks};
+      return PairWalk{PairUnits(sched, total_units, kWaitTimeoutNs, abort_flag, warp == 0 && !leader), kblocks};
     else
       return GroupedRange(total_units, kblocks, worker, workers);
   }();
@@ -543,6 +543,11 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
           const int64_t unit_end = static_cast<int64_t>(u + 1) * kblocks;
           while (c_last + 1 < workers && rg.begin_of(c_last + 1) < unit_end) ++c_last;
         }
+        if (!rg.wait_partials(a.flags + q, worker + 1, c_last, abort_flag)) {
+          ok = false;
+          where = kWaitPartials;
+          break;
+        }
         for (int c0 = 0; c0 < un.n; c0 += 16) {
           uint32_t r[16];
           __syncwarp();  // tcgen05.ld is warp-aligned
@@ -551,21 +556,12 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
           float v[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-          bool good = true;
+#pragma unroll 2
           for (int c = worker + 1; c <= c_last; ++c) {
             if (rg.begin_of(c) == rg.begin_of(c + 1)) continue;  // empty range
-            if (c0 == 0 && !wait_flag(a.flags + c * 4 + q, abort_flag, kWaitTimeoutNs)) {
-              good = false;
-              break;
-            }
             const float* slot = a.partials + static_cast<int64_t>(c) * BN * 128;
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] += __ldcg(slot + (c0 + j) * 128 + row);
-          }
-          if (!__all_sync(0xFFFFFFFFu, good)) {
-            ok = false;
-            where = kWaitPartials;
-            break;
           }
           if (mine) {
 #pragma unroll

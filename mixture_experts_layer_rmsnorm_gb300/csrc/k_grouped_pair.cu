@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total_units = tables.unit_off[a.G];
   const int kblocks = (a.R + 63) / 64;
   GroupedUnits units(tables, a.G, 1, a.bn, true);  // each warp walks its role's units
-  PairUnits walk(sched, total_units, kWaitTimeoutNs, abort_flag);
+  PairUnits walk(sched, total_units, kWaitTimeoutNs, abort_flag, warp == 0 && !leader);
 
   if (warp == 0 || warp == 2 + kEpiWarps) {
     // ---------------- TMA producers: one warp for the weight tiles, one for the

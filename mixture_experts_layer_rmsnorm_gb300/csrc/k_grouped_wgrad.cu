@@ -27,7 +27,7 @@
 // Bound: by writing dw where groups are short (a tile of fp32 moves 128 KB per
 // CTA for 64 KB of operands per 64 rows), else by the tensor cores; in between by shared memory, which
 // the operands cross twice and the tile too.  Measured, fp32: 64 groups of 32768 rows in all,
-// N = K = 4096: 1026 us under the power cap (0.69 of the bytes' time; its L1 / shared-memory pipe
+// N = K = 4096: 983 to 1035 us under the power cap (0.72 to 0.69 of the bytes' time; its L1 / shared-memory pipe
 // is 81% busy); 64 x 512 even rows 895 us, into 16 bits 722 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

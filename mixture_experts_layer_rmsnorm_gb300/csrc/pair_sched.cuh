@@ -3,7 +3,13 @@
 // Units of ragged groups differ in length, and their order (a weight tile's
 // chunks next to one another, for L2) is periodic: dealt round-robin, one
 // worker would get every short last chunk and its neighbour every full one.  So
-// a pair takes the next unit from a counter in global memory.  The odd CTA's
+// a pair starts with the unit of its index and takes the next ones from a counter in global
+// memory, each when its weights' producer starts on the last; one earlier where there are at
+// least eight units a pair, to hide the counter's latency (NVFP4, 64 x 512 rows, N = K = 4096: 239 -> 231 us).
+// A pair that fetches as far as it has slots takes five units of a small product while others
+// have none, more with several fetches under way (3190 rows of 59 groups, N = 360, K = 160, NVFP4: 19.6
+// instead of 15.4 us; 64 ragged groups of about 512 rows, N = 8192, K = 4096: 1375 instead of 1351; the input
+// gradient of 134 rows, N = 2192, K = 1864, with one, two and four fetches under way: 19, 32, 54, here 20).  The odd CTA's
 // MMA warp, which has no MMAs to issue, is the scheduler: it fetches units
 // ahead and puts them into a ring of kSchedSlots in both CTAs' shared memory,
 // where every other warp of the pair reads them in order.  Which pair computes
@@ -17,44 +23,45 @@
 namespace moe {
 
 constexpr int kSchedSlots = 4;
-constexpr int kSchedBytes = kSchedSlots * (8 + 8 + 4) + 16;
+constexpr int kSchedBytes = kSchedSlots * (8 + 8 + 8 + 4) + 16;
 
 struct PairSched {
   uint64_t* full;   // a slot's unit is there (in each CTA)
   uint64_t* empty;  // every warp of the pair has read it (the odd CTA's)
+  uint64_t* taken;  // the odd CTA's producer of the weights has read it
   volatile int32_t* unit;
 
   __device__ explicit PairSched(uint8_t* smem)
-      : full(reinterpret_cast<uint64_t*>(smem)), empty(full + kSchedSlots),
-        unit(reinterpret_cast<volatile int32_t*>(empty + kSchedSlots)) {}
+      : full(reinterpret_cast<uint64_t*>(smem)), empty(full + kSchedSlots), taken(empty + kSchedSlots),
+        unit(reinterpret_cast<volatile int32_t*>(taken + kSchedSlots)) {}
 
   // one thread of each CTA, before the pair's cluster barrier; readers: warps of both CTAs that walk the units
   __device__ __forceinline__ void init(int readers) const {
     for (int s = 0; s < kSchedSlots; ++s) {
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], readers);
+      ptx::mbar_init(&taken[s], 1);
     }
   }
 
-  // The scheduler (one thread of the odd CTA): units counter, counter + 1, ...
+  // The scheduler (one thread of the odd CTA): units pair, then pairs + counter, ...
   // until one >= total, which ends the readers' walks.  False: a wait ran out.
   __device__ bool schedule(int32_t* counter, int total, uint64_t timeout_ns, const volatile int* abort) const {
     using namespace ptx;
-    int slot = 0;
-    uint32_t phase = 0;
-    while (true) {
-      const int u = atomicAdd(counter, 1);
-      if (!mbar_wait(&empty[slot], phase ^ 1u, timeout_ns, abort)) return false;
+    const int pairs = static_cast<int>(gridDim.x >> 1), early = total >= 8 * pairs ? 1 : 0;
+    int u = static_cast<int>(blockIdx.x >> 1);
+    for (int i = 0;; ++i) {
+      const int slot = i % kSchedSlots;
+      if (!mbar_wait(&empty[slot], (i / kSchedSlots & 1) ^ 1u, timeout_ns, abort)) return false;
       unit[slot] = u;
       const uint32_t theirs = mapa_shared(smem_u32(const_cast<int32_t*>(unit) + slot), 0);
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(theirs), "r"(u) : "memory");
       mbar_arrive_cluster(mapa_shared(smem_u32(&full[slot]), 0));
       mbar_arrive(&full[slot]);
       if (u >= total) return true;
-      if (++slot == kSchedSlots) {
-        slot = 0;
-        phase ^= 1u;
-      }
+      const int last = i - early;
+      if (last >= 0 && !mbar_wait(&taken[last % kSchedSlots], last / kSchedSlots & 1, timeout_ns, abort)) return false;
+      u = pairs + atomicAdd(counter, 1);
     }
   }
 };
@@ -66,13 +73,14 @@ struct PairUnits {
   const volatile int* abort;
   const uint64_t timeout_ns;
   const uint32_t empty_odd;
+  const bool taker;  // the odd CTA's producer of the weights
   int slot = 0;
   uint32_t phase = 0;
   bool ok = true;  // false: a wait ran out
 
-  __device__ PairUnits(const PairSched& s, int units, uint64_t timeout, const volatile int* a)
+  __device__ PairUnits(const PairSched& s, int units, uint64_t timeout, const volatile int* a, bool taker_)
       : sched(s), total(units), abort(a), timeout_ns(timeout),
-        empty_odd(ptx::mapa_shared(ptx::smem_u32(s.empty), 1)) {}
+        empty_odd(ptx::mapa_shared(ptx::smem_u32(s.empty), 1)), taker(taker_) {}
 
   // the next unit (warp-uniform; a whole warp calls), or -1
   __device__ __forceinline__ int next() {
@@ -83,7 +91,10 @@ struct PairUnits {
     }
     const int u = sched.unit[slot];
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive_remote(empty_odd + 8u * slot);
+    if ((threadIdx.x & 31) == 0) {
+      if (taker) mbar_arrive(&sched.taken[slot]);
+      mbar_arrive_remote(empty_odd + 8u * slot);
+    }
     if (++slot == kSchedSlots) {
       slot = 0;
       phase ^= 1u;

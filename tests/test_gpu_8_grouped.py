@@ -513,3 +513,23 @@ def test_rows_behind_2_to_the_32_elements():
     act = torch.ones((rows, k // 2), dtype=BF16, device="cuda")
     want = binding.swiglu_grad(packed, act)
     assert torch.equal(binding.swiglu_grad(x, act, dh=x), want)  # in place
+
+
+@pytest.mark.parametrize("op", ["forward", "dgrad"])
+@pytest.mark.parametrize("rows,n,k", [(8, 152, 5168), (1, 2096, 200), (3, 72, 8), (32, 128, 640), (9, 5168, 136)])
+def test_few_blocks_are_shared_by_few_workers(op, rows, n, k):
+    """Products with fewer K-blocks than SMs, of one group among empty ones: parts of several K-blocks, joined."""
+    lists = Lists([0, rows, 0])
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    w = (torch.randn((3, n, k), generator=gen, device="cuda") * 0.05).to(BF16)
+    gp = binding.GroupedProducts(3, n, k, BF16)
+    wd = w[1].double()
+    if op == "forward":
+        x = lists.matrix(gen, k, BF16)
+        y = gp.forward(x, w, lists.offsets)
+        check(y, x.double() @ wd.T, x.double().abs() @ wd.abs().T, k)
+    else:
+        x = lists.matrix(gen, n, BF16)
+        y = gp.dgrad(x, w, lists.offsets)
+        check(y, x.double() @ wd, x.double().abs() @ wd.abs(), n)
+    assert gp.device_status()[0] == binding.MOE_OK
