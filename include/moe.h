@@ -542,9 +542,10 @@ MOE_API moe_status moe_qk_norm(int64_t T, int32_t Hq, int32_t Hk, int32_t D, moe
  *   ldx ...  row strides in elements: >= the row's width, multiples of 8
  *   N, K     multiples of 8, <= 2^20; groups <= 1024; rows <= 2^31 - 512
  *            (others: MOE_ERR_UNSUPPORTED)
- *   workspace  moe_grouped_workspace_size() bytes, 256-byte aligned; contents
- *            on entry do not matter; one call at a time uses it (two graphs
- *            that share one are replayed one after the other).
+ *   workspace  moe_grouped_workspace_size() bytes of the shape (of as many rows as
+ *            any call brings), 256-byte aligned; contents on entry do not matter;
+ *            one call at a time uses it (two graphs that share one are replayed
+ *            one after the other).
  * Matrices 16-byte aligned, outputs apart from the inputs.  Asynchronous on
  * `stream`, capturable like every call.  rows = 0 is a no-op (the weight
  * gradient still writes its zeros). */
@@ -574,10 +575,12 @@ MOE_API moe_status moe_grouped_gemm_dgrad(const moe_grouped_shape* shape, const 
 /* dw [groups, N, K] of dw_type (the operands' type, or MOE_TYPE_FP32): written
  * whole, zeros for an empty group; or, with accumulate != 0 (MOE_TYPE_FP32
  * only, else MOE_ERR_INVALID_ARG), added to what dw holds.  The tensor core cuts
- * its fp32 sums towards zero: up to rows * 2^-28 of the sum of |dy x|.  Into fp32 that
- * is 768 rows at most, the rest is added rounded to nearest; into 16 bits it is all
- * rows of the group (2^20 rows: half a bf16 step), rows <= 2^26 (else
- * MOE_ERR_UNSUPPORTED). */
+ * its fp32 sums towards zero, each step of 16 rows by at most 17 * 2^-23 of the sum of
+ * |dy x| (measured: some 2^-24).  So it accumulates 768 rows of a group at most, or 3840
+ * for a dw of 16 bits (in all below half an fp16 step of the sum of |dy x|); the sums of
+ * such segments are added in fp32, rounded to nearest, and dw is rounded once.  Into
+ * 16 bits: rows <= 2^26 (else MOE_ERR_UNSUPPORTED); more than 3840 rows want the workspace
+ * that moe_grouped_workspace_size() gives for them, 33 MB more. */
 MOE_API moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy, int64_t lddy, const void* x,
                                           int64_t ldx, const int32_t* offsets, const int32_t* counts, void* dw,
                                           int32_t dw_type, int32_t accumulate, void* workspace,

@@ -567,6 +567,9 @@ class GroupedProducts(_Workspace):
     groups, and the gradients (moe_grouped_gemm*), with a workspace of their
     own.  Calls go to the current stream of the tensors' device; calls of one
     object on several streams share its workspace and must not overlap.
+    max_rows: rows the workspace is made for; weight gradients into 16 bits of more
+    get a larger one (the outgrown one lives as long as the object, for graphs that
+    were captured with it and work still queued on other streams).
     offsets: int32 [groups + 1] on the device, or None (equal groups);
     counts: int32 [groups] or None (offsets[g + 1] - offsets[g])."""
 
@@ -575,10 +578,21 @@ class GroupedProducts(_Workspace):
         self.groups, self.N, self.K, self.dtype = int(groups), int(N), int(K), dtype
         self.device = torch.empty(0, device=device or "cuda").device
         self._shape, self.int32 = None, torch.int32
-        st, n = moe_grouped_workspace_size(self.shape(max_rows))
+        self.workspace, self._outgrown = None, []
+        self._ensure_workspace(int(max_rows))
+
+    def _ensure_workspace(self, rows):
+        """A workspace for calls of up to ``rows`` rows."""
+        import torch
+        st, n = moe_grouped_workspace_size(self.shape(rows))
         if st != MOE_OK:
             raise MoeError(st, "moe_grouped_workspace_size")
-        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+        if self.workspace is None or n > self.workspace.numel():
+            workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+            if self.workspace is not None:
+                self._outgrown.append(self.workspace)
+            self.workspace, self.called = workspace, False
+        self.max_rows = rows
 
     def shape(self, rows) -> MoeGroupedShape:
         s = self._shape  # (kept by one assignment: other host threads may ask too)
@@ -623,6 +637,8 @@ class GroupedProducts(_Workspace):
             dw = _empty((self.groups, self.N, self.K), dtype or self.dtype, self.device)
         else:
             _check("dw", dw, self.device, dtype or dw.dtype, (self.groups, self.N, self.K))
+        if rows > self.max_rows and dw.dtype == self.dtype:
+            self._ensure_workspace(rows)
         self._call("moe_grouped_gemm_wgrad", self.shape(rows), yp, ldy, xp, ldx, *_lists(self, offsets, counts),
                    dw.data_ptr(), _type_of(dw.dtype), 1 if accumulate else 0)
         return dw

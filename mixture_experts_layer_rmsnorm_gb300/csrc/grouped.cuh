@@ -63,7 +63,8 @@ struct GroupedGemmArgs {
   const int32_t* unit_off;
   const CUtensorMap* maps;  // weight gradient: see GroupedPlanArgs
   int32_t* err;
-  float* partials;  // stream-K partial sums: [kMaxGemmCtas][BN][128] fp32
+  float* partials;  // stream-K partial sums: [kMaxGemmCtas][BN][128] fp32; weight gradient into 16 bits:
+                    // sums of the segments so far, [kMaxGemmCtas][256][128]
   int32_t* flags;   // [kMaxGemmCtas * 4], zero on entry
   int32_t* next_unit;  // CTA pairs: the next unit to hand out, zero on entry
   void* out;        // forward / input gradient: rows of ldo elements of the operand type
@@ -85,6 +86,8 @@ int grouped_tile(GroupedPlan plan);       // features per unit
 int grouped_tok_box(GroupedPlan plan);    // token rows per TMA box
 size_t grouped_partial_bytes();           // stream-K partial sums
 constexpr int kWgradTile = 256;           // rows and columns of a unit of the weight gradient
+constexpr int kWgradSegment16 = 3840;     // rows whose sum the tensor core accumulates, into 16 bits
+size_t grouped_wgrad_sum_bytes();         // sums of longer groups into 16 bits
 
 // tm_x: the token rows in boxes of kTokBox[plan] rows; tm_x32: of 32 (large plan)
 cudaError_t launch_grouped_gemm(GroupedOp op, GroupedPlan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,

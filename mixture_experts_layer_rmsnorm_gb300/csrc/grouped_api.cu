@@ -19,8 +19,8 @@ using moe::GroupedPlan;
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;         // N, K
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;  // 32-bit row coordinates, a token box past the end
-// Weight gradient into 16 bits: one accumulation per group, which a wait of the epilogue (two
-// seconds at most) spans: 2^20 blocks of 64 rows at 500 to 1000 cycles take up to half a second.
+// Weight gradient into 16 bits: the fp32 additions of a group's segments (2^26 / 3840, 2^-24 each) stay
+// below a third of the half step that bf16's rounding takes.
 constexpr int64_t kMaxRows16 = int64_t(1) << 26;
 constexpr int64_t kMaxLd = int64_t(1) << 36;          // elements: row strides within the tensor maps' 2^40 bytes
 
@@ -33,7 +33,8 @@ struct Layout {
 
 constexpr int kFlagInts = moe::kMaxGemmCtas * 4;
 
-Layout make_layout(int G) {
+// wgrad_rows: rows of a weight gradient into 16 bits, whose long groups need room for their sums; else 0
+Layout make_layout(int G, int64_t wgrad_rows = 0) {
   Layout L{};
   size_t off = 64;  // the error word
   auto take = [&](size_t bytes) {
@@ -47,7 +48,7 @@ Layout make_layout(int G) {
   L.unit_off = take(static_cast<size_t>(G + 1) * 4);
   L.flags = take(static_cast<size_t>(kFlagInts) * 4);
   L.maps = take(static_cast<size_t>(G) * 2 * sizeof(CUtensorMap));
-  L.partials = take(moe::grouped_partial_bytes());
+  L.partials = take(wgrad_rows > moe::kWgradSegment16 ? moe::grouped_wgrad_sum_bytes() : moe::grouped_partial_bytes());
   L.total = align_up(off, 256);
   return L;
 }
@@ -76,11 +77,11 @@ moe_status check_rows(const void* p, int64_t rows, int64_t ld, int64_t width) {
 }
 
 moe_status check_call(const moe_grouped_shape* s, const int32_t* offsets, const int32_t* counts, void* ws,
-                      size_t ws_bytes) {
+                      size_t ws_bytes, int64_t wgrad_rows = 0) {
   if (!offsets && s->rows % s->groups != 0) return MOE_ERR_INVALID_ARG;
   if (!aligned(offsets, 4) || !aligned(counts, 4)) return MOE_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < make_layout(s->groups).total) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < make_layout(s->groups, wgrad_rows).total) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -296,7 +297,7 @@ moe_status moe_grouped_workspace_size(const moe_grouped_shape* shape, size_t* by
   const moe_status st = check_shape(shape);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = make_layout(shape->groups).total;
+  *bytes = make_layout(shape->groups, shape->rows).total;
   return MOE_OK;
 }
 
@@ -326,11 +327,12 @@ moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy
   if (!dw || !aligned(dw, 16)) return MOE_ERR_INVALID_ARG;
   if (dw_type != s->type && dw_type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
   if (accumulate && dw_type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
-  if ((st = check_call(s, offsets, counts, workspace, workspace_bytes)) != MOE_OK) return st;
+  const int64_t rows16 = dw_type != MOE_TYPE_FP32 ? s->rows : 0;
+  if ((st = check_call(s, offsets, counts, workspace, workspace_bytes, rows16)) != MOE_OK) return st;
   const int tile = moe::kWgradTile;
   const int64_t tiles_m = (s->N + tile - 1) / tile, tiles_n = (s->K + tile - 1) / tile;
   if (tiles_m * tiles_n * s->groups >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
-  if (dw_type != MOE_TYPE_FP32 && s->rows > kMaxRows16) return MOE_ERR_UNSUPPORTED;
+  if (rows16 > kMaxRows16) return MOE_ERR_UNSUPPORTED;
   if (s->rows == 0 && accumulate) return MOE_OK;
   // no rows: every group is empty and dw becomes zero; nothing is loaded through the row maps
   const int64_t map_rows = s->rows > 0 ? s->rows : 1;
@@ -339,7 +341,7 @@ moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy
       !make_rows_map(&tx, s->type, s->rows > 0 ? x : dw, s->K, map_rows, ldx, 64) ||
       !make_matrix_map(&tdw, dw_type, dw, s->groups, s->N, s->K, 32))
     return MOE_ERR_CUDA;
-  const Layout L = make_layout(s->groups);
+  const Layout L = make_layout(s->groups, rows16);
   moe::GroupedPlanArgs p = plan_args(s, L, workspace, offsets, counts);
   p.bn = 0;
   p.tiles = static_cast<int>(tiles_m * tiles_n);

@@ -17,12 +17,19 @@
 // order changes a result.  An empty group's tile is stored as zeros, without MMAs.
 // Tiles go round-robin to the CTA pairs (a group's tiles are equally long).
 //
-// Long groups into fp32.  The tensor core cuts each addition to its fp32
-// accumulator, towards zero: the error grows with the number of additions
-// (relative, 2-norm, random signs: 4.7e-7 for 512 rows, 9.1e-6 for 8192; all signs
-// equal: 8.0e-7 and 3.1e-5).  So a tile in fp32 is accumulated over at most kSegment
-// rows in TMEM, and later segments are added to dw by TMA, rounded to nearest,
-// in order (a warp waits for its earlier stores before it adds to them).
+// Long groups.  The tensor core cuts each addition to its fp32 accumulator,
+// towards zero: the error grows with the number of additions (relative, 2-norm,
+// random signs: 4.7e-7 for 512 rows, 9.1e-6 for 8192; all signs equal: 8.0e-7 and
+// 3.1e-5).  So TMEM accumulates segments of a group, and their sums are added in
+// fp32, rounded to nearest, in order.
+//   Into fp32: segments of 768 rows; later ones are added to dw by TMA (a warp
+//   waits for its earlier stores before it adds to them).
+//   Into 16 bits, which cannot hold the sum: even segments of at most 3840 rows.
+//   A step of 16 rows cuts at most 17 terms by 2^-23 of the largest, so one loses
+//   less than 3840 * 17 / 16 * 2^-23 = 4.9e-4 of sum |dy x|, half an fp16 step.
+//   Every thread keeps the sums of its row of the tile in the workspace (128 KB per
+//   CTA, in L2) and rounds once, with the last segment.  Measured, N = K = 4096: 8 groups
+//   of 8192 rows 1222 us (accumulated whole 1187); 2 of 65536, N = K = 2048: 650 (625).
 //
 // Bound: by writing dw where groups are short (a tile of fp32 moves 128 KB per
 // CTA for 64 KB of operands per 64 rows), else by the tensor cores; in between by shared memory, which
@@ -47,7 +54,10 @@ constexpr int kMnBox = 64 * 128;                // 64 columns x 64 rows, 16 bits
 constexpr int kOperand = 2 * kMnBox;            // this CTA's 128 columns of dy, or of x
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kStages = 6;
-constexpr int kSegment = 768;                   // rows per accumulation of an fp32 tile: a multiple of 64
+// rows per accumulation: multiples of 64
+constexpr int kSegment32 = 768, kSegment16 = kWgradSegment16;
+static_assert(kSegment32 % 64 == 0 && kSegment16 % 64 == 0, "whole stages");
+static_assert(2 * kMaxPairs <= kMaxGemmCtas, "a place of its own for each CTA's sums");
 constexpr int kEpiWarps = 4;
 constexpr int kBox = 32 * 128;                  // an epilogue warp has two boxes of 32 rows x 128 bytes
 constexpr int kThreads = 32 * (2 + kEpiWarps);
@@ -105,7 +115,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int total_units = tables.unit_off[a.G];
   GroupedUnits units(tables, a.G, a.tiles_n, 0);  // each thread walks its role's units
-  const int segment = a.out_fp32 ? kSegment : 0x7FFFFFC0;
+  // rows of a unit's segments (into 16 bits even ones: a short last one would wait for the sums' way through L2)
+  auto segment_of = [&](int n) {
+    if (a.out_fp32 || n <= kSegment16) return a.out_fp32 ? kSegment32 : kSegment16;
+    const int parts = (n + kSegment16 - 1) / kSegment16;
+    return ((n + parts - 1) / parts + 63) / 64 * 64;
+  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -168,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = worker; ok && u < total_units; u += workers) {
         const GroupedUnit un = units.at(u);
+        const int segment = segment_of(un.n);
         for (int row0 = 0; ok && row0 < un.n; row0 += segment) {  // (an empty group: the epilogue writes zeros)
           if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag))) {
             ok = false;
@@ -225,12 +241,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty_cl = mapa_shared(smem_u32(tempty), 0);
     const int span = a.out_fp32 ? 32 : 64;  // columns of a box
     const bool fp16 = a.fp16 != 0;
+    // [256 columns][128 rows] of this CTA, this thread's row: read and written by this thread alone
+    float* sums = a.partials + static_cast<int64_t>(blockIdx.x) * (kWgradTile * 128) + q * 32 + lane;
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int u = worker; ok && u < total_units; u += workers) {
       const GroupedUnit un = units.at(u);
       const int row0 = un.tile * 256 + static_cast<int>(rank) * 128 + q * 32;
+      const int segment = segment_of(un.n);
       int left = un.n;
       do {  // segments; an empty group: zeros once
         const bool has_acc = left > 0, first = left == un.n;
@@ -242,10 +261,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
         }
-        const bool add = a.accumulate || !first;
-        if (!first && lane == 0) bulk_wait_all();  // the earlier segments are in dw
+        const bool add = a.out_fp32 && (a.accumulate || !first);
+        const bool to_sums = !a.out_fp32 && left > segment;  // into 16 bits, and not the last segment
+        if (add && !first && lane == 0) bulk_wait_all();  // the earlier segments are in dw
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
-        for (int c0 = 0; c0 < 256 && row0 < a.F; c0 += span) {
+        if (to_sums) {
+          for (int c0 = 0; c0 < 256 && row0 < a.F && un.tile_n * 256 + c0 < a.C; c0 += 32) {
+            float* at = sums + c0 * 128;
+            float before[32];  // every load ahead of the stores (one by one: 84 us a segment)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) before[j] = first ? 0.0f : __ldcg(at + j * 128);
+            uint32_t r[32];
+            __syncwarp();  // tcgen05.ld is warp-aligned
+            tmem_ld_32x32b_x32(t_row + c0, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) __stcg(at + j * 128, before[j] + __uint_as_float(r[j]));
+          }
+        }
+        for (int c0 = to_sums ? 256 : 0; c0 < 256 && row0 < a.F; c0 += span) {
           const int col = un.tile_n * 256 + c0;
           if (col >= a.C) break;
           uint8_t* box = my_boxes + buf * kBox;
@@ -265,6 +299,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t r[32];
               tmem_ld_32x32b_x32(t_row + c0 + 32 * h, r);
               tmem_ld_wait();
+              if (!first) {
+                const float* at = sums + (c0 + 32 * h) * 128;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__ldcg(at + j * 128) + __uint_as_float(r[j]));
+              }
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 w[16 * h + j] = pack16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), fp16);
@@ -310,6 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 }  // namespace
+
+size_t grouped_wgrad_sum_bytes() { return static_cast<size_t>(kMaxGemmCtas) * kWgradTile * 128 * 4; }
 
 cudaError_t launch_grouped_wgrad(const CUtensorMap& tm_dw, const GroupedGemmArgs& a, cudaStream_t stream) {
   static PerDevice config;

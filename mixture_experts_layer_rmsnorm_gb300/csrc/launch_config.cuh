@@ -52,12 +52,13 @@ cudaError_t launch_ctas(Kernel kernel, PerDevice& config, int ctas, int threads,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+constexpr int kMaxPairs = 128;
+
 // Launch `kernel` (programmatic dependent launch) on clusters of two CTAs, as
-// many as fit on the device at once.  `config`: one per kernel.
+// many as fit on the device at once, kMaxPairs at most.  `config`: one per kernel.
 template <typename Kernel, typename... Args>
 cudaError_t launch_pairs(Kernel kernel, PerDevice& config, int threads, size_t smem_bytes, cudaStream_t stream,
                          const Args&... args) {
-  constexpr int kMostPairs = 128;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem_bytes;
@@ -76,7 +77,7 @@ cudaError_t launch_pairs(Kernel kernel, PerDevice& config, int threads, size_t s
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes));
         if (ce != cudaSuccess) return ce;
         cudaLaunchConfig_t q = cfg;
-        q.gridDim = dim3(2 * kMostPairs);
+        q.gridDim = dim3(2 * kMaxPairs);
         q.attrs = attr + 1;
         q.numAttrs = 1;
         int n = 0;
@@ -88,7 +89,7 @@ cudaError_t launch_pairs(Kernel kernel, PerDevice& config, int threads, size_t s
       },
       &fit);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(2 * (fit < kMostPairs ? fit : kMostPairs));
+  cfg.gridDim = dim3(2 * (fit < kMaxPairs ? fit : kMaxPairs));
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args...);

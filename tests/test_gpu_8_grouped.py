@@ -533,3 +533,23 @@ def test_few_blocks_are_shared_by_few_workers(op, rows, n, k):
         y = gp.dgrad(x, w, lists.offsets)
         check(y, x.double() @ wd, x.double().abs() @ wd.abs(), n)
     assert gp.device_status()[0] == binding.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=str)
+def test_long_sums_into_16_bits_keep_their_precision(dtype):
+    """2^19 rows of one sign: accumulated whole, the tensor core's cuts take some 2e-3 of the sum, half a bf16 step and four
+    fp16 steps.  A segment of 3840 rows takes 240 steps of 9 2^-23 (as above: 2.6e-4), the 137 segments' additions 2^-24
+    each, and the output is rounded once."""
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    rows = 1 << 19
+    x = torch.rand((rows, 136), generator=gen, device="cuda").to(dtype)
+    dy = torch.rand((rows, 264), generator=gen, device="cuda").mul_(0.125).to(dtype)  # (sums of 16384: fp16 holds them)
+    lists = [None, torch.tensor([0, rows - 3840 * 5 + 1, rows], dtype=torch.int32, device="cuda")]
+    for offsets in lists:
+        groups = 1 if offsets is None else 2
+        spans = [(0, rows)] if offsets is None else [(0, rows - 3840 * 5 + 1), (rows - 3840 * 5 + 1, rows)]
+        dw = binding.GroupedProducts(groups, 264, 136, dtype).wgrad(dy, x, offsets)
+        for g, (a, b) in enumerate(spans):
+            want = dy[a:b].double().T @ x[a:b].double()
+            rel = ((dw[g].double() - want) / want).abs().max().item()
+            assert rel <= half_step(dtype) + 240 * 9 * 2.0 ** -23 + 137 * 2.0 ** -24, rel

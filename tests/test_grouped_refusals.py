@@ -136,3 +136,10 @@ def test_weight_gradient_into_16_bits_of_too_many_rows():
         s = binding.grouped_shape(4, 64, 128, rows)
         ws = 64 if want == WS else BIG
         assert binding.moe_grouped_gemm_wgrad(s, A, 64, A, 128, A, None, A, 0, 0, A, ws, None) == want
+
+
+def test_weight_gradient_into_16_bits_of_long_groups_wants_its_larger_workspace():
+    sizes = [binding.moe_grouped_workspace_size(binding.grouped_shape(4, 64, 128, rows))[1] for rows in (0, 3840, 3841)]
+    assert sizes[0] == sizes[1] < sizes[2]
+    s = binding.grouped_shape(4, 64, 128, 3841)
+    assert binding.moe_grouped_gemm_wgrad(s, A, 64, A, 128, A, None, A, 0, 0, A, sizes[2] - 1, None) == WS
