@@ -544,13 +544,19 @@ def swiglu_grad(h, dact, dh=None):
 class _Workspace:
     """A workspace of the grouped calls, for an object with ``device`` and ``workspace``."""
 
-    called = False
+    called = False  # a call was accepted
+
+    def _new_workspace(self, bytes_):
+        import torch
+        workspace = torch.empty(bytes_, dtype=torch.uint8, device=self.device)
+        workspace[:16].zero_()  # no status yet: a captured call may be replayed later, or never
+        return workspace
 
     def _call(self, name, shape_, *args):
-        self.called = True
         if shape_.rows == 0:  # nothing is enqueued: what a call before it reported is not its own
             self.workspace[:16].zero_()
         _enqueue(name, self.device, ctypes.byref(shape_), *args, self.workspace.data_ptr(), self.workspace.numel())
+        self.called = True
 
     def device_status(self):
         """(status, detail) of the last call, after waiting for the current stream (moe_device_status)."""
@@ -583,12 +589,11 @@ class GroupedProducts(_Workspace):
 
     def _ensure_workspace(self, rows):
         """A workspace for calls of up to ``rows`` rows."""
-        import torch
         st, n = moe_grouped_workspace_size(self.shape(rows))
         if st != MOE_OK:
             raise MoeError(st, "moe_grouped_workspace_size")
         if self.workspace is None or n > self.workspace.numel():
-            workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+            workspace = self._new_workspace(n)
             if self.workspace is not None:
                 self._outgrown.append(self.workspace)
             self.workspace, self.called = workspace, False
@@ -749,7 +754,7 @@ class Fp4Weights(_Workspace):
         st, n = moe_grouped_workspace_size(grouped_shape(self.groups, self.N, self.K, 0))
         if st != MOE_OK:
             raise MoeError(st, "moe_grouped_workspace_size")
-        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self.workspace = self._new_workspace(n)
 
     def shape(self, rows, type) -> MoeGroupedShape:
         s = self._shape  # (kept by one assignment: other host threads may ask too)

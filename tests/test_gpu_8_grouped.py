@@ -553,3 +553,33 @@ def test_long_sums_into_16_bits_keep_their_precision(dtype):
             want = dy[a:b].double().T @ x[a:b].double()
             rel = ((dw[g].double() - want) / want).abs().max().item()
             assert rel <= half_step(dtype) + 240 * 9 * 2.0 ** -23 + 137 * 2.0 ** -24, rel
+
+
+def test_status_of_an_object_whose_calls_never_ran():
+    """A refused first call and a captured one that is not replayed leave no status: what the workspace's memory held
+    before (here an error of another object's) is not theirs."""
+    x, w = torch.ones((6, 64), dtype=BF16, device="cuda"), torch.ones((2, 8, 64), dtype=BF16, device="cuda")
+    bad = torch.tensor([0, 9, 6], dtype=torch.int32, device="cuda")
+
+    def used():  # an object on memory that holds an error word
+        gp = binding.GroupedProducts(2, 8, 64, BF16)
+        gp.forward(x, w, bad)
+        assert gp.device_status()[0] == binding.MOE_ERR_DEVICE
+        place = gp.workspace.data_ptr()
+        del gp
+        gp = binding.GroupedProducts(2, 8, 64, BF16)
+        assert gp.workspace.data_ptr() == place  # (the allocator hands the block on)
+        return gp
+
+    gp = used()
+    with pytest.raises(binding.MoeError):
+        gp.forward(x[:5], w)  # five rows do not make two equal groups
+    assert gp.device_status() == (binding.MOE_OK, [0] * 4)
+    gp, y = used(), torch.zeros((6, 8), dtype=BF16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gp.forward(x, w, bad, y=y)
+    assert gp.device_status() == (binding.MOE_OK, [0] * 4)
+    graph.replay()
+    assert gp.device_status()[0] == binding.MOE_ERR_DEVICE
