@@ -681,6 +681,7 @@ class Fp4Rows:
         return s
 
     def ensure_capacity(self, rows):
+        """Buffers for up to ``rows`` rows; new ones hold no rows yet (``rows`` becomes 0)."""
         if rows <= self.max_rows and self.max_rows > 0:
             return
         import torch
@@ -689,13 +690,15 @@ class Fp4Rows:
         st, (n_codes, n_scales) = moe_fp4_sizes(fp4_shape(self.format, self.groups, rows, self.K))
         if st != MOE_OK:
             raise MoeError(st, "moe_fp4_sizes")
+        # (all of them before any takes its place: where one does not fit, the rows before stay)
+        codes = torch.empty(n_codes, dtype=torch.uint8, device=self.device)
+        scales = torch.empty(n_scales, dtype=torch.uint8, device=self.device)
+        gscale = (torch.empty(rows, dtype=torch.float32, device=self.device)
+                  if self.format == MOE_FORMAT_NVFP4 else None)
         if self.max_rows > 0:
             self._outgrown.append((self.codes, self.scales, self.gscale))
-        self.codes = torch.empty(n_codes, dtype=torch.uint8, device=self.device)
-        self.scales = torch.empty(n_scales, dtype=torch.uint8, device=self.device)
-        self.gscale = (torch.empty(rows, dtype=torch.float32, device=self.device)
-                       if self.format == MOE_FORMAT_NVFP4 else None)
-        self.max_rows = rows
+        self.codes, self.scales, self.gscale, self.max_rows = codes, scales, gscale, rows
+        self.rows, self._listed = 0, None
 
     def quantize(self, x, offsets=None, counts=None):
         """x [rows, K] (bf16, fp16 or fp32) to 4 bits; returns self."""

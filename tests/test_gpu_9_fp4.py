@@ -501,3 +501,36 @@ def test_a_refused_quantize_leaves_the_rows_before():
     with pytest.raises(TypeError):
         r4.quantize(torch.zeros((500, 64), device="cuda").double())
     assert torch.equal(r4.dequantize(), want)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_larger_buffers_hold_no_rows_yet(fmt):
+    """Buffers that grew hold none of the rows quantized before: they are forgotten, not read from new memory."""
+    x = torch.ones((10, 64), dtype=BF16, device="cuda")
+    r4 = binding.Fp4Rows(fmt, 64, 1, 10).quantize(x)
+    r4.ensure_capacity(10)
+    assert r4.rows == 10 and (r4.dequantize() == 1).all()
+    r4.ensure_capacity(1000)
+    assert r4.rows == 0 and r4.dequantize().shape == (0, 64)
+    w4 = binding.Fp4Weights.quantize(torch.ones((1, 8, 64), dtype=BF16, device="cuda"), fmt)
+    assert w4.forward(r4).shape == (0, 8) and (w4.forward(r4.quantize(x)) == 64).all()
+
+
+def test_an_allocation_that_fails_leaves_the_rows_before(monkeypatch):
+    x = torch.ones((10, 64), dtype=BF16, device="cuda")
+    r4 = binding.Fp4Rows("nv", 64, 1, 10).quantize(x)
+    big, real = torch.ones((1000, 64), dtype=BF16, device="cuda"), torch.empty
+    for fail_at in range(3):  # codes, scales, gscale
+        left = [fail_at]
+
+        def empty(*args, **kw):
+            if left[0] == 0:
+                raise MemoryError
+            left[0] -= 1
+            return real(*args, **kw)
+
+        monkeypatch.setattr(torch, "empty", empty)
+        with pytest.raises(MemoryError):
+            r4.quantize(big)
+        monkeypatch.undo()
+        assert r4.rows == 10 and (r4.dequantize() == 1).all()
