@@ -499,19 +499,39 @@ def _empty(shape_, dtype, device):
 _C = None  # torch's native module, once it is needed
 
 
-def _enqueue(name, device, *args):
-    """name(*args, stream) of the library with ``device`` current, on its current stream; MoeError if it fails."""
+class _Buffers:
+    """An object that keeps buffers on ``device``, listed by ``_buffers()``.  A stream that uses them is made known to
+    the allocator once, so that the object may go while its work is queued there."""
+
+    _streams = frozenset()
+
+    def _used_on(self, stream):
+        import torch
+        for t in self._buffers():
+            if t is not None:
+                t.record_stream(torch.cuda.current_stream(self.device))
+        self._streams = self._streams | {stream}  # (one assignment: other host threads may ask too)
+
+
+def _enqueue(name, device, *args, of=()):
+    """name(*args, stream) of the library with ``device`` current, on its current stream; MoeError if it fails.  of:
+    the objects whose buffers it uses."""
     global _C
     if _C is None:
         from torch import _C as native
         _C = native
     index, fn = device.index, getattr(_lib or load(), name)
-    if _C._cuda_getDevice() == index:  # (the tensors exist: CUDA is initialised)
-        st = fn(*args, _C._cuda_getCurrentRawStream(index))
+    here = _C._cuda_getDevice() == index  # (the tensors exist: CUDA is initialised)
+    stream = _C._cuda_getCurrentRawStream(index)
+    for o in of:
+        if stream not in o._streams:
+            o._used_on(stream)
+    if here:
+        st = fn(*args, stream)
     else:
         from torch import cuda
         with cuda.device(device):
-            st = fn(*args, _C._cuda_getCurrentRawStream(index))
+            st = fn(*args, stream)
     if st != MOE_OK:
         raise MoeError(st, name)
 
@@ -541,7 +561,7 @@ def swiglu_grad(h, dact, dh=None):
     return dh
 
 
-class _Workspace:
+class _Workspace(_Buffers):
     """A workspace of the grouped calls, for an object with ``device`` and ``workspace``."""
 
     called = False  # a call was accepted
@@ -552,10 +572,14 @@ class _Workspace:
         workspace[:16].zero_()  # no status yet: a captured call may be replayed later, or never
         return workspace
 
-    def _call(self, name, shape_, *args):
+    def _buffers(self):
+        return (self.workspace,)
+
+    def _call(self, name, shape_, *args, of=()):
         if shape_.rows == 0:  # nothing is enqueued: what a call before it reported is not its own
             self.workspace[:16].zero_()
-        _enqueue(name, self.device, ctypes.byref(shape_), *args, self.workspace.data_ptr(), self.workspace.numel())
+        _enqueue(name, self.device, ctypes.byref(shape_), *args, self.workspace.data_ptr(), self.workspace.numel(),
+                 of=(self, *of))
         self.called = True
 
     def device_status(self):
@@ -596,7 +620,7 @@ class GroupedProducts(_Workspace):
             workspace = self._new_workspace(n)
             if self.workspace is not None:
                 self._outgrown.append(self.workspace)
-            self.workspace, self.called = workspace, False
+            self.workspace, self.called, self._streams = workspace, False, frozenset()
         self.max_rows = rows
 
     def shape(self, rows) -> MoeGroupedShape:
@@ -656,7 +680,7 @@ def _format_of(name) -> int:
     return formats[name]
 
 
-class Fp4Rows:
+class Fp4Rows(_Buffers):
     """Rows of groups in 4 bits (moe_fp4_quantize, moe_fp4_dequantize): buffers
     for up to ``max_rows`` rows of K elements, filled by :meth:`quantize`.
     format: "mx" (MXFP4) or "nv" (NVFP4, one fp32 scale per row).  offsets and
@@ -698,7 +722,10 @@ class Fp4Rows:
         if self.max_rows > 0:
             self._outgrown.append((self.codes, self.scales, self.gscale))
         self.codes, self.scales, self.gscale, self.max_rows = codes, scales, gscale, rows
-        self.rows, self._listed = 0, None
+        self.rows, self._listed, self._streams = 0, None, frozenset()
+
+    def _buffers(self):
+        return self.codes, self.scales, self.gscale
 
     def quantize(self, x, offsets=None, counts=None):
         """x [rows, K] (bf16, fp16 or fp32) to 4 bits; returns self."""
@@ -708,7 +735,7 @@ class Fp4Rows:
         self.ensure_capacity(rows)
         self.rows = 0  # (until they are on their way)
         _enqueue("moe_fp4_quantize", self.device, ctypes.byref(self.shape(rows)), type_, xp, ldx, *lists,
-                 self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.gscale), MOE_SCALE_PER_ROW)
+                 self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.gscale), MOE_SCALE_PER_ROW, of=(self,))
         self.rows, self._listed = rows, offsets is not None
         return self
 
@@ -726,7 +753,7 @@ class Fp4Rows:
         yp, ldy = _matrix("y", y, self.device, dtype or y.dtype, (self.rows, self.K))
         _enqueue("moe_fp4_dequantize", self.device, ctypes.byref(self.shape(self.rows)), self.codes.data_ptr(),
                  self.scales.data_ptr(), _ptr(self.gscale), MOE_SCALE_PER_ROW, *_lists(self, offsets, counts),
-                 _type_of(y.dtype), yp, ldy)
+                 _type_of(y.dtype), yp, ldy, of=(self,))
         return y
 
 
@@ -759,6 +786,9 @@ class Fp4Weights(_Workspace):
             raise MoeError(st, "moe_grouped_workspace_size")
         self.workspace = self._new_workspace(n)
 
+    def _buffers(self):
+        return self.workspace, self.codes, self.scales, self.gscale
+
     def shape(self, rows, type) -> MoeGroupedShape:
         s = self._shape  # (kept by one assignment: other host threads may ask too)
         if s is None or s.rows != rows or s.type != type:
@@ -789,7 +819,7 @@ class Fp4Weights(_Workspace):
         _enqueue("moe_fp4_dequantize", self.device,
                  ctypes.byref(fp4_shape(self.format, self.groups, self.groups * self.N, self.K)), _ptr(self.codes),
                  _ptr(self.scales), _ptr(self.gscale), MOE_SCALE_PER_GROUP, None, None, _type_of(w.dtype), _ptr(w),
-                 self.K)
+                 self.K, of=(self,))
         return w
 
     def forward(self, rows: Fp4Rows, offsets=None, counts=None, y=None, dtype=None):
@@ -801,9 +831,9 @@ class Fp4Weights(_Workspace):
             import torch
             y = torch.empty((rows.rows, self.N), dtype=dtype or torch.bfloat16, device=self.device)
         yp, ldy = _matrix("y", y, self.device, dtype or y.dtype, (rows.rows, self.N))
-        self._call("moe_fp4_gemm", self.shape(rows.rows, _type_of(y.dtype)), self.format, rows.codes.data_ptr(), rows.scales.data_ptr(), _ptr(rows.gscale),
-                   self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.gscale), *_lists(self, offsets, counts),
-                   yp, ldy)
+        self._call("moe_fp4_gemm", self.shape(rows.rows, _type_of(y.dtype)), self.format, rows.codes.data_ptr(),
+                   rows.scales.data_ptr(), _ptr(rows.gscale), self.codes.data_ptr(), self.scales.data_ptr(),
+                   _ptr(self.gscale), *_lists(self, offsets, counts), yp, ldy, of=(rows,))
         return y
 
 

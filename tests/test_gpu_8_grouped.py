@@ -583,3 +583,27 @@ def test_status_of_an_object_whose_calls_never_ran():
     assert gp.device_status() == (binding.MOE_OK, [0] * 4)
     graph.replay()
     assert gp.device_status()[0] == binding.MOE_ERR_DEVICE
+
+
+def test_objects_may_go_while_their_work_is_queued_on_another_stream():
+    """Their memory is nobody else's until the stream that uses it has come past."""
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    x = torch.randn((40, 64), generator=gen, device="cuda").to(BF16)
+    w = torch.randn((2, 72, 64), generator=gen, device="cuda").to(BF16)
+    off = torch.tensor([0, 9, 40], dtype=torch.int32, device="cuda")
+    want = binding.GroupedProducts(2, 72, 64, BF16).forward(x, w, off)
+    want4 = binding.Fp4Weights.quantize(w, "nv").forward(binding.Fp4Rows("nv", 64, 2, 40).quantize(x, off), off)
+    gp, r4, w4 = binding.GroupedProducts(2, 72, 64, BF16), binding.Fp4Rows("nv", 64, 2, 40), binding.Fp4Weights.quantize(w, "nv")
+    buffers = [gp.workspace, r4.codes, r4.scales, r4.gscale, w4.workspace, w4.codes, w4.scales, w4.gscale]
+    places, sizes = {t.data_ptr() for t in buffers}, [t.numel() * t.element_size() for t in buffers]
+    del buffers
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1_000_000_000)  # (some 0.5 s)
+        y, y4 = gp.forward(x, w, off), w4.forward(r4.quantize(x, off), off)
+    del gp, r4, w4
+    others = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    assert not side.query() and not places & {t.data_ptr() for t in others}
+    side.synchronize()
+    assert torch.equal(y, want) and torch.equal(y4, want4)
