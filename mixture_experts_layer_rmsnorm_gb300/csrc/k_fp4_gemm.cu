@@ -68,8 +68,10 @@ struct Cfg {
   static constexpr int kTmemNeed = kAccBufs * BN + STAGES * kSfCols;
   static constexpr uint32_t kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
   static constexpr int kEpiWarps = PAIR ? 8 : 4;  // two per TMEM lane quarter for the pair's single accumulator
-  static constexpr int kThreads = 32 * (3 + kEpiWarps + 4);  // + the weights' producer, the MMA warp, the rows' producer; 4 scale warps
-  static constexpr int kReaders = 2 * (2 + kEpiWarps + 4) + 1;  // warps of a pair that walk the units
+  // the weights' producer, the MMA warp, the epilogue, 4 scale warps, the rows' producer; in pairs the relay
+  static constexpr int kRowsWarp = 2 + kEpiWarps + 4, kRelayWarp = PAIR ? kRowsWarp + 1 : -1;
+  static constexpr int kThreads = 32 * (kRowsWarp + (PAIR ? 2 : 1));
+  static constexpr int kReaders = 2 + kEpiWarps + 4;  // warps of a pair's odd CTA that walk the units
   static constexpr int kBarBytes = 512;
   static constexpr int kTabGroups = kGroupsSmem[PAIR];
   static constexpr int kTabBytes = 3 * (kTabGroups + 1) * 4;
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
   // single CTAs: a stream-K range; pairs: whole units as they are handed out
   auto rg = [&] {
     if constexpr (PAIR)
-      return PairWalk{PairUnits(sched, total_units, kWaitTimeoutNs, abort_flag, warp == 0 && !leader), kblocks};
+      return PairWalk{PairUnits(sched, total_units, kWaitTimeoutNs, abort_flag, leader, warp == 0), kblocks};
     else
       return GroupedRange(total_units, kblocks, worker, workers);
   }();
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
   auto valid_chunks = [&](int kb) { return min(C::kChunks, chunks_k - kb * C::kChunks); };
   auto n_of = [](int n) { return PAIR ? (n + 31) / 32 * 32 : (n + 15) / 16 * 16; };
 
-  if (warp == 0 || warp == C::kThreads / 32 - 1) {
+  if (warp == 0 || warp == C::kRowsWarp) {
     // ---------------- TMA producers, one warp for the weights and their scales,
     // one for the rows and theirs; one lane issues
     const bool weights = warp == 0, issue = elect_one();
@@ -383,6 +385,9 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       if (!sched.schedule(a.next_unit, total_units, kWaitTimeoutNs, abort_flag))
         raise_timeout(a.err, abort_flag, kKernFp4Gemm, kWaitUnit);
     }
+  } else if (PAIR && warp == C::kRelayWarp) {
+    if (leader && lane == 0 && !sched.relay(total_units, kWaitTimeoutNs, abort_flag))
+      raise_timeout(a.err, abort_flag, kKernFp4Gemm, kWaitUnit);
   } else if (warp >= 2 + C::kEpiWarps) {
     // ---------------- scale warps: lane l of a quarter takes the 16 bytes of
     // rows l, 32 + l, 64 + l, 96 + l of each tile (its four TMEM columns)
@@ -490,15 +495,21 @@ __global__ void __launch_bounds__(Cfg<F, BN, STAGES, TOKBOX, PAIR>::kThreads, 1)
       if constexpr (PAIR) {
         const int odd = lane & 1;
         uint32_t packed[kCols / 2];
+        // columns a load: NVFP4, whose scales take registers too, would spill with 32 (256 groups of 64
+        // rows, N = 1536, K = 256: 132 instead of 122 us); MXFP4 is slower with 16 (102 instead of 89 us)
+        constexpr int kLoad = F == Fp4Format::kNv ? 16 : 32;
 #pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += 32) {
+        for (int c0 = 0; c0 < kCols; c0 += kLoad) {
           if (col0 + c0 < un.n) {
-            uint32_t r[32];
+            uint32_t r[kLoad];
             __syncwarp();  // tcgen05.ld is warp-aligned
-            tmem_ld_32x32b_x32(t_row + col0 + c0, r);
+            if constexpr (kLoad == 16)
+              tmem_ld_32x32b_x16(t_row + col0 + c0, r);
+            else
+              tmem_ld_32x32b_x32(t_row + col0 + c0, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
+            for (int j = 0; j < kLoad; j += 4) {
               float4 v = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
                                      __uint_as_float(r[j + 3]));
               if (F == Fp4Format::kNv) {

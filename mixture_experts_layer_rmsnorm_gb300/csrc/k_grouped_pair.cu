@@ -45,7 +45,8 @@ constexpr int kRing = 224 * 1024;    // bytes: 7 stages of 256 rows, 4 of 512
 constexpr int kStages = 11;          // stages in flight at most (the smallest are 20 KB)
 constexpr int kAccCols = 256;
 constexpr int kEpiWarps = 8;         // two per TMEM lane quarter, alternate groups of 32 columns
-constexpr int kThreads = 32 * (3 + kEpiWarps);  // + the weights' producer, the MMA warp, the rows' producer
+constexpr int kRowsWarp = 2 + kEpiWarps, kRelayWarp = kRowsWarp + 1;
+constexpr int kThreads = 32 * (kRelayWarp + 1);  // + the weights' producer, the MMA warp, the rows' producer, the relay
 constexpr int kBarBytes = 256;
 constexpr int kTabBytes = 3 * (kGroupsSmem[1] + 1) * 4;
 constexpr size_t kSmemBytes = 1024 + kRing + kBarBytes + kSchedBytes + kTabBytes;
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tempty[b], 2 * kEpiWarps);
     }
     mbar_init(done, 1);
-    sched.init(2 * (2 + kEpiWarps) + 1);  // producers and epilogue of both CTAs, the MMA warp
+    sched.init(2 + kEpiWarps);  // producers and epilogue
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tm_w);
@@ -178,9 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total_units = tables.unit_off[a.G];
   const int kblocks = (a.R + 63) / 64;
   GroupedUnits units(tables, a.G, 1, a.bn, true);  // each warp walks its role's units
-  PairUnits walk(sched, total_units, kWaitTimeoutNs, abort_flag, warp == 0 && !leader);
+  PairUnits walk(sched, total_units, kWaitTimeoutNs, abort_flag, leader, warp == 0);
 
-  if (warp == 0 || warp == 2 + kEpiWarps) {
+  if (warp == 0 || warp == kRowsWarp) {
     // ---------------- TMA producers: one warp for the weight tiles, one for the
     // rows (one thread that issues both, three to five copies a stage, is
     // slower than the copies); one lane issues
@@ -301,6 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!sched.schedule(a.next_unit, total_units, kWaitTimeoutNs, abort_flag))
         raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitUnit);
     }
+  } else if (warp == kRelayWarp) {
+    if (leader && lane == 0 && !sched.relay(total_units, kWaitTimeoutNs, abort_flag))
+      raise_timeout(a.err, abort_flag, kKernGroupedGemm, kWaitUnit);
   } else {
     // ---------------- epilogue: TMEM lane quarter = warp % 4; a quarter's two
     // warps take alternate groups of 32 columns

@@ -3,17 +3,27 @@
 // Units of ragged groups differ in length, and their order (a weight tile's
 // chunks next to one another, for L2) is periodic: dealt round-robin, one
 // worker would get every short last chunk and its neighbour every full one.  So
-// a pair starts with the unit of its index and takes the next ones from a counter in global
-// memory, each when its weights' producer starts on the last; one earlier where there are at
-// least eight units a pair, to hide the counter's latency (NVFP4, 64 x 512 rows, N = K = 4096: 239 -> 231 us).
-// A pair that fetches as far as it has slots takes five units of a small product while others
-// have none, more with several fetches under way (3190 rows of 59 groups, N = 360, K = 160, NVFP4: 19.6
-// instead of 15.4 us; 64 ragged groups of about 512 rows, N = 8192, K = 4096: 1375 instead of 1351; the input
-// gradient of 134 rows, N = 2192, K = 1864, with one, two and four fetches under way: 19, 32, 54, here 20).  The odd CTA's
-// MMA warp, which has no MMAs to issue, is the scheduler: it fetches units
-// ahead and puts them into a ring of kSchedSlots in both CTAs' shared memory,
-// where every other warp of the pair reads them in order.  Which pair computes
-// a unit does not change its result.
+// a pair starts with the unit of its index and takes the next ones from a counter
+// in global memory.  When it takes one:
+//   - when its weights' producer starts on the last unit: a pair that fetches
+//     further ahead takes units of a small product while others have none;
+//   - one earlier where there are at least eight units a pair, which hides the
+//     counter's latency.
+// Measured (us): 3190 rows of 59 groups, N = 360, K = 160, NVFP4: 15.4, fetching as far
+// as there are slots 19.6; the input gradient of 134 rows, N = 2192, K = 1864: 20, with two
+// and four fetches under way 32 and 54; NVFP4, 64 x 512 rows, N = K = 4096: one earlier 231, else 239.
+//
+// The odd CTA's MMA warp, which has no MMAs to issue, is the scheduler: it
+// fetches units and puts them into a ring of kSchedSlots in both CTAs' shared
+// memory, where every other warp of the pair reads them in order.  Which pair
+// computes a unit does not change its result.
+//
+// The scheduler overwrites a slot once every warp has read it, so the even CTA's
+// readings have to be ordered before its remote store: a release at cluster scope.
+// Given by the reading warps themselves it waits for the epilogue's stores to
+// global memory (256 groups of 64 rows, N = 1536, K = 256: 66 -> 76 us).  So the
+// warps of each CTA signal inside it, and a warp of the even CTA without stores of
+// its own, the relay, passes its CTA's signals on (63 to 66 us).
 #pragma once
 
 #include <cstdint>
@@ -23,24 +33,27 @@
 namespace moe {
 
 constexpr int kSchedSlots = 4;
-constexpr int kSchedBytes = kSchedSlots * (8 + 8 + 8 + 4) + 16;
+constexpr int kSchedBytes = kSchedSlots * (8 + 8 + 8 + 8 + 4) + 16;
 
 struct PairSched {
   uint64_t* full;   // a slot's unit is there (in each CTA)
-  uint64_t* empty;  // every warp of the pair has read it (the odd CTA's)
-  uint64_t* taken;  // the odd CTA's producer of the weights has read it
+  uint64_t* empty;  // the odd CTA's: its warps, and the relay, have read it
+  uint64_t* taken;  // the odd CTA's: its producer of the weights has read it
+  uint64_t* seen;   // the even CTA's: its warps have read it
   volatile int32_t* unit;
 
   __device__ explicit PairSched(uint8_t* smem)
       : full(reinterpret_cast<uint64_t*>(smem)), empty(full + kSchedSlots), taken(empty + kSchedSlots),
-        unit(reinterpret_cast<volatile int32_t*>(taken + kSchedSlots)) {}
+        seen(taken + kSchedSlots), unit(reinterpret_cast<volatile int32_t*>(seen + kSchedSlots)) {}
 
-  // one thread of each CTA, before the pair's cluster barrier; readers: warps of both CTAs that walk the units
-  __device__ __forceinline__ void init(int readers) const {
+  // one thread of each CTA, before the pair's cluster barrier; odd_readers: warps of the odd CTA that walk
+  // the units (of the even one one more, the MMA warp)
+  __device__ __forceinline__ void init(int odd_readers) const {
     for (int s = 0; s < kSchedSlots; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], readers);
+      ptx::mbar_init(&empty[s], odd_readers + 1);
       ptx::mbar_init(&taken[s], 1);
+      ptx::mbar_init(&seen[s], odd_readers + 1);
     }
   }
 
@@ -52,7 +65,7 @@ struct PairSched {
     int u = static_cast<int>(blockIdx.x >> 1);
     for (int i = 0;; ++i) {
       const int slot = i % kSchedSlots;
-      if (!mbar_wait(&empty[slot], (i / kSchedSlots & 1) ^ 1u, timeout_ns, abort)) return false;
+      if (!mbar_wait_cluster(&empty[slot], (i / kSchedSlots & 1) ^ 1u, timeout_ns, abort)) return false;
       unit[slot] = u;
       const uint32_t theirs = mapa_shared(smem_u32(const_cast<int32_t*>(unit) + slot), 0);
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(theirs), "r"(u) : "memory");
@@ -64,6 +77,19 @@ struct PairSched {
       u = pairs + atomicAdd(counter, 1);
     }
   }
+
+  // The relay (one thread of the even CTA).  False: a wait ran out.
+  __device__ bool relay(int total, uint64_t timeout_ns, const volatile int* abort) const {
+    using namespace ptx;
+    const uint32_t empty_odd = mapa_shared(smem_u32(empty), 1);
+    for (int i = 0;; ++i) {
+      const int slot = i % kSchedSlots;
+      if (!mbar_wait(&seen[slot], i / kSchedSlots & 1, timeout_ns, abort)) return false;
+      const int u = unit[slot];
+      mbar_arrive_cluster(empty_odd + 8u * slot);
+      if (u >= total) return true;
+    }
+  }
 };
 
 // One warp's walk along the scheduled units.
@@ -72,15 +98,16 @@ struct PairUnits {
   const int total;
   const volatile int* abort;
   const uint64_t timeout_ns;
-  const uint32_t empty_odd;
-  const bool taker;  // the odd CTA's producer of the weights
+  uint64_t* const read;  // where this CTA's warps signal that they have read a slot
+  const bool taker;      // the odd CTA's producer of the weights
   int slot = 0;
   uint32_t phase = 0;
   bool ok = true;  // false: a wait ran out
 
-  __device__ PairUnits(const PairSched& s, int units, uint64_t timeout, const volatile int* a, bool taker_)
-      : sched(s), total(units), abort(a), timeout_ns(timeout),
-        empty_odd(ptx::mapa_shared(ptx::smem_u32(s.empty), 1)), taker(taker_) {}
+  __device__ PairUnits(const PairSched& s, int units, uint64_t timeout, const volatile int* a, bool even,
+                       bool weights_producer)
+      : sched(s), total(units), abort(a), timeout_ns(timeout), read(even ? s.seen : s.empty),
+        taker(!even && weights_producer) {}
 
   // the next unit (warp-uniform; a whole warp calls), or -1
   __device__ __forceinline__ int next() {
@@ -93,7 +120,7 @@ struct PairUnits {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
       if (taker) mbar_arrive(&sched.taken[slot]);
-      mbar_arrive_remote(empty_odd + 8u * slot);
+      mbar_arrive(&read[slot]);
     }
     if (++slot == kSchedSlots) {
       slot = 0;

@@ -71,7 +71,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 
 // The same without cluster-scope ordering of this thread's memory accesses:
 // for signals that guard TMEM contents alone, which tcgen05.wait and the
-// tcgen05 fences order.  (A cluster-scope release waits for every earlier store
+// tcgen05 fences order (not for shared memory that the other CTA writes).  (A cluster-scope release waits for every earlier store
 // of the thread: some 1500 cycles once a stage.)
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");

@@ -607,3 +607,34 @@ def test_objects_may_go_while_their_work_is_queued_on_another_stream():
     assert not side.query() and not places & {t.data_ptr() for t in others}
     side.synchronize()
     assert torch.equal(y, want) and torch.equal(y4, want4)
+
+
+@pytest.mark.parametrize("op", ["forward", "dgrad", "mx", "nv"])
+def test_many_short_units_pass_through_the_pairs(op):
+    """Units of one or two K-blocks, some 25 a CTA pair: each slot of the ring that hands them out is written again soon
+    after its last reader.  Every row of every call comes from its own unit, and calls repeat bit for bit."""
+    groups, rows_each = 500, 40
+    n, k = (1024, 64) if op != "dgrad" else (64, 1024)
+    lists = Lists([rows_each + (7 * i) % 25 for i in range(groups)])
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    w = (torch.randn((groups, n, k), generator=gen, device="cuda") * 0.1).to(BF16)
+    a = lists.matrix(gen, k if op != "dgrad" else n, BF16)
+    if op in ("mx", "nv"):
+        r4, w4 = binding.Fp4Rows(op, k, groups, lists.rows).quantize(a, lists.offsets), binding.Fp4Weights.quantize(w, op)
+        of, call = w4, lambda: w4.forward(r4, lists.offsets)
+        ad, wd = r4.dequantize(lists.offsets, dtype=FP32).double(), w4.dequantize(FP32).double()
+    else:
+        of = binding.GroupedProducts(groups, n, k, BF16)
+        call = (lambda: of.forward(a, w, lists.offsets)) if op == "forward" else lambda: of.dgrad(a, w, lists.offsets)
+        ad, wd = a.double(), w.double()
+    if op == "dgrad":
+        wd = wd.mT.contiguous()
+    out = call()
+    assert of.device_status()[0] == binding.MOE_OK
+    want = torch.empty((lists.rows, wd.shape[1]), dtype=torch.float64, device="cuda")
+    s = torch.empty_like(want)
+    for g, (lo, hi) in enumerate(lists.spans):
+        want[lo:hi], s[lo:hi] = ad[lo:hi] @ wd[g].T, ad[lo:hi].abs() @ wd[g].abs().T
+    check(out, want, s, 128)  # (the 4-bit values and steps: 65 / 64 (64 + 64) + 264 2^-23 S, below 17 / 16 (128 + 16) + 256)
+    for _ in range(20):
+        assert torch.equal(call(), out)
