@@ -20,7 +20,10 @@
 //     One rounded reciprocal y = 1 / d serves 16 of them by Markstein's correction
 //     ("Computation of elementary functions on the IBM RISC System/6000", 1990):
 //     q = x y, r = x - q d (exact in a fused multiply-add), x / d = q + r y rounded, on two elements an
-//     instruction.  (Products with a lowered and a raised reciprocal, whose codes agree unless the
+//     instruction.  (The theorem excepts divisors whose significand is all ones, which d and 6 g
+//     can have.  Enumerated with fused multiply-adds on a CPU, all 2^23 significands of the divisor,
+//     nine dividends around each border of E2M1 and of E4M3: every quotient is the rounded one, those divisors'
+//     too.)  (Products with a lowered and a raised reciprocal, whose codes agree unless the
 //     quotient lies at a border, cost a second conversion, the slowest
 //     instruction here: 105 us for 134 M elements.)
 // Measured, 134 M bf16 elements: NVFP4 65 us (0.78 of the copy rate), MXFP4 48 to

@@ -534,3 +534,33 @@ def test_an_allocation_that_fails_leaves_the_rows_before(monkeypatch):
             r4.quantize(big)
         monkeypatch.undo()
         assert r4.rows == 10 and (r4.dequantize() == 1).all()
+
+
+def test_quotients_by_divisors_of_ones_alone():
+    """Divisors with the significand 0x7FFFFF, which the correction's theorem excepts: the codes and scales are still those
+    of the rounded quotients.  amax 0x40BFFFFF gives g = amax / 2688, scale 448 and d = RN(448 g) = 1 - 2^-24 (or d 2^k), so
+    x = 0.25 lies just above a border (0.25 / d rounds to 0.25 + 2^-25, code 1, not the tie's 0)."""
+    amax = np.array([0x40BFFFFF], np.uint32).view(np.float32)[0]
+    assert (np.float32(448) * (amax / np.float32(2688))).view(np.uint32) == 0x3F7FFFFF
+    x = np.zeros((8, 64), np.float32)
+    x[:, ::16] = amax
+    near = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    x[:, 1:8], x[:, 8:15] = near, -near
+    x[1, 1:8], x[2, 1:8] = np.nextafter(near, np.float32(0)), np.nextafter(near, np.float32(9))
+    x[3:] *= np.exp2(np.array([-40, -7, 1, 9, 40], np.float32))[:, None]
+    r4 = binding.Fp4Rows("nv", 64, 1, 8).quantize(torch.tensor(x).cuda())
+    c, s, _ = quantise(x, "nv", False)
+    assert (s == 126).all() and c[0, 1] == 1 and c[1, 1] == 0  # 126: 448
+    assert np.array_equal(unpack(r4.codes, 8, 64), c)
+    # the scale's own quotient, amax of a block / (6 g): 6 g of ones alone, blocks next to every border of E4M3
+    top = np.array([0x3FDFFFFF], np.uint32).view(np.float32)[0]
+    six_g = np.float32(6) * (top / np.float32(2688))
+    assert six_g.view(np.uint32) & 0x7FFFFF == 0x7FFFFF
+    border = ((E4M3[1:] + E4M3[:-1]) / np.float32(2) * six_g).astype(np.float32)
+    x = np.zeros((3, 128 * 16), np.float32)
+    x[:, 0] = top
+    x[:, 16:127 * 16:16] = border, np.nextafter(border, np.float32(0)), np.nextafter(border, np.float32(np.inf))
+    r4 = binding.Fp4Rows("nv", 2048, 1, 3).quantize(torch.tensor(x).cuda())
+    c, s, _ = quantise(x, "nv", False)
+    assert np.array_equal(scale_of(r4.scales, Lists([3]), 0, 3, 2048, "nv"), s)
+    assert np.array_equal(unpack(r4.codes, 3, 2048), c)
