@@ -526,17 +526,22 @@ MOE_API moe_status moe_qk_norm(int64_t T, int32_t Hq, int32_t Hk, int32_t D, moe
  *   input gradient   dx[p, :] = dy[p, :] w_g
  *   weight gradient  dw_g     = sum over the group's p of dy[p, :]^T x[p, :]
  * The lists moe_route_debug and moe_views give (offsets with padding between
- * the groups, counts) are such groups.  Products are summed in fp32 in one
- * fixed order for a given shape and device, so calls repeat bit for bit; each
- * output is rounded once.
+ * the groups, counts) are such groups.  Products are summed in fp32 and each
+ * output is rounded once.  The order of the sums follows the shape, the lists
+ * and the device: calls with the same ones repeat bit for bit.  A row's last bits
+ * can change with other groups' counts: forward and input gradient of at most 24
+ * rows a group on average split the sums wherever the lists make the work even.
+ * The tensor core cuts an fp32 sum towards zero once for every 16 products (4
+ * bits: 64), by at most 17 * 2^-23 (65 * 2^-23) of the sum of their magnitudes;
+ * measured, some 2^-24.
  *   offsets  [groups + 1] int32, device: offsets[g] + counts[g] <= offsets[g+1]
  *            and offsets[groups] <= rows; or NULL: equal groups of
  *            rows / groups rows (rows a multiple of groups, else
  *            MOE_ERR_INVALID_ARG)
  *   counts   [groups] int32, device, or NULL: offsets[g + 1] - offsets[g]
  * Rows that belong to no group are not written, and what they hold (NaN
- * included) reaches no output.  Offsets that break the rules above are found on the device:
- * nothing is written then, and moe_device_status() returns MOE_ERR_DEVICE with
+ * included) reaches no output.  Offsets that break the rules above are found on
+ * the device: nothing is written then, and moe_device_status() returns MOE_ERR_DEVICE with
  * kernel id 9 and the first such group's index (detail[2]).
  *   type     of x, w, y, dy, dx: MOE_TYPE_BF16 or MOE_TYPE_FP16
  *   ldx ...  row strides in elements: >= the row's width, multiples of 8
@@ -548,7 +553,9 @@ MOE_API moe_status moe_qk_norm(int64_t T, int32_t Hq, int32_t Hk, int32_t D, moe
  *            one after the other).
  * Matrices 16-byte aligned, outputs apart from the inputs.  Asynchronous on
  * `stream`, capturable like every call.  rows = 0 is a no-op (the weight
- * gradient still writes its zeros). */
+ * gradient still writes its zeros, unless it accumulates): nothing is enqueued, and
+ * moe_device_status() goes on to say what the call before reported, or on a workspace
+ * that no call has used, whatever its memory holds. */
 #define MOE_TYPE_BF16 0
 #define MOE_TYPE_FP16 1
 #define MOE_TYPE_FP32 2
@@ -574,13 +581,12 @@ MOE_API moe_status moe_grouped_gemm_dgrad(const moe_grouped_shape* shape, const 
 
 /* dw [groups, N, K] of dw_type (the operands' type, or MOE_TYPE_FP32): written
  * whole, zeros for an empty group; or, with accumulate != 0 (MOE_TYPE_FP32
- * only, else MOE_ERR_INVALID_ARG), added to what dw holds.  The tensor core cuts
- * its fp32 sums towards zero, each step of 16 rows by at most 17 * 2^-23 of the sum of
- * |dy x| (measured: some 2^-24).  So it accumulates 768 rows of a group at most, or 3840
- * for a dw of 16 bits (in all below half an fp16 step of the sum of |dy x|); the sums of
- * such segments are added in fp32, rounded to nearest, and dw is rounded once.  Into
- * 16 bits: rows <= 2^26 (else MOE_ERR_UNSUPPORTED); more than 3840 rows want the workspace
- * that moe_grouped_workspace_size() gives for them, 33 MB more. */
+ * only, else MOE_ERR_INVALID_ARG), added to what dw holds.  The tensor core (which
+ * cuts, see above) accumulates 768 rows of a group at most, or 3840 for a dw of 16
+ * bits, where the cuts stay below half an fp16 step of the sum of |dy x|; the sums
+ * of such segments are added in fp32, rounded to nearest, and dw is rounded once.
+ * Into 16 bits: rows <= 2^26 (else MOE_ERR_UNSUPPORTED); more than 3840 rows want
+ * the workspace that moe_grouped_workspace_size() gives for them, 29 MB more. */
 MOE_API moe_status moe_grouped_gemm_wgrad(const moe_grouped_shape* shape, const void* dy, int64_t lddy, const void* x,
                                           int64_t ldx, const int32_t* offsets, const int32_t* counts, void* dw,
                                           int32_t dw_type, int32_t accumulate, void* workspace,

@@ -638,3 +638,14 @@ def test_many_short_units_pass_through_the_pairs(op):
     check(out, want, s, 128)  # (the 4-bit values and steps: 65 / 64 (64 + 64) + 264 2^-23 S, below 17 / 16 (128 + 16) + 256)
     for _ in range(20):
         assert torch.equal(call(), out)
+
+
+def test_a_c_call_without_rows_leaves_the_status():
+    x, w = torch.ones((6, 64), dtype=BF16, device="cuda"), torch.ones((2, 8, 64), dtype=BF16, device="cuda")
+    bad = torch.tensor([0, 9, 6], dtype=torch.int32, device="cuda")
+    gp = binding.GroupedProducts(2, 8, 64, BF16)
+    gp.forward(x, w, bad)
+    stream = torch.cuda.current_stream().cuda_stream
+    args = (None, 64, w.data_ptr(), bad.data_ptr(), None, None, 8, gp.workspace.data_ptr(), gp.workspace.numel(), stream)
+    assert binding.moe_grouped_gemm(gp.shape(0), *args) == binding.MOE_OK
+    assert gp.device_status()[0] == binding.MOE_ERR_DEVICE
