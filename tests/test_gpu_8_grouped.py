@@ -649,3 +649,27 @@ def test_a_c_call_without_rows_leaves_the_status():
     args = (None, 64, w.data_ptr(), bad.data_ptr(), None, None, 8, gp.workspace.data_ptr(), gp.workspace.numel(), stream)
     assert binding.moe_grouped_gemm(gp.shape(0), *args) == binding.MOE_OK
     assert gp.device_status()[0] == binding.MOE_ERR_DEVICE
+
+
+@pytest.mark.parametrize("out", ["same", "fp32", "accumulate"])
+@pytest.mark.parametrize("groups,n,k,dtype", [(300, 520, 776, BF16), (900, 136, 264, FP16), (60, 1032, 1544, FP16)])
+def test_weight_gradient_of_many_tiles(groups, n, k, dtype, out):
+    """Dozens of tiles for each CTA pair, nearly every one of another group (other tensor maps), empty groups and rests of
+    every length among them."""
+    lists = Lists([(37 * i) % 150 if i % 5 else 0 for i in range(groups)], gap=1)
+    gen = torch.Generator(device="cuda").manual_seed(groups)
+    x, dy = lists.matrix(gen, k, dtype), lists.matrix(gen, n, dtype, scale=0.25)
+    gp = binding.GroupedProducts(groups, n, k, dtype)
+    start = torch.full((groups, n, k), 0.5, device="cuda") if out == "accumulate" else None
+    for _ in range(2):
+        if out == "accumulate":
+            dw = gp.wgrad(dy, x, lists.offsets, lists.counts, dw=start.clone(), accumulate=True)
+        else:
+            dw = gp.wgrad(dy, x, lists.offsets, lists.counts, dtype=FP32 if out == "fp32" else None)
+        assert gp.device_status()[0] == binding.MOE_OK
+        for g, (a, b) in enumerate(lists.spans):
+            dd, xd = dy[a:b].double(), x[a:b].double()
+            want, s = dd.T @ xd, dd.abs().T @ xd.abs()
+            if out == "accumulate":
+                want, s = want + 0.5, s + 0.5
+            check(dw[g], want, s, b - a)

@@ -564,3 +564,68 @@ def test_quotients_by_divisors_of_ones_alone():
     c, s, _ = quantise(x, "nv", False)
     assert np.array_equal(scale_of(r4.scales, Lists([3]), 0, 3, 2048, "nv"), s)
     assert np.array_equal(unpack(r4.codes, 3, 2048), c)
+
+
+def hard_matrix(rows, k, dtype, hard, seed):
+    """Rows of many binades made on the GPU, those of ``hard`` from hard_rows."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((rows, k), generator=gen, device="cuda")
+    x *= torch.exp2(torch.randint(-6, 7, (rows, k // 16), generator=gen, device="cuda").float()).repeat_interleave(16, 1)
+    x = x.to(dtype)
+    x[torch.tensor(hard, device="cuda")] = hard_rows(np.random.default_rng(seed), len(hard), k, dtype).cuda()
+    return x
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("rows,k", [(2500, 2048), (2500, 4128), (1500, 4096), (1500, 8224), (700, 8192), (700, 16416),
+                                    (40, 32800)])
+def test_rows_of_every_number_of_threads(rows, k, fmt, dtype):
+    """32, 64, 128 and 256 threads a row (fewer where there are more rows), their vectors held at once or in several
+    rounds: codes, scales and values of rows in every part, the first, the last and those at tile edges among them."""
+    lists = Lists([rows // 2 + 1, 0, rows // 8, rows - rows // 2 - 1 - rows // 8 - 3], tail=3)
+    at = sorted({min(a + d, b - 1) for a, b in lists.spans if b > a for d in (0, 1, 31, 32, 127, 128, 129, 10 ** 6)}
+                | set(range(5, rows - 3, max(1, rows // 11))))
+    x = hard_matrix(rows, k, dtype, at[::2], len(at))
+    r4 = binding.Fp4Rows(fmt, k, 4, rows).quantize(x, lists.offsets)
+    c, s, gs = quantise(x[torch.tensor(at, device="cuda")].float().cpu().numpy(), fmt, False)
+    raw = unpack(r4.codes, rows, k)[at]
+    if fmt == "nv":
+        assert np.array_equal(r4.gscale[torch.tensor(at, device="cuda")].cpu().numpy(), gs)
+        c = np.where(np.repeat(E4M3[s] * gs[:, None] == 0, 16, axis=1), 0, c)
+    assert np.array_equal(raw, c)
+    for g, (a, b) in enumerate(lists.spans):
+        mine = [i for i, p in enumerate(at) if a <= p < b]
+        if mine:
+            assert np.array_equal(scale_of(r4.scales, lists, g, b - a, k, fmt)[[at[i] - a for i in mine]], s[mine])
+    want = torch.tensor(values(c, s, gs, fmt))
+    for out in (BF16, FP16, FP32):
+        got = r4.dequantize(lists.offsets, dtype=out)[torch.tensor(at, device="cuda")].cpu().double()
+        over = want.abs() > torch.finfo(out).max
+        tiny = torch.finfo(out).smallest_normal * torch.finfo(out).eps / 2
+        # (the roundings of test_quantise_and_back)
+        rel = torch.finfo(out).eps / 2 + (2.0 ** -24 if out != FP32 else 0.0)
+        assert ((got - want).abs() <= want.abs() * rel * (1 + 2.0 ** -20) + tiny)[~over].all()
+        assert (got[over].abs() >= torch.finfo(out).max).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("groups,n,k", [(2, 1304, 4128), (3, 400, 8224), (5, 136, 16416)])
+def test_large_weights(groups, n, k, fmt):
+    """Matrices whose rows take 32, 64 and 128 threads in several rounds, one NVFP4 scale each."""
+    w = torch.stack([hard_matrix(n, k, BF16, [0, 1, n // 2, n - 1], g) * 2.0 ** (3 * g - 4) for g in range(groups)]).to(BF16)
+    w4 = binding.Fp4Weights.quantize(w, fmt)
+    lists, back = Lists([n] * groups, equal=True), w4.dequantize(FP32)
+    codes = unpack(w4.codes.view(-1), groups * n, k).reshape(groups, n, k)
+    for g in range(groups):
+        top = int(w[g].abs().amax(1).argmax())  # (its row sets the matrix's scale)
+        at = sorted({0, 1, 31, 32, 127, 128, n // 2, n // 2 + 1, n - 2, n - 1, top})
+        c, s, gs = quantise(w[g][torch.tensor(at, device="cuda")].float().cpu().numpy(), fmt, True)
+        assert np.array_equal(scale_of(w4.scales, lists, g, n, k, fmt)[at], s)
+        if fmt == "nv":
+            assert w4.gscale[g].item() == gs[0]
+            c = np.where(np.repeat(E4M3[s] * gs[:, None] == 0, 16, axis=1), 0, c)
+        assert np.array_equal(codes[g][at], c)
+        want = values(c, s, gs, fmt)
+        got = back[g][torch.tensor(at, device="cuda")].cpu().double().numpy()
+        assert (np.abs(got - want) <= 2.0 ** -24 * np.abs(want) + 2.0 ** -150).all()
