@@ -673,3 +673,24 @@ def test_weight_gradient_of_many_tiles(groups, n, k, dtype, out):
             if out == "accumulate":
                 want, s = want + 0.5, s + 0.5
             check(dw[g], want, s, b - a)
+
+
+def test_a_long_sum_into_16_bits_captured_first():
+    """The workspace's growth inside a capture, replayed on new rows and called beside it."""
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    x, dy = (torch.randn((9000, c), generator=gen, device="cuda").to(BF16) for c in (72, 136))
+    gp = binding.GroupedProducts(1, 136, 72, BF16)
+    gp.wgrad(dy[:100], x[:100])
+    dw = torch.zeros((1, 136, 72), dtype=BF16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gp.wgrad(dy, x, dw=dw)
+    eager = gp.wgrad(dy, x)
+    graph.replay()
+    assert gp.device_status()[0] == binding.MOE_OK and torch.equal(dw, eager)
+    x.copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+    graph.replay()
+    assert torch.equal(dw, gp.wgrad(dy, x))
+    dd, xd = dy.double(), x.double()
+    check(dw[0], dd.T @ xd, dd.abs().T @ xd.abs(), 3840)
