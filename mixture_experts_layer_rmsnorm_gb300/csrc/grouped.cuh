@@ -205,10 +205,12 @@ struct GroupedUnits {
 
 // A worker's share of a stream-K split, as segments: K-blocks [kb0, kb1) of
 // unit u.  The (unit, K-block) iterations form one list; every worker takes a
-// contiguous range of equal length.  Where there is little to do, fewer workers: four K-blocks
-// each, an eighth of a unit where that is more, at most a whole unit (each part is one more to
-// join: 8 rows, N = 152, K = 5168: parts of one K-block 50.6 us, of 2 33.3, of 4 18.4, of 8 13.6, of 16 12.7;
-// 8 groups of a row, N = 512, K = 128: parts of 1, 2, 4, 8 K-blocks 8.1, 5.8, 6.6, 8.6 us).
+// contiguous range of equal length.  Where there is little to do, fewer workers, since each
+// part of a unit is one more to join: at least four K-blocks each, or an eighth of a unit
+// where that is more, but never more than a whole unit.
+//   us for parts of           1     2     4     8    16 K-blocks
+//   8 rows, N 152, K 5168   50.6  33.3  18.4  13.6  12.7
+//   8 x 1 row, N 512, K 128  8.1   5.8   6.6   8.6
 struct GroupedRange {
   int64_t it, end, W;
   int kblocks, workers;

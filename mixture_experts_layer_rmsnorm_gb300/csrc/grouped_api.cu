@@ -164,15 +164,21 @@ bool too_many_units(const moe_grouped_shape* s, int F) {
   return (s->rows / 32 + s->groups) * ((F + 127) / 128) >= (int64_t(1) << 31);
 }
 
-// The tile plan follows the rows a group can be expected to hold: few, the product is
-// bound by streaming the weights once (32-row units on single CTAs, stream-K), else by reuse of
-// the weight tiles (units of up to 512 rows, 4 bits 256, on CTA pairs).  Up to 16 rows: single CTAs, also because
-// fewer groups than all may hold them.  Up to 24 (of ragged groups few are longer than
-// 32 rows then): single CTAs where whole units leave pairs idle for over 5% of their waves, or where a
-// 4-bit unit is short (K <= 2048).  Measured (us, pairs / single CTAs), 16 bits forward: 16 groups, N = K = 4096 (3.4
-// waves), 16 rows: 91 / 83, 24: 102 / 85; 64 groups, N = 8192, K = 4096 (26.9 waves), 16 rows: 616 / 628, 24: 627 / 647,
-// 64: 649 / 1438.  NVFP4 of these: 37 / 32, 37 / 34; 187 / 187, 189 / 197, 207 / 308; 256 groups, N = 1536, K = 2048, 16
-// rows: 106 / 78, 24: 107 / 81, 64: 125 / 137.
+// The tile plan follows the rows a group can be expected to hold, the mean: few, the product
+// is bound by streaming the weights once (32-row units on single CTAs, stream-K), else by reuse
+// of the weight tiles (units of up to 512 rows, 4 bits 256, on CTA pairs).
+//   up to 16 rows: single CTAs, also because fewer groups than all may hold them
+//   up to 24 (of ragged groups few are longer than 32 rows then): single CTAs where whole units
+//   leave pairs idle for over 5% of their waves, or where a 4-bit unit is short (K <= 2048)
+//   more: pairs
+// The host does not see the lists: where a few of many groups hold nearly all rows, the mean
+// chooses single CTAs, and groups of 64 rows and more take two to three times as long as they need.
+//   us on pairs / single CTAs                       16 rows    24         64
+//   16 bits, 16 groups, N = K = 4096 (3.4 waves)    91 / 83    102 / 85
+//   16 bits, 64 groups, N 8192, K 4096 (26.9)       616 / 628  627 / 647  649 / 1438
+//   NVFP4, 16 groups, N = K = 4096                  37 / 32    37 / 34
+//   NVFP4, 64 groups, N 8192, K 4096                187 / 187  189 / 197  207 / 308
+//   NVFP4, 256 groups, N 1536, K 2048               106 / 78   107 / 81   125 / 137
 GroupedPlan choose_plan(const moe_grouped_shape* s, int F, int sms, bool fp4) {
   if (s->rows <= int64_t(16) * s->groups) return GroupedPlan::kSmall;
   if (s->rows > int64_t(24) * s->groups) return GroupedPlan::kLarge;

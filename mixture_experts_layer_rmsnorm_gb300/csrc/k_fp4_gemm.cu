@@ -29,9 +29,12 @@
 // stores after that.
 //
 // Few rows a group: bound by HBM (64 rows in 41 of 64 groups, N = 8192, K = 4096,
-// MXFP4: 117 us with the rows' quantizer, 0.92 of the measured rate).  Many: bound by the fill of
-// shared memory; at the FP4 rate a pair would take a stage of 38 KB per SM every 341 cycles, 111
-// bytes a cycle, where the 16-bit kernel's loads alone reach 68 and this one takes 48.  Measured,
+// MXFP4: 117 us with the rows' quantizer, 0.92 of the measured rate).  Many: at the FP4
+// rate a pair would take a stage of 38 KB per SM every 341 cycles, 111 bytes a cycle.  The 16-bit
+// kernel's loads reach 68, so the fill of shared memory bounds it, but this one takes 48: what holds it
+// there is not isolated.  Ragged groups pay more: a rest unit of 20 rows fills its weight tile and
+// boxes of 128 rows like a full one (64 groups of 512, 520, 540 rows, N = K = 4096, NVFP4: 230 to 255, 344 to
+// 379, 379 us).  Measured,
 // 64 groups of 512 rows, N = K = 4096: NVFP4 230 us (4.8 PFLOP/s), MXFP4 191 us; one group of
 // 8192 rows, N = K = 8192: NVFP4 184 to 191 us (5.7 to 6.0 PFLOP/s).  In one comparison five,
 // four and three stages took 224, 237 and 269 us (NVFP4; MXFP4's six and five 188 and 193).  The hand-over

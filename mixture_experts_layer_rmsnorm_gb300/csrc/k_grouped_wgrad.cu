@@ -34,8 +34,9 @@
 // Bound: by writing dw where groups are short (a tile of fp32 moves 128 KB per
 // CTA for 64 KB of operands per 64 rows), else by the tensor cores; in between by shared memory, which
 // the operands cross twice and the tile too.  Measured, fp32: 64 groups of 32768 rows in all,
-// N = K = 4096: 983 to 1035 us under the power cap (0.72 to 0.69 of the bytes' time; its L1 / shared-memory pipe
-// is 81% busy); 64 x 512 even rows 895 us, into 16 bits 722 us.
+// N = K = 4096: 983 to 1045 us under the power cap (0.72 to 0.68 of the bytes' time; its L1 / shared-memory pipe
+// is 80% busy); 64 x 512 even rows 891 to 972 us, added to dw 1730 us (0.78 of the bytes' time: dw is read
+// too), into 16 bits 700 to 762 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -537,8 +537,8 @@ def test_few_blocks_are_shared_by_few_workers(op, rows, n, k):
 
 @pytest.mark.parametrize("dtype", [BF16, FP16], ids=str)
 def test_long_sums_into_16_bits_keep_their_precision(dtype):
-    """2^19 rows of one sign: accumulated whole, the tensor core's cuts take some 2e-3 of the sum, half a bf16 step and four
-    fp16 steps.  A segment of 3840 rows takes 240 steps of 9 2^-23 (as above: 2.6e-4), the 137 segments' additions 2^-24
+    """2^19 rows of one sign: accumulated whole, the tensor core's cuts take some 3e-3 of the sum, most of half a bf16 step and six
+    half fp16 steps.  A segment of 3840 rows takes 240 steps of 9 2^-23 (as above: 2.6e-4), the 137 segments' additions 2^-24
     each, and the output is rounded once."""
     gen = torch.Generator(device="cuda").manual_seed(13)
     rows = 1 << 19
