@@ -517,6 +517,8 @@ def _enqueue(name, device, *args, of=()):
     """name(*args, stream) of the library with ``device`` current, on its current stream; MoeError if it fails.  of:
     the objects whose buffers it uses."""
     global _C
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors on {device}, not on a CUDA device")
     if _C is None:
         from torch import _C as native
         _C = native

@@ -143,3 +143,16 @@ def test_weight_gradient_into_16_bits_of_long_groups_wants_its_larger_workspace(
     assert sizes[0] == sizes[1] < sizes[2]
     s = binding.grouped_shape(4, 64, 128, 3841)
     assert binding.moe_grouped_gemm_wgrad(s, A, 64, A, 128, A, None, A, 0, 0, A, sizes[2] - 1, None) == WS
+
+
+def test_tensors_on_the_cpu_are_refused():
+    import torch
+    bf16, w = torch.bfloat16, torch.zeros((2, 64, 128), dtype=torch.bfloat16)
+    h, act = torch.zeros((4, 128), dtype=bf16), torch.zeros((4, 64), dtype=bf16)
+    gp, r4 = binding.GroupedProducts(2, 64, 128, bf16, device="cpu"), binding.Fp4Rows("nv", 128, 2, 4, device="cpu")
+    for call in (lambda: binding.swiglu(h), lambda: binding.swiglu_grad(h, act), lambda: gp.forward(h, w),
+                 lambda: gp.dgrad(act, w), lambda: gp.wgrad(act, h), lambda: r4.quantize(h),
+                 lambda: binding.Fp4Weights.quantize(w, "mx")):
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            call()
+    assert gp.device_status() == (OK, [0] * 4) and r4.rows == 0
