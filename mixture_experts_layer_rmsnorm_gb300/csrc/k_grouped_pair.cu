@@ -21,7 +21,7 @@
 // A group's rows are cut into units of up to bn rows, evenly (full units and a
 // rest, 512 + 8 for 2 x 260 rows, measured 1.2 times as long), and units are handed out as
 // pairs ask for them (pair_sched.cuh; dealt round-robin 1.14 times as long).
-// Measured, 64 groups, N = 8192, K = 4096 (from box to box, as the power cap lets them): 512 rows
+// Measured, 64 groups, N = 8192, K = 4096 (from card to card, as the power cap lets them): 512 rows
 // 1179 to 1245 us (1.87 to 1.77 PFLOP/s, 0.96 to 0.91 of the burst rate), 520 rows 1362 to 1433 us,
 // 256 rows 709 to 733 us (0.95 to 0.92 of HBM: the weights alone); one group of 8192 rows, N = K = 8192:
 // 571 to 613 us (1.93 to 1.79 PFLOP/s).
