@@ -351,7 +351,7 @@ MOE_API moe_status moe_workspace_views(const moe_shape* shape, void* workspace, 
  * four raw int32 words: the code, the id of the kernel that recorded it
  * (1 norm/router, 2 top-k, 3 align, 4 gather, 5 gate/up GEMM, 6 down GEMM,
  * 7 combine, 8 self-test, 9 grouped products' tables, 10 grouped GEMM,
- * 11 grouped 4-bit GEMM), for the expert GEMMs a bit mask of the waits that
+ * 11 grouped 4-bit GEMM, 12 grouped 8-bit GEMM), for the expert GEMMs a bit mask of the waits that
  * ran out (bit 1 producer: ring slot free; 2 MMA: accumulator free; 3 MMA:
  * ring slot loaded; 4 epilogue: accumulator complete; 5 epilogue: stream-K
  * partial sums; 6 epilogue: fused-combine rendezvous; 7 MMA: a stage's scales
@@ -649,6 +649,58 @@ MOE_API moe_status moe_fp4_gemm(const moe_grouped_shape* shape, int32_t format, 
                                 const int32_t* counts, void* y, int64_t ldy, void* workspace,
                                 size_t workspace_bytes, moe_stream_t stream);
 
+/* ---- Rows in 8 bits with scales of 128, and their grouped products ------
+ * E4M3 codes under fp32 scales: 128 consecutive elements of a row share one, or
+ * (weights) a block of 128 x 128:
+ *   s = (largest magnitude) / 448, or 1 where that is 0;  code = E4M3(x / s)
+ * each division one fp32 operation, codes to nearest with ties to the even one;
+ * a block that holds a NaN or an infinity gets a NaN scale (what it stands for is
+ * NaN).  The products sum each block's codes on the tensor core (kind::f8f6f4)
+ * and add sx sw times that sum in fp32, so the scales may be any numbers.  (sx sw is
+ * one fp32 operation: where it lies below 2^-126 it loses bits.)
+ *   codes   [rows, K] bytes
+ *   scales  MOE_SCALE_PER_ROW: [ceil(K / 128)][lds] fp32, block b of row p at
+ *           b * lds + p (lds >= rows); MOE_SCALE_PER_BLOCK: `groups` matrices of
+ *           N = rows / groups rows each, [groups][ceil(N / 128)][ceil(K / 128)]
+ *           (lds unused, blocks at the edges smaller)
+ * K a multiple of 16 and <= 2^20; rows <= 2^31 - 512; row strides in elements,
+ * multiples of 8; src, dst and codes 16-byte, scales 4-byte aligned.  No lists:
+ * all rows are quantized, those of no group reach no product. */
+#define MOE_SCALE_PER_BLOCK 2
+
+typedef struct {
+  int32_t scale_per; /* MOE_SCALE_PER_ROW or MOE_SCALE_PER_BLOCK */
+  int32_t groups;    /* MOE_SCALE_PER_BLOCK: matrices, 1 .. 1024, rows a multiple of it (else unused) */
+  int64_t rows;
+  int32_t K;
+} moe_fp8_shape;
+
+/* Byte sizes of codes and scales (lds = rows).  Host only. */
+MOE_API moe_status moe_fp8_sizes(const moe_fp8_shape* shape, size_t* codes, size_t* scales);
+
+/* src [rows, K] of src_type (MOE_TYPE_*) -> codes, scales. */
+MOE_API moe_status moe_fp8_quantize(const moe_fp8_shape* shape, int32_t src_type, const void* src, int64_t ldsrc,
+                                    uint8_t* codes, float* scales, int64_t lds, moe_stream_t stream);
+
+/* The values the codes stand for (code * s), rounded to dst_type, into dst [rows, K]. */
+MOE_API moe_status moe_fp8_dequantize(const moe_fp8_shape* shape, const uint8_t* codes, const float* scales,
+                                      int64_t lds, int32_t dst_type, void* dst, int64_t lddst, moe_stream_t stream);
+
+/* y[p, :] = x[p, :] w_g^T and dx[p, :] = dy[p, :] w_g as moe_grouped_gemm and its
+ * input gradient (lists, workspace of moe_grouped_workspace_size(), errors; GEMM
+ * kernel id 12), with x [rows, K] (dy [rows, N]) quantized per row and w
+ * [groups, N, K] quantized per block, once for both products.  N and K multiples
+ * of 16 (else MOE_ERR_UNSUPPORTED).  shape->type: the type of y (dx).  (The weight
+ * gradient sums over rows, whose scales differ: moe_grouped_gemm_wgrad takes 16 bits.) */
+MOE_API moe_status moe_fp8_gemm(const moe_grouped_shape* shape, const uint8_t* x_codes, const float* x_scales,
+                                int64_t ldxs, const uint8_t* w_codes, const float* w_scales, const int32_t* offsets,
+                                const int32_t* counts, void* y, int64_t ldy, void* workspace,
+                                size_t workspace_bytes, moe_stream_t stream);
+MOE_API moe_status moe_fp8_gemm_dgrad(const moe_grouped_shape* shape, const uint8_t* dy_codes,
+                                      const float* dy_scales, int64_t ldds, const uint8_t* w_codes,
+                                      const float* w_scales, const int32_t* offsets, const int32_t* counts, void* dx,
+                                      int64_t lddx, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* SwiGLU of separate rows, between the gate/up and the down product: h
  * [rows, 2I] holds gate in columns [0, I) and up in [I, 2I) (the order of a
  * W13 product), act [rows, I] = SiLU(gate) * up; and its gradient,
@@ -658,6 +710,84 @@ MOE_API moe_status moe_swiglu(int32_t type, int64_t rows, int32_t I, const void*
                               int64_t ldact, moe_stream_t stream);
 MOE_API moe_status moe_swiglu_grad(int32_t type, int64_t rows, int32_t I, const void* h, int64_t ldh,
                                    const void* dact, int64_t lddact, void* dh, int64_t lddh, moe_stream_t stream);
+
+/* ---- The norm of rows, and its gradient --------------------------------
+ * What the layer does to its tokens first, on its own, with the layer norm
+ * beside it and the gradients of both:
+ *   n = (x - m) r,  r = 1 / sqrt(mean((x - m)^2) + eps),  y = n weight + bias
+ * over the H elements of each row, m the row's mean (MOE_NORM_LAYER) or 0
+ * (MOE_NORM_RMS, no bias); and with e = dy weight
+ *   dx = r (e - mean(e) - n mean(e n))       (MOE_NORM_RMS: without mean(e))
+ *   dweight = sum over the rows of dy n,  dbias = sum over the rows of dy
+ * fp32 inside, one rounding per output; a row's results depend on the row alone,
+ * and calls repeat bit for bit.  Squares and sums are fp32 numbers: rows whose
+ * squares do not fit them (|x| above some 1e18) get r = 0.
+ *   type         of x, y, dy, dx: MOE_TYPE_*
+ *   weight_type  of weight and bias: type, or MOE_TYPE_FP32
+ *   weight, bias [H], NULL for ones and zeros
+ *   mean, rstd   [rows] fp32: m and r, written by moe_norm (NULL: not kept) and
+ *                read by the gradient; MOE_NORM_RMS has no mean (NULL)
+ *   dweight, dbias  [H] of dweight_type (weight_type or MOE_TYPE_FP32), NULL where not
+ *                wanted; or, with accumulate != 0 (MOE_TYPE_FP32 only), added to
+ *                what they hold; MOE_NORM_RMS has no dbias (NULL)
+ *   workspace    moe_norm_grad_workspace_size() bytes, 256-byte aligned, contents on entry
+ *                do not matter, one call at a time uses it; unused (NULL) without dweight and dbias
+ * H a multiple of 8, <= 16384; rows <= 2^31 - 512; row strides in elements,
+ * multiples of 8; matrices, weight, bias and their gradients 16-byte aligned.  y may be x, and dx
+ * dy or x, with the same row stride.  rows = 0 is a no-op, but the gradient still writes
+ * zeros into dweight and dbias, unless it accumulates.  Asynchronous on `stream`. */
+#define MOE_NORM_RMS 0
+#define MOE_NORM_LAYER 1
+
+typedef struct {
+  int32_t kind;
+  int32_t type, weight_type;
+  int32_t H;
+  int64_t rows;
+  float eps; /* >= 0, finite */
+} moe_norm_shape;
+
+MOE_API moe_status moe_norm(const moe_norm_shape* shape, const void* x, int64_t ldx, const void* weight,
+                            const void* bias, void* y, int64_t ldy, float* mean, float* rstd, moe_stream_t stream);
+
+/* Host only; makes no CUDA call. */
+MOE_API moe_status moe_norm_grad_workspace_size(const moe_norm_shape* shape, size_t* bytes);
+
+MOE_API moe_status moe_norm_grad(const moe_norm_shape* shape, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                 const void* weight, const float* mean, const float* rstd, void* dx, int64_t lddx,
+                                 void* dweight, void* dbias, int32_t dweight_type, int32_t accumulate,
+                                 void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ---- The norm of all gradients, and clipping ---------------------------
+ *   norm = sqrt(sum of the squares of all elements of all tensors)
+ *   out = data * min(1, max_norm / (norm + eps))
+ * `tensors` is a host array that the call reads before it returns: any number of
+ * tensors of any size (n = 0 too; n <= 2^40) and type, n contiguous elements each, aligned
+ * to their elements (16-byte borders are faster).  Squares are summed in fp32 for 64
+ * elements at most, in fp64 beyond, in a fixed order; no finite element overflows or
+ * vanishes, and a norm above fp32's range is infinity.
+ *   norm   fp32, device: written by moe_grad_norm, read by moe_grad_clip
+ *   out    of out_type; may be data itself (with the same type), else apart from
+ *          every tensor.  Unused by moe_grad_norm.
+ * Where the norm is a NaN or infinite, nothing is clipped (the factor is 1).  A
+ * factor of 1 leaves a tensor in place untouched.  max_norm >= 0 (infinity: never
+ * clip), eps >= 0 and finite.  No tensors: the norm is 0.
+ *   workspace  moe_grad_norm_workspace_size() bytes for as many tensors, 256-byte aligned,
+ *              contents on entry do not matter, one call at a time uses it
+ * Asynchronous on `stream`, capturable like every call. */
+typedef struct {
+  const void* data;
+  void* out;
+  int64_t n;
+  int32_t type, out_type; /* MOE_TYPE_* */
+} moe_grad_tensor;
+
+/* Host only; makes no CUDA call. */
+MOE_API moe_status moe_grad_norm_workspace_size(int32_t n_tensors, size_t* bytes);
+MOE_API moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n_tensors, float* norm, void* workspace,
+                                 size_t workspace_bytes, moe_stream_t stream);
+MOE_API moe_status moe_grad_clip(const moe_grad_tensor* tensors, int32_t n_tensors, const float* norm,
+                                 double max_norm, double eps, moe_stream_t stream);
 
 /* Self-test of the failure path of the library's bounded device waits (no
  * counterpart on the pages): enqueues one small kernel whose two waits -- on

@@ -52,6 +52,21 @@ class MoeFp4Shape(ctypes.Structure):
                 ("K", ctypes.c_int32)]
 
 
+class MoeFp8Shape(ctypes.Structure):
+    _fields_ = [("scale_per", ctypes.c_int32), ("groups", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("K", ctypes.c_int32)]
+
+
+class MoeNormShape(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("type", ctypes.c_int32), ("weight_type", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("rows", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
+class MoeGradTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {moe_status_string(status)} (status {status})")
@@ -116,6 +131,19 @@ def load(build: bool = True):
             lib.moe_fp4_quantize.argtypes = [fp, i32, p, i64, p, p, p, p, p, i32, p]
             lib.moe_fp4_dequantize.argtypes = [fp, p, p, p, i32, p, p, i32, p, i64, p]
             lib.moe_fp4_gemm.argtypes = [gp, i32, p, p, p, p, p, p, p, p, p, i64, p, sz, p]
+            ep = ctypes.POINTER(MoeFp8Shape)
+            lib.moe_fp8_sizes.argtypes = [ep, psz, psz]
+            lib.moe_fp8_quantize.argtypes = [ep, i32, p, i64, p, p, i64, p]
+            lib.moe_fp8_dequantize.argtypes = [ep, p, p, i64, i32, p, i64, p]
+            lib.moe_fp8_gemm.argtypes = [gp, p, p, i64, p, p, p, p, p, i64, p, sz, p]
+            lib.moe_fp8_gemm_dgrad.argtypes = [gp, p, p, i64, p, p, p, p, p, i64, p, sz, p]
+            np_, tp, f64 = ctypes.POINTER(MoeNormShape), ctypes.POINTER(MoeGradTensor), ctypes.c_double
+            lib.moe_norm.argtypes = [np_, p, i64, p, p, p, i64, p, p, p]
+            lib.moe_norm_grad_workspace_size.argtypes = [np_, psz]
+            lib.moe_norm_grad.argtypes = [np_, p, i64, p, i64, p, p, p, p, i64, p, p, i32, i32, p, sz, p]
+            lib.moe_grad_norm_workspace_size.argtypes = [i32, psz]
+            lib.moe_grad_norm.argtypes = [tp, i32, p, p, sz, p]
+            lib.moe_grad_clip.argtypes = [tp, i32, p, f64, f64, p]
             lib.moe_status_string.argtypes = [ctypes.c_int]
             lib.moe_status_string.restype = ctypes.c_char_p
             for f in ("moe_workspace_size", "moe_forward", "moe_forward_events", "moe_route_debug",
@@ -129,7 +157,10 @@ def load(build: bool = True):
                       "moe_forward_mxfp4a4", "moe_nvfp4_weight_sizes", "moe_nvfp4_quantize_weights",
                       "moe_forward_nvfp4", "moe_forward_fused_mlp", "moe_grouped_workspace_size",
                       "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_swiglu",
-                      "moe_swiglu_grad", "moe_fp4_sizes", "moe_fp4_quantize", "moe_fp4_dequantize", "moe_fp4_gemm"):
+                      "moe_swiglu_grad", "moe_fp4_sizes", "moe_fp4_quantize", "moe_fp4_dequantize", "moe_fp4_gemm",
+                      "moe_fp8_sizes", "moe_fp8_quantize", "moe_fp8_dequantize", "moe_fp8_gemm", "moe_fp8_gemm_dgrad",
+                      "moe_norm", "moe_norm_grad_workspace_size", "moe_norm_grad", "moe_grad_norm_workspace_size",
+                      "moe_grad_norm", "moe_grad_clip"):
                 getattr(lib, f).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -438,6 +469,81 @@ def moe_fp4_gemm(s: MoeGroupedShape, format, x_codes, x_scales, x_gscale, w_code
                  y, ldy, workspace, workspace_bytes, stream) -> int:
     return load().moe_fp4_gemm(ctypes.byref(s), int(format), x_codes, x_scales, x_gscale, w_codes, w_scales, w_gscale,
                                offsets, counts, y, ldy, workspace, workspace_bytes, stream)
+
+
+MOE_SCALE_PER_BLOCK = 2
+
+
+def fp8_shape(scale_per, groups, rows, K) -> MoeFp8Shape:
+    return MoeFp8Shape(int(scale_per), int(groups), int(rows), int(K))
+
+
+def moe_fp8_sizes(s: MoeFp8Shape) -> tuple[int, tuple[int, int]]:
+    v = [ctypes.c_size_t(0) for _ in range(2)]
+    st = load().moe_fp8_sizes(ctypes.byref(s), *[ctypes.byref(a) for a in v])
+    return st, tuple(a.value for a in v)
+
+
+def moe_fp8_quantize(s: MoeFp8Shape, src_type, src, ldsrc, codes, scales, lds, stream) -> int:
+    return load().moe_fp8_quantize(ctypes.byref(s), int(src_type), src, ldsrc, codes, scales, lds, stream)
+
+
+def moe_fp8_dequantize(s: MoeFp8Shape, codes, scales, lds, dst_type, dst, lddst, stream) -> int:
+    return load().moe_fp8_dequantize(ctypes.byref(s), codes, scales, lds, int(dst_type), dst, lddst, stream)
+
+
+def moe_fp8_gemm(s: MoeGroupedShape, x_codes, x_scales, ldxs, w_codes, w_scales, offsets, counts, y, ldy, workspace,
+                 workspace_bytes, stream) -> int:
+    return load().moe_fp8_gemm(ctypes.byref(s), x_codes, x_scales, ldxs, w_codes, w_scales, offsets, counts, y, ldy,
+                               workspace, workspace_bytes, stream)
+
+
+def moe_fp8_gemm_dgrad(s: MoeGroupedShape, dy_codes, dy_scales, ldds, w_codes, w_scales, offsets, counts, dx, lddx,
+                       workspace, workspace_bytes, stream) -> int:
+    return load().moe_fp8_gemm_dgrad(ctypes.byref(s), dy_codes, dy_scales, ldds, w_codes, w_scales, offsets, counts, dx,
+                                     lddx, workspace, workspace_bytes, stream)
+
+
+MOE_NORM_RMS, MOE_NORM_LAYER = range(2)
+
+
+def norm_shape(kind, type, weight_type, H, rows, eps) -> MoeNormShape:
+    return MoeNormShape(int(kind), int(type), int(weight_type), int(H), int(rows), float(eps))
+
+
+def moe_norm(s: MoeNormShape, x, ldx, weight, bias, y, ldy, mean, rstd, stream) -> int:
+    return load().moe_norm(ctypes.byref(s), x, ldx, weight, bias, y, ldy, mean, rstd, stream)
+
+
+def moe_norm_grad_workspace_size(s: MoeNormShape) -> tuple[int, int]:
+    n = ctypes.c_size_t(0)
+    st = load().moe_norm_grad_workspace_size(ctypes.byref(s), ctypes.byref(n))
+    return st, n.value
+
+
+def moe_norm_grad(s: MoeNormShape, dy, lddy, x, ldx, weight, mean, rstd, dx, lddx, dweight, dbias, dweight_type,
+                  accumulate, workspace, workspace_bytes, stream) -> int:
+    return load().moe_norm_grad(ctypes.byref(s), dy, lddy, x, ldx, weight, mean, rstd, dx, lddx, dweight, dbias,
+                                int(dweight_type), int(bool(accumulate)), workspace, workspace_bytes, stream)
+
+
+def grad_tensors(tensors):
+    """An array of moe_grad_tensor from (data, out, n, type, out_type) each."""
+    return (MoeGradTensor * len(tensors))(*[MoeGradTensor(*t) for t in tensors])
+
+
+def moe_grad_norm_workspace_size(n_tensors) -> tuple[int, int]:
+    n = ctypes.c_size_t(0)
+    st = load().moe_grad_norm_workspace_size(int(n_tensors), ctypes.byref(n))
+    return st, n.value
+
+
+def moe_grad_norm(tensors, n_tensors, norm, workspace, workspace_bytes, stream) -> int:
+    return load().moe_grad_norm(tensors, int(n_tensors), norm, workspace, workspace_bytes, stream)
+
+
+def moe_grad_clip(tensors, n_tensors, norm, max_norm, eps, stream) -> int:
+    return load().moe_grad_clip(tensors, int(n_tensors), norm, float(max_norm), float(eps), stream)
 
 
 _types = {}
@@ -837,6 +943,262 @@ class Fp4Weights(_Workspace):
                    rows.scales.data_ptr(), _ptr(rows.gscale), self.codes.data_ptr(), self.scales.data_ptr(),
                    _ptr(self.gscale), *_lists(self, offsets, counts), yp, ldy, of=(rows,))
         return y
+
+
+class Fp8Rows(_Buffers):
+    """Rows in 8 bits (moe_fp8_quantize, one scale for each 128 elements): buffers for up to
+    ``max_rows`` rows of K elements, filled by :meth:`quantize`.  Calls go to the
+    current stream of the device.  More rows than ``max_rows`` get larger buffers; the
+    outgrown ones live as long as the object, for graphs that were captured with them and
+    work still queued on other streams."""
+
+    def __init__(self, K, max_rows=0, device=None):
+        import torch
+        self.K, self.device = int(K), torch.empty(0, device=device or "cuda").device
+        self.rows = self.max_rows = 0
+        self._shape, self._outgrown = None, []
+        self.ensure_capacity(max_rows)
+
+    def shape(self, rows) -> MoeFp8Shape:
+        s = self._shape  # (kept by one assignment: other host threads may ask too)
+        if s is None or s.rows != rows:
+            s = self._shape = fp8_shape(MOE_SCALE_PER_ROW, 1, rows, self.K)
+        return s
+
+    def ensure_capacity(self, rows):
+        """Buffers for up to ``rows`` rows; new ones hold no rows yet (``rows`` becomes 0)."""
+        if rows <= self.max_rows and self.max_rows > 0:
+            return
+        import torch
+        # (by half at least: what outgrown buffers hold stays below twice the last ones)
+        rows = max(rows, min(self.max_rows * 3 // 2, 2 ** 31 - 512), 1)
+        st, (n_codes, n_scales) = moe_fp8_sizes(fp8_shape(MOE_SCALE_PER_ROW, 1, rows, self.K))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_fp8_sizes")
+        # (both before either takes its place: where one does not fit, the rows before stay)
+        codes = torch.empty(n_codes, dtype=torch.uint8, device=self.device)
+        scales = torch.empty(n_scales // 4, dtype=torch.float32, device=self.device)
+        if self.max_rows > 0:
+            self._outgrown.append((self.codes, self.scales))
+        self.codes, self.scales, self.max_rows = codes, scales, rows
+        self.rows, self._streams = 0, frozenset()
+
+    def _buffers(self):
+        return self.codes, self.scales
+
+    def quantize(self, x):
+        """x [rows, K] (bf16, fp16 or fp32) to 8 bits; returns self."""
+        rows = x.shape[0]
+        xp, ldx = _matrix("x", x, self.device, x.dtype, (rows, self.K))
+        type_ = _type_of(x.dtype)
+        self.ensure_capacity(rows)
+        self.rows = 0  # (until they are on their way)
+        _enqueue("moe_fp8_quantize", self.device, ctypes.byref(self.shape(rows)), type_, xp, ldx, self.codes.data_ptr(),
+                 self.scales.data_ptr(), self.max_rows, of=(self,))
+        self.rows = rows
+        return self
+
+    def dequantize(self, y=None, dtype=None):
+        """The values of the rows quantized last, in ``dtype`` (bf16 by default) or y's type."""
+        if y is None:
+            import torch
+            y = torch.empty((self.rows, self.K), dtype=dtype or torch.bfloat16, device=self.device)
+        yp, ldy = _matrix("y", y, self.device, dtype or y.dtype, (self.rows, self.K))
+        _enqueue("moe_fp8_dequantize", self.device, ctypes.byref(self.shape(self.rows)), self.codes.data_ptr(),
+                 self.scales.data_ptr(), self.max_rows, _type_of(y.dtype), yp, ldy, of=(self,))
+        return y
+
+
+class Fp8Weights(_Workspace):
+    """Weights of ``groups`` matrices [N, K] in 8 bits (one scale for each 128 x 128) and their
+    products with 8-bit rows (moe_fp8_gemm, moe_fp8_gemm_dgrad).  codes: uint8 [groups, N, K];
+    scales: fp32 [groups, ceil(N / 128), ceil(K / 128)]."""
+
+    def __init__(self, codes, scales):
+        import torch
+        self.groups, self.N, self.K = codes.shape
+        self.device, self.int32 = codes.device, torch.int32
+        _check("codes", codes, self.device, torch.uint8, codes.shape)
+        _check("scales", scales, self.device, torch.float32, (self.groups, -(-self.N // 128), -(-self.K // 128)))
+        self.codes, self.scales, self._shape = codes, scales, None
+        st, n = moe_grouped_workspace_size(grouped_shape(self.groups, self.N, self.K, 0))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_grouped_workspace_size")
+        self.workspace = self._new_workspace(n)
+
+    def _buffers(self):
+        return self.workspace, self.codes, self.scales
+
+    def shape(self, rows, type) -> MoeGroupedShape:
+        s = self._shape  # (kept by one assignment: other host threads may ask too)
+        if s is None or s.rows != rows or s.type != type:
+            s = self._shape = grouped_shape(self.groups, self.N, self.K, rows, type)
+        return s
+
+    @classmethod
+    def quantize(cls, w):
+        """From w [groups, N, K] (bf16, fp16 or fp32)."""
+        import torch
+        groups, N, K = w.shape
+        _check("w", w, w.device, w.dtype, w.shape)
+        codes = torch.empty((groups, N, K), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((groups, -(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
+        _enqueue("moe_fp8_quantize", w.device, ctypes.byref(fp8_shape(MOE_SCALE_PER_BLOCK, groups, groups * N, K)),
+                 _type_of(w.dtype), _ptr(w), -(-K // 8) * 8, _ptr(codes), _ptr(scales), 0)
+        return cls(codes, scales)
+
+    def dequantize(self, dtype=None):
+        """The values the weights stand for, [groups, N, K] in ``dtype`` (bf16 by default)."""
+        import torch
+        w = torch.empty((self.groups, self.N, self.K), dtype=dtype or torch.bfloat16, device=self.device)
+        _enqueue("moe_fp8_dequantize", self.device,
+                 ctypes.byref(fp8_shape(MOE_SCALE_PER_BLOCK, self.groups, self.groups * self.N, self.K)),
+                 _ptr(self.codes), _ptr(self.scales), 0, _type_of(w.dtype), _ptr(w), self.K, of=(self,))
+        return w
+
+    def _product(self, name, rows, K, N, offsets, counts, out, dtype):
+        if rows.K != K or rows.device != self.device:
+            raise ValueError(f"rows of {rows.K} elements on {rows.device}, {K} on {self.device} wanted")
+        if out is None:
+            import torch
+            out = torch.empty((rows.rows, N), dtype=dtype or torch.bfloat16, device=self.device)
+        op, ldo = _matrix("the output", out, self.device, dtype or out.dtype, (rows.rows, N))
+        self._call(name, self.shape(rows.rows, _type_of(out.dtype)), rows.codes.data_ptr(), rows.scales.data_ptr(),
+                   rows.max_rows, self.codes.data_ptr(), self.scales.data_ptr(), *_lists(self, offsets, counts), op, ldo,
+                   of=(rows,))
+        return out
+
+    def forward(self, rows: Fp8Rows, offsets=None, counts=None, y=None, dtype=None):
+        """y[p] = x[p] w_g^T in ``dtype`` (bf16 by default, or fp16) or y's type, for the rows p of every group g (lists as
+        for :class:`GroupedProducts`); other rows of y stay as they are.  rows: x in 8 bits."""
+        return self._product("moe_fp8_gemm", rows, self.K, self.N, offsets, counts, y, dtype)
+
+    def dgrad(self, rows: Fp8Rows, offsets=None, counts=None, dx=None, dtype=None):
+        """dx[p] = dy[p] w_g.  rows: dy [rows, N] in 8 bits."""
+        return self._product("moe_fp8_gemm_dgrad", rows, self.N, self.K, offsets, counts, dx, dtype)
+
+
+class RowNorm(_Buffers):
+    """The RMS norm ("rms") or layer norm ("layer") of rows of H elements, and its gradient (moe_norm,
+    moe_norm_grad), with a workspace of its own.  dtype: of the rows; weight_dtype: of weight and bias,
+    dtype (the default) or fp32.  Calls go to the current stream of the rows' device; gradients of one
+    object on several streams share its workspace and must not overlap."""
+
+    def __init__(self, H, kind, dtype, weight_dtype=None, eps=1e-6, device=None):
+        import torch
+        kinds = {"rms": MOE_NORM_RMS, "layer": MOE_NORM_LAYER}
+        if kind not in kinds:
+            raise ValueError(f"kind {kind!r}: 'rms' or 'layer' wanted")
+        self.H, self.kind, self.layer, self.dtype = int(H), kinds[kind], kind == "layer", dtype
+        self.weight_dtype, self.eps, self.fp32 = weight_dtype or dtype, float(eps), torch.float32
+        self.device = torch.empty(0, device=device or "cuda").device
+        self._shape = None
+        st, n = moe_norm_grad_workspace_size(self.shape(0))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_norm_grad_workspace_size")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def _buffers(self):
+        return (self.workspace,)
+
+    def shape(self, rows) -> MoeNormShape:
+        s = self._shape  # (kept by one assignment: other host threads may ask too)
+        if s is None or s.rows != rows:
+            s = self._shape = norm_shape(self.kind, _type_of(self.dtype), _type_of(self.weight_dtype), self.H, rows,
+                                         self.eps)
+        return s
+
+    def _vector(self, what, t, dtype):
+        return None if t is None else _check(what, t, self.device, dtype, (self.H,)).data_ptr()
+
+    def forward(self, x, weight=None, bias=None, y=None, stats=False):
+        """y = n weight + bias for x [rows, H]; y may be x.  stats: also what the gradient needs, (y, rstd), or (y, rstd,
+        mean) of the layer norm."""
+        rows = x.shape[0]
+        xp, ldx = _matrix("x", x, self.device, self.dtype, (rows, self.H))
+        if y is None:
+            y = _empty((rows, self.H), self.dtype, self.device)
+        yp, ldy = _matrix("y", y, self.device, self.dtype, (rows, self.H))
+        rstd = _empty((rows,), self.fp32, self.device) if stats else None
+        mean = _empty((rows,), self.fp32, self.device) if stats and self.layer else None
+        _enqueue("moe_norm", self.device, ctypes.byref(self.shape(rows)), xp, ldx,
+                 self._vector("weight", weight, self.weight_dtype), self._vector("bias", bias, self.weight_dtype), yp, ldy,
+                 _ptr(mean), _ptr(rstd))
+        if not stats:
+            return y
+        return (y, rstd, mean) if self.layer else (y, rstd)
+
+    def grad(self, dy, x, weight, rstd, mean=None, dx=None, dweight=None, dbias=None, dtype=None, accumulate=False):
+        """(dx, dweight), or (dx, dweight, dbias) of the layer norm.  dx may be dy or x.  dweight and dbias: in ``dtype``
+        (fp32 or the weight's type, the default) or their own; accumulate (fp32): added to them."""
+        rows = x.shape[0]
+        dp, lddy = _matrix("dy", dy, self.device, self.dtype, (rows, self.H))
+        xp, ldx = _matrix("x", x, self.device, self.dtype, (rows, self.H))
+        rp = _check("rstd", rstd, self.device, self.fp32, (rows,)).data_ptr()
+        mp = None if mean is None else _check("mean", mean, self.device, self.fp32, (rows,)).data_ptr()
+        if dx is None:
+            dx = _empty((rows, self.H), self.dtype, self.device)
+        op, lddx = _matrix("dx", dx, self.device, self.dtype, (rows, self.H))
+        if accumulate and (dweight is None or (self.layer and dbias is None)):
+            raise ValueError("accumulate adds to dweight and dbias: pass them")
+        dtype = dtype or (dweight.dtype if dweight is not None else dbias.dtype if dbias is not None else self.weight_dtype)
+        if dweight is None:
+            dweight = _empty((self.H,), dtype, self.device)
+        if dbias is None and self.layer:
+            dbias = _empty((self.H,), dtype, self.device)
+        _enqueue("moe_norm_grad", self.device, ctypes.byref(self.shape(rows)), dp, lddy, xp, ldx,
+                 self._vector("weight", weight, self.weight_dtype), mp, rp, op, lddx, self._vector("dweight", dweight, dtype),
+                 self._vector("dbias", dbias, dtype), _type_of(dtype), 1 if accumulate else 0, self.workspace.data_ptr(),
+                 self.workspace.numel(), of=(self,))
+        return (dx, dweight, dbias) if self.layer else (dx, dweight)
+
+
+class Gradients(_Buffers):
+    """Tensors whose elements have one norm (moe_grad_norm) and are clipped together (moe_grad_clip): contiguous, of any
+    size, bf16, fp16 or fp32, on one device.  out: where the clipped ones go, tensors of the same sizes and of any of the
+    types; None: in place.  The tensors are kept, so their places must not change (fill them, do not replace them).
+    Calls go to the current stream of the device; calls of one object on several streams share its workspace and
+    must not overlap."""
+
+    def __init__(self, tensors, out=None, device=None):
+        import torch
+        self.tensors = list(tensors)
+        self.out = self.tensors if out is None else list(out)
+        if len(self.out) != len(self.tensors):
+            raise ValueError(f"{len(self.out)} tensors in out, {len(self.tensors)} wanted")
+        self.device = self.tensors[0].device if self.tensors else torch.empty(0, device=device or "cuda").device
+        for i, (t, o) in enumerate(zip(self.tensors, self.out)):
+            _check(f"tensor {i}", t, self.device, t.dtype, t.shape)
+            _check(f"out {i}", o, self.device, o.dtype, t.shape)
+        self._table = grad_tensors([(t.data_ptr(), o.data_ptr(), t.numel(), _type_of(t.dtype), _type_of(o.dtype))
+                                    for t, o in zip(self.tensors, self.out)])
+        st, n = moe_grad_norm_workspace_size(len(self.tensors))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_grad_norm_workspace_size")
+        self.workspace, self.fp32 = torch.empty(n, dtype=torch.uint8, device=self.device), torch.float32
+
+    def _buffers(self):
+        return (self.workspace, *self.tensors, *self.out)
+
+    def norm(self):
+        """The norm, a tensor of one fp32 number."""
+        norm = _empty((), self.fp32, self.device)
+        _enqueue("moe_grad_norm", self.device, self._table, len(self.tensors), norm.data_ptr(), self.workspace.data_ptr(),
+                 self.workspace.numel(), of=(self,))
+        return norm
+
+    def clip(self, max_norm, eps=1e-6, norm=None):
+        """out = tensor * min(1, max_norm / (norm + eps)); returns the norm (before clipping).  norm: one already known,
+        such as that of these gradients and others."""
+        if norm is None:
+            norm = self.norm()
+        else:
+            _check("norm", norm, self.device, self.fp32, norm.shape)
+            if norm.numel() != 1:
+                raise ValueError(f"norm is {tuple(norm.shape)}, not one number")
+        _enqueue("moe_grad_clip", self.device, self._table, len(self.tensors), norm.data_ptr(), float(max_norm),
+                 float(eps), of=(self,))
+        return norm
 
 
 class MoeLayer:

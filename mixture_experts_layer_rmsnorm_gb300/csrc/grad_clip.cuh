@@ -1,0 +1,37 @@
+// grad_clip.cuh -- the norm of many tensors together, and their clipping (internal).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+namespace moe {
+
+struct GradTensor {
+  const void* src;
+  void* dst;
+  int64_t n;
+  int32_t first;  // its first chunk in the launch's order
+  uint8_t type, dst_type;  // 0 bf16, 1 fp16, 2 fp32
+  uint8_t vec, dst_vec;    // addresses on 16-byte borders
+};
+
+// Tensors go to the kernels as parameters, so that a call is complete in itself (captured,
+// replayed, several at once): launches of up to kGradTensors of them (32,764 bytes of
+// parameters are allowed), or of kGradFew where that is all, which takes less time to launch.
+constexpr int kGradTensors = 1000, kGradFew = 32;
+constexpr int kGradCtas = 640;       // of a launch, at most: a partial sum each
+constexpr int64_t kGradChunk = 16384;  // elements
+
+inline int64_t grad_launches(int64_t tensors) { return tensors > 0 ? (tensors + kGradTensors - 1) / kGradTensors : 1; }
+inline size_t grad_partial_bytes(int64_t tensors) {
+  return static_cast<size_t>(grad_launches(tensors)) * kGradCtas * sizeof(double);
+}
+
+// norm [1] from the tensors (empty ones left out, chunks counted from 0 in each launch)
+cudaError_t launch_grad_norm(const GradTensor* t, int64_t n, float* norm, double* partials, int num_sms,
+                             cudaStream_t stream);
+cudaError_t launch_grad_clip(const GradTensor* t, int64_t n, const float* norm, double max_norm, double eps, int num_sms,
+                             cudaStream_t stream);
+
+}  // namespace moe

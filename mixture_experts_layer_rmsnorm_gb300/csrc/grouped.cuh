@@ -20,7 +20,7 @@
 
 namespace moe {
 
-enum : int32_t { kKernGroupedPlan = 9, kKernGroupedGemm = 10, kKernFp4Gemm = 11 };
+enum : int32_t { kKernGroupedPlan = 9, kKernGroupedGemm = 10, kKernFp4Gemm = 11, kKernFp8Gemm = 12 };
 
 constexpr int kGroupsMax = 1024;
 // the GEMM kernels keep the tables in shared memory up to this many groups

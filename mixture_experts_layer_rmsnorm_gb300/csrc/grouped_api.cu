@@ -1,5 +1,5 @@
-// grouped_api.cu -- the C ABI of the grouped products (16-bit and 4-bit), of
-// rows in 4 bits and of SwiGLU on separate rows: argument checks, workspace
+// grouped_api.cu -- the C ABI of the grouped products (16-bit, 4-bit and 8-bit), of
+// rows in 4 and 8 bits and of SwiGLU on separate rows: argument checks, workspace
 // layout, tensor maps, launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -8,6 +8,7 @@
 
 #include "../../include/moe.h"
 #include "fp4.cuh"
+#include "fp8.cuh"
 #include "grouped.cuh"
 #include "grouped_elementwise.cuh"
 #include "tensor_map.h"
@@ -282,17 +283,105 @@ moe_status fp4_rows(const moe_fp4_shape* s, int32_t type, const void* rows, int6
   return MOE_OK;
 }
 
-// Code rows: boxes of 128 bytes x box_rows, 128-byte swizzle; matrices [G, N, K / 2] or rows (G = 0).
-bool make_codes_map(CUtensorMap* m, const void* base, int64_t K, int64_t N, int64_t G, uint32_t box_rows) {
+// Code rows of `bytes` each: boxes of 128 bytes x box_rows, 128-byte swizzle; matrices [G, N, bytes] or rows (G = 0).
+bool make_codes_map(CUtensorMap* m, const void* base, int64_t bytes, int64_t N, int64_t G, uint32_t box_rows) {
   auto fn = moe::encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(G)};
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(G)};
   cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
   cuuint32_t box[3] = {128, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, G > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---- 8 bits
+
+moe_status check_fp8(const moe_fp8_shape* s) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->scale_per != MOE_SCALE_PER_ROW && s->scale_per != MOE_SCALE_PER_BLOCK) return MOE_ERR_INVALID_ARG;
+  if (s->K <= 0 || s->rows < 0) return MOE_ERR_INVALID_ARG;
+  const bool blocks = s->scale_per == MOE_SCALE_PER_BLOCK;
+  if (blocks && (s->groups <= 0 || s->rows % s->groups != 0)) return MOE_ERR_INVALID_ARG;
+  // K: 16-byte rows of codes for TMA
+  if ((blocks && s->groups > moe::kGroupsMax) || s->K % 16 != 0 || s->K > kMaxDim || s->rows > kMaxRows)
+    return MOE_ERR_UNSUPPORTED;
+  // (a matrix's block for each CTA)
+  if (blocks && s->groups * ((s->rows / s->groups + 127) / 128) * ((s->K + 127) / 128) >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status fp8_rows(const moe_fp8_shape* s, int32_t type, const void* rows, int64_t ld, const uint8_t* codes,
+                    const float* scales, int64_t lds, moe::Fp8Args* out) {
+  moe_status st = check_fp8(s);
+  if (st != MOE_OK) return st;
+  if (type != MOE_TYPE_BF16 && type != MOE_TYPE_FP16 && type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
+  if ((st = check_rows(rows, s->rows, ld, s->K)) != MOE_OK) return st;
+  if (s->rows > 0 && (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 4))) return MOE_ERR_INVALID_ARG;
+  const bool blocks = s->scale_per == MOE_SCALE_PER_BLOCK;
+  if (!blocks && (lds < s->rows || lds > kMaxLd)) return MOE_ERR_INVALID_ARG;
+  moe::Fp8Args a{};
+  a.rows = s->rows;
+  a.per = blocks ? s->rows / s->groups : 0;
+  a.K = s->K;
+  a.codes = const_cast<uint8_t*>(codes);
+  a.scales = const_cast<float*>(scales);
+  a.lds = lds;
+  a.ld = ld;
+  a.type = type;
+  *out = a;
+  return MOE_OK;
+}
+
+// forward (F = N features, R = K) and input gradient (F = K, R = N)
+moe_status fp8_product(GroupedOp op, const moe_grouped_shape* s, const uint8_t* codes, const float* scales, int64_t lds,
+                       const uint8_t* w_codes, const float* w_scales, const int32_t* offsets, const int32_t* counts,
+                       void* out, int64_t ldout, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (s->N % 16 != 0 || s->K % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  const int F = op == GroupedOp::kForward ? s->N : s->K, R = op == GroupedOp::kForward ? s->K : s->N;
+  if ((st = check_rows(out, s->rows, ldout, F)) != MOE_OK) return st;
+  if (s->rows > 0 && (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 4))) return MOE_ERR_INVALID_ARG;
+  if (lds < s->rows || lds > kMaxLd) return MOE_ERR_INVALID_ARG;
+  if (!w_codes || !aligned(w_codes, 16) || !w_scales || !aligned(w_scales, 4)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_call(s, offsets, counts, ws, ws_bytes)) != MOE_OK) return st;
+  if (too_many_units(s, F)) return MOE_ERR_UNSUPPORTED;
+  if (s->rows == 0) return MOE_OK;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  const GroupedPlan plan = choose_plan(s, F, sms, false);
+  const int tile = moe::grouped_tile(plan), tiles = (F + tile - 1) / tile;
+  const bool large = plan == GroupedPlan::kLarge;
+  CUtensorMap tw, tx, tx32;
+  if (!make_codes_map(&tw, w_codes, s->K, s->N, s->groups, 128) ||
+      !make_codes_map(&tx, codes, R, s->rows, 0, static_cast<uint32_t>(moe::fp8_tok_box(plan))) ||
+      (large && !make_codes_map(&tx32, codes, R, s->rows, 0, 32)))
+    return MOE_ERR_CUDA;
+  const Layout L = make_layout(s->groups);
+  moe::GroupedPlanArgs p = plan_args(s, L, ws, offsets, counts);
+  p.bn = moe::fp8_bn(plan, s->rows, s->groups, tiles, sms);
+  p.tiles = tiles;
+  moe::Fp8GemmArgs a{};
+  a.g = gemm_args(s, L, ws);
+  a.g.out = out;
+  a.g.ldo = ldout;
+  a.g.F = F;
+  a.g.R = R;
+  a.g.tiles = tiles;
+  a.g.bn = p.bn;
+  a.x_scales = scales;
+  a.ldxs = lds;
+  a.w_scales = w_scales;
+  a.w_rows = (s->N + 127) / 128;
+  a.w_cols = (s->K + 127) / 128;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (moe::launch_grouped_plan(p, tx, tx, cs) != cudaSuccess ||
+      moe::launch_fp8_gemm(op, plan, tw, tx, large ? tx32 : tx, a, sms, cs) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
 }
 
 }  // namespace
@@ -456,8 +545,8 @@ moe_status moe_fp4_gemm(const moe_grouped_shape* shape, int32_t format, const ui
   const int bn = moe::fp4_bn(plan), tile = moe::fp4_tile(plan);
   const int tiles = (s->N + tile - 1) / tile;
   CUtensorMap tw, tx;
-  if (!make_codes_map(&tw, w_codes, s->K, s->N, s->groups, 128) ||
-      !make_codes_map(&tx, x_codes, s->K, s->rows, 0, static_cast<uint32_t>(moe::fp4_tok_box(plan))))
+  if (!make_codes_map(&tw, w_codes, s->K / 2, s->N, s->groups, 128) ||
+      !make_codes_map(&tx, x_codes, s->K / 2, s->rows, 0, static_cast<uint32_t>(moe::fp4_tok_box(plan))))
     return MOE_ERR_CUDA;
   const Layout L = make_layout(s->groups);
   moe::GroupedPlanArgs p = plan_args(s, L, workspace, offsets, counts);
@@ -481,6 +570,54 @@ moe_status moe_fp4_gemm(const moe_grouped_shape* shape, int32_t format, const ui
       moe::launch_fp4_gemm(format_of(format), plan, tw, tx, a, sms, cs) != cudaSuccess)
     return MOE_ERR_CUDA;
   return MOE_OK;
+}
+
+moe_status moe_fp8_sizes(const moe_fp8_shape* shape, size_t* codes, size_t* scales) {
+  const moe_status st = check_fp8(shape);
+  if (st != MOE_OK) return st;
+  if (!codes || !scales) return MOE_ERR_INVALID_ARG;
+  const size_t rows = static_cast<size_t>(shape->rows), blocks = (static_cast<size_t>(shape->K) + 127) / 128;
+  *codes = rows * static_cast<size_t>(shape->K);
+  if (shape->scale_per == MOE_SCALE_PER_ROW) {
+    *scales = rows * blocks * 4;
+  } else {
+    const size_t groups = static_cast<size_t>(shape->groups);
+    *scales = groups * ((rows / groups + 127) / 128) * blocks * 4;
+  }
+  return MOE_OK;
+}
+
+moe_status moe_fp8_quantize(const moe_fp8_shape* shape, int32_t src_type, const void* src, int64_t ldsrc,
+                            uint8_t* codes, float* scales, int64_t lds, moe_stream_t stream) {
+  moe::Fp8Args a;
+  const moe_status st = fp8_rows(shape, src_type, src, ldsrc, codes, scales, lds, &a);
+  if (st != MOE_OK || shape->rows == 0) return st;
+  a.src = src;
+  return moe::launch_fp8_quantize(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_fp8_dequantize(const moe_fp8_shape* shape, const uint8_t* codes, const float* scales, int64_t lds,
+                              int32_t dst_type, void* dst, int64_t lddst, moe_stream_t stream) {
+  moe::Fp8Args a;
+  const moe_status st = fp8_rows(shape, dst_type, dst, lddst, codes, scales, lds, &a);
+  if (st != MOE_OK || shape->rows == 0) return st;
+  a.dst = dst;
+  return moe::launch_fp8_dequantize(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_fp8_gemm(const moe_grouped_shape* shape, const uint8_t* x_codes, const float* x_scales, int64_t ldxs,
+                        const uint8_t* w_codes, const float* w_scales, const int32_t* offsets, const int32_t* counts,
+                        void* y, int64_t ldy, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  return fp8_product(GroupedOp::kForward, shape, x_codes, x_scales, ldxs, w_codes, w_scales, offsets, counts, y, ldy,
+                     workspace, workspace_bytes, stream);
+}
+
+moe_status moe_fp8_gemm_dgrad(const moe_grouped_shape* shape, const uint8_t* dy_codes, const float* dy_scales,
+                              int64_t ldds, const uint8_t* w_codes, const float* w_scales, const int32_t* offsets,
+                              const int32_t* counts, void* dx, int64_t lddx, void* workspace, size_t workspace_bytes,
+                              moe_stream_t stream) {
+  return fp8_product(GroupedOp::kDgrad, shape, dy_codes, dy_scales, ldds, w_codes, w_scales, offsets, counts, dx, lddx,
+                     workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -647,5 +647,46 @@ __host__ __device__ __forceinline__ constexpr uint32_t idesc_f16_f32(uint32_t M,
          ((M >> 4) << 24);
 }
 
+// MMA on 8-bit operands (kind::f8f6f4, one byte a code; K = 32 per instruction), fp32 accumulators.  One thread.
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same over a CTA pair (M = 256), issued by one thread of the even CTA; operands as for mma_bf16_ss_pair.
+__device__ __forceinline__ void mma_f8_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4 with fp32 accumulators: both operands E4M3 (format 0), B K-major; a_mn: A is
+// MN-major (bit 15).
+__host__ __device__ __forceinline__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t a_mn) {
+  return (1u << 4) | (a_mn << 15) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// 16 lanes x 32 consecutive 32-bit columns, spread like the accumulators of a warp's 16 x 8 matrix product: of
+// columns 8 j .. 8 j + 7 thread i holds r[4 j], r[4 j + 1] (lane i / 4, columns 2 (i % 4) and the next) and
+// r[4 j + 2], r[4 j + 3] (lane i / 4 + 8).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 }  // namespace ptx
 }  // namespace moe
