@@ -9,20 +9,23 @@
 // registers, one fp32 multiply-add per element and block.  That sum rounds to nearest;
 // the tensor core's own cuts towards zero stay inside a block of 128.
 //
-// Mapping, units and work split as in k_grouped_gemm.cu and k_grouped_pair.cu: the
-// weights take the MMA's M side, a group's rows its N side; the input gradient
-// reads the stored matrix as an MN-major operand; few rows a group: single CTAs,
-// stream-K; many: CTA pairs, units of up to 256 rows handed out on demand.
-// A K-block is one block of scales, 128 bytes of codes a row.
+// Units and work split as in k_grouped_gemm.cu and k_grouped_pair.cu; the input gradient
+// reads the stored matrix as an MN-major operand.  A K-block is one block of scales, 128
+// bytes of codes a row.
 //
-// Pairs.  A block's MMAs (256 features x 256 rows x 128) take 512 cycles at the FP8
-// rate.  In that time the eight epilogue warps of each CTA read 128 x 256 accumulators
-// and issue as many multiply-adds, paired (fma.f32x2), 64 a thread.
-//   - Columns are rows of x with a scale each.  With the plain TMEM load (a lane one
-//     feature, all columns) every thread would need every column's scale, half a shared-memory
-//     read for each multiply-add.  The 16x256b load gives a thread 4 features of
-//     every fourth pair of columns, so it needs a quarter of the scales, in pairs as
-//     the multiply-add wants them.
+// Few rows a group: single CTAs, stream-K, the weights on the MMA's M side (128 features x
+// 32 rows a unit), bound by HBM.
+//
+// Many: CTA pairs, units of up to 256 rows x 256 features handed out on demand, here with
+// the rows on the MMA's M side, so that a TMEM lane is a row of x and an epilogue
+// warp's 128 columns are one block of features: a thread multiplies a whole block with one
+// scale, which it has loaded ahead.  (With the weights on the M side columns are rows with a scale
+// each, and reading them from shared memory, beside the tensor core's own reads, took
+// half of the time: one group of 8192 rows, N = K = 8192: 772 us.)  MMAs of M = 256 take the same
+// time for any number of rows, but up to 256 rows a group HBM bounds the product all the same.
+//   - A block's MMAs (256 x 256 x 128) take 512 cycles at the FP8 rate.  In that time the
+//     eight epilogue warps of each CTA read 128 x 256 accumulators and issue as many
+//     multiply-adds, paired (fma.f32x2), 64 a thread; a load is under way while the one before it is summed.
 //   - The sums take 128 registers of each epilogue thread: setmaxnreg moves them there.
 //   - TMEM holds two blocks of 256 columns: one is read while the next is computed.
 #include <cuda_bf16.h>
@@ -51,15 +54,15 @@ enum : int {
   kWaitUnit = 10
 };
 
-// a stage's operands as the MMA reads them: K-major rows of 128 codes; the input
-// gradient's weights as MN-major rows of 128 features
+// A stage's weights as the MMA reads them: K-major rows of 128 codes, or (input gradient)
+// MN-major rows of 128 features.  Steps of K = 32.
 template <bool DGRAD>
-__device__ __forceinline__ uint64_t a_desc(uint32_t saddr) {
+__device__ __forceinline__ uint64_t w_desc(uint32_t saddr) {
   return DGRAD ? sdesc_mnmajor_sw128(saddr, kABytes) : sdesc_kmajor_sw128(saddr);
 }
 template <bool DGRAD>
-constexpr uint64_t kStepA = (DGRAD ? 32 * 128 : 32) >> 4;  // K = 32
-constexpr uint64_t kStepB = 32 >> 4;
+constexpr uint64_t kStepW = (DGRAD ? 32 * 128 : 32) >> 4;
+constexpr uint64_t kStepX = 32 >> 4;
 
 __device__ __forceinline__ uint16_t to16(float v, bool fp16) {
   return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
@@ -190,13 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- MMA issuer: the whole warp walks the units, one lane issues
     const bool issue = elect_one();
     const uint32_t s0 = smem_u32(smem);
-    const uint64_t a0 = a_desc<DGRAD>(s0), b0 = sdesc_kmajor_sw128(s0 + kABytes);
+    const uint64_t a0 = w_desc<DGRAD>(s0), b0 = sdesc_kmajor_sw128(s0 + kABytes);
     int stage = 0, acc = 0, where = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     while (ok && rg.next(u, kb0, kb1)) {
       const GroupedUnit un = units.at(u);
-      const uint32_t idesc = idesc_e4m3_f32(128, static_cast<uint32_t>((un.n + 15) & ~15), DGRAD);
+      const uint32_t idesc = idesc_e4m3_f32(128, static_cast<uint32_t>((un.n + 15) & ~15), DGRAD, 0);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag))) {
           ok = false;
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t at = static_cast<uint64_t>(stage * (kStageBytes >> 4));
           const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kUnitRows);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f8_ss(d, a0 + at + k * kStepA<DGRAD>, b0 + at + k * kStepB, idesc, k > 0);
+          for (int k = 0; k < 4; ++k) mma_f8_ss(d, a0 + at + k * kStepW<DGRAD>, b0 + at + k * kStepX, idesc, k > 0);
           mma_commit(&empty[stage]);
           mma_commit(&tfull[acc]);
         }
@@ -349,32 +352,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace pair {
 
-constexpr int kRows = 256;                         // of a unit
-constexpr int kBBytes = kRows / 2 * 128;           // each CTA holds half of them
-constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kRows = 256;                         // of a unit: half in each CTA
+constexpr int kFeatures = 256;                     // of a unit: each CTA holds half of the weight tile
+constexpr int kStageBytes = 2 * kABytes;
 constexpr int kStages = 6;
-constexpr int kEpiWarps = 8;                       // two per TMEM lane quarter, 128 columns each
-constexpr int kCols = kRows * 4 / kEpiWarps;
+constexpr int kEpiWarps = 8;                       // two per TMEM lane quarter, 128 features each
 constexpr int kRowsWarp = 2;                       // 0 the weights' producer, 1 the MMA warp, 3 the relay, the epilogue from 4
 constexpr int kThreads = 32 * (4 + kEpiWarps);
 // registers: 168 a thread at launch; the first four warps give theirs up
 constexpr int kLaunchRegs = 168, kControlRegs = 64, kEpiRegs = 216;
 static_assert(128 * kControlRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * kLaunchRegs, "register shares");
+constexpr int kAhead = 3;                          // blocks whose scales are loaded ahead
 constexpr int kBarBytes = 256;
 constexpr int kTabBytes = 3 * (kGroupsSmem[1] + 1) * 4;
-constexpr int kScaleBytes = kEpiWarps * 2 * kCols * 4;  // per epilogue warp, two blocks
-constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + kScaleBytes + kSchedBytes + kTabBytes;
+constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + kSchedBytes + kTabBytes;
 static_assert((2 * kStages + 5) * 8 + 8 <= kBarBytes, "barrier area");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
-// a unit's MMA columns, rows of each CTA, and rows loaded (one box of 128, or boxes of 32)
-struct Size {
-  int cols, half, rows;
-  __device__ explicit Size(int n) {
-    cols = (n + 31) & ~31;
-    half = cols / 2;
-    rows = half > 96 ? 128 : (half + 31) & ~31;
+// the rows of a unit that a CTA holds: the first half in the even one
+struct Half {
+  int from, n, loaded;  // loaded: one box of 128, or boxes of 32
+  __device__ Half(int rows, uint32_t rank) {
+    const int first = (rows + 1) / 2;
+    from = rank ? first : 0;
+    n = rank ? rows - first : first;
+    loaded = boxes(first);  // (both alike)
   }
+  static __device__ __forceinline__ int boxes(int n) { return n > 96 ? 128 : (n + 31) & ~31; }
 };
 
 template <int N>
@@ -386,11 +390,6 @@ __device__ __forceinline__ void set_registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
 // sum += (d0, d1) * s, both halves
 __device__ __forceinline__ void fma2(uint64_t& sum, uint32_t d0, uint32_t d1, uint64_t s) {
   asm("{\n\t.reg .b64 d;\n\t"
@@ -398,26 +397,6 @@ __device__ __forceinline__ void fma2(uint64_t& sum, uint32_t d0, uint32_t d1, ui
       "fma.rn.f32x2 %0, d, %3, %0;\n\t}"
       : "+l"(sum)
       : "r"(d0), "r"(d1), "l"(s));
-}
-
-// the transpose of an 8 x 8 matrix of 16 bits: lane l holds row l / 4, columns 2 (l % 4) and the next
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-
-// Of the four lanes of a row, lane t holds words 4 m + t of it in w[m]; afterwards words 4 t .. 4 t + 3.
-__device__ __forceinline__ uint4 gather_row(const uint32_t (&w)[4]) {
-  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
-  // between neighbours: lanes 0, 1 keep m = 0 / 1 (and 2 / 3)
-  const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[0] : w[1], 1);
-  const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[2] : w[3], 1);
-  // m of this lane's parity, words t and t ^ 1, in order
-  const uint32_t lo0 = odd ? a : w[0], lo1 = odd ? w[1] : a, hi0 = odd ? b : w[2], hi1 = odd ? w[3] : b;
-  const uint32_t c = __shfl_xor_sync(0xFFFFFFFFu, high ? lo0 : hi0, 2);
-  const uint32_t d = __shfl_xor_sync(0xFFFFFFFFu, high ? lo1 : hi1, 2);
-  return high ? make_uint4(c, d, hi0, hi1) : make_uint4(lo0, lo1, c, d);
 }
 
 template <bool DGRAD>
@@ -434,9 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* scales = reinterpret_cast<float*>(smem + kStages * kStageBytes + kBarBytes);
-  const PairSched sched(smem + kStages * kStageBytes + kBarBytes + kScaleBytes);
-  int32_t* tab = reinterpret_cast<int32_t*>(smem + kStages * kStageBytes + kBarBytes + kScaleBytes + kSchedBytes);
+  const PairSched sched(smem + kStages * kStageBytes + kBarBytes);
+  int32_t* tab = reinterpret_cast<int32_t*>(smem + kStages * kStageBytes + kBarBytes + kSchedBytes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -460,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tm_x32);
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, 2 * kRows);
+    tmem_alloc_pair(tmem_slot, 2 * kFeatures);
     tmem_relinquish_pair();
   }
   pdl_wait();  // the plan kernel's tables
@@ -488,9 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u; ok && (u = walk.next()) >= 0;) {
         const GroupedUnit un = units.at(u);
-        const Size z(un.n);
-        const int feat = un.tile * 256 + static_cast<int>(rank) * 128;
-        const int tok = un.tok0 + static_cast<int>(rank) * z.half;
+        const Half z(un.n, rank);
+        const int feat = un.tile * kFeatures + static_cast<int>(rank) * 128, tok = un.tok0 + z.from;
         // a weight tile read by one chunk only is streamed; by more, kept
         const uint64_t pol_w = units.chunks > 1 ? pol_keep : pol_stream;
         for (int kb = 0; kb < kblocks; ++kb) {
@@ -502,17 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* sa = smem + stage * kStageBytes;
             const uint32_t bar = full_cl + 8u * stage;
             if (weights) {
-              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (kABytes + z.rows * 128));
+              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (kABytes + z.loaded * 128));
               if constexpr (DGRAD)  // 128 rows of w x 128 of its columns, which are the features
-                tma_load_3d_pair(sa, &tm_w, bar, feat, kb * 128, un.g, pol_w);
+                tma_load_3d_pair(sa + kABytes, &tm_w, bar, feat, kb * 128, un.g, pol_w);
               else
-                tma_load_3d_pair(sa, &tm_w, bar, kb * 128, feat, un.g, pol_w);
+                tma_load_3d_pair(sa + kABytes, &tm_w, bar, kb * 128, feat, un.g, pol_w);
+            } else if (z.loaded == 128) {
+              tma_load_2d_pair(sa, &tm_x, bar, kb * 128, tok, pol_keep);
             } else {
-              uint8_t* sb = sa + kABytes;
-              if (z.rows == 128)
-                tma_load_2d_pair(sb, &tm_x, bar, kb * 128, tok, pol_keep);
-              else
-                for (int r = 0; r < z.rows; r += 32) tma_load_2d_pair(sb + r * 128, &tm_x32, bar, kb * 128, tok + r, pol_keep);
+              for (int r = 0; r < z.loaded; r += 32) tma_load_2d_pair(sa + r * 128, &tm_x32, bar, kb * 128, tok + r, pol_keep);
             }
           }
           __syncwarp();
@@ -537,14 +512,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- MMA issuer for both CTAs: the whole warp walks the units, one lane issues
         const bool issue = elect_one();
         const uint32_t s0 = smem_u32(smem);
-        const uint64_t a0 = a_desc<DGRAD>(s0), b0 = sdesc_kmajor_sw128(s0 + kABytes);
+        const uint64_t a0 = sdesc_kmajor_sw128(s0), b0 = w_desc<DGRAD>(s0 + kABytes);
+        const uint32_t idesc = idesc_e4m3_f32(256, kFeatures, 0, DGRAD);
         int stage = 0, acc = 0, where = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
         for (int u; ok && (u = walk.next()) >= 0;) {
-          const GroupedUnit un = units.at(u);
-          const Size z(un.n);
-          const uint32_t idesc = idesc_e4m3_f32(256, static_cast<uint32_t>(z.cols), DGRAD);
           for (int kb = 0; kb < kblocks; ++kb) {
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag))) {
               ok = false;
@@ -559,10 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (issue) {
               const uint64_t at = static_cast<uint64_t>(stage * (kStageBytes >> 4));
-              const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kRows);
+              const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kFeatures);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_f8_ss_pair(d, a0 + at + k * kStepA<DGRAD>, b0 + at + k * kStepB, idesc, k > 0);
+                mma_f8_ss_pair(d, a0 + at + k * kStepX, b0 + at + k * kStepW<DGRAD>, idesc, k > 0);
               mma_commit_pair_mc(&empty[stage], 0x3);
               mma_commit_pair_mc(&tfull[acc], 0x3);
             }
@@ -595,45 +568,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     set_registers_up<kEpiRegs>();
     // ---------------- epilogue: TMEM lane quarter = warp % 4; a quarter's two warps
-    // take 128 columns each.  A thread holds features 16 h + 8 i + lane / 4 of the
-    // warp's 32 (h, i: 0, 1) of columns 8 j + 2 (lane % 4) and the next (j: 0..15).
+    // take 128 features each, a lane one row
     GroupedUnits units(tables, a.G, 1, a.bn, true);
     PairUnits walk(sched, total_units, kWaitTimeoutNs, abort_flag, leader, false);
-    const int q = warp & 3, col0 = (warp - 4) / 4 * kCols;
+    const int q = warp & 3, col0 = (warp - 4) / 4 * 128, row = q * 32 + lane;
     const bool fp16 = a.fp16 != 0;
     const uint32_t tempty_cl = mapa_shared(smem_u32(tempty), 0);
     const uint32_t t_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(col0);
-    float* s_buf = scales + (warp - 4) * 2 * kCols;
-    // column c's scale lies at c / 16 * 16 + (c % 8) / 2 * 4 + (c / 8 % 2) * 2 + c % 2 of a block: a thread
-    // reads the four of two neighbouring j at once
-    const int s_put = (lane >> 4) * 16 + ((lane & 7) >> 1) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1);
-    const int s_get = (lane & 3) * 4;
     const int64_t w_step = DGRAD ? args.w_cols : 1;
     int acc = 0, where = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int u; ok && (u = walk.next()) >= 0;) {
       const GroupedUnit un = units.at(u);
-      const int feat0 = un.tile * 256 + static_cast<int>(rank) * 128;
-      const float* sw = feature_scales<DGRAD>(args, un.g, feat0);
-      const float* sx = args.x_scales + un.tok0 + col0 + lane;
-      const int left = un.n - col0;  // columns of this warp that are rows of the unit
-      uint64_t sum[64];              // [j][h][i]
+      const Half z(un.n, rank);
+      const int feat = un.tile * kFeatures + col0;
+      const bool mine = row < z.n;
+      const float* sw = feature_scales<DGRAD>(args, un.g, feat);
+      const float* sx = args.x_scales + un.tok0 + z.from + row;
+      float next_w[kAhead], next_x[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        next_w[k] = k < kblocks ? __ldg(sw) : 0.0f;
+        next_x[k] = k < kblocks && mine ? __ldg(sx) : 0.0f;
+        sw += w_step;
+        sx += args.ldxs;
+      }
+      uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
-      float next_w = __ldg(sw), next_x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) next_x[i] = 32 * i + lane < left ? __ldg(sx + 32 * i) : 0.0f;
       for (int kb = 0; kb < kblocks; ++kb) {
-        float* s = s_buf + (kb & 1) * kCols;  // (the other one may still be read by slower lanes)
+        const float s = __fmul_rn(next_x[0], next_w[0]);
+        uint64_t s2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[32 * i + s_put] = __fmul_rn(next_x[i], next_w);
-        if (kb + 1 < kblocks) {  // the next block's, while this one's MMAs run
-          sx += args.ldxs;
+        for (int k = 0; k + 1 < kAhead; ++k) {
+          next_w[k] = next_w[k + 1];
+          next_x[k] = next_x[k + 1];
+        }
+        if (kb + kAhead < kblocks) {
+          next_w[kAhead - 1] = __ldg(sw);
+          if (mine) next_x[kAhead - 1] = __ldg(sx);
           sw += w_step;
-          next_w = __ldg(sw);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) next_x[i] = 32 * i + lane < left ? __ldg(sx + 32 * i) : 0.0f;
+          sx += args.ldxs;
         }
         // warp-uniform outcome: tcgen05.ld below is executed by all 32 lanes
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_phase, kWaitTimeoutNs, abort_flag))) {
@@ -643,58 +620,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         __syncwarp();
-        const uint32_t t = t_base + static_cast<uint32_t>(acc * kRows);
+        const uint32_t t = t_base + static_cast<uint32_t>(acc * kFeatures);
+        uint32_t r[2][32];
+        tmem_ld_32x32b_x32(t, r[0]);
 #pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += 32) {
-          if (c0 < left) {  // (warp-uniform)
-            uint32_t r[2][16];
-            tmem_ld_16x256b_x4(t + c0, r[0]);
-            tmem_ld_16x256b_x4(t + c0 + (16u << 16), r[1]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              const float4 v = *reinterpret_cast<const float4*>(s + c0 + j * 8 + s_get);
-              const uint64_t s0 = pack2(v.x, v.y), s1 = pack2(v.z, v.w);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int at = (c0 / 8 + j) * 4 + 2 * h;
-                fma2(sum[at], r[h][4 * j], r[h][4 * j + 1], s0);
-                fma2(sum[at + 1], r[h][4 * j + 2], r[h][4 * j + 3], s0);
-                fma2(sum[at + 4], r[h][4 * j + 4], r[h][4 * j + 5], s1);
-                fma2(sum[at + 5], r[h][4 * j + 6], r[h][4 * j + 7], s1);
-              }
-            }
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait(r[c & 1]);
+          if (c < 3) {
+            tmem_ld_32x32b_x32(t + 32 * (c + 1), r[(c + 1) & 1]);
+          } else {  // hand the accumulator back to the MMA thread
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(tempty_cl + 8u * acc);
           }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) fma2(sum[16 * c + i / 2], r[c & 1][i], r[c & 1][i + 1], s2);
         }
-        // hand the accumulator back to the MMA thread
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(tempty_cl + 8u * acc);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
       if (!ok) break;
-      // Each group of 8 columns (rows of the output) x 32 features: transposed in 16
-      // bits, then gathered, so that a lane stores 8 features of one row.
-      const int feat = feat0 + q * 32 + 8 * (lane & 3);
-      uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(un.tok0 + col0 + (lane >> 2)) * a.ldo + feat;
+      if (mine) {
+        uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(un.tok0 + z.from + row) * a.ldo + feat;
 #pragma unroll
-      for (int j = 0; j < kCols / 8; ++j) {
-        if (8 * j < left) {  // (warp-uniform)
+        for (int i = 0; i < 64; i += 4) {
           uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int k = 0; k < 4; ++k) {
             float lo, hi;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(sum[4 * j + i]));
-            w[i] = transpose8x8(pack16(lo, hi, fp16));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(sum[i + k]));
+            w[k] = pack16(lo, hi, fp16);
           }
-          const uint4 v = gather_row(w);
-          if (8 * j + (lane >> 2) < left && feat < a.F)  // (F is a multiple of 8)
-            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(8 * j) * a.ldo) = v;
+          if (feat + 2 * i < a.F) *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);  // (F: a multiple of 8)
         }
       }
+      __syncwarp();
     }
     if (!walk.ok) where = kWaitUnit;
     if (!(ok && walk.ok) && lane == 0) raise_timeout(a.err, abort_flag, kKernFp8Gemm, where);
@@ -705,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, 2 * kRows);
+    tmem_dealloc_pair(tmem_base, 2 * kFeatures);
   }
 }
 
