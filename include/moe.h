@@ -659,12 +659,12 @@ MOE_API moe_status moe_fp4_gemm(const moe_grouped_shape* shape, int32_t format, 
  * and add sx sw times that sum in fp32, so the scales may be any numbers.  (sx sw is
  * one fp32 operation: where it lies below 2^-126 it loses bits.)
  *   codes   [rows, K] bytes
- *   scales  MOE_SCALE_PER_ROW: [ceil(K / 128)][lds] fp32, block b of row p at
- *           b * lds + p (lds >= rows); MOE_SCALE_PER_BLOCK: `groups` matrices of
- *           N = rows / groups rows each, [groups][ceil(N / 128)][ceil(K / 128)]
- *           (lds unused, blocks at the edges smaller)
+ *   scales  MOE_SCALE_PER_ROW: [rows][lds] fp32, block b of row p at p * lds + b
+ *           (lds >= ceil(K / 128), a multiple of 4; what lies between them is unspecified);
+ *           MOE_SCALE_PER_BLOCK: `groups` matrices of N = rows / groups rows each,
+ *           [groups][ceil(N / 128)][ceil(K / 128)] (lds unused, blocks at the edges smaller)
  * K a multiple of 16 and <= 2^20; rows <= 2^31 - 512; row strides in elements,
- * multiples of 8; src, dst and codes 16-byte, scales 4-byte aligned.  No lists:
+ * multiples of 8; src, dst, codes and scales 16-byte aligned.  No lists:
  * all rows are quantized, those of no group reach no product. */
 #define MOE_SCALE_PER_BLOCK 2
 
@@ -675,7 +675,7 @@ typedef struct {
   int32_t K;
 } moe_fp8_shape;
 
-/* Byte sizes of codes and scales (lds = rows).  Host only. */
+/* Byte sizes of codes and scales (lds = ceil(K / 128) rounded up to 4).  Host only. */
 MOE_API moe_status moe_fp8_sizes(const moe_fp8_shape* shape, size_t* codes, size_t* scales);
 
 /* src [rows, K] of src_type (MOE_TYPE_*) -> codes, scales. */

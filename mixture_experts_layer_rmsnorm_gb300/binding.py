@@ -955,6 +955,7 @@ class Fp8Rows(_Buffers):
     def __init__(self, K, max_rows=0, device=None):
         import torch
         self.K, self.device = int(K), torch.empty(0, device=device or "cuda").device
+        self.lds = (-(-self.K // 128) + 3) // 4 * 4  # of the scales
         self.rows = self.max_rows = 0
         self._shape, self._outgrown = None, []
         self.ensure_capacity(max_rows)
@@ -972,12 +973,12 @@ class Fp8Rows(_Buffers):
         import torch
         # (by half at least: what outgrown buffers hold stays below twice the last ones)
         rows = max(rows, min(self.max_rows * 3 // 2, 2 ** 31 - 512), 1)
-        st, (n_codes, n_scales) = moe_fp8_sizes(fp8_shape(MOE_SCALE_PER_ROW, 1, rows, self.K))
+        st, (n_codes, _) = moe_fp8_sizes(fp8_shape(MOE_SCALE_PER_ROW, 1, rows, self.K))
         if st != MOE_OK:
             raise MoeError(st, "moe_fp8_sizes")
         # (both before either takes its place: where one does not fit, the rows before stay)
         codes = torch.empty(n_codes, dtype=torch.uint8, device=self.device)
-        scales = torch.empty(n_scales // 4, dtype=torch.float32, device=self.device)
+        scales = torch.empty((rows, self.lds), dtype=torch.float32, device=self.device)
         if self.max_rows > 0:
             self._outgrown.append((self.codes, self.scales))
         self.codes, self.scales, self.max_rows = codes, scales, rows
@@ -994,7 +995,7 @@ class Fp8Rows(_Buffers):
         self.ensure_capacity(rows)
         self.rows = 0  # (until they are on their way)
         _enqueue("moe_fp8_quantize", self.device, ctypes.byref(self.shape(rows)), type_, xp, ldx, self.codes.data_ptr(),
-                 self.scales.data_ptr(), self.max_rows, of=(self,))
+                 self.scales.data_ptr(), self.lds, of=(self,))
         self.rows = rows
         return self
 
@@ -1005,7 +1006,7 @@ class Fp8Rows(_Buffers):
             y = torch.empty((self.rows, self.K), dtype=dtype or torch.bfloat16, device=self.device)
         yp, ldy = _matrix("y", y, self.device, dtype or y.dtype, (self.rows, self.K))
         _enqueue("moe_fp8_dequantize", self.device, ctypes.byref(self.shape(self.rows)), self.codes.data_ptr(),
-                 self.scales.data_ptr(), self.max_rows, _type_of(y.dtype), yp, ldy, of=(self,))
+                 self.scales.data_ptr(), self.lds, _type_of(y.dtype), yp, ldy, of=(self,))
         return y
 
 
@@ -1064,7 +1065,7 @@ class Fp8Weights(_Workspace):
             out = torch.empty((rows.rows, N), dtype=dtype or torch.bfloat16, device=self.device)
         op, ldo = _matrix("the output", out, self.device, dtype or out.dtype, (rows.rows, N))
         self._call(name, self.shape(rows.rows, _type_of(out.dtype)), rows.codes.data_ptr(), rows.scales.data_ptr(),
-                   rows.max_rows, self.codes.data_ptr(), self.scales.data_ptr(), *_lists(self, offsets, counts), op, ldo,
+                   rows.lds, self.codes.data_ptr(), self.scales.data_ptr(), *_lists(self, offsets, counts), op, ldo,
                    of=(rows,))
         return out
 

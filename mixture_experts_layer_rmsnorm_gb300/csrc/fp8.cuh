@@ -1,9 +1,9 @@
 // fp8.cuh -- rows and matrices in 8 bits (E4M3 under fp32 scales of 128 elements
 // or of 128 x 128) and their grouped products (internal).
 //
-//   rows      codes [rows, K], scales [ceil(K / 128)][lds]: block b of row p at
-//             b * lds + p, so that the products' epilogue reads one block of
-//             neighbouring rows at once
+//   rows      codes [rows, K], scales [rows][lds]: block b of row p at p * lds + b,
+//             lds a multiple of 4, so that the products' epilogue, a lane a row,
+//             reads four blocks at once
 //   matrices  codes [G, N, K], scales [G][ceil(N / 128)][ceil(K / 128)]
 #pragma once
 
@@ -34,15 +34,18 @@ cudaError_t launch_fp8_dequantize(const Fp8Args& a, cudaStream_t stream);
 // and input gradient, and the scales.
 struct Fp8GemmArgs {
   GroupedGemmArgs g;
-  const float* x_scales;  // of the rows, [ceil(R / 128)][ldxs]
+  const float* x_scales;  // of the rows, [rows][ldxs]
   int64_t ldxs;
   const float* w_scales;  // [G][w_rows][w_cols]
   int w_rows, w_cols;     // ceil(N / 128), ceil(K / 128)
 };
-int fp8_bn(GroupedPlan plan, int64_t rows, int64_t groups, int64_t tiles, int num_sms);
-// tm_x: the rows' codes in boxes of fp8_tok_box(plan) rows; tm_x32: of 32 (large plan)
-int fp8_tok_box(GroupedPlan plan);
-cudaError_t launch_fp8_gemm(GroupedOp op, GroupedPlan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
+// Tile plans: stream-K on single CTAs, units of 32 rows; units of 128 rows on single CTAs; of 256 on CTA pairs.
+enum class Fp8Plan : int { kSmall, kSingle, kPairs };
+int fp8_bn(Fp8Plan plan);    // rows of a unit
+int fp8_tile(Fp8Plan plan);  // features of a unit
+// tm_x: the rows' codes in boxes of fp8_tok_box(plan) rows; tm_x32: of 32 (unused by the small plan)
+int fp8_tok_box(Fp8Plan plan);
+cudaError_t launch_fp8_gemm(GroupedOp op, Fp8Plan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
                             const CUtensorMap& tm_x32, const Fp8GemmArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace moe

@@ -313,15 +313,21 @@ moe_status check_fp8(const moe_fp8_shape* s) {
   return MOE_OK;
 }
 
+// Scales of rows: four blocks are read at once.
+moe_status check_lds(int64_t lds, int64_t K) {
+  if (lds < (K + 127) / 128) return MOE_ERR_INVALID_ARG;
+  return lds % 4 != 0 || lds > kMaxLd ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
 moe_status fp8_rows(const moe_fp8_shape* s, int32_t type, const void* rows, int64_t ld, const uint8_t* codes,
                     const float* scales, int64_t lds, moe::Fp8Args* out) {
   moe_status st = check_fp8(s);
   if (st != MOE_OK) return st;
   if (type != MOE_TYPE_BF16 && type != MOE_TYPE_FP16 && type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
   if ((st = check_rows(rows, s->rows, ld, s->K)) != MOE_OK) return st;
-  if (s->rows > 0 && (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 4))) return MOE_ERR_INVALID_ARG;
+  if (s->rows > 0 && (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 16))) return MOE_ERR_INVALID_ARG;
   const bool blocks = s->scale_per == MOE_SCALE_PER_BLOCK;
-  if (!blocks && (lds < s->rows || lds > kMaxLd)) return MOE_ERR_INVALID_ARG;
+  if (!blocks && (st = check_lds(lds, s->K)) != MOE_OK) return st;
   moe::Fp8Args a{};
   a.rows = s->rows;
   a.per = blocks ? s->rows / s->groups : 0;
@@ -335,6 +341,12 @@ moe_status fp8_rows(const moe_fp8_shape* s, int32_t type, const void* rows, int6
   return MOE_OK;
 }
 
+// The plan follows the mean of the rows, as for 16 bits.
+moe::Fp8Plan choose_fp8_plan(const moe_grouped_shape* s) {
+  if (s->rows <= int64_t(16) * s->groups) return moe::Fp8Plan::kSmall;
+  return s->rows <= int64_t(128) * s->groups ? moe::Fp8Plan::kSingle : moe::Fp8Plan::kPairs;
+}
+
 // forward (F = N features, R = K) and input gradient (F = K, R = N)
 moe_status fp8_product(GroupedOp op, const moe_grouped_shape* s, const uint8_t* codes, const float* scales, int64_t lds,
                        const uint8_t* w_codes, const float* w_scales, const int32_t* offsets, const int32_t* counts,
@@ -344,17 +356,17 @@ moe_status fp8_product(GroupedOp op, const moe_grouped_shape* s, const uint8_t* 
   if (s->N % 16 != 0 || s->K % 16 != 0) return MOE_ERR_UNSUPPORTED;
   const int F = op == GroupedOp::kForward ? s->N : s->K, R = op == GroupedOp::kForward ? s->K : s->N;
   if ((st = check_rows(out, s->rows, ldout, F)) != MOE_OK) return st;
-  if (s->rows > 0 && (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 4))) return MOE_ERR_INVALID_ARG;
-  if (lds < s->rows || lds > kMaxLd) return MOE_ERR_INVALID_ARG;
-  if (!w_codes || !aligned(w_codes, 16) || !w_scales || !aligned(w_scales, 4)) return MOE_ERR_INVALID_ARG;
+  if (s->rows > 0 && (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 16))) return MOE_ERR_INVALID_ARG;
+  if ((st = check_lds(lds, R)) != MOE_OK) return st;
+  if (!w_codes || !aligned(w_codes, 16) || !w_scales || !aligned(w_scales, 16)) return MOE_ERR_INVALID_ARG;
   if ((st = check_call(s, offsets, counts, ws, ws_bytes)) != MOE_OK) return st;
   if (too_many_units(s, F)) return MOE_ERR_UNSUPPORTED;
   if (s->rows == 0) return MOE_OK;
   const int sms = num_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
-  const GroupedPlan plan = choose_plan(s, F, sms, false);
-  const int tile = moe::grouped_tile(plan), tiles = (F + tile - 1) / tile;
-  const bool large = plan == GroupedPlan::kLarge;
+  const moe::Fp8Plan plan = choose_fp8_plan(s);
+  const int tile = moe::fp8_tile(plan), tiles = (F + tile - 1) / tile;
+  const bool large = plan != moe::Fp8Plan::kSmall;
   CUtensorMap tw, tx, tx32;
   if (!make_codes_map(&tw, w_codes, s->K, s->N, s->groups, 128) ||
       !make_codes_map(&tx, codes, R, s->rows, 0, static_cast<uint32_t>(moe::fp8_tok_box(plan))) ||
@@ -362,7 +374,7 @@ moe_status fp8_product(GroupedOp op, const moe_grouped_shape* s, const uint8_t* 
     return MOE_ERR_CUDA;
   const Layout L = make_layout(s->groups);
   moe::GroupedPlanArgs p = plan_args(s, L, ws, offsets, counts);
-  p.bn = moe::fp8_bn(plan, s->rows, s->groups, tiles, sms);
+  p.bn = moe::fp8_bn(plan);
   p.tiles = tiles;
   moe::Fp8GemmArgs a{};
   a.g = gemm_args(s, L, ws);
@@ -579,7 +591,7 @@ moe_status moe_fp8_sizes(const moe_fp8_shape* shape, size_t* codes, size_t* scal
   const size_t rows = static_cast<size_t>(shape->rows), blocks = (static_cast<size_t>(shape->K) + 127) / 128;
   *codes = rows * static_cast<size_t>(shape->K);
   if (shape->scale_per == MOE_SCALE_PER_ROW) {
-    *scales = rows * blocks * 4;
+    *scales = rows * align_up(blocks, 4) * 4;
   } else {
     const size_t groups = static_cast<size_t>(shape->groups);
     *scales = groups * ((rows / groups + 127) / 128) * blocks * 4;

@@ -16,18 +16,27 @@
 // Few rows a group: single CTAs, stream-K, the weights on the MMA's M side (128 features x
 // 32 rows a unit), bound by HBM.
 //
-// Many: CTA pairs, units of up to 256 rows x 256 features handed out on demand, here with
-// the rows on the MMA's M side, so that a TMEM lane is a row of x and an epilogue
-// warp's 128 columns are one block of features: a thread multiplies a whole block with one
-// scale, which it has loaded ahead.  (With the weights on the M side columns are rows with a scale
-// each, and reading them from shared memory, beside the tensor core's own reads, took
-// half of the time: one group of 8192 rows, N = K = 8192: 772 us.)  MMAs of M = 256 take the same
-// time for any number of rows, but up to 256 rows a group HBM bounds the product all the same.
-//   - A block's MMAs (256 x 256 x 128) take 512 cycles at the FP8 rate.  In that time the
-//     eight epilogue warps of each CTA read 128 x 256 accumulators and issue as many
+// More: units of 256 features, here with the rows on the MMA's M side, so that a TMEM
+// lane is a row of x and an epilogue warp's 128 columns are one block of features: a
+// thread multiplies a whole block with one scale.  (With the weights on the M side columns
+// are rows with a scale each, and reading them from shared memory took half of the time: one
+// group of 8192 rows, N = K = 8192: 772 us.)  MMAs of M = 128 (256 for pairs) take the same time for
+// any number of rows.
+//   up to 128 rows a group: single CTAs, units of 128 rows, bound by HBM
+//   more: CTA pairs, units of 256 rows handed out on demand
+//                                         pairs   single CTAs
+//   64 x 100 rows, N = 8192, K = 4096      441    354 us
+//   64 x 512 rows, N = K = 4096            453    507
+//   8192 rows, N = K = 8192                421    483
+//   - A block's MMAs (128 x 256 x 128 an SM) take 512 cycles at the FP8 rate.  The
+//     eight epilogue warps read 128 x 256 accumulators for it and issue as many
 //     multiply-adds, paired (fma.f32x2), 64 a thread; a load is under way while the one before it is summed.
 //   - The sums take 128 registers of each epilogue thread: setmaxnreg moves them there.
+//     What leads from one unit to the next is worked out anew for each, since registers kept for it
+//     would spill, and any spill costs a quarter of the rate.
 //   - TMEM holds two blocks of 256 columns: one is read while the next is computed.
+// Bound: reading TMEM beside the MMAs that write it.  One group of 8192 rows, N = K = 8192, pairs: 421 us (2.6 PFLOP/s,
+// 870 cycles a block); with a quarter of the multiply-adds 417, without reading TMEM 333.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -82,6 +91,7 @@ constexpr int kUnitRows = 32, kRowBox = 16;
 constexpr int kStageBytes = kABytes + kUnitRows * 128;
 constexpr int kStages = 10;
 constexpr int kAccs = 4;
+constexpr int kAhead = 3;  // blocks whose scales are loaded ahead
 constexpr int kThreads = 192;
 constexpr uint32_t kTmemCols = kAccs * kUnitRows;
 constexpr int kBarBytes = 256;
@@ -250,22 +260,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && rg.next(u, kb0, kb1)) {
       const GroupedUnit un = units.at(u);
-      const float* sw = feature_scales<DGRAD>(args, un.g, un.tile * 128) + kb0 * w_step;
-      const float* sx = args.x_scales + kb0 * args.ldxs + un.tok0 + lane;
+      const float* sw = feature_scales<DGRAD>(args, un.g, un.tile * 128);
+      const float* sx = args.x_scales + (un.tok0 + lane) * args.ldxs;
       const bool valid = lane < un.n;
+      float next[kAhead], next_w[kAhead];
+      auto scales_of = [&](int kb, float& x, float& w) {
+        if (kb < kb1) {
+          w = __ldg(sw + kb * w_step);
+          x = valid ? __ldg(sx + kb) : 0.0f;
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) scales_of(kb0 + k, next[k], next_w[k]);
       float sum[kUnitRows];
 #pragma unroll
       for (int c = 0; c < kUnitRows; ++c) sum[c] = 0.0f;
-      float next_x = valid ? __ldg(sx) : 0.0f, next_w = __ldg(sw);
       for (int kb = kb0; kb < kb1; ++kb) {
         float* s = s_buf + (kb & 1) * kUnitRows;  // (the other one may still be read by slower lanes)
-        s[lane] = __fmul_rn(next_x, next_w);
-        if (kb + 1 < kb1) {  // the next block's, while this one's MMAs run
-          sx += args.ldxs;
-          sw += w_step;
-          next_x = valid ? __ldg(sx) : 0.0f;
-          next_w = __ldg(sw);
+        s[lane] = __fmul_rn(next[0], next_w[0]);
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k) {
+          next[k] = next[k + 1];
+          next_w[k] = next_w[k + 1];
         }
+        scales_of(kb + kAhead, next[kAhead - 1], next_w[kAhead - 1]);
         // warp-uniform outcome: tcgen05.ld below is executed by all 32 lanes
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_phase, kWaitTimeoutNs, abort_flag))) {
           ok = false;
@@ -350,35 +368,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ many rows: CTA pairs
 
-namespace pair {
+// ------------------------------------------------------------------ more rows: single CTAs and CTA pairs
 
-constexpr int kRows = 256;                         // of a unit: half in each CTA
-constexpr int kFeatures = 256;                     // of a unit: each CTA holds half of the weight tile
-constexpr int kStageBytes = 2 * kABytes;
-constexpr int kStages = 6;
-constexpr int kEpiWarps = 8;                       // two per TMEM lane quarter, 128 features each
-constexpr int kRowsWarp = 2;                       // 0 the weights' producer, 1 the MMA warp, 3 the relay, the epilogue from 4
-constexpr int kThreads = 32 * (4 + kEpiWarps);
-// registers: 168 a thread at launch; the first four warps give theirs up
-constexpr int kLaunchRegs = 168, kControlRegs = 64, kEpiRegs = 216;
-static_assert(128 * kControlRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * kLaunchRegs, "register shares");
-constexpr int kAhead = 3;                          // blocks whose scales are loaded ahead
-constexpr int kBarBytes = 256;
-constexpr int kTabBytes = 3 * (kGroupsSmem[1] + 1) * 4;
-constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + kSchedBytes + kTabBytes;
-static_assert((2 * kStages + 5) * 8 + 8 <= kBarBytes, "barrier area");
-static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+template <bool PAIR>
+struct Large {
+  static constexpr int kRows = PAIR ? 256 : 128;     // of a unit (pairs: half in each CTA)
+  static constexpr int kFeatures = 256;              // of a unit (pairs: each CTA holds half of the weight tile)
+  static constexpr int kWBoxes = PAIR ? 1 : 2;       // of 128 features
+  static constexpr int kStageBytes = (1 + kWBoxes) * kABytes;
+  static constexpr int kStages = PAIR ? 5 : 4;
+  static constexpr int kEpiWarps = 8;                // two per TMEM lane quarter, 128 features each
+  static constexpr int kRowsWarp = 2;                // 0 the weights' producer, 1 the MMA warp, 3 a pair's relay, the epilogue from 4
+  static constexpr int kThreads = 32 * (4 + kEpiWarps);
+  // registers: 168 a thread at launch; the first four warps give theirs up
+  static constexpr int kLaunchRegs = 168, kControlRegs = 64, kEpiRegs = 216;
+  static_assert(128 * kControlRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * kLaunchRegs, "register shares");
+  static constexpr int kPass = PAIR ? 64 : 32;       // features of an output row that go out at once
+  static constexpr int kOutRow = kPass * 2 + 16;     // (the rows in different banks)
+  static constexpr int kOutBytes = kEpiWarps * 32 * kOutRow;
+  static constexpr int kBarBytes = 256;
+  static constexpr int kTabGroups = kGroupsSmem[1];
+  static constexpr int kTabBytes = 3 * (kTabGroups + 1) * 4;
+  static constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kOutBytes + kBarBytes + kSchedBytes + kTabBytes;
+  static_assert((2 * kStages + 5) * 8 + 8 <= kBarBytes, "barrier area");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+};
 
-// the rows of a unit that a CTA holds: the first half in the even one
-struct Half {
-  int from, n, loaded;  // loaded: one box of 128, or boxes of 32
-  __device__ Half(int rows, uint32_t rank) {
-    const int first = (rows + 1) / 2;
+// the rows of a unit that a CTA holds (pairs: the first half in the even one)
+template <bool PAIR>
+struct Part {
+  int from, n, loaded;  // loaded: one box of 128, or boxes of 32 (both CTAs alike)
+  __device__ Part(int rows, uint32_t rank) {
+    const int first = PAIR ? (rows + 1) / 2 : rows;
     from = rank ? first : 0;
     n = rank ? rows - first : first;
-    loaded = boxes(first);  // (both alike)
+    loaded = first > 96 ? 128 : (first + 31) & ~31;
   }
-  static __device__ __forceinline__ int boxes(int n) { return n > 96 ? 128 : (n + 31) & ~31; }
 };
 
 template <int N>
@@ -399,38 +424,41 @@ __device__ __forceinline__ void fma2(uint64_t& sum, uint32_t d0, uint32_t d1, ui
       : "r"(d0), "r"(d1), "l"(s));
 }
 
-template <bool DGRAD>
-__global__ void __launch_bounds__(kThreads, 1)
-    fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                    const __grid_constant__ CUtensorMap tm_x32, const __grid_constant__ Fp8GemmArgs args) {
+template <bool DGRAD, bool PAIR>
+__global__ void __launch_bounds__(Large<PAIR>::kThreads, 1)
+    fp8_large_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                     const __grid_constant__ CUtensorMap tm_x32, const __grid_constant__ Fp8GemmArgs args) {
+  using C = Large<PAIR>;
   const GroupedGemmArgs& a = args.g;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;  // a block's MMAs are complete
-  uint64_t* tempty = tfull + 2;       // it is read, by the epilogue of both CTAs
+  uint8_t* const outs = smem + C::kStages * C::kStageBytes;  // the epilogue warps' rows on their way out
+  uint8_t* const bars = outs + C::kOutBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(bars);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;  // a block's MMAs are complete
+  uint64_t* tempty = tfull + 2;          // it is read, by the epilogue (of both CTAs)
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const PairSched sched(smem + kStages * kStageBytes + kBarBytes);
-  int32_t* tab = reinterpret_cast<int32_t*>(smem + kStages * kStageBytes + kBarBytes + kSchedBytes);
+  const PairSched sched(bars + C::kBarBytes);
+  int32_t* tab = reinterpret_cast<int32_t*>(bars + C::kBarBytes + kSchedBytes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * kEpiWarps);
+      mbar_init(&tempty[b], (PAIR ? 2 : 1) * C::kEpiWarps);
     }
     mbar_init(done, 1);
-    sched.init(2 + kEpiWarps);  // producers and epilogue
+    if (PAIR) sched.init(2 + C::kEpiWarps);  // producers and epilogue
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tm_w);
@@ -438,36 +466,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tm_x32);
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, 2 * kFeatures);
-    tmem_relinquish_pair();
+    if (PAIR) {
+      tmem_alloc_pair(tmem_slot, 2 * C::kFeatures);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 2 * C::kFeatures);
+      tmem_relinquish();
+    }
   }
   pdl_wait();  // the plan kernel's tables
-  const GroupedTables tables = grouped_tables(a, tab, kGroupsSmem[1], kThreads);
+  const GroupedTables tables = grouped_tables(a, tab, C::kTabGroups, C::kThreads);
   tc_fence_before();
-  cluster_sync();  // the peer's barriers are initialised before any remote signal
+  if (PAIR)
+    cluster_sync();  // the peer's barriers are initialised before any remote signal
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  const int total_units = tables.unit_off[a.G];
   const int kblocks = (a.R + 127) / 128;
+  // Each warp's walk along the units: as the pair hands them out, or (single CTAs, whose units take the
+  // same time each) with the grid's stride.  Only the place is kept.
+  int place = PAIR ? 0 : static_cast<int>(blockIdx.x);
+  uint32_t place_phase = 0;
+  bool walked = true;  // no wait for a unit ran out
+  auto next_unit = [&]() -> int {
+    const int total = tables.unit_off[a.G];
+    if constexpr (PAIR) {
+      PairUnits walk(sched, total, kWaitTimeoutNs, abort_flag, leader, warp == 0);
+      walk.slot = place;
+      walk.phase = place_phase;
+      const int u = walk.next();
+      place = walk.slot;
+      place_phase = walk.phase;
+      walked = walked && walk.ok;
+      return u;
+    } else {
+      const int u = place;
+      place += static_cast<int>(gridDim.x);
+      return u < total ? u : -1;
+    }
+  };
 
   if (warp < 4) {
-    set_registers_down<kControlRegs>();
-    GroupedUnits units(tables, a.G, 1, a.bn, true);  // each warp walks its role's units
-    PairUnits walk(sched, total_units, kWaitTimeoutNs, abort_flag, leader, warp == 0);
-    if (warp == 0 || warp == kRowsWarp) {
+    set_registers_down<C::kControlRegs>();
+    if (warp == 0 || warp == C::kRowsWarp) {
       // ---------------- TMA producers: one warp for the weight tiles, one for the rows; one lane issues
       const bool weights = warp == 0, issue = elect_one();
       const uint64_t pol_stream = policy_evict_first(), pol_keep = policy_evict_last();
-      const uint32_t full_cl = mapa_shared(smem_u32(full), 0);  // both CTAs signal the even one
+      const uint32_t full_cl = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;  // both CTAs signal the even one
       int stage = 0;
       uint32_t phase = 0;
       int64_t issued = 0;
       bool ok = true;
-      for (int u; ok && (u = walk.next()) >= 0;) {
+      for (int u; ok && (u = next_unit()) >= 0;) {
+        GroupedUnits units(tables, a.G, 1, a.bn, true);
         const GroupedUnit un = units.at(u);
-        const Half z(un.n, rank);
-        const int feat = un.tile * kFeatures + static_cast<int>(rank) * 128, tok = un.tok0 + z.from;
+        const Part<PAIR> z(un.n, rank);
+        const int feat = un.tile * C::kFeatures + static_cast<int>(rank) * 128, tok = un.tok0 + z.from;
         // a weight tile read by one chunk only is streamed; by more, kept
         const uint64_t pol_w = units.chunks > 1 ? pol_keep : pol_stream;
         for (int kb = 0; kb < kblocks; ++kb) {
@@ -476,32 +532,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (issue) {
-            uint8_t* sa = smem + stage * kStageBytes;
-            const uint32_t bar = full_cl + 8u * stage;
+            uint8_t* sa = smem + stage * C::kStageBytes;
+            uint64_t* const bar = &full[stage];
+            const uint32_t bar_cl = full_cl + 8u * stage;
             if (weights) {
-              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (kABytes + z.loaded * 128));
-              if constexpr (DGRAD)  // 128 rows of w x 128 of its columns, which are the features
-                tma_load_3d_pair(sa + kABytes, &tm_w, bar, feat, kb * 128, un.g, pol_w);
-              else
-                tma_load_3d_pair(sa + kABytes, &tm_w, bar, kb * 128, feat, un.g, pol_w);
+              if (leader)
+                mbar_arrive_expect_tx(bar, (PAIR ? 2 : 1) * (C::kWBoxes * kABytes + z.loaded * 128));
+#pragma unroll
+              for (int b = 0; b < C::kWBoxes; ++b) {
+                // 128 features x 128 of the reduction; the input gradient's features are w's columns
+                const int c0 = DGRAD ? feat + 128 * b : kb * 128, c1 = DGRAD ? kb * 128 : feat + 128 * b;
+                if (PAIR)
+                  tma_load_3d_pair(sa + kABytes, &tm_w, bar_cl, c0, c1, un.g, pol_w);
+                else
+                  tma_load_3d(sa + (1 + b) * kABytes, &tm_w, bar, c0, c1, un.g, pol_w);
+              }
             } else if (z.loaded == 128) {
-              tma_load_2d_pair(sa, &tm_x, bar, kb * 128, tok, pol_keep);
+              if (PAIR)
+                tma_load_2d_pair(sa, &tm_x, bar_cl, kb * 128, tok, pol_keep);
+              else
+                tma_load_2d(sa, &tm_x, bar, kb * 128, tok, pol_keep);
             } else {
-              for (int r = 0; r < z.loaded; r += 32) tma_load_2d_pair(sa + r * 128, &tm_x32, bar, kb * 128, tok + r, pol_keep);
+              for (int r = 0; r < z.loaded; r += 32) {
+                if (PAIR)
+                  tma_load_2d_pair(sa + r * 128, &tm_x32, bar_cl, kb * 128, tok + r, pol_keep);
+                else
+                  tma_load_2d(sa + r * 128, &tm_x32, bar, kb * 128, tok + r, pol_keep);
+              }
             }
           }
           __syncwarp();
           ++issued;
-          if (++stage == kStages) {
+          if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (!(ok && walk.ok) && issue)
-        raise_timeout(a.err, abort_flag, kKernFp8Gemm, walk.ok ? kWaitSlotFree : kWaitUnit);
+      if (!(ok && walked) && issue)
+        raise_timeout(a.err, abort_flag, kKernFp8Gemm, walked ? kWaitSlotFree : kWaitUnit);
       // every load issued has been used before the CTA exits
-      for (int s = 0; s < kStages; ++s) {
+      for (int s = 0; s < C::kStages; ++s) {
         if (issued <= s) break;
         const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
         const int never = 0;
@@ -509,15 +580,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1) {
       if (leader) {
-        // ---------------- MMA issuer for both CTAs: the whole warp walks the units, one lane issues
+        // ---------------- MMA issuer (for both CTAs): the whole warp walks the units, one lane issues
         const bool issue = elect_one();
         const uint32_t s0 = smem_u32(smem);
         const uint64_t a0 = sdesc_kmajor_sw128(s0), b0 = w_desc<DGRAD>(s0 + kABytes);
-        const uint32_t idesc = idesc_e4m3_f32(256, kFeatures, 0, DGRAD);
+        const uint32_t idesc = idesc_e4m3_f32(PAIR ? 256 : 128, C::kFeatures, 0, DGRAD);
         int stage = 0, acc = 0, where = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
-        for (int u; ok && (u = walk.next()) >= 0;) {
+        while (ok && next_unit() >= 0) {
           for (int kb = 0; kb < kblocks; ++kb) {
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, kWaitTimeoutNs, abort_flag))) {
               ok = false;
@@ -531,16 +602,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             if (issue) {
-              const uint64_t at = static_cast<uint64_t>(stage * (kStageBytes >> 4));
-              const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kFeatures);
+              const uint64_t at = static_cast<uint64_t>(stage * (C::kStageBytes >> 4));
+              const uint32_t d = tmem_base + static_cast<uint32_t>(acc * C::kFeatures);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f8_ss_pair(d, a0 + at + k * kStepX, b0 + at + k * kStepW<DGRAD>, idesc, k > 0);
-              mma_commit_pair_mc(&empty[stage], 0x3);
-              mma_commit_pair_mc(&tfull[acc], 0x3);
+              for (int k = 0; k < 4; ++k) {
+                if (PAIR)
+                  mma_f8_ss_pair(d, a0 + at + k * kStepX, b0 + at + k * kStepW<DGRAD>, idesc, k > 0);
+                else
+                  mma_f8_ss(d, a0 + at + k * kStepX, b0 + at + k * kStepW<DGRAD>, idesc, k > 0);
+              }
+              if (PAIR) {
+                mma_commit_pair_mc(&empty[stage], 0x3);
+                mma_commit_pair_mc(&tfull[acc], 0x3);
+              } else {
+                mma_commit(&empty[stage]);
+                mma_commit(&tfull[acc]);
+              }
             }
             __syncwarp();
-            if (++stage == kStages) {
+            if (++stage == C::kStages) {
               stage = 0;
               phase ^= 1u;
             }
@@ -550,67 +630,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!walk.ok) where = kWaitUnit;
-        if (!(ok && walk.ok) && issue) raise_timeout(a.err, abort_flag, kKernFp8Gemm, where);
+        if (!walked) where = kWaitUnit;
+        if (!(ok && walked) && issue) raise_timeout(a.err, abort_flag, kKernFp8Gemm, where);
         // all MMAs issued have finished before TMEM is released
-        if (issue) mma_commit_pair(done);
+        if (issue) {
+          if (PAIR)
+            mma_commit_pair(done);
+          else
+            mma_commit(done);
+        }
         __syncwarp();
         int dummy = 0;
         mbar_wait(done, 0, kWaitTimeoutNs, &dummy);
       } else if (lane == 0) {
-        if (!sched.schedule(a.next_unit, total_units, kWaitTimeoutNs, abort_flag))
+        if (!sched.schedule(a.next_unit, tables.unit_off[a.G], kWaitTimeoutNs, abort_flag))
           raise_timeout(a.err, abort_flag, kKernFp8Gemm, kWaitUnit);
       }
-    } else {
-      if (leader && lane == 0 && !sched.relay(total_units, kWaitTimeoutNs, abort_flag))
+    } else if (PAIR) {
+      if (leader && lane == 0 && !sched.relay(tables.unit_off[a.G], kWaitTimeoutNs, abort_flag))
         raise_timeout(a.err, abort_flag, kKernFp8Gemm, kWaitUnit);
     }
   } else {
-    set_registers_up<kEpiRegs>();
+    set_registers_up<C::kEpiRegs>();
     // ---------------- epilogue: TMEM lane quarter = warp % 4; a quarter's two warps
     // take 128 features each, a lane one row
-    GroupedUnits units(tables, a.G, 1, a.bn, true);
-    PairUnits walk(sched, total_units, kWaitTimeoutNs, abort_flag, leader, false);
-    const int q = warp & 3, col0 = (warp - 4) / 4 * 128, row = q * 32 + lane;
+    const int q = warp & 3, col0 = (warp - 4) / 4 * 128;
     const bool fp16 = a.fp16 != 0;
-    const uint32_t tempty_cl = mapa_shared(smem_u32(tempty), 0);
+    const uint32_t tempty_cl = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
     const uint32_t t_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(col0);
     const int64_t w_step = DGRAD ? args.w_cols : 1;
     int acc = 0, where = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int u; ok && (u = walk.next()) >= 0;) {
-      const GroupedUnit un = units.at(u);
-      const Half z(un.n, rank);
-      const int feat = un.tile * kFeatures + col0;
-      const bool mine = row < z.n;
-      const float* sw = feature_scales<DGRAD>(args, un.g, feat);
-      const float* sx = args.x_scales + un.tok0 + z.from + row;
-      float next_w[kAhead], next_x[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        next_w[k] = k < kblocks ? __ldg(sw) : 0.0f;
-        next_x[k] = k < kblocks && mine ? __ldg(sx) : 0.0f;
-        sw += w_step;
-        sx += args.ldxs;
+    for (int u; ok && (u = next_unit()) >= 0;) {
+      int tok, rows, feat;  // this warp's first row, its rows, its first feature
+      const float *sx, *sw;
+      {
+        const GroupedUnit un = GroupedUnits(tables, a.G, 1, a.bn, true).at(u);
+        const Part<PAIR> z(un.n, rank);
+        feat = un.tile * C::kFeatures + col0;
+        tok = un.tok0 + z.from + q * 32;
+        rows = z.n - q * 32;
+        sw = feature_scales<DGRAD>(args, un.g, feat);
+        // (lanes without a row read another one's scales)
+        sx = args.x_scales + (un.tok0 + min(z.from + q * 32 + lane, un.n - 1)) * args.ldxs;
       }
+      float next_w = __ldg(sw), next_x = __ldg(sx);
       uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
       for (int kb = 0; kb < kblocks; ++kb) {
-        const float s = __fmul_rn(next_x[0], next_w[0]);
+        const float s = __fmul_rn(next_x, next_w);
         uint64_t s2;
         asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
-#pragma unroll
-        for (int k = 0; k + 1 < kAhead; ++k) {
-          next_w[k] = next_w[k + 1];
-          next_x[k] = next_x[k + 1];
-        }
-        if (kb + kAhead < kblocks) {
-          next_w[kAhead - 1] = __ldg(sw);
-          if (mine) next_x[kAhead - 1] = __ldg(sx);
-          sw += w_step;
-          sx += args.ldxs;
+        if (kb + 1 < kblocks) {  // the next block's, while this one's MMAs run
+          next_w = __ldg(sw + (kb + 1) * w_step);
+          next_x = __ldg(sx + kb + 1);
         }
         // warp-uniform outcome: tcgen05.ld below is executed by all 32 lanes
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_phase, kWaitTimeoutNs, abort_flag))) {
@@ -620,21 +695,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         __syncwarp();
-        const uint32_t t = t_base + static_cast<uint32_t>(acc * kFeatures);
-        uint32_t r[2][32];
-        tmem_ld_32x32b_x32(t, r[0]);
+        const uint32_t t = t_base + static_cast<uint32_t>(acc * C::kFeatures);
+        uint32_t r[2][16];
+        tmem_ld_32x32b_x16(t, r[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 8; ++c) {
           tmem_ld_wait(r[c & 1]);
-          if (c < 3) {
-            tmem_ld_32x32b_x32(t + 32 * (c + 1), r[(c + 1) & 1]);
+          if (c < 7) {
+            tmem_ld_32x32b_x16(t + 16 * (c + 1), r[(c + 1) & 1]);
           } else {  // hand the accumulator back to the MMA thread
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(tempty_cl + 8u * acc);
+            if (lane == 0) {
+              if (PAIR)
+                mbar_arrive_remote(tempty_cl + 8u * acc);
+              else
+                mbar_arrive(&tempty[acc]);
+            }
           }
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) fma2(sum[16 * c + i / 2], r[c & 1][i], r[c & 1][i + 1], s2);
+          for (int i = 0; i < 16; i += 2) fma2(sum[8 * c + i / 2], r[c & 1][i], r[c & 1][i + 1], s2);
         }
         if (++acc == 2) {
           acc = 0;
@@ -642,44 +722,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (mine) {
-        uint16_t* out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(un.tok0 + z.from + row) * a.ldo + feat;
+      // A pass's features of the 32 rows through shared memory, so that a store covers whole sectors of
+      // few rows: 16-byte stores of 32 rows at once take 32 cycles each, copies of each row by TMA as long
+      // (64 x 512 rows, N = K = 4096: 87 us of 560).
+      constexpr int kLanes = C::kPass / 8, kPer = 32 / kLanes;  // lanes a row, rows a store
+      uint8_t* const buf = outs + (warp - 4) * 32 * C::kOutRow;
+      uint16_t* const out = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(tok) * a.ldo + feat;
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
+      for (int c = 0; c < 128; c += C::kPass) {
+#pragma unroll
+        for (int i = 0; i < C::kPass / 2; i += 4) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float lo, hi;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(sum[i + k]));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(sum[c / 2 + i + k]));
             w[k] = pack16(lo, hi, fp16);
           }
-          if (feat + 2 * i < a.F) *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);  // (F: a multiple of 8)
+          *reinterpret_cast<uint4*>(buf + lane * C::kOutRow + 4 * i) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        __syncwarp();
+        const int at = c + 8 * (lane % kLanes);
+        if (feat + at < a.F) {  // (F is a multiple of 8)
+#pragma unroll
+          for (int i = 0; i < 32; i += kPer) {
+            const int r = i + lane / kLanes;
+            if (r < rows)
+              *reinterpret_cast<uint4*>(out + r * a.ldo + at) =
+                  *reinterpret_cast<const uint4*>(buf + r * C::kOutRow + 16 * (lane % kLanes));
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-    if (!walk.ok) where = kWaitUnit;
-    if (!(ok && walk.ok) && lane == 0) raise_timeout(a.err, abort_flag, kKernFp8Gemm, where);
+    if (!walked) where = kWaitUnit;
+    if (!(ok && walked) && lane == 0) raise_timeout(a.err, abort_flag, kKernFp8Gemm, where);
   }
 
   __syncthreads();
-  cluster_sync();  // both CTAs keep their shared memory, barriers and TMEM until both are done
+  if (PAIR) cluster_sync();  // both CTAs keep their shared memory, barriers and TMEM until both are done
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, 2 * kFeatures);
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, 2 * C::kFeatures);
+    else
+      tmem_dealloc(tmem_base, 2 * C::kFeatures);
   }
 }
 
-}  // namespace pair
+template <bool DGRAD, bool PAIR>
+cudaError_t launch_large(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx32, const Fp8GemmArgs& a,
+                         int num_sms, cudaStream_t stream) {
+  using C = Large<PAIR>;
+  static PerDevice config;
+  auto kernel = fp8_large_kernel<DGRAD, PAIR>;
+  if constexpr (PAIR) return launch_pairs(kernel, config, C::kThreads, C::kSmemBytes, stream, tw, tx, tx32, a);
+  return launch_ctas(kernel, config, num_sms, C::kThreads, C::kSmemBytes, stream, tw, tx, tx32, a);
+}
 
 template <bool DGRAD>
-cudaError_t launch(GroupedPlan plan, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx32,
+cudaError_t launch(Fp8Plan plan, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tx32,
                    const Fp8GemmArgs& a, int num_sms, cudaStream_t stream) {
-  if (plan == GroupedPlan::kLarge) {
-    static PerDevice config;
-    return launch_pairs(pair::fp8_pair_kernel<DGRAD>, config, pair::kThreads, pair::kSmemBytes, stream, tw, tx, tx32, a);
-  }
+  if (plan == Fp8Plan::kPairs) return launch_large<DGRAD, true>(tw, tx, tx32, a, num_sms, stream);
+  if (plan == Fp8Plan::kSingle) return launch_large<DGRAD, false>(tw, tx, tx32, a, num_sms, stream);
   static PerDevice config;
   return launch_ctas(fp8_small_kernel<DGRAD>, config, num_sms < kMaxGemmCtas ? num_sms : kMaxGemmCtas, kThreads,
                      kSmemBytes, stream, tw, tx, a);
@@ -687,12 +793,13 @@ cudaError_t launch(GroupedPlan plan, const CUtensorMap& tw, const CUtensorMap& t
 
 }  // namespace
 
-int fp8_bn(GroupedPlan plan, int64_t, int64_t, int64_t, int) {
-  return plan == GroupedPlan::kSmall ? kUnitRows : pair::kRows;
+int fp8_bn(Fp8Plan plan) {
+  return plan == Fp8Plan::kSmall ? kUnitRows : plan == Fp8Plan::kSingle ? Large<false>::kRows : Large<true>::kRows;
 }
-int fp8_tok_box(GroupedPlan plan) { return plan == GroupedPlan::kSmall ? kRowBox : 128; }
+int fp8_tile(Fp8Plan plan) { return plan == Fp8Plan::kSmall ? 128 : Large<true>::kFeatures; }
+int fp8_tok_box(Fp8Plan plan) { return plan == Fp8Plan::kSmall ? kRowBox : 128; }
 
-cudaError_t launch_fp8_gemm(GroupedOp op, GroupedPlan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
+cudaError_t launch_fp8_gemm(GroupedOp op, Fp8Plan plan, const CUtensorMap& tm_w, const CUtensorMap& tm_x,
                             const CUtensorMap& tm_x32, const Fp8GemmArgs& a, int num_sms, cudaStream_t stream) {
   return op == GroupedOp::kForward ? launch<false>(plan, tm_w, tm_x, tm_x32, a, num_sms, stream)
                                    : launch<true>(plan, tm_w, tm_x, tm_x32, a, num_sms, stream);

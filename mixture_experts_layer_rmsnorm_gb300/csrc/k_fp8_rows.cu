@@ -158,16 +158,23 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_rows_kernel(const __gri
       else
         v[i].zero();
     }
+    float s[HOLD];
 #pragma unroll
     for (int i = 0; i < HOLD; ++i) {
       uint32_t m = v[i].magnitude();
 #pragma unroll
       for (int d = 4; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
       const int at = (b0 + i) * 8 + part;
-      if (!mine || at >= vecs) continue;
-      const float s = scale_of(m);
-      if (part == 0) a.scales[(b0 + i) * a.lds + row] = s;
-      *reinterpret_cast<uint4*>(a.codes + static_cast<size_t>(row) * a.K + static_cast<size_t>(at) * 16) = encode(v[i], s);
+      s[i] = scale_of(m);
+      if (mine && at < vecs)
+        *reinterpret_cast<uint4*>(a.codes + static_cast<size_t>(row) * a.K + static_cast<size_t>(at) * 16) = encode(v[i], s[i]);
+    }
+    if (part == 0 && mine) {  // (lds is a multiple of 4: blocks past K get the 1 of zeros)
+      float* to = a.scales + row * a.lds + b0;
+      if constexpr (HOLD == 4)
+        *reinterpret_cast<float4*>(to) = make_float4(s[0], s[1], s[2], s[3]);
+      else
+        *reinterpret_cast<float2*>(to) = make_float2(s[0], s[1]);
     }
   }
 }
@@ -221,12 +228,10 @@ __global__ void __launch_bounds__(kThreads) fp8_dequantize_kernel(const __grid_c
   const int part = threadIdx.x & 7, vecs = a.K / 16, b0 = blockIdx.x * HOLD;
   for (int64_t row = static_cast<int64_t>(blockIdx.y) * kTileRows + (threadIdx.x >> 3); row < a.rows;
        row += static_cast<int64_t>(gridDim.y) * kTileRows) {
-    const float* sc = a.scales + row;
-    int64_t step = a.lds;
+    const float* sc = a.scales + row * a.lds;
     if (a.per) {
       const int64_t g = static_cast<uint32_t>(row) / static_cast<uint32_t>(a.per);
       sc = a.scales + (g * tiles + (row - g * a.per) / 128) * kblocks;
-      step = 1;
     }
     uint4 c[HOLD];
     float s[HOLD];
@@ -235,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) fp8_dequantize_kernel(const __grid_c
       const int at = (b0 + i) * 8 + part;
       if (at >= vecs) continue;
       c[i] = __ldg(reinterpret_cast<const uint4*>(a.codes + static_cast<size_t>(row) * a.K + static_cast<size_t>(at) * 16));
-      s[i] = __ldg(sc + (b0 + i) * step);
+      s[i] = __ldg(sc + b0 + i);
     }
 #pragma unroll
     for (int i = 0; i < HOLD; ++i) {

@@ -89,7 +89,7 @@ def test_rows_to_8_bits_and_back(rows, k, dtype, pad):
     assert r8.quantize(x) is r8 and r8.rows == rows
     codes, scales, values = define(x, 1)
     assert torch.equal(r8.codes[:rows * k].view(rows, k), codes)
-    assert same_bits(r8.scales.view(-1, rows + 5)[:, :rows].t().contiguous(), scales)
+    assert same_bits(r8.scales[:rows, :scales.shape[1]].contiguous(), scales)
     for out in (BF16, FP16, FP32):
         y = torch.full((rows, k + pad), 7.0, dtype=out, device="cuda")
         assert r8.dequantize(y[:, :k]).data_ptr() == y.data_ptr()
@@ -125,7 +125,7 @@ def test_extreme_blocks():
     r8 = binding.Fp8Rows(384, max_rows=6).quantize(x)
     codes, scales, values = define(x, 1)
     assert torch.equal(r8.codes.view(6, 384), codes)
-    got = r8.scales.view(3, 6).t()
+    got = r8.scales[:, :3]
     assert torch.equal(torch.isnan(got), torch.isnan(scales)) and same_bits(got[~torch.isnan(got)], scales[~torch.isnan(scales)])
     y = r8.dequantize(dtype=FP32)
     assert torch.isnan(y[1, :256]).all() and torch.isnan(y[2, 256:]).all() and torch.isfinite(y[2, :256]).all()
@@ -134,7 +134,7 @@ def test_extreme_blocks():
     assert torch.isnan(w8.scales[0, 0]).all() and torch.all(w8.scales[0, 1] == 1.0)
 
 
-# counts, N, K, type, gap, tail, pad: both tile plans, single rows, empty groups, chunk edges (16, 32, 256), sizes that
+# counts, N, K, type, gap, tail, pad: every tile plan, single rows, empty groups, chunk edges (16, 32, 128, 256), sizes that
 # are no multiple of a tile or a block, strided outputs, more groups than the shared-memory table holds
 CASES = {
     "one": ([1], 16, 16, BF16, 0, 0, 0),
@@ -146,6 +146,8 @@ CASES = {
     "large_fp16": ([100, 0, 700, 33], 1424, 640, FP16, 7, 9, 24),
     "large_skewed": ([1500, 1, 0, 2, 40], 256, 128, BF16, 1, 0, 0),
     "large_deep": ([250, 190, 70, 130], 384, 4096, BF16, 0, 0, 0),
+    "single_edges": ([300, 0, 2, 129, 128, 127, 1, 60, 0, 33], 528, 336, BF16, 0, 0, 0),
+    "single_fp16_deep": ([90, 20, 0, 64, 97], 400, 2064, FP16, 3, 1, 8),
     "many_groups": ([(7 * i) % 5 for i in range(300)], 144, 80, BF16, 0, 2, 0),
     "most_groups": ([(i * i) % 61 for i in range(1024)], 64, 64, FP16, 0, 0, 0),
     "some_rows": ([20, 40, 0, 17, 24, 21, 19], 272, 208, BF16, 0, 3, 0),
@@ -200,7 +202,7 @@ def test_input_gradient(name):
     assert torch.all(dx[lists.free] == 7.0)
 
 
-@pytest.mark.parametrize("rows", [6, 399])
+@pytest.mark.parametrize("rows", [6, 99, 399])
 def test_equal_groups_without_lists(rows):
     gen = torch.Generator(device="cuda").manual_seed(3)
     w8 = binding.Fp8Weights.quantize(torch.randn((3, 144, 272), generator=gen, device="cuda"))
@@ -215,7 +217,7 @@ def test_equal_groups_without_lists(rows):
         check(dx[at], dv[at], wv[g], 144)
 
 
-@pytest.mark.parametrize("counts", [[3, 2, 4], [40, 21, 64]])
+@pytest.mark.parametrize("counts", [[3, 2, 4], [40, 21, 64], [300, 150, 200]])
 def test_nan_stays_in_its_row_and_its_block_of_weights(counts):
     lists = Lists(counts)
     gen = torch.Generator(device="cuda").manual_seed(4)
@@ -250,7 +252,7 @@ def test_bad_lists_write_nothing_and_are_reported(offsets, counts, group):
     assert w8.device_status()[0] == binding.MOE_OK and torch.all(out[:30] == 64.0)
 
 
-@pytest.mark.parametrize("counts", [[5, 0, 9, 2], [300, 0, 190, 64]])
+@pytest.mark.parametrize("counts", [[5, 0, 9, 2], [100, 0, 90, 64], [300, 0, 190, 264]])
 def test_calls_repeat_bit_for_bit_and_replay_from_a_graph_on_new_rows_and_lists(counts):
     lists = Lists(counts)
     gen = torch.Generator(device="cuda").manual_seed(6)

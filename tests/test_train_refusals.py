@@ -23,19 +23,20 @@ def test_fp8_shapes(per, groups, rows, k, want):
     assert st == want
     if want == OK:
         assert codes == rows * k
-        assert scales == 4 * -(-k // 128) * (rows if per == ROW else groups * -(-(rows // groups) // 128))
+        blocks = -(-k // 128)
+        assert scales == 4 * ((blocks + 3) // 4 * 4 * rows if per == ROW else blocks * groups * -(-(rows // groups) // 128))
 
 
 QUANT = [
     (dict(src=None), INV), (dict(src=A + 8), INV), (dict(codes=None), INV), (dict(codes=A + 8), INV),
-    (dict(scales=None), INV), (dict(scales=A + 2), INV), (dict(lds=19), INV), (dict(ld=120), INV), (dict(ld=132), UNS),
+    (dict(scales=None), INV), (dict(scales=A + 8), INV), (dict(lds=0), INV), (dict(lds=6), UNS), (dict(ld=120), INV), (dict(ld=132), UNS),
     (dict(type=3), INV), (dict(K=120), UNS), (dict(rows=-1), INV),
 ]
 
 
 @pytest.mark.parametrize("over,want", QUANT)
 def test_fp8_rows_refuse(over, want):
-    a = dict(rows=20, K=128, type=0, src=A, ld=128, codes=A, scales=A, lds=20)
+    a = dict(rows=20, K=128, type=0, src=A, ld=128, codes=A, scales=A, lds=4)
     a.update(over)
     s = binding.fp8_shape(ROW, 1, a["rows"], a["K"])
     assert binding.moe_fp8_quantize(s, a["type"], a["src"], a["ld"], a["codes"], a["scales"], a["lds"], None) == want
@@ -43,7 +44,7 @@ def test_fp8_rows_refuse(over, want):
 
 
 def call(fn, **over):
-    a = dict(groups=4, N=64, K=128, rows=20, type=0, a=A, s=A, lds=20, w=A, ws_=A, off=A, cnt=None, out=A, ldo=64, ws=A,
+    a = dict(groups=4, N=64, K=128, rows=20, type=0, a=A, s=A, lds=4, w=A, ws_=A, off=A, cnt=None, out=A, ldo=64, ws=A,
              ws_bytes=BIG)
     a.update(over)
     s = binding.grouped_shape(a["groups"], a["N"], a["K"], a["rows"], a["type"])
@@ -52,11 +53,11 @@ def call(fn, **over):
 
 
 @pytest.mark.parametrize("over,want", [
-    (dict(a=None), INV), (dict(a=A + 8), INV), (dict(s=None), INV), (dict(s=A + 2), INV), (dict(lds=19), INV),
-    (dict(w=None), INV), (dict(w=A + 8), INV), (dict(ws_=None), INV), (dict(ws_=A + 1), INV), (dict(out=None), INV),
-    (dict(out=A + 8), INV), (dict(off=A + 2), INV), (dict(cnt=A + 1), INV), (dict(rows=21, lds=21, off=None), INV),
+    (dict(a=None), INV), (dict(a=A + 8), INV), (dict(s=None), INV), (dict(s=A + 4), INV), (dict(lds=0), INV), (dict(lds=5), UNS),
+    (dict(w=None), INV), (dict(w=A + 8), INV), (dict(ws_=None), INV), (dict(ws_=A + 8), INV), (dict(out=None), INV),
+    (dict(out=A + 8), INV), (dict(off=A + 2), INV), (dict(cnt=A + 1), INV), (dict(rows=21, off=None), INV),
     (dict(ws=None), INV), (dict(ws=A + 64), INV), (dict(ws_bytes=1024), WS), (dict(type=2), INV), (dict(groups=0), INV),
-    (dict(N=56), UNS), (dict(K=72), UNS), (dict(rows=0, a=None, s=None, out=None, lds=0), OK),
+    (dict(N=56), UNS), (dict(K=72), UNS), (dict(rows=0, a=None, s=None, out=None), OK),
 ])
 def test_fp8_products_refuse(over, want):
     assert call(binding.moe_fp8_gemm, **{"ldo": 1024, **over}) == want
