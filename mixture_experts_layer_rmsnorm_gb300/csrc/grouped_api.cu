@@ -341,10 +341,14 @@ moe_status fp8_rows(const moe_fp8_shape* s, int32_t type, const void* rows, int6
   return MOE_OK;
 }
 
-// The plan follows the mean of the rows, as for 16 bits.
+// The plan follows the mean of the rows, as for 16 bits.  A pair takes 12/7 of a single CTA's time for a unit of
+// twice the rows, whether they are all there or not.
+//   us on pairs / single CTAs, 64 groups, N = K = 4096     160 rows    256        300        384        512
+//                                                          237 / 258   249 / 275  437 / 379  441 / 396  463 / 507
 moe::Fp8Plan choose_fp8_plan(const moe_grouped_shape* s) {
-  if (s->rows <= int64_t(16) * s->groups) return moe::Fp8Plan::kSmall;
-  return s->rows <= int64_t(128) * s->groups ? moe::Fp8Plan::kSingle : moe::Fp8Plan::kPairs;
+  const int64_t per_group = (s->rows + s->groups - 1) / s->groups;
+  if (per_group <= 16) return moe::Fp8Plan::kSmall;
+  return 12 * ((per_group + 255) / 256) <= 7 * ((per_group + 127) / 128) ? moe::Fp8Plan::kPairs : moe::Fp8Plan::kSingle;
 }
 
 // forward (F = N features, R = K) and input gradient (F = K, R = N)

@@ -15,7 +15,13 @@
 // Gradient.  A CTA walks rows with the grid's stride and keeps its threads' columns
 // of dw and db in registers; the sums of all CTAs are added by a second kernel in a
 // fixed order, so results repeat bit for bit.  Between a row's sums and its dx lies a
-// reduction, so the next rows are loaded before it, into registers, packed.
+// reduction: what dx needs (n and e) is held in registers, so that the next row's loads can
+// take this one's place before it; the row after that is asked into the L2 (one bulk
+// prefetch each of x and dy; 16384 rows of 4096, bf16: 79 -> 69 us).
+//
+// Measured (bf16, inputs not in the L2; of the measured copy rate): forward, rms 16384 x 4096 45 us (0.88), 4096 x
+// 7168 22 (0.78); gradient, rms 16384 x 4096 69 (0.86), 4096 x 7168 38 (0.67), 163840 x 128 27 (0.68); the layer norm's
+// second sum and its db cost 15 to 45% more.  What is missing is latency: a row's barrier, and 3 us of the second kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,8 +34,9 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;    // of CTAs whose rows are held by 8, 16 or 32 lanes
+constexpr int kThreads = 256;     // of CTAs whose rows are held by 8, 16 or 32 lanes
 constexpr int kRowThreads = 512;  // of CTAs that hold a row each, at most
+constexpr int kWarps = kRowThreads / 32;
 
 template <int TYPE>
 constexpr size_t kSize = TYPE == 2 ? 4 : 2;
@@ -71,8 +78,19 @@ __device__ __forceinline__ void load_weight8(const void* w, int weight_type, int
   }
 }
 
+template <int TYPE, int Q>
+__device__ __forceinline__ void unpack(const uint4 (&p)[Q], float (&f)[8]) {
+  if constexpr (TYPE == 2) {
+    f[0] = __uint_as_float(p[0].x), f[1] = __uint_as_float(p[0].y), f[2] = __uint_as_float(p[0].z);
+    f[3] = __uint_as_float(p[0].w), f[4] = __uint_as_float(p[1].x), f[5] = __uint_as_float(p[1].y);
+    f[6] = __uint_as_float(p[1].z), f[7] = __uint_as_float(p[1].w);
+  } else {
+    unpack8<TYPE == 1>(p[0], f);
+  }
+}
+
 // Sums of N values over the L lanes of a row (xor butterfly), or (L = 0) over the
-// CTA; every thread gets them.  buf: [2][16][N] floats, the halves in turn (`turn`), so
+// CTA; every thread gets them.  buf: [2][kWarps][N] floats, the halves in turn (`turn`), so
 // that one barrier serves each sum.
 template <int L, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* buf, int turn) {
@@ -81,7 +99,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* buf, int turn) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
   if constexpr (L == 0) {
-    float* b = buf + turn * 16 * N;
+    float* b = buf + turn * kWarps * N;
     const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -97,92 +115,130 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* buf, int turn) {
 
 // ------------------------------------------------------------------ forward
 
-// One row for each group of L lanes (L = 0: for the CTA), V vectors of 8 a thread.
+// One row at a time for each group of L lanes (L = 0: for the CTA), V vectors of 8 a thread, kept packed: the more
+// a thread holds, the fewer warps a row's sums have to join (4096 rows of 7168, bf16: 62, 35, 25, 22 us with 1, 2,
+// 4, 8 vectors).  Rows of up to 256 elements are walked with the grid's stride, the weight in registers and the next row
+// on its way (163840 rows of 128, bf16: 18.2 instead of 20.9 us; with more vectors it costs: 65536 x 1024 55 -> 63 us).
 template <int TYPE, int L, int V>
-__global__ void __launch_bounds__(L ? kThreads : kRowThreads)
+__global__ void __launch_bounds__(L || V == 8 ? kThreads : kRowThreads)
     row_norm_kernel(const __grid_constant__ RowNormArgs a, bool layer) {
-  __shared__ float buf[2 * 16 * 2];
+  constexpr int Q = TYPE == 2 ? 2 : 1, kGroups = L ? kThreads / (L ? L : 1) : 1;  // Q: 16-byte pieces of a vector
+  constexpr bool kWalk = L > 0 && V == 1;  // over rows, weight and bias in registers (else they are read from L1)
+  __shared__ float buf[2 * kWarps * 2];
   pdl_wait();
   pdl_launch_dependents();
   const int lanes = L ? L : blockDim.x, lane = L ? threadIdx.x & (L - 1) : threadIdx.x, vecs = a.H / 8;
-  const int64_t row = L ? static_cast<int64_t>(blockIdx.x) * (kThreads / (L ? L : 1)) + threadIdx.x / (L ? L : 1) : blockIdx.x;
-  const bool mine = row < a.rows;
-  const char* src = static_cast<const char*>(a.x) + static_cast<size_t>(row) * a.ldx * kSize<TYPE>;
-  float x[V][8];
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kGroups;
+  int64_t tile = static_cast<int64_t>(blockIdx.x) * kGroups;  // (a tile's rows are walked together: its first one decides)
+  int64_t row = tile + (L ? threadIdx.x / (L ? L : 1) : 0);
+  uint4 x[V][Q];
+  auto load = [&](int64_t at_row) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) + static_cast<size_t>(at_row) * a.ldx * kSize<TYPE>);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int at = v * lanes + lane;
-    if (mine && at < vecs) {
-      load8<TYPE>(src + static_cast<size_t>(at) * 8 * kSize<TYPE>, x[v]);
-    } else {
+    for (int v = 0; v < V; ++v) {
+      const int at = v * lanes + lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[v][i] = 0.0f;
+      for (int q = 0; q < Q; ++q) x[v][q] = at_row < a.rows && at < vecs ? __ldcs(src + at * Q + q) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load(row);
+  float w[kWalk ? V : 1][8], b[kWalk ? V : 1][8];
+  if constexpr (kWalk) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool in = v * lanes + lane < vecs;
+      load_weight8<TYPE>(in ? a.weight : nullptr, a.weight_type, (v * lanes + lane) * 8, 1.0f, w[v]);
+      load_weight8<TYPE>(in ? a.bias : nullptr, a.weight_type, (v * lanes + lane) * 8, 0.0f, b[v]);
     }
   }
   const float inv_h = __fdiv_rn(1.0f, static_cast<float>(a.H));
-  float m = 0.0f, shift = 0.0f, s[2] = {0.0f, 0.0f};
-  if (layer) {
-    float t[1] = {0.0f};
+  for (; tile < a.rows; tile += stride, row += stride) {
+    uint4 now[V][Q];
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[0] += x[v][i];
-    row_sums<L>(t, buf + 32, 1);
-    m = t[0] * inv_h;
+      for (int q = 0; q < Q; ++q) now[v][q] = x[v][q];
+    if constexpr (kWalk) load(row + stride);
+    float m = 0.0f, shift = 0.0f, s[2] = {0.0f, 0.0f};
+    if (layer) {
+      float t[1] = {0.0f};
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * lanes + lane < vecs)
+      for (int v = 0; v < V; ++v) {
+        float f[8];
+        unpack<TYPE>(now[v], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] -= m;
+        for (int i = 0; i < 8; ++i) t[0] += f[i];
+      }
+      row_sums<L>(t, buf + 2 * kWarps, 1);
+      m = t[0] * inv_h;
+    }
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      if (v * lanes + lane >= vecs) continue;
+      float f[8];
+      unpack<TYPE>(now[v], f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += x[v][i];
-  }
+      for (int i = 0; i < 8; ++i) {
+        const float d = layer ? f[i] - m : f[i];
+        if (layer) s[0] += d;
+        s[1] = __fmaf_rn(d, d, s[1]);
+      }
+    }
+    if (layer) {
+      row_sums<L>(s, buf, 0);
+      shift = s[0] * inv_h;  // (what the rounding of m left)
+    } else {
+      float t[1] = {s[1]};
+      row_sums<L>(t, buf, 0);
+      s[1] = t[0];
+    }
+    float var = __fmaf_rn(-shift, shift, s[1] * inv_h);
+    if (var < 0.0f) var = 0.0f;  // (NaN stays NaN)
+    const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+    if (row < a.rows) {
+      if (lane == 0) {
+        if (layer && a.mean) a.mean[row] = m + shift;
+        if (a.rstd) a.rstd[row] = r;
+      }
+      char* dst = static_cast<char*>(a.y) + static_cast<size_t>(row) * a.ldy * kSize<TYPE>;
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        const int at = v * lanes + lane;
+        if (at >= vecs) continue;
+        float f[8];
+        unpack<TYPE>(now[v], f);
+        if constexpr (!kWalk) {
+          load_weight8<TYPE>(a.weight, a.weight_type, at * 8, 1.0f, w[0]);
+          load_weight8<TYPE>(a.bias, a.weight_type, at * 8, 0.0f, b[0]);
+        }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[1] = __fmaf_rn(x[v][i], x[v][i], s[1]);
-  row_sums<L>(s, buf, 0);
-  if (layer) shift = s[0] * inv_h;  // (what the rounding of m left)
-  float var = __fmaf_rn(-shift, shift, s[1] * inv_h);
-  if (var < 0.0f) var = 0.0f;  // (NaN stays NaN)
-  const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
-  if (!mine) return;
-  if (lane == 0) {
-    if (layer && a.mean) a.mean[row] = m + shift;
-    if (a.rstd) a.rstd[row] = r;
-  }
-  char* dst = static_cast<char*>(a.y) + static_cast<size_t>(row) * a.ldy * kSize<TYPE>;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int at = v * lanes + lane;
-    if (at >= vecs) continue;
-    float w[8], b[8];
-    load_weight8<TYPE>(a.weight, a.weight_type, at * 8, 1.0f, w);
-    load_weight8<TYPE>(a.bias, a.weight_type, at * 8, 0.0f, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __fmaf_rn((x[v][i] - shift) * r, w[i], b[i]);
-    store8<TYPE>(dst + static_cast<size_t>(at) * 8 * kSize<TYPE>, w);
+        for (int i = 0; i < 8; ++i)
+          f[i] = __fmaf_rn(((layer ? f[i] - m : f[i]) - shift) * r, w[kWalk ? v : 0][i], b[kWalk ? v : 0][i]);
+        store8<TYPE>(dst + static_cast<size_t>(at) * 8 * kSize<TYPE>, f);
+      }
+    }
+    if constexpr (!kWalk) break;
   }
 }
 
 template <int TYPE, int L, int V>
-cudaError_t forward(bool layer, const RowNormArgs& a, cudaStream_t stream) {
+cudaError_t forward(bool layer, const RowNormArgs& a, int num_sms, cudaStream_t stream) {
   const int threads = L ? kThreads : (a.H / 8 + 32 * V - 1) / (32 * V) * 32;
   const int64_t per = L ? kThreads / (L ? L : 1) : 1;
-  return launch_pdl(row_norm_kernel<TYPE, L, V>, dim3(static_cast<unsigned>((a.rows + per - 1) / per)), dim3(threads), 0,
-                    stream, a, layer);
+  int64_t ctas = (a.rows + per - 1) / per;
+  if (L && V == 1 && ctas > static_cast<int64_t>(num_sms) * 4) ctas = static_cast<int64_t>(num_sms) * 4;  // (those resident)
+  return launch_pdl(row_norm_kernel<TYPE, L, V>, dim3(static_cast<unsigned>(ctas)), dim3(threads), 0, stream, a, layer);
 }
 
 template <int TYPE>
-cudaError_t forward_of(bool layer, const RowNormArgs& a, cudaStream_t stream) {
-  if (a.H <= 64) return forward<TYPE, 8, 1>(layer, a, stream);
-  if (a.H <= 128) return forward<TYPE, 16, 1>(layer, a, stream);
-  if (a.H <= 256) return forward<TYPE, 32, 1>(layer, a, stream);
-  if (a.H <= 1024) return forward<TYPE, 32, 4>(layer, a, stream);
-  if (a.H <= 8192) return forward<TYPE, 0, 2>(layer, a, stream);
-  return forward<TYPE, 0, 4>(layer, a, stream);
+cudaError_t forward_of(bool layer, const RowNormArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.H <= 64) return forward<TYPE, 8, 1>(layer, a, num_sms, stream);
+  if (a.H <= 128) return forward<TYPE, 16, 1>(layer, a, num_sms, stream);
+  if (a.H <= 256) return forward<TYPE, 32, 1>(layer, a, num_sms, stream);
+  if (a.H <= 512) return forward<TYPE, 32, 2>(layer, a, num_sms, stream);
+  if (a.H <= 1024) return forward<TYPE, 32, 4>(layer, a, num_sms, stream);
+  if (TYPE == 2 || a.H <= 2048) return forward<TYPE, 0, 4>(layer, a, num_sms, stream);
+  return forward<TYPE, 0, 8>(layer, a, num_sms, stream);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -225,28 +281,15 @@ struct RowData {
     m = layer ? __ldg(a.mean + row) : 0.0f;
     r = __ldg(a.rstd + row);
   }
-  static __device__ __forceinline__ void unpack(const uint4 (&p)[kQuads], float (&f)[8]) {
-    if constexpr (TYPE == 2) {
-      f[0] = __uint_as_float(p[0].x), f[1] = __uint_as_float(p[0].y), f[2] = __uint_as_float(p[0].z);
-      f[3] = __uint_as_float(p[0].w), f[4] = __uint_as_float(p[1].x), f[5] = __uint_as_float(p[1].y);
-      f[6] = __uint_as_float(p[1].z), f[7] = __uint_as_float(p[1].w);
-    } else {
-      unpack8<TYPE == 1>(p[0], f);
-    }
-  }
 };
 
-// rows a thread holds beside the one it computes: as many as the registers take
-template <int TYPE, int V>
-constexpr int kAhead = V == 4 ? 0 : TYPE == 2 || V == 2 ? 1 : 2;
-
-template <int TYPE, bool LAYER, int L, int V>
-__global__ void __launch_bounds__(L ? kThreads : kRowThreads, L ? 2 : 1)
+// MAX: threads of a CTA at most.  AHEAD: rows beyond the next one that are on their way.
+template <int TYPE, bool LAYER, int L, int V, int MAX, int AHEAD>
+__global__ void __launch_bounds__(MAX, L ? (V == 1 ? (LAYER ? 3 : 4) : 2) : 1)
     row_norm_grad_kernel(const __grid_constant__ RowNormArgs a) {
   constexpr int kRows = L ? kThreads / (L ? L : 1) : 1;  // rows of a tile
-  constexpr int A = kAhead<TYPE, V>;
-  __shared__ float buf[2 * 16 * 2];
-  __shared__ float all[L ? kThreads * 8 : 1];
+  __shared__ float buf[2 * kWarps * 2];
+  __shared__ float all[L ? kThreads * 8 * V : 1];
   pdl_wait();
   pdl_launch_dependents();
   const int lanes = L ? L : blockDim.x, lane = L ? threadIdx.x & (L - 1) : threadIdx.x, vecs = a.H / 8;
@@ -254,73 +297,91 @@ __global__ void __launch_bounds__(L ? kThreads : kRowThreads, L ? 2 : 1)
   int64_t tile = static_cast<int64_t>(blockIdx.x) * kRows;  // (a tile's rows are walked together: its first one decides)
   int64_t row = tile + (L ? threadIdx.x / (L ? L : 1) : 0);
 
-  float dw[V][8], db[LAYER ? V : 1][8];
+  constexpr bool kHold = V <= 2;  // n, e and the weight stay in registers; else they are worked out (read) again
+  float dw[V][8], db[LAYER ? V : 1][8], w[kHold ? V : 1][8];
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+  for (int v = 0; v < V; ++v) {
+    if (kHold)
+      load_weight8<TYPE>(v * lanes + lane < vecs ? a.weight : nullptr, a.weight_type, (v * lanes + lane) * 8, 1.0f,
+                         w[kHold ? v : 0]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       dw[v][i] = 0.0f;
       if (LAYER) db[LAYER ? v : 0][i] = 0.0f;
     }
-  // the weight: kept where two vectors leave the registers for it, else read again (from L1)
-  constexpr bool kKeep = V <= 2;
-  float kept[kKeep ? V : 1][8];
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      load_weight8<TYPE>(v * lanes + lane < vecs ? a.weight : nullptr, a.weight_type, (v * lanes + lane) * 8, 1.0f, kept[v]);
   }
   const float inv_h = __fdiv_rn(1.0f, static_cast<float>(a.H));
 
-  RowData<TYPE, V> data[A + 1];
+  RowData<TYPE, V> data[AHEAD + 1];
 #pragma unroll
-  for (int k = 0; k < A; ++k) data[k].load(a, LAYER, row + k * stride, lane, lanes, vecs);
+  for (int k = 0; k <= AHEAD; ++k) data[k].load(a, LAYER, row + k * stride, lane, lanes, vecs);
   int turn = 0;
   for (; tile < a.rows; tile += stride, row += stride) {
-    data[A].load(a, LAYER, row + A * stride, lane, lanes, vecs);
-    const RowData<TYPE, V>& now = data[0];
+    if (L == 0 && threadIdx.x < 2 && row + 2 * stride < a.rows) {
+      const char* p = threadIdx.x ? static_cast<const char*>(a.dy) + static_cast<size_t>(row + 2 * stride) * a.lddy * kSize<TYPE>
+                                  : static_cast<const char*>(a.x) + static_cast<size_t>(row + 2 * stride) * a.ldx * kSize<TYPE>;
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(static_cast<uint32_t>(a.H * static_cast<int>(kSize<TYPE>))) : "memory");
+    }
     const bool mine = row < a.rows;
-    const float m = now.m, r = now.r;
-    float c[2] = {0.0f, 0.0f};  // sums of e and e n
+    const float m = data[0].m, r = data[0].r;
+    float n[V][8], e[V][8], c[2] = {0.0f, 0.0f};  // c: the sums of e n and e
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (mine && v * lanes + lane < vecs) {
-        float x[8], d[8], again[8];
-        RowData<TYPE, V>::unpack(now.x[v], x);
-        RowData<TYPE, V>::unpack(now.d[v], d);
-        if constexpr (!kKeep) load_weight8<TYPE>(a.weight, a.weight_type, (v * lanes + lane) * 8, 1.0f, again);
+        float x[8], d[8];
+        unpack<TYPE>(data[0].x[v], x);
+        unpack<TYPE>(data[0].d[v], d);
+        if constexpr (!kHold) load_weight8<TYPE>(a.weight, a.weight_type, (v * lanes + lane) * 8, 1.0f, w[0]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float e = d[i] * (kKeep ? kept[kKeep ? v : 0][i] : again[i]);
-          if (LAYER) c[0] += e;
-          c[1] = __fmaf_rn(e, (LAYER ? x[i] - m : x[i]) * r, c[1]);
+          n[v][i] = (LAYER ? x[i] - m : x[i]) * r;
+          e[v][i] = d[i] * w[kHold ? v : 0][i];
+          c[0] = __fmaf_rn(e[v][i], n[v][i], c[0]);
+          dw[v][i] = __fmaf_rn(d[i], n[v][i], dw[v][i]);
+          if (LAYER) {
+            c[1] += e[v][i];
+            db[LAYER ? v : 0][i] += d[i];
+          }
         }
       }
     }
-    row_sums<L>(c, buf, turn);
+    // the next row's loads, whose place has just become free, before the sums are joined
+    if constexpr (kHold) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) data[k] = data[k + 1];
+      data[AHEAD].load(a, LAYER, row + (AHEAD + 1) * stride, lane, lanes, vecs);
+    }
+    if constexpr (LAYER) {
+      row_sums<L>(c, buf, turn);
+    } else {
+      float one[1] = {c[0]};
+      row_sums<L>(one, buf, turn);
+      c[0] = one[0];
+    }
     turn ^= 1;
-    const float c0 = LAYER ? c[0] * inv_h : 0.0f, c1 = c[1] * inv_h;
+    const float c1 = c[0] * inv_h, c0 = LAYER ? c[1] * inv_h : 0.0f;
     char* dst = static_cast<char*>(a.dx) + static_cast<size_t>(row) * a.lddx * kSize<TYPE>;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (mine && v * lanes + lane < vecs) {
-        float x[8], d[8], again[8], o[8];
-        RowData<TYPE, V>::unpack(now.x[v], x);
-        RowData<TYPE, V>::unpack(now.d[v], d);
-        if constexpr (!kKeep) load_weight8<TYPE>(a.weight, a.weight_type, (v * lanes + lane) * 8, 1.0f, again);
+        float o[8];
+        if constexpr (!kHold) {
+          float x[8], d[8];
+          unpack<TYPE>(data[0].x[v], x);
+          unpack<TYPE>(data[0].d[v], d);
+          load_weight8<TYPE>(a.weight, a.weight_type, (v * lanes + lane) * 8, 1.0f, w[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float n = (LAYER ? x[i] - m : x[i]) * r;
-          const float e = d[i] * (kKeep ? kept[kKeep ? v : 0][i] : again[i]);
-          o[i] = r * __fmaf_rn(-n, c1, e - c0);
-          dw[v][i] = __fmaf_rn(d[i], n, dw[v][i]);
-          if (LAYER) db[LAYER ? v : 0][i] += d[i];
+          for (int i = 0; i < 8; ++i) {
+            n[v][i] = (LAYER ? x[i] - m : x[i]) * r;
+            e[v][i] = d[i] * w[0][i];
+          }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = r * __fmaf_rn(-n[v][i], c1, LAYER ? e[v][i] - c0 : e[v][i]);
         store8<TYPE>(dst + static_cast<size_t>(v * lanes + lane) * 8 * kSize<TYPE>, o);
       }
     }
-#pragma unroll
-    for (int k = 0; k < A; ++k) data[k] = data[k + 1];
+    if constexpr (!kHold) data[0].load(a, LAYER, row + stride, lane, lanes, vecs);
   }
   if (!a.dweight && !a.dbias) return;
 
@@ -346,14 +407,18 @@ __global__ void __launch_bounds__(L ? kThreads : kRowThreads, L ? 2 : 1)
         }
     }
   } else {
-    // the tile's rows meet in shared memory: [kRows][H], 8 L >= H
+    // the tile's rows meet in shared memory: [kRows][H], 8 L V >= H
 #pragma unroll
     for (int which = 0; which < (LAYER ? 2 : 1); ++which) {
       __syncthreads();
-      if (lane < vecs)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          all[(threadIdx.x / (L ? L : 1)) * a.H + lane * 8 + i] = which ? db[0][i] : dw[0][i];
+      for (int v = 0; v < V; ++v) {
+        const int at = v * lanes + lane;
+        if (at < vecs)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            all[(threadIdx.x / (L ? L : 1)) * a.H + at * 8 + i] = which ? db[LAYER ? v : 0][i] : dw[v][i];
+      }
       __syncthreads();
       for (int h = threadIdx.x; h < a.H; h += kThreads) {
         float sum = 0.0f;
@@ -364,8 +429,8 @@ __global__ void __launch_bounds__(L ? kThreads : kRowThreads, L ? 2 : 1)
   }
 }
 
-// dw and db from the CTAs' sums: a CTA takes 32 columns of one of them, 16 sums at a time.
-constexpr int kSumRows = 16;
+// dw and db from the CTAs' sums: a CTA takes 32 columns of one of them, 32 sums at a time.
+constexpr int kSumRows = 32;
 __global__ void __launch_bounds__(32 * kSumRows) row_norm_sum_kernel(const __grid_constant__ RowNormArgs a, int n) {
   __shared__ float part[kSumRows][33];
   pdl_wait();
@@ -375,7 +440,7 @@ __global__ void __launch_bounds__(32 * kSumRows) row_norm_sum_kernel(const __gri
   if (!out) return;
   float sum = 0.0f;
   if (h < a.H)
-#pragma unroll 4
+#pragma unroll 8
     for (int p = threadIdx.y; p < n; p += kSumRows) sum += __ldcg(a.partials + (static_cast<int64_t>(p) * 2 + which) * a.H + h);
   part[threadIdx.y][threadIdx.x] = sum;
   __syncthreads();
@@ -389,11 +454,11 @@ cudaError_t sum_partials(const RowNormArgs& a, int n, cudaStream_t stream) {
   return launch_pdl(row_norm_sum_kernel, dim3((a.H + 31) / 32, 2), dim3(32, kSumRows), 0, stream, a, n);
 }
 
-template <int TYPE, bool LAYER, int L, int V>
+template <int TYPE, bool LAYER, int L, int V, int MAX, int AHEAD>
 cudaError_t gradient(const RowNormArgs& a, int num_sms, cudaStream_t stream) {
   constexpr int kRows = L ? kThreads / (L ? L : 1) : 1;
   const int threads = L ? kThreads : (a.H / 8 + 32 * V - 1) / (32 * V) * 32;
-  auto kernel = row_norm_grad_kernel<TYPE, LAYER, L, V>;
+  auto kernel = row_norm_grad_kernel<TYPE, LAYER, L, V, MAX, AHEAD>;
   static PerDevice config;  // registers a thread
   int regs = 0;
   cudaError_t e = config.get(
@@ -419,12 +484,13 @@ cudaError_t gradient(const RowNormArgs& a, int num_sms, cudaStream_t stream) {
 
 template <int TYPE, bool LAYER>
 cudaError_t gradient_of(const RowNormArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.H <= 64) return gradient<TYPE, LAYER, 8, 1>(a, num_sms, stream);
-  if (a.H <= 128) return gradient<TYPE, LAYER, 16, 1>(a, num_sms, stream);
-  if (a.H <= 256) return gradient<TYPE, LAYER, 32, 1>(a, num_sms, stream);
-  if (a.H <= 4096) return gradient<TYPE, LAYER, 0, 1>(a, num_sms, stream);
-  if (a.H <= 8192) return gradient<TYPE, LAYER, 0, 2>(a, num_sms, stream);
-  return gradient<TYPE, LAYER, 0, 4>(a, num_sms, stream);
+  if (a.H <= 64) return gradient<TYPE, LAYER, 8, 1, kThreads, 0>(a, num_sms, stream);
+  if (a.H <= 128) return gradient<TYPE, LAYER, 16, 1, kThreads, 0>(a, num_sms, stream);
+  if (a.H <= 256) return gradient<TYPE, LAYER, 32, 1, kThreads, 0>(a, num_sms, stream);
+  if (a.H <= 512) return gradient<TYPE, LAYER, 32, 2, kThreads, 0>(a, num_sms, stream);
+  if (a.H <= 4096) return gradient<TYPE, LAYER, 0, 2, 256, 0>(a, num_sms, stream);
+  if (a.H <= 8192) return gradient<TYPE, LAYER, 0, 2, 512, 0>(a, num_sms, stream);
+  return gradient<TYPE, LAYER, 0, 4, 512, 0>(a, num_sms, stream);
 }
 
 template <int TYPE>
@@ -434,10 +500,10 @@ cudaError_t gradient_of(bool layer, const RowNormArgs& a, int num_sms, cudaStrea
 
 }  // namespace
 
-cudaError_t launch_row_norm(bool layer, const RowNormArgs& a, cudaStream_t stream) {
-  return a.type == 2   ? forward_of<2>(layer, a, stream)
-         : a.type == 1 ? forward_of<1>(layer, a, stream)
-                       : forward_of<0>(layer, a, stream);
+cudaError_t launch_row_norm(bool layer, const RowNormArgs& a, int num_sms, cudaStream_t stream) {
+  return a.type == 2   ? forward_of<2>(layer, a, num_sms, stream)
+         : a.type == 1 ? forward_of<1>(layer, a, num_sms, stream)
+                       : forward_of<0>(layer, a, num_sms, stream);
 }
 
 cudaError_t launch_row_norm_grad(bool layer, const RowNormArgs& a, int num_sms, cudaStream_t stream) {

@@ -35,7 +35,7 @@ struct RowNormArgs {
   int accumulate;   // dweight, dbias (fp32): added to what they hold
   float* partials;  // [norm_max_ctas(H)][2][H]
 };
-cudaError_t launch_row_norm(bool layer, const RowNormArgs& a, cudaStream_t stream);
+cudaError_t launch_row_norm(bool layer, const RowNormArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_row_norm_grad(bool layer, const RowNormArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace moe

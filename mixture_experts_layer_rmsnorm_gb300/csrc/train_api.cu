@@ -124,7 +124,10 @@ moe_status moe_norm(const moe_norm_shape* shape, const void* x, int64_t ldx, con
   a.ldy = ldy;
   a.mean = mean;
   a.rstd = rstd;
-  return moe::launch_row_norm(layer, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  return moe::launch_row_norm(layer, a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
+                                                                                                    : MOE_ERR_CUDA;
 }
 
 moe_status moe_norm_grad_workspace_size(const moe_norm_shape* shape, size_t* bytes) {
