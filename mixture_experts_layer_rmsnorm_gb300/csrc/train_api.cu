@@ -79,22 +79,19 @@ moe_status grad_tensors(const moe_grad_tensor* t, int32_t n, bool clip, std::uni
   }
   out.reset(new (std::nothrow) moe::GradTensor[n > 0 ? n : 1]);
   if (!out) return MOE_ERR_CUDA;
-  int64_t first = 0;
+  int64_t chunks = 0;
   for (int32_t i = 0; i < n; ++i) {
     if (t[i].n == 0) continue;
-    if (used % moe::kGradTensors == 0) first = 0;
-    const int64_t chunks = (t[i].n + moe::kGradChunk - 1) / moe::kGradChunk;
-    if (first + chunks >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    chunks += (t[i].n + moe::kGradChunk - 1) / moe::kGradChunk;
+    if (chunks > (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
     moe::GradTensor& g = out[used++];
     g.src = t[i].data;
     g.dst = clip ? t[i].out : nullptr;
     g.n = t[i].n;
-    g.first = static_cast<int32_t>(first);
     g.type = static_cast<uint8_t>(t[i].type);
     g.dst_type = static_cast<uint8_t>(clip ? t[i].out_type : t[i].type);
     g.vec = aligned(t[i].data, 16);
     g.dst_vec = clip && aligned(t[i].out, 16);
-    first += chunks;
   }
   return MOE_OK;
 }
