@@ -766,7 +766,8 @@ MOE_API moe_status moe_norm_grad(const moe_norm_shape* shape, const void* dy, in
  * to their elements (16-byte borders are faster).  Squares are summed in fp32 for 64
  * elements at most, in fp64 beyond, in a fixed order; no finite element overflows or
  * vanishes, and a norm above fp32's range is infinity.
- *   norm   fp32, device: written by moe_grad_norm, read by moe_grad_clip
+ *   norm   fp32, device: written by moe_grad_norm and moe_grad_norm_clip, read by
+ *          moe_grad_clip (one already known, such as that of these tensors and others)
  *   out    of out_type; may be data itself (with the same type), else apart from
  *          every tensor.  Unused by moe_grad_norm.
  * Where the norm is a NaN or infinite, nothing is clipped (the factor is 1).  A
@@ -788,6 +789,9 @@ MOE_API moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n_tenso
                                  size_t workspace_bytes, moe_stream_t stream);
 MOE_API moe_status moe_grad_clip(const moe_grad_tensor* tensors, int32_t n_tensors, const float* norm,
                                  double max_norm, double eps, moe_stream_t stream);
+/* moe_grad_norm and moe_grad_clip by its norm, with less to launch. */
+MOE_API moe_status moe_grad_norm_clip(const moe_grad_tensor* tensors, int32_t n_tensors, double max_norm, double eps,
+                                      float* norm, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* Self-test of the failure path of the library's bounded device waits (no
  * counterpart on the pages): enqueues one small kernel whose two waits -- on

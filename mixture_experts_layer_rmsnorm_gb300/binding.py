@@ -144,6 +144,7 @@ def load(build: bool = True):
             lib.moe_grad_norm_workspace_size.argtypes = [i32, psz]
             lib.moe_grad_norm.argtypes = [tp, i32, p, p, sz, p]
             lib.moe_grad_clip.argtypes = [tp, i32, p, f64, f64, p]
+            lib.moe_grad_norm_clip.argtypes = [tp, i32, f64, f64, p, p, sz, p]
             lib.moe_status_string.argtypes = [ctypes.c_int]
             lib.moe_status_string.restype = ctypes.c_char_p
             for f in ("moe_workspace_size", "moe_forward", "moe_forward_events", "moe_route_debug",
@@ -160,7 +161,7 @@ def load(build: bool = True):
                       "moe_swiglu_grad", "moe_fp4_sizes", "moe_fp4_quantize", "moe_fp4_dequantize", "moe_fp4_gemm",
                       "moe_fp8_sizes", "moe_fp8_quantize", "moe_fp8_dequantize", "moe_fp8_gemm", "moe_fp8_gemm_dgrad",
                       "moe_norm", "moe_norm_grad_workspace_size", "moe_norm_grad", "moe_grad_norm_workspace_size",
-                      "moe_grad_norm", "moe_grad_clip"):
+                      "moe_grad_norm", "moe_grad_clip", "moe_grad_norm_clip"):
                 getattr(lib, f).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -544,6 +545,11 @@ def moe_grad_norm(tensors, n_tensors, norm, workspace, workspace_bytes, stream) 
 
 def moe_grad_clip(tensors, n_tensors, norm, max_norm, eps, stream) -> int:
     return load().moe_grad_clip(tensors, int(n_tensors), norm, float(max_norm), float(eps), stream)
+
+
+def moe_grad_norm_clip(tensors, n_tensors, max_norm, eps, norm, workspace, workspace_bytes, stream) -> int:
+    return load().moe_grad_norm_clip(tensors, int(n_tensors), float(max_norm), float(eps), norm, workspace,
+                                     workspace_bytes, stream)
 
 
 _types = {}
@@ -1179,7 +1185,8 @@ class Gradients(_Buffers):
         self.workspace, self.fp32 = torch.empty(n, dtype=torch.uint8, device=self.device), torch.float32
 
     def _buffers(self):
-        return (self.workspace, *self.tensors, *self.out)
+        # one tensor of each allocation stands for it
+        return tuple({t.untyped_storage().data_ptr(): t for t in (self.workspace, *self.tensors, *self.out)}.values())
 
     def norm(self):
         """The norm, a tensor of one fp32 number."""
@@ -1192,11 +1199,13 @@ class Gradients(_Buffers):
         """out = tensor * min(1, max_norm / (norm + eps)); returns the norm (before clipping).  norm: one already known,
         such as that of these gradients and others."""
         if norm is None:
-            norm = self.norm()
-        else:
-            _check("norm", norm, self.device, self.fp32, norm.shape)
-            if norm.numel() != 1:
-                raise ValueError(f"norm is {tuple(norm.shape)}, not one number")
+            norm = _empty((), self.fp32, self.device)
+            _enqueue("moe_grad_norm_clip", self.device, self._table, len(self.tensors), float(max_norm), float(eps),
+                     norm.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(), of=(self,))
+            return norm
+        _check("norm", norm, self.device, self.fp32, norm.shape)
+        if norm.numel() != 1:
+            raise ValueError(f"norm is {tuple(norm.shape)}, not one number")
         _enqueue("moe_grad_clip", self.device, self._table, len(self.tensors), norm.data_ptr(), float(max_norm),
                  float(eps), of=(self,))
         return norm

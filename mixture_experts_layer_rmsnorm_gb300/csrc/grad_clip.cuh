@@ -11,15 +11,15 @@ struct GradTensor {
   const void* src;
   void* dst;
   int64_t n;
-  int32_t first;  // its first chunk in the launch's order
   uint8_t type, dst_type;  // 0 bf16, 1 fp16, 2 fp32
   uint8_t vec, dst_vec;    // addresses on 16-byte borders
 };
 
-// Tensors go to the kernels as parameters, so that a call is complete in itself (captured,
-// replayed, several at once): launches of up to kGradTensors of them (32,764 bytes of
-// parameters are allowed), or of kGradFew where that is all, which takes less time to launch.
-constexpr int kGradTensors = 1000, kGradFew = 32;
+// Tensors go to the kernels as parameters, so that a call is complete in itself (captured, replayed, several at
+// once): as many of them as fit 32,764 bytes a launch, or kGradFew where that is all, which takes less time to launch.
+constexpr int kGradTensors = 1600;  // of the norm, and clipped in place
+constexpr int kGradApart = 1150;    // clipped into other tensors
+constexpr int kGradFew = 32;
 constexpr int kGradCtas = 640;       // of a launch, at most: a partial sum each
 constexpr int64_t kGradChunk = 16384;  // elements
 
@@ -28,10 +28,11 @@ inline size_t grad_partial_bytes(int64_t tensors) {
   return static_cast<size_t>(grad_launches(tensors)) * kGradCtas * sizeof(double);
 }
 
-// norm [1] from the tensors (empty ones left out, chunks counted from 0 in each launch)
+// norm [1] from the tensors (empty ones left out)
 cudaError_t launch_grad_norm(const GradTensor* t, int64_t n, float* norm, double* partials, int num_sms,
                              cudaStream_t stream);
-cudaError_t launch_grad_clip(const GradTensor* t, int64_t n, const float* norm, double max_norm, double eps, int num_sms,
-                             cudaStream_t stream);
+// clipping by a norm that is there (partials null), or by the one that it computes and writes (n > 0)
+cudaError_t launch_grad_clip(const GradTensor* t, int64_t n, float* norm, double* partials, double max_norm, double eps,
+                             int num_sms, cudaStream_t stream);
 
 }  // namespace moe

@@ -13,20 +13,18 @@
 // of 16 bytes in flight, four CTAs an SM (two: 598 for 584 us; six with four loads: 585;
 // loads of 32 bytes for fp32: 630).  The clipping walks the chunks backwards: what the
 // norm read last still lies in the L2 (loads that mark lines for eviction: 990 for 976 us).
-// Where nothing is clipped in place, it reads the norm and ends.
-// Beyond 1000 tensors a call is several launches of alike many: the later ones read what
-// no launch of the call writes, so they begin beside the one before and wait for it at
-// their end (1200 tensors of 25,000: 40 -> 33 us for the norm, 27 with the loads above).
-//   24 tensors, 1.07 G elements: norm 584 us in fp32 (1.08 of a copy's rate), 302 in bf16
-//   and clipping bf16 to bf16 976 together (1.00), 0.54 G fp32 to bf16 788 (1.02)
-//   1200 tensors of 25,000: norm 27 us (fp32), with nothing to clip 37; bf16 clipped 42
+// Where nothing is clipped in place, it ends there.  Norm and clipping in one call: each CTA
+// of the clipping adds the sums itself (a launch less; one warp does, see block_sum).
+// Beyond 1600 tensors (1150 into others) a call is several launches of alike many: the later
+// ones read what no launch of the call writes, so they begin beside the one before and wait
+// for it at their end (two launches for 1200 tensors of 25,000: 40 -> 33 us for the norm).
+//   24 tensors, 1.07 G elements: norm 590 us in fp32 (1.07 of a copy's rate), 302 in bf16;
+//   with the clipping, bf16 to bf16 971 (0.98), 0.54 G fp32 to bf16 788 (1.00)
+//   1200 tensors of 25,000: norm 25 us (fp32), and nothing to clip 27; bf16 clipped 38
 //   (the floors are 18, 18 and 27: launches of 32 KB of parameters are the rest)
-// Each chunk's tensor comes from kernel parameters: from device memory the compiler has
-// to take it for different in each thread (norm of 1.07 G fp32 elements: 1130 us).
+// Each chunk's tensor comes from kernel parameters, alike for all threads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-
-#include <cstring>
 
 #include "grad_clip.cuh"
 #include "grouped_elementwise.cuh"
@@ -46,19 +44,42 @@ template <int TYPE>
 constexpr int kVecs = static_cast<int>(kGradChunk / (kWidth<TYPE> * kThreads));
 static_assert(kVecs<0> % kLoads == 0 && kVecs<2> % kLoads == 0, "whole batches");
 
-template <int N>
+// The tensors of a launch, packed.
+template <int N, bool APART>
 struct Table {
   int n, chunks;
-  bool in_place;  // all of them
-  GradTensor t[N];
+  bool in_place;        // all of them
+  int first[N];         // a tensor's first chunk
+  uint64_t meta[N];     // elements (48 bits), type (2), dst_type (2), vec, dst_vec
+  const void* src[N];
+  void* dst[APART ? N : 1];
+
+  void put(int i, const GradTensor& t) {
+    first[i] = chunks;
+    meta[i] = static_cast<uint64_t>(t.n) | static_cast<uint64_t>(t.type) << 48 | static_cast<uint64_t>(t.dst_type) << 50 |
+              static_cast<uint64_t>(t.vec) << 52 | static_cast<uint64_t>(t.dst_vec) << 53;
+    src[i] = t.src;
+    if (APART) dst[i] = t.dst;
+    chunks += static_cast<int>((t.n + kGradChunk - 1) / kGradChunk);
+    if (t.dst != t.src) in_place = false;
+  }
+  __device__ __forceinline__ GradTensor get(int i) const {
+    const uint64_t m = meta[i];
+    GradTensor t;
+    t.src = src[i];
+    t.dst = APART ? dst[i] : const_cast<void*>(src[i]);
+    t.n = static_cast<int64_t>(m & 0xFFFFFFFFFFFFull);
+    t.type = m >> 48 & 3, t.dst_type = m >> 50 & 3, t.vec = m >> 52 & 1, t.dst_vec = m >> 53 & 1;
+    return t;
+  }
 };
 
-template <int N>
-__device__ __forceinline__ int tensor_of(const Table<N>& table, int chunk) {
+template <typename T>
+__device__ __forceinline__ int tensor_of(const T& table, int chunk) {
   int lo = 0, hi = table.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (table.t[mid].first <= chunk)
+    if (table.first[mid] <= chunk)
       lo = mid;
     else
       hi = mid;
@@ -131,9 +152,9 @@ __device__ __forceinline__ void load_batch(const void* base, int b, int n, uint4
 
 // ------------------------------------------------------------------ norm
 
-// What 8 squares add: to `part` in fp32, or to `far` in fp64.
+// What 8 squares add: to `part` in fp32, or to `sum` in fp64.
 template <int TYPE>
-__device__ __forceinline__ void add_squares(const float (&f)[8], float& part, double& far) {
+__device__ __forceinline__ void add_squares(const float (&f)[8], float& part, double& sum) {
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s = __fmaf_rn(f[i], f[i], s);
@@ -146,11 +167,11 @@ __device__ __forceinline__ void add_squares(const float (&f)[8], float& part, do
   for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
   if (s == 0.0f && top == 0.0f) return;  // zeros
 #pragma unroll
-  for (int i = 0; i < 8; ++i) far += static_cast<double>(f[i]) * static_cast<double>(f[i]);
+  for (int i = 0; i < 8; ++i) sum += static_cast<double>(f[i]) * static_cast<double>(f[i]);
 }
 
 template <int TYPE, bool WHOLE>
-__device__ __forceinline__ void vector_squares(const void* src, int n, float& part, double& far) {
+__device__ __forceinline__ void vector_squares(const void* src, int n, float& part, double& sum) {
 #pragma unroll 1
   for (int b = 0; b < kVecs<TYPE>; b += kLoads) {
     if (!WHOLE && b * kThreads * kWidth<TYPE> >= n) break;
@@ -168,26 +189,25 @@ __device__ __forceinline__ void vector_squares(const void* src, int n, float& pa
       } else {
         values<TYPE>(raw[i], f);
       }
-      add_squares<TYPE>(f, part, far);
+      add_squares<TYPE>(f, part, sum);
     }
   }
 }
 
 template <int TYPE>
-__device__ __forceinline__ double chunk_squares(const GradTensor& t, int64_t from) {
+__device__ __forceinline__ void chunk_squares(const GradTensor& t, int64_t from, double& sum) {
   constexpr int kSize = TYPE == 2 ? 4 : 2;
   const void* src = static_cast<const char*>(t.src) + from * kSize;
   const int n = static_cast<int>(min(t.n - from, kGradChunk));
   float part = 0.0f;
-  double far = 0.0;
   if (t.vec && n == kGradChunk) {
-    vector_squares<TYPE, true>(src, n, part, far);
+    vector_squares<TYPE, true>(src, n, part, sum);
   } else if (t.vec) {
-    vector_squares<TYPE, false>(src, n, part, far);
+    vector_squares<TYPE, false>(src, n, part, sum);
     const int at = n / kWidth<TYPE> * kWidth<TYPE> + threadIdx.x;
     if (at < n) {
       const double x = value_at<TYPE>(src, at);
-      far += x * x;
+      sum += x * x;
     }
   } else {
 #pragma unroll 1
@@ -195,38 +215,56 @@ __device__ __forceinline__ double chunk_squares(const GradTensor& t, int64_t fro
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = at + j * kThreads < n ? value_at<TYPE>(src, at + j * kThreads) : 0.0f;
-      add_squares<TYPE>(f, part, far);
+      add_squares<TYPE>(f, part, sum);
     }
   }
-  return static_cast<double>(part) + far;
+  sum += static_cast<double>(part);
 }
 
-// the sum over the CTA, in thread 0
+// The sum over the CTA, in warp 0's threads, in a fixed order.  (An SM adds about two fp64
+// numbers a clock, so 13 additions of one warp are cheaper than 5 of each and 8.)
 __device__ __forceinline__ double block_sum(double v) {
-  __shared__ double warp_sum[kThreads / 32];
+  __shared__ double all[kThreads];
+  all[threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.x >= 32) return 0.0;
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v += all[w * 32 + threadIdx.x];
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0;
-  if (threadIdx.x == 0)
-    for (int w = 0; w < kThreads / 32; ++w) v += warp_sum[w];
   return v;
 }
 
+// The norm from n partial sums, by one warp, alike in every CTA.
+__device__ __forceinline__ float norm_of_sums(const double* partials, int n) {
+  double sum = 0.0;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < n; i += 32) sum += __ldcg(partials + i);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  return static_cast<float>(sqrt(sum));
+}
+
 // norm: written where this CTA is the only one
-template <int N>
-__global__ void __launch_bounds__(kThreads, kCtas) grad_squares_kernel(const __grid_constant__ Table<N> table, double* partials,
-                                                                float* norm, bool first) {
+template <int N, bool APART>
+__global__ void __launch_bounds__(kThreads, kCtas)
+    grad_squares_kernel(const __grid_constant__ Table<N, APART> table, double* partials, float* norm, bool first) {
   if (first) {
     pdl_wait();
     pdl_launch_dependents();
   }
   double sum = 0.0;
   for (int c = blockIdx.x; c < table.chunks; c += gridDim.x) {
-    const GradTensor& t = table.t[tensor_of(table, c)];
-    const int64_t from = static_cast<int64_t>(c - t.first) * kGradChunk;
-    sum += t.type == 2 ? chunk_squares<2>(t, from) : t.type == 1 ? chunk_squares<1>(t, from) : chunk_squares<0>(t, from);
+    const int at = tensor_of(table, c);
+    const GradTensor t = table.get(at);
+    const int64_t from = static_cast<int64_t>(c - table.first[at]) * kGradChunk;
+    if (t.type == 2)
+      chunk_squares<2>(t, from, sum);
+    else if (t.type == 1)
+      chunk_squares<1>(t, from, sum);
+    else
+      chunk_squares<0>(t, from, sum);
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) {
@@ -239,14 +277,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) grad_squares_kernel(const __g
   }
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* partials, int n, float* norm) {
+__global__ void __launch_bounds__(32) grad_norm_kernel(const double* partials, int n, float* norm) {
   pdl_wait();
   pdl_launch_dependents();
-  double sum = 0.0;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < n; i += kThreads) sum += __ldcg(partials + i);
-  sum = block_sum(sum);
-  if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(sum));
+  const float total = norm_of_sums(partials, n);
+  if (threadIdx.x == 0) *norm = total;
 }
 
 // ------------------------------------------------------------------ clipping
@@ -295,25 +330,37 @@ __device__ __forceinline__ void clip_chunk(const GradTensor& t, int64_t from, fl
   }
 }
 
-template <int N>
-__global__ void __launch_bounds__(kThreads, kCtas) grad_clip_kernel(const __grid_constant__ Table<N> table, const float* norm,
-                                                             double max_norm, double eps, bool first) {
+// sums > 0: from that many partial sums, and the first launch writes the norm; else the norm is read
+template <int N, bool APART>
+__global__ void __launch_bounds__(kThreads, kCtas)
+    grad_clip_kernel(const __grid_constant__ Table<N, APART> table, const double* partials, int sums, float* norm,
+                     double max_norm, double eps, bool first) {
   if (first) {
     pdl_wait();
     pdl_launch_dependents();
   }
-  const float total = __ldcg(norm);
-  float factor = 1.0f;
-  if (total < __int_as_float(0x7F800000)) {  // (a norm that is no number clips nothing)
-    const double f = max_norm / (static_cast<double>(total) + eps);
-    if (f < 1.0) factor = static_cast<float>(f);
+  __shared__ float clipping;
+  if (threadIdx.x < 32) {
+    const float total = sums > 0 ? norm_of_sums(partials, sums) : __ldcg(norm);
+    if (threadIdx.x == 0) {
+      if (sums > 0 && first && blockIdx.x == 0) *norm = total;
+      float f = 1.0f;
+      if (total < __int_as_float(0x7F800000)) {  // (a norm that is no number clips nothing)
+        const double exact = max_norm / (static_cast<double>(total) + eps);
+        if (exact < 1.0) f = static_cast<float>(exact);
+      }
+      clipping = f;
+    }
   }
+  __syncthreads();
+  const float factor = clipping;
   const bool nothing = factor == 1.0f && table.in_place;
   for (int i = nothing ? table.chunks : blockIdx.x; i < table.chunks; i += gridDim.x) {
     const int c = table.chunks - 1 - i;
-    const GradTensor& t = table.t[tensor_of(table, c)];
+    const int at = tensor_of(table, c);
+    const GradTensor t = table.get(at);
     if (factor == 1.0f && t.dst == t.src) continue;
-    const int64_t from = static_cast<int64_t>(c - t.first) * kGradChunk;
+    const int64_t from = static_cast<int64_t>(c - table.first[at]) * kGradChunk;
     if (t.type == 2)
       clip_chunk<2>(t, from, factor);
     else if (t.type == 1)
@@ -329,21 +376,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) grad_clip_kernel(const __grid
 
 // ------------------------------------------------------------------ launches
 
-// Calls f(table, CTAs) for each launch's tensors.
-template <int N, typename F>
+// Calls f(table, CTAs, first launch) for each launch's tensors.
+template <int N, bool APART, typename F>
 cudaError_t each_launch(const GradTensor* t, int64_t n, int num_sms, F&& f) {
+  static_assert(sizeof(Table<N, APART>) + 64 <= 32764, "a kernel's parameters");
   const int64_t launches = (n + N - 1) / N, each = launches > 0 ? (n + launches - 1) / launches : 1;
   for (int64_t i = 0; i < n; i += each) {
-    Table<N> table;
+    Table<N, APART> table;
     table.n = static_cast<int>(n - i < each ? n - i : each);
-    std::memcpy(table.t, t + i, table.n * sizeof(GradTensor));
     table.chunks = 0;
     table.in_place = true;
-    for (int j = 0; j < table.n; ++j) {
-      table.t[j].first = table.chunks;
-      table.chunks += static_cast<int>((table.t[j].n + kGradChunk - 1) / kGradChunk);
-      if (table.t[j].dst != table.t[j].src) table.in_place = false;
-    }
+    for (int j = 0; j < table.n; ++j) table.put(j, t[i + j]);
     int ctas = num_sms * kCtas < kGradCtas ? num_sms * kCtas : kGradCtas;
     if (ctas > table.chunks) ctas = table.chunks;
     const cudaError_t e = f(table, ctas, i == 0);
@@ -352,27 +395,55 @@ cudaError_t each_launch(const GradTensor* t, int64_t n, int num_sms, F&& f) {
   return cudaSuccess;
 }
 
-template <int N>
-cudaError_t norm_of(const GradTensor* t, int64_t n, float* norm, double* partials, int num_sms, cudaStream_t stream) {
-  int sums = 0;
-  const bool alone = n <= N;
-  bool done = false;
-  cudaError_t e = each_launch<N>(t, n, num_sms, [&](const Table<N>& table, int ctas, bool first) {
-    done = alone && ctas == 1;
-    double* to = partials + sums;
-    sums += ctas;
-    return launch_pdl(grad_squares_kernel<N>, dim3(ctas), dim3(kThreads), 0, stream, table, to,
-                      done ? norm : static_cast<float*>(nullptr), first);
-  });
-  if (e != cudaSuccess || done) return e;
-  return launch_pdl(grad_norm_kernel, dim3(1), dim3(kThreads), 0, stream, static_cast<const double*>(partials), sums, norm);
+template <int N, bool APART>
+cudaError_t squares(const Table<N, APART>& table, int ctas, double* partials, float* norm, bool first, cudaStream_t stream) {
+  return launch_pdl(grad_squares_kernel<N, APART>, dim3(ctas), dim3(kThreads), 0, stream, table, partials, norm, first);
 }
 
 template <int N>
-cudaError_t clip(const GradTensor* t, int64_t n, const float* norm, double max_norm, double eps, int num_sms,
+cudaError_t all_squares(const GradTensor* t, int64_t n, double* partials, int& sums, int num_sms, cudaStream_t stream) {
+  sums = 0;
+  return each_launch<N, false>(t, n, num_sms, [&](const Table<N, false>& table, int ctas, bool first) {
+    sums += ctas;
+    return squares(table, ctas, partials + (sums - ctas), nullptr, first, stream);
+  });
+}
+
+template <int N>
+cudaError_t norm_of(const GradTensor* t, int64_t n, float* norm, double* partials, int num_sms, cudaStream_t stream) {
+  int sums = 0;
+  bool done = false;
+  cudaError_t e;
+  if (n > 0 && n <= N) {
+    e = each_launch<N, false>(t, n, num_sms, [&](const Table<N, false>& table, int ctas, bool first) {
+      sums = ctas;
+      done = ctas == 1;
+      return squares(table, ctas, partials, done ? norm : nullptr, first, stream);
+    });
+  } else {
+    e = all_squares<N>(t, n, partials, sums, num_sms, stream);
+  }
+  if (e != cudaSuccess || done) return e;
+  return launch_pdl(grad_norm_kernel, dim3(1), dim3(32), 0, stream, static_cast<const double*>(partials), sums, norm);
+}
+
+// partials: null where the norm is there
+template <int N, bool APART>
+cudaError_t clip(const GradTensor* t, int64_t n, float* norm, double* partials, double max_norm, double eps, int num_sms,
                  cudaStream_t stream) {
-  return each_launch<N>(t, n, num_sms, [&](const Table<N>& table, int ctas, bool first) {
-    return launch_pdl(grad_clip_kernel<N>, dim3(ctas), dim3(kThreads), 0, stream, table, norm, max_norm, eps, first);
+  int sums = 0;
+  if (partials && n > N) {
+    const cudaError_t e = all_squares<kGradTensors>(t, n, partials, sums, num_sms, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return each_launch<N, APART>(t, n, num_sms, [&](const Table<N, APART>& table, int ctas, bool first) {
+    if (partials && n <= N) {  // one table for both
+      sums = ctas;
+      const cudaError_t e = squares(table, ctas, partials, nullptr, first, stream);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(grad_clip_kernel<N, APART>, dim3(ctas), dim3(kThreads), 0, stream, table,
+                      static_cast<const double*>(partials), sums, norm, max_norm, eps, first);
   });
 }
 
@@ -384,10 +455,13 @@ cudaError_t launch_grad_norm(const GradTensor* t, int64_t n, float* norm, double
                        : norm_of<kGradTensors>(t, n, norm, partials, num_sms, stream);
 }
 
-cudaError_t launch_grad_clip(const GradTensor* t, int64_t n, const float* norm, double max_norm, double eps, int num_sms,
-                             cudaStream_t stream) {
-  return n <= kGradFew ? clip<kGradFew>(t, n, norm, max_norm, eps, num_sms, stream)
-                       : clip<kGradTensors>(t, n, norm, max_norm, eps, num_sms, stream);
+cudaError_t launch_grad_clip(const GradTensor* t, int64_t n, float* norm, double* partials, double max_norm, double eps,
+                             int num_sms, cudaStream_t stream) {
+  if (n <= kGradFew) return clip<kGradFew, true>(t, n, norm, partials, max_norm, eps, num_sms, stream);
+  bool apart = false;
+  for (int64_t i = 0; i < n; ++i) apart = apart || t[i].dst != t[i].src;
+  return apart ? clip<kGradApart, true>(t, n, norm, partials, max_norm, eps, num_sms, stream)
+               : clip<kGradTensors, false>(t, n, norm, partials, max_norm, eps, num_sms, stream);
 }
 
 }  // namespace moe

@@ -96,6 +96,10 @@ moe_status grad_tensors(const moe_grad_tensor* t, int32_t n, bool clip, std::uni
   return MOE_OK;
 }
 
+bool good_limits(const float* norm, double max_norm, double eps) {
+  return norm && aligned(norm, 4) && max_norm >= 0.0 && eps >= 0.0 && std::isfinite(eps);
+}
+
 }  // namespace
 
 extern "C" {
@@ -207,13 +211,31 @@ moe_status moe_grad_clip(const moe_grad_tensor* tensors, int32_t n_tensors, cons
   int64_t n = 0;
   const moe_status st = grad_tensors(tensors, n_tensors, true, t, n);
   if (st != MOE_OK) return st;
-  if (!norm || !aligned(norm, 4) || !(max_norm >= 0.0) || !(eps >= 0.0) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if (!good_limits(norm, max_norm, eps)) return MOE_ERR_INVALID_ARG;
   if (n == 0) return MOE_OK;
   const int sms = num_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
-  return moe::launch_grad_clip(t.get(), n, norm, max_norm, eps, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return moe::launch_grad_clip(t.get(), n, const_cast<float*>(norm), nullptr, max_norm, eps, sms,
+                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
+}
+
+moe_status moe_grad_norm_clip(const moe_grad_tensor* tensors, int32_t n_tensors, double max_norm, double eps, float* norm,
+                              void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  std::unique_ptr<moe::GradTensor[]> t;
+  int64_t n = 0;
+  const moe_status st = grad_tensors(tensors, n_tensors, true, t, n);
+  if (st != MOE_OK) return st;
+  if (!good_limits(norm, max_norm, eps) || !workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < moe::grad_partial_bytes(n_tensors)) return MOE_ERR_WORKSPACE;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  double* partials = static_cast<double*>(workspace);
+  const cudaError_t e = n > 0 ? moe::launch_grad_clip(t.get(), n, norm, partials, max_norm, eps, sms, s)
+                              : moe::launch_grad_norm(t.get(), n, norm, partials, sms, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -132,18 +132,20 @@ def test_gradient_norm_and_clipping_refuse_tensors(over, want):
     t = tensors(**over)
     assert binding.moe_grad_norm(t, 2, A, A, BIG, None) == want
     assert binding.moe_grad_clip(t, 2, A, 1.0, 0.0, None) == want
+    assert binding.moe_grad_norm_clip(t, 2, 1.0, 0.0, A, A, BIG, None) == want
 
 
 @pytest.mark.parametrize("over", [dict(out=None), dict(out=A + 2), dict(out_type=3), dict(out_type=0)])
 def test_clipping_refuses_outputs(over):
     assert binding.moe_grad_clip(tensors(**over), 2, A, 1.0, 0.0, None) == INV
+    assert binding.moe_grad_norm_clip(tensors(**over), 2, 1.0, 0.0, A, A, BIG, None) == INV
 
 
 def test_gradient_norm_and_clipping_refuse_the_rest():
     t = tensors()
     assert binding.moe_grad_norm_workspace_size(-1)[0] == INV
     need = binding.moe_grad_norm_workspace_size(2)[1]
-    assert binding.moe_grad_norm_workspace_size(2001)[1] == 3 * need
+    assert binding.moe_grad_norm_workspace_size(3201)[1] == 3 * need
     assert binding.moe_grad_norm(t, -1, A, A, BIG, None) == INV
     assert binding.moe_grad_norm(None, 2, A, A, BIG, None) == INV
     assert binding.moe_grad_norm(t, 2, None, A, BIG, None) == INV
@@ -154,6 +156,10 @@ def test_gradient_norm_and_clipping_refuse_the_rest():
     for norm_, max_norm, eps in ((None, 1.0, 0.0), (A + 2, 1.0, 0.0), (A, -1.0, 0.0), (A, NAN, 0.0), (A, 1.0, -1.0),
                                  (A, 1.0, INF), (A, 1.0, NAN)):
         assert binding.moe_grad_clip(t, 2, norm_, max_norm, eps, None) == INV
+        assert binding.moe_grad_norm_clip(t, 2, max_norm, eps, norm_, A, BIG, None) == INV
+    assert binding.moe_grad_norm_clip(t, 2, 1.0, 0.0, A, None, BIG, None) == INV
+    assert binding.moe_grad_norm_clip(t, 2, 1.0, 0.0, A, A + 8, BIG, None) == INV
+    assert binding.moe_grad_norm_clip(t, 2, 1.0, 0.0, A, A, need - 1, None) == WS
     assert binding.moe_grad_clip(None, 0, A, 1.0, 0.0, None) == OK
     assert binding.moe_grad_clip(tensors(n=0, data=None, out=None), 0, A, 1.0, 0.0, None) == OK
 
