@@ -166,8 +166,10 @@ __global__ void __launch_bounds__(L || V == 8 ? kThreads : kRowThreads)
       for (int v = 0; v < V; ++v) {
         float f[8];
         unpack<TYPE>(now[v], f);
+        float part = 0.0f;  // (sums of 8, then of those: fewer roundings one after the other)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[0] += f[i];
+        for (int i = 0; i < 8; ++i) part += f[i];
+        t[0] += part;
       }
       row_sums<L>(t, buf + 2 * kWarps, 1);
       m = t[0] * inv_h;
@@ -177,12 +179,14 @@ __global__ void __launch_bounds__(L || V == 8 ? kThreads : kRowThreads)
       if (v * lanes + lane >= vecs) continue;
       float f[8];
       unpack<TYPE>(now[v], f);
+      float part[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float d = layer ? f[i] - m : f[i];
-        if (layer) s[0] += d;
-        s[1] = __fmaf_rn(d, d, s[1]);
+        if (layer) part[0] += d;
+        part[1] = __fmaf_rn(d, d, part[1]);
       }
+      s[0] += part[0], s[1] += part[1];
     }
     if (layer) {
       row_sums<L>(s, buf, 0);
@@ -332,17 +336,20 @@ __global__ void __launch_bounds__(MAX, L ? (V == 1 ? (LAYER ? 3 : 4) : 2) : 1)
         unpack<TYPE>(data[0].x[v], x);
         unpack<TYPE>(data[0].d[v], d);
         if constexpr (!kHold) load_weight8<TYPE>(a.weight, a.weight_type, (v * lanes + lane) * 8, 1.0f, w[0]);
+        float part[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           n[v][i] = (LAYER ? x[i] - m : x[i]) * r;
           e[v][i] = d[i] * w[kHold ? v : 0][i];
-          c[0] = __fmaf_rn(e[v][i], n[v][i], c[0]);
+          part[0] = __fmaf_rn(e[v][i], n[v][i], part[0]);
           dw[v][i] = __fmaf_rn(d[i], n[v][i], dw[v][i]);
           if (LAYER) {
-            c[1] += e[v][i];
+            part[1] += e[v][i];
             db[LAYER ? v : 0][i] += d[i];
           }
         }
+        c[0] += part[0];
+        if (LAYER) c[1] += part[1];
       }
     }
     // the next row's loads, whose place has just become free, before the sums are joined
