@@ -20,8 +20,8 @@
 // prefetch each of x and dy; 16384 rows of 4096, bf16: 79 -> 69 us).
 //
 // Measured (bf16, inputs not in the L2; of the measured copy rate): forward, rms 16384 x 4096 45 us (0.88), 4096 x
-// 7168 22 (0.78); gradient, rms 16384 x 4096 69 (0.86), 4096 x 7168 38 (0.67), 163840 x 128 27 (0.68); the layer norm's
-// second sum and its db cost 15 to 45% more.  What is missing is latency: a row's barrier, and 3 us of the second kernel.
+// 7168 22 (0.78); gradient, rms 16384 x 4096 69 (0.86), 4096 x 7168 38 (0.67), 163840 x 128 27 (0.68), layer 16384 x 4096
+// 88 (0.67), 6141 x 1408 23 (0.33).  What is missing is latency: a row's barrier, and 5 us of the second kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -287,9 +287,9 @@ struct RowData {
   }
 };
 
-// MAX: threads of a CTA at most.  AHEAD: rows beyond the next one that are on their way.
-template <int TYPE, bool LAYER, int L, int V, int MAX, int AHEAD>
-__global__ void __launch_bounds__(MAX, L ? (V == 1 ? (LAYER ? 3 : 4) : 2) : 1)
+// MAX: threads of a CTA at most, MIN: CTAs of that size that an SM holds at least.
+template <int TYPE, bool LAYER, int L, int V, int MAX, int MIN>
+__global__ void __launch_bounds__(MAX, MIN)
     row_norm_grad_kernel(const __grid_constant__ RowNormArgs a) {
   constexpr int kRows = L ? kThreads / (L ? L : 1) : 1;  // rows of a tile
   __shared__ float buf[2 * kWarps * 2];
@@ -316,9 +316,8 @@ __global__ void __launch_bounds__(MAX, L ? (V == 1 ? (LAYER ? 3 : 4) : 2) : 1)
   }
   const float inv_h = __fdiv_rn(1.0f, static_cast<float>(a.H));
 
-  RowData<TYPE, V> data[AHEAD + 1];
-#pragma unroll
-  for (int k = 0; k <= AHEAD; ++k) data[k].load(a, LAYER, row + k * stride, lane, lanes, vecs);
+  RowData<TYPE, V> data;
+  data.load(a, LAYER, row, lane, lanes, vecs);
   int turn = 0;
   for (; tile < a.rows; tile += stride, row += stride) {
     if (L == 0 && threadIdx.x < 2 && row + 2 * stride < a.rows) {
@@ -327,14 +326,14 @@ __global__ void __launch_bounds__(MAX, L ? (V == 1 ? (LAYER ? 3 : 4) : 2) : 1)
       asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(static_cast<uint32_t>(a.H * static_cast<int>(kSize<TYPE>))) : "memory");
     }
     const bool mine = row < a.rows;
-    const float m = data[0].m, r = data[0].r;
+    const float m = data.m, r = data.r;
     float n[V][8], e[V][8], c[2] = {0.0f, 0.0f};  // c: the sums of e n and e
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (mine && v * lanes + lane < vecs) {
         float x[8], d[8];
-        unpack<TYPE>(data[0].x[v], x);
-        unpack<TYPE>(data[0].d[v], d);
+        unpack<TYPE>(data.x[v], x);
+        unpack<TYPE>(data.d[v], d);
         if constexpr (!kHold) load_weight8<TYPE>(a.weight, a.weight_type, (v * lanes + lane) * 8, 1.0f, w[0]);
         float part[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -353,11 +352,7 @@ __global__ void __launch_bounds__(MAX, L ? (V == 1 ? (LAYER ? 3 : 4) : 2) : 1)
       }
     }
     // the next row's loads, whose place has just become free, before the sums are joined
-    if constexpr (kHold) {
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) data[k] = data[k + 1];
-      data[AHEAD].load(a, LAYER, row + (AHEAD + 1) * stride, lane, lanes, vecs);
-    }
+    if constexpr (kHold) data.load(a, LAYER, row + stride, lane, lanes, vecs);
     if constexpr (LAYER) {
       row_sums<L>(c, buf, turn);
     } else {
@@ -374,8 +369,8 @@ __global__ void __launch_bounds__(MAX, L ? (V == 1 ? (LAYER ? 3 : 4) : 2) : 1)
         float o[8];
         if constexpr (!kHold) {
           float x[8], d[8];
-          unpack<TYPE>(data[0].x[v], x);
-          unpack<TYPE>(data[0].d[v], d);
+          unpack<TYPE>(data.x[v], x);
+          unpack<TYPE>(data.d[v], d);
           load_weight8<TYPE>(a.weight, a.weight_type, (v * lanes + lane) * 8, 1.0f, w[0]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -388,7 +383,7 @@ __global__ void __launch_bounds__(MAX, L ? (V == 1 ? (LAYER ? 3 : 4) : 2) : 1)
         store8<TYPE>(dst + static_cast<size_t>(v * lanes + lane) * 8 * kSize<TYPE>, o);
       }
     }
-    if constexpr (!kHold) data[0].load(a, LAYER, row + stride, lane, lanes, vecs);
+    if constexpr (!kHold) data.load(a, LAYER, row + stride, lane, lanes, vecs);
   }
   if (!a.dweight && !a.dbias) return;
 
@@ -461,11 +456,11 @@ cudaError_t sum_partials(const RowNormArgs& a, int n, cudaStream_t stream) {
   return launch_pdl(row_norm_sum_kernel, dim3((a.H + 31) / 32, 2), dim3(32, kSumRows), 0, stream, a, n);
 }
 
-template <int TYPE, bool LAYER, int L, int V, int MAX, int AHEAD>
+template <int TYPE, bool LAYER, int L, int V, int MAX, int MIN>
 cudaError_t gradient(const RowNormArgs& a, int num_sms, cudaStream_t stream) {
   constexpr int kRows = L ? kThreads / (L ? L : 1) : 1;
   const int threads = L ? kThreads : (a.H / 8 + 32 * V - 1) / (32 * V) * 32;
-  auto kernel = row_norm_grad_kernel<TYPE, LAYER, L, V, MAX, AHEAD>;
+  auto kernel = row_norm_grad_kernel<TYPE, LAYER, L, V, MAX, MIN>;
   static PerDevice config;  // registers a thread
   int regs = 0;
   cudaError_t e = config.get(
@@ -491,13 +486,17 @@ cudaError_t gradient(const RowNormArgs& a, int num_sms, cudaStream_t stream) {
 
 template <int TYPE, bool LAYER>
 cudaError_t gradient_of(const RowNormArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.H <= 64) return gradient<TYPE, LAYER, 8, 1, kThreads, 0>(a, num_sms, stream);
-  if (a.H <= 128) return gradient<TYPE, LAYER, 16, 1, kThreads, 0>(a, num_sms, stream);
-  if (a.H <= 256) return gradient<TYPE, LAYER, 32, 1, kThreads, 0>(a, num_sms, stream);
-  if (a.H <= 512) return gradient<TYPE, LAYER, 32, 2, kThreads, 0>(a, num_sms, stream);
-  if (a.H <= 4096) return gradient<TYPE, LAYER, 0, 2, 256, 0>(a, num_sms, stream);
-  if (a.H <= 8192) return gradient<TYPE, LAYER, 0, 2, 512, 0>(a, num_sms, stream);
-  return gradient<TYPE, LAYER, 0, 4, 512, 0>(a, num_sms, stream);
+  constexpr int kMin = LAYER ? 3 : 4;
+  if (a.H <= 64) return gradient<TYPE, LAYER, 8, 1, kThreads, kMin>(a, num_sms, stream);
+  if (a.H <= 128) return gradient<TYPE, LAYER, 16, 1, kThreads, kMin>(a, num_sms, stream);
+  if (a.H <= 256) return gradient<TYPE, LAYER, 32, 1, kThreads, kMin>(a, num_sms, stream);
+  if (a.H <= 512) return gradient<TYPE, LAYER, 32, 2, kThreads, 2>(a, num_sms, stream);
+  // Registers for two CTAs an SM where a CTA is near 256 threads (layer norm, 16384 rows of 4096, bf16: 102 -> 89 us;
+  // below, they are as many without the limit: 16384 rows of 2048 50 us, 55 with it)
+  if (a.H <= 2048) return gradient<TYPE, LAYER, 0, 2, 256, 1>(a, num_sms, stream);
+  if (a.H <= 4096) return gradient<TYPE, LAYER, 0, 2, 256, 2>(a, num_sms, stream);
+  if (a.H <= 8192) return gradient<TYPE, LAYER, 0, 2, 512, 1>(a, num_sms, stream);
+  return gradient<TYPE, LAYER, 0, 4, 512, 1>(a, num_sms, stream);
 }
 
 template <int TYPE>
