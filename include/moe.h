@@ -769,7 +769,8 @@ MOE_API moe_status moe_norm_grad(const moe_norm_shape* shape, const void* dy, in
  *   norm   fp32, device: written by moe_grad_norm and moe_grad_norm_clip, read by
  *          moe_grad_clip (one already known, such as that of these tensors and others)
  *   out    of out_type; may be data itself (with the same type), else apart from
- *          every tensor.  Unused by moe_grad_norm.
+ *          every tensor, and each apart from the others: a tensor given twice would
+ *          be clipped twice, or in part.  Unused by moe_grad_norm.
  * Where the norm is a NaN or infinite, nothing is clipped (the factor is 1).  A
  * factor of 1 leaves a tensor in place untouched.  max_norm >= 0 (infinity: never
  * clip), eps >= 0 and finite.  No tensors: the norm is 0.

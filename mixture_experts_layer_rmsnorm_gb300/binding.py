@@ -1177,12 +1177,30 @@ class Gradients(_Buffers):
         for i, (t, o) in enumerate(zip(self.tensors, self.out)):
             _check(f"tensor {i}", t, self.device, t.dtype, t.shape)
             _check(f"out {i}", o, self.device, o.dtype, t.shape)
+        self._apart()
         self._table = grad_tensors([(t.data_ptr(), o.data_ptr(), t.numel(), _type_of(t.dtype), _type_of(o.dtype))
                                     for t, o in zip(self.tensors, self.out)])
         st, n = moe_grad_norm_workspace_size(len(self.tensors))
         if st != MOE_OK:
             raise MoeError(st, "moe_grad_norm_workspace_size")
         self.workspace, self.fp32 = torch.empty(n, dtype=torch.uint8, device=self.device), torch.float32
+
+    def _apart(self):
+        """What is written has to lie apart from everything else: a tensor given twice would be clipped twice."""
+        def span(t):
+            return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+        spans = []
+        for t, o in zip(self.tensors, self.out):
+            if t.numel():
+                spans.append((*span(o), True))
+                if o is not t and o.data_ptr() != t.data_ptr():
+                    spans.append((*span(t), False))
+        end = written = 0  # of all spans so far, and of those that are written
+        for a, b, out in sorted(spans):
+            if a < (end if out else written):
+                raise ValueError("two tensors overlap (or one is given twice), and one of them is written")
+            end, written = max(end, b), max(written, b) if out else written
 
     def _buffers(self):
         # one tensor of each allocation stands for it

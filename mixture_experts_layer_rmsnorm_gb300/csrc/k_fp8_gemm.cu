@@ -366,8 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------ many rows: CTA pairs
-
 // ------------------------------------------------------------------ more rows: single CTAs and CTA pairs
 
 template <bool PAIR>

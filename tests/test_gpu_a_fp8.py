@@ -113,6 +113,37 @@ def test_matrices_to_8_bits_and_back(g, n, k, dtype):
     assert torch.equal(w8.dequantize(FP32).double(), (values.float()).double())
 
 
+def test_quotients_next_to_every_border():
+    """Codes are decided by x / s rounded to fp32, which the kernel works out from one reciprocal.  Divisors whose
+    significand is all ones (which the method's theorem excepts), next to a power of two, and others; dividends at up to four
+    steps of fp32 from every border between two codes, and at the borders."""
+    gen = torch.Generator().manual_seed(5)
+    ones = [(2 - 2.0 ** -23) * 2.0 ** e for e in (-60, -9, 0, 3, 50)]
+    others = [1.0, 1 + 2.0 ** -23, 1 - 2.0 ** -24, 4 / 3, *(1 + torch.rand(150, generator=gen)).tolist()]
+    table = e4m3_table().cpu()
+    mids = (table[1:] + table[:-1]) / 2
+    rows = []
+    for s in ones + others:
+        s = torch.tensor(s, dtype=torch.float32)
+        for k in range(-2, 3):  # the largest magnitude that gives this scale
+            top = (448 * s.double()).float()
+            top = (top.view(torch.int32) + k).view(torch.float32)
+            if (top.double() / 448).float() == s:
+                break
+        else:
+            continue
+        near = (mids * s.double()).float()
+        for k in range(-4, 5):
+            row = (near.view(torch.int32) + k).view(torch.float32)
+            rows.append(torch.cat([top[None], torch.where(torch.arange(126) % 2 == 1, -row, row), torch.zeros(1)]))
+    x = torch.stack(rows).cuda()
+    assert x.shape[0] > 9 * 100
+    codes, scales, _ = define(x, 1)
+    r8 = binding.Fp8Rows(128, max_rows=x.shape[0]).quantize(x)
+    assert same_bits(r8.scales[:x.shape[0], :1].contiguous(), scales)
+    assert torch.equal(r8.codes[:x.numel()].view(x.shape), codes)
+
+
 def test_extreme_blocks():
     """Blocks of zeros, of subnormal numbers, near the largest, with a NaN or an infinity."""
     x = torch.zeros((6, 384), device="cuda")
@@ -315,3 +346,41 @@ def test_objects_refuse_what_does_not_fit():
         w8.forward(x8, dtype=FP32)
     y = w8.forward(binding.Fp8Rows(64).quantize(torch.ones((0, 64), device="cuda")))
     assert y.shape == (0, 32) and w8.device_status()[0] == binding.MOE_OK
+
+
+def test_rows_and_weights_behind_2_to_the_32_elements():
+    """Sources, codes, weights and results whose offsets pass 32 bits: the last rows, and the last group's product."""
+    rows, k, n = 2 ** 19 + 40, 8208, 144
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.zeros((rows, k), dtype=BF16, device="cuda")
+    x[-70:] = torch.randn((70, k), generator=gen, device="cuda").to(BF16)
+    r8 = binding.Fp8Rows(k, rows).quantize(x)
+    codes, scales, values = define(x[-70:], 1)
+    assert torch.equal(r8.codes[:rows * k].view(rows, k)[-70:], codes)
+    assert same_bits(r8.scales[rows - 70:rows, :scales.shape[1]].contiguous(), scales)
+    out = torch.full((rows, 8216), 7.0, dtype=BF16, device="cuda")
+    r8.dequantize(out[:, :k])
+    assert ((out[-70:, :k].double() - values).abs() <= values.abs() * (2.0 ** -8 * (1 + 2.0 ** -24) + 2.0 ** -24)).all()
+    assert torch.all(out[0, :k] == 0.0) and torch.all(out[-70:, k:] == 7.0)
+    w = (torch.randn((1, n, k), generator=gen, device="cuda") * 0.02).to(BF16)
+    w8 = binding.Fp8Weights.quantize(w)
+    wv = define(w, 128)[2][0]
+    y = w8.forward(r8, y=out[:, -n:])
+    check(y[-70:], values, wv.T, k)
+    assert torch.all(y[:-70] == 0.0)
+    del x, r8, out, y
+    groups, n, k = 65, 8192, 8192
+    w = torch.zeros((groups, n, k), dtype=BF16, device="cuda")
+    w[-1] = (torch.randn((n, k), generator=gen, device="cuda") * 0.02).to(BF16)
+    w8 = binding.Fp8Weights.quantize(w)
+    wv = define(w[-1:], 128)[2][0]
+    assert torch.all(w8.codes[-2] == 0)
+    for count in (3, 40, 300):
+        x = torch.randn((count, k), generator=gen, device="cuda").to(BF16)
+        off = torch.tensor([0] * groups + [count], dtype=torch.int32, device="cuda")
+        y = w8.forward(binding.Fp8Rows(k, count).quantize(x), off)
+        xv = define(x, 1)[2]
+        check(y, xv, wv.T, k)
+        check(w8.dgrad(binding.Fp8Rows(n, count).quantize(x), off), xv, wv, n)
+    back = w8.dequantize(BF16)
+    assert torch.all(back[:-1] == 0.0) and torch.equal(back[-1], wv.float().to(BF16))

@@ -168,6 +168,13 @@ def test_objects_refuse_what_does_not_fit():
         binding.Gradients([torch.ones((4, 4), device="cuda").t()])
     with pytest.raises(ValueError):
         binding.Gradients([t, t.cpu()])
+    pair, half = torch.ones(16, device="cuda"), torch.ones(16, dtype=BF16, device="cuda")
+    for tensors, out in (([t, t], None), ([pair[:9], pair[8:]], None), ([pair[:8], pair[8:]], [pair[8:], pair[:8]]),
+                         ([pair[:4], pair[4:8]], [pair[8:12], pair[10:14]]), ([half[:8]], [half[4:12]])):
+        with pytest.raises(ValueError):
+            binding.Gradients(tensors, out)
+    binding.Gradients([pair[:8], pair[8:]]).clip(1.0)  # side by side
+    binding.Gradients([pair, pair], [t.new_empty(16), t.new_empty(16)]).clip(1.0)  # read twice, written apart
     for max_norm, eps in ((-1.0, 0.0), (NAN, 0.0), (1.0, -1e-6), (1.0, INF)):
         with pytest.raises(binding.MoeError):
             binding.Gradients([t]).clip(max_norm, eps)
