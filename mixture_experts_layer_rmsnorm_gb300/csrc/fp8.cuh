@@ -2,8 +2,7 @@
 // or of 128 x 128) and their grouped products (internal).
 //
 //   rows      codes [rows, K], scales [rows][lds]: block b of row p at p * lds + b,
-//             lds a multiple of 4, so that the products' epilogue, a lane a row,
-//             reads four blocks at once
+//             lds a multiple of 4, since the quantizer writes four at once
 //   matrices  codes [G, N, K], scales [G][ceil(N / 128)][ceil(K / 128)]
 #pragma once
 

@@ -313,7 +313,7 @@ moe_status check_fp8(const moe_fp8_shape* s) {
   return MOE_OK;
 }
 
-// Scales of rows: four blocks are read at once.
+// Scales of rows: four blocks are written at once.
 moe_status check_lds(int64_t lds, int64_t K) {
   if (lds < (K + 127) / 128) return MOE_ERR_INVALID_ARG;
   return lds % 4 != 0 || lds > kMaxLd ? MOE_ERR_UNSUPPORTED : MOE_OK;
