@@ -72,6 +72,8 @@ CASES = {
     "cta": ("rms", 700, 1032, BF16, FP32, 8),
     "cta_layer": ("layer", 333, 1408, FP16, FP16),
     "cta_4096": ("rms", 2050, 4096, BF16, BF16),
+    "cta_layer_2056": ("layer", 130, 2056, FP32, FP32, 8),
+    "cta_layer_4096": ("layer", 611, 4096, BF16, FP32),
     "cta_7168": ("layer", 401, 7168, BF16, FP32),
     "cta_8192_fp32": ("rms", 161, 8192, FP32, FP32),
     "cta_wide": ("layer", 323, 8200, FP16, FP16, 16),

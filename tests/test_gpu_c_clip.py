@@ -123,7 +123,35 @@ def test_a_norm_of_these_and_others():
     check_clipped(kept, g, 500.0, 5.0)
 
 
-@pytest.mark.parametrize("sizes", [[7], [100000, 33, 5], [777] * 1500])
+@pytest.mark.parametrize("n", [1, 20, 1300, 3500])
+def test_calls_follow_one_another_without_a_pause(n):
+    """Each call reads what the one before wrote, in place; a call of many tensors is several launches, whose later ones
+    begin beside the first."""
+    sizes = [1 + (i * 7919) % 20000 for i in range(n)]
+    flat = torch.randn(sum(sizes), generator=torch.Generator(device="cuda").manual_seed(n), device="cuda")
+    start, src = flat.clone(), flat * 3
+
+    def run(pause):
+        flat.copy_(src)
+        flat.mul_(1 / 3)
+        grads = binding.Gradients(list(flat.split(sizes)))
+        norms = []
+        for k in range(8):
+            norms.append(grads.clip(first * 0.7 ** (k + 1)) if k % 2 else grads.clip(first * 0.7 ** (k + 1), norm=grads.norm()))
+            if pause:
+                torch.cuda.synchronize()
+        return torch.stack(norms), flat.clone()
+
+    first = norm_of([start])
+    norms, out = run(False)
+    paused, same = run(True)
+    assert torch.equal(norms, paused) and torch.equal(out, same)
+    for k, norm in enumerate(norms.tolist()):  # each clipping leaves 36 u, and the source's two roundings
+        want = first * 0.7 ** k
+        assert abs(norm - want) <= (36 * k + 33 + 4) * U * want + EPS * k
+
+
+@pytest.mark.parametrize("sizes", [[7], [100000, 33, 5], [777] * 1500, [33] * 3500])
 def test_replays_from_a_graph_on_new_gradients(sizes):
     g = make(sizes, [FP32] * len(sizes))
     out = [torch.empty_like(t) for t in g]
