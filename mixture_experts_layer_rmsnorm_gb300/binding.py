@@ -1024,7 +1024,7 @@ class Fp8Weights(_Workspace):
     def __init__(self, codes, scales):
         import torch
         self.groups, self.N, self.K = codes.shape
-        self.device, self.int32 = codes.device, torch.int32
+        self.device, self.int32, self.bf16 = codes.device, torch.int32, torch.bfloat16
         _check("codes", codes, self.device, torch.uint8, codes.shape)
         _check("scales", scales, self.device, torch.float32, (self.groups, -(-self.N // 128), -(-self.K // 128)))
         self.codes, self.scales, self._shape = codes, scales, None
@@ -1067,8 +1067,7 @@ class Fp8Weights(_Workspace):
         if rows.K != K or rows.device != self.device:
             raise ValueError(f"rows of {rows.K} elements on {rows.device}, {K} on {self.device} wanted")
         if out is None:
-            import torch
-            out = torch.empty((rows.rows, N), dtype=dtype or torch.bfloat16, device=self.device)
+            out = _empty((rows.rows, N), dtype or self.bf16, self.device)
         op, ldo = _matrix("the output", out, self.device, dtype or out.dtype, (rows.rows, N))
         self._call(name, self.shape(rows.rows, _type_of(out.dtype)), rows.codes.data_ptr(), rows.scales.data_ptr(),
                    rows.lds, self.codes.data_ptr(), self.scales.data_ptr(), *_lists(self, offsets, counts), op, ldo,
