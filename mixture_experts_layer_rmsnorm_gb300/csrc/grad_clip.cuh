@@ -16,10 +16,12 @@ struct GradTensor {
 };
 
 // Tensors go to the kernels as parameters, so that a call is complete in itself (captured, replayed, several at
-// once): as many of them as fit 32,764 bytes a launch, or kGradFew where that is all, which takes less time to launch.
+// once): as many of them as fit 32,764 bytes a launch, or kGradFew where that is all, since many bytes of parameters
+// cost host time (norm and clipping in place, us on the host without / with kGradFew: 33 tensors 14.8 / 11.6, 300 18.7 /
+// 14.5; but a still smaller table, of 32 tensors, costs more: 3 tensors 12.3 to 14.1 instead of 9.7 to 12.0).
 constexpr int kGradTensors = 1600;  // of the norm, and clipped in place
 constexpr int kGradApart = 1150;    // clipped into other tensors
-constexpr int kGradFew = 32;
+constexpr int kGradFew = 300;
 constexpr int kGradCtas = 640;       // of a launch, at most: a partial sum each
 constexpr int64_t kGradChunk = 16384;  // elements
 

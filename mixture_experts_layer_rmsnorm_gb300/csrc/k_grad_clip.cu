@@ -452,7 +452,7 @@ cudaError_t clip(const GradTensor* t, int64_t n, float* norm, double* partials, 
 cudaError_t launch_grad_norm(const GradTensor* t, int64_t n, float* norm, double* partials, int num_sms,
                              cudaStream_t stream) {
   return n <= kGradFew ? norm_of<kGradFew>(t, n, norm, partials, num_sms, stream)
-                       : norm_of<kGradTensors>(t, n, norm, partials, num_sms, stream);
+                          : norm_of<kGradTensors>(t, n, norm, partials, num_sms, stream);
 }
 
 cudaError_t launch_grad_clip(const GradTensor* t, int64_t n, float* norm, double* partials, double max_norm, double eps,

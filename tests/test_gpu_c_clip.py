@@ -41,6 +41,8 @@ SETS = {
     "a_chunk_and_a_number": ([16385, 0, 3], [FP32, FP32, FP16]),
     "few": ([5, 70000, 1, 16383, 8, 200001], [BF16, FP16, FP32, FP32, BF16, BF16]),
     "thirty_three": ([i * i * 37 for i in range(33)], [(BF16, FP16, FP32)[i % 3] for i in range(33)]),
+    "a_small_table": ([1 + (i * 131) % 700 for i in range(300)], [(BF16, FP32)[i % 2] for i in range(300)]),
+    "one_more": ([1 + (i * 131) % 700 for i in range(301)], [(FP32, FP16)[i % 2] for i in range(301)]),
     "more_than_a_launch": ([1 + (i * 7919) % 3000 for i in range(2001)], [(FP32, BF16)[i % 2] for i in range(2001)]),
     "large": ([30000000, 1, 20000003], [FP32, BF16, BF16]),
 }
