@@ -1054,6 +1054,15 @@ class Fp8Weights(_Workspace):
                  _type_of(w.dtype), _ptr(w), -(-K // 8) * 8, _ptr(codes), _ptr(scales), 0)
         return cls(codes, scales)
 
+    def update(self, w):
+        """The weights anew, from w of the same sizes, in the same buffers (so that captured graphs read the new ones);
+        returns self."""
+        _check("w", w, self.device, w.dtype, (self.groups, self.N, self.K))
+        _enqueue("moe_fp8_quantize", self.device,
+                 ctypes.byref(fp8_shape(MOE_SCALE_PER_BLOCK, self.groups, self.groups * self.N, self.K)),
+                 _type_of(w.dtype), w.data_ptr(), self.K, self.codes.data_ptr(), self.scales.data_ptr(), 0, of=(self,))
+        return self
+
     def dequantize(self, dtype=None):
         """The values the weights stand for, [groups, N, K] in ``dtype`` (bf16 by default)."""
         import torch

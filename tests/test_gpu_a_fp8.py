@@ -318,6 +318,34 @@ def test_calls_repeat_bit_for_bit_and_replay_from_a_graph_on_new_rows_and_lists(
     assert not torch.equal(y, first[0])
 
 
+def test_updated_weights_in_their_buffers():
+    """An optimizer's step between two replays: the graph's product reads the new weights."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    w = torch.randn((3, 144, 272), generator=gen, device="cuda")
+    w8, r8 = binding.Fp8Weights.quantize(w), binding.Fp8Rows(272, 40)
+    x, off = torch.randn((40, 272), generator=gen, device="cuda").to(BF16), torch.tensor([0, 9, 9, 40], dtype=torch.int32, device="cuda")
+    y = w8.forward(r8.quantize(x), off)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        w8.update(w)
+        w8.forward(r8.quantize(x), off, y=y)
+    w.mul_(-1.5).add_(0.01)
+    graph.replay()
+    fresh = binding.Fp8Weights.quantize(w)
+    assert torch.equal(y, fresh.forward(r8, off))
+    w.add_(0.25)
+    kept = w8.codes.data_ptr()
+    assert w8.update(w.to(BF16)) is w8 and w8.codes.data_ptr() == kept
+    codes, scales, _ = define(w.to(BF16), 128)
+    assert torch.equal(w8.codes, codes) and same_bits(w8.scales, scales)
+    with pytest.raises(ValueError):
+        w8.update(w[:2])
+    with pytest.raises(ValueError):
+        w8.update(w.transpose(1, 2).contiguous().transpose(1, 2))
+
+
 def test_more_rows_get_larger_buffers_and_a_refused_call_keeps_them():
     r8 = binding.Fp8Rows(64, max_rows=4)
     x = torch.randn((9, 64), device="cuda")
