@@ -656,8 +656,8 @@ MOE_API moe_status moe_fp4_gemm(const moe_grouped_shape* shape, int32_t format, 
  * each division one fp32 operation, codes to nearest with ties to the even one;
  * a block that holds a NaN or an infinity gets a NaN scale (what it stands for is
  * NaN).  The products sum each block's codes on the tensor core (kind::f8f6f4)
- * and add sx sw times that sum in fp32, so the scales may be any numbers.  (sx sw is
- * one fp32 operation: where it lies below 2^-126 it loses bits.)
+ * and add sx sw times that sum in fp32, so the scales may be any numbers: where sx sw
+ * is no normal fp32 number, the sum is multiplied by the larger scale, then by the smaller.
  *   codes   [rows, K] bytes
  *   scales  MOE_SCALE_PER_ROW: [rows][lds] fp32, block b of row p at p * lds + b
  *           (lds >= ceil(K / 128), a multiple of 4; what lies between them is unspecified);

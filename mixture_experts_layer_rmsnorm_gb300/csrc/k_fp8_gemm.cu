@@ -7,7 +7,8 @@
 // Only D_b is the tensor core's (kind::f8f6f4, fp32 in TMEM, K = 32 an MMA); the
 // scales are no powers of two, so D_b leaves TMEM block by block and is summed in
 // registers, one fp32 multiply-add per element and block.  That sum rounds to nearest;
-// the tensor core's own cuts towards zero stay inside a block of 128.
+// the tensor core's own cuts towards zero stay inside a block of 128.  Scales whose product
+// is no normal fp32 number meet the block's sum one after the other (one_factor).
 //
 // Units and work split as in k_grouped_gemm.cu and k_grouped_pair.cu; the input gradient
 // reads the stored matrix as an MN-major operand.  A K-block is one block of scales, 128
@@ -77,6 +78,28 @@ __device__ __forceinline__ uint16_t to16(float v, bool fp16) {
   return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// A block's sum times sx sw.  Where the product of the scales is a normal fp32 number (or a NaN), that is one factor.
+// Elsewhere the sum meets the larger scale, then the smaller one: it is 0 or lies in [2^-18, 2^25), so if it overflows with the
+// larger scale the result does too (beyond fp32's largest product the smaller scale is above 1), and if it falls below the normal
+// range with it the result vanishes (the scales are then below 2^-108).
+__device__ __forceinline__ bool one_factor(float product) {
+  const float m = fabsf(product);
+  return !(m < 0x1p-126f || m > 0x1.fffffep127f);
+}
+// The first factor and s, the second, from two scales; 1 and their product where one factor does.
+__device__ __forceinline__ void two_factors(float& s, float& first) {
+  const float product = __fmul_rn(s, first), a = s, b = first;
+  const bool one = one_factor(product), a_larger = fabsf(a) > fabsf(b);
+  first = one ? 1.0f : a_larger ? a : b;
+  s = one ? product : a_larger ? b : a;
+}
+
+__device__ __forceinline__ uint64_t twice(float v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
+}
+
 // The scales of a unit's features (one block of 128) along the reduction.
 template <bool DGRAD>
 __device__ __forceinline__ const float* feature_scales(const Fp8GemmArgs& a, int g, int feat) {
@@ -96,7 +119,7 @@ constexpr int kThreads = 192;
 constexpr uint32_t kTmemCols = kAccs * kUnitRows;
 constexpr int kBarBytes = 256;
 constexpr int kTabBytes = 3 * (kGroupsSmem[0] + 1) * 4;
-constexpr int kScaleBytes = 4 * 2 * kUnitRows * 4;  // per epilogue warp, two blocks
+constexpr int kScaleBytes = 4 * 2 * 2 * kUnitRows * 4;  // per epilogue warp, two blocks, two factors
 constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kBarBytes + kScaleBytes + kTabBytes;
 static_assert((2 * kStages + 2 * kAccs + 1) * 8 + 8 <= kBarBytes, "barrier area");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
@@ -253,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     const int row = q * 32 + lane;  // this thread's TMEM lane = feature of the unit's 128
     const bool fp16 = a.fp16 != 0;
-    float* s_buf = scales + (warp - 2) * 2 * kUnitRows;
+    float* s_buf = scales + (warp - 2) * 4 * kUnitRows;
     const int64_t w_step = DGRAD ? args.w_cols : 1;
     int acc = 0, where = 0;
     uint32_t acc_phase = 0;
@@ -276,8 +299,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < kUnitRows; ++c) sum[c] = 0.0f;
       for (int kb = kb0; kb < kb1; ++kb) {
-        float* s = s_buf + (kb & 1) * kUnitRows;  // (the other one may still be read by slower lanes)
-        s[lane] = __fmul_rn(next[0], next_w[0]);
+        float* s = s_buf + (kb & 1) * 2 * kUnitRows;  // (the other one may still be read by slower lanes)
+        const float product = __fmul_rn(next[0], next_w[0]);
+        s[lane] = product;
+        const bool two = __any_sync(0xFFFFFFFFu, valid && !one_factor(product));
+        if (two) {  // (rare: some row's scales; the other rows' first factor is 1)
+          float second = next[0], first = next_w[0];
+          two_factors(second, first);
+          s[lane] = second;
+          s[kUnitRows + lane] = first;
+        }
 #pragma unroll
         for (int k = 0; k + 1 < kAhead; ++k) {
           next[k] = next[k + 1];
@@ -299,6 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t r[16];
           tmem_ld_32x32b_x16(t_row + c0, r);
           tmem_ld_wait();
+          if (two) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              r[j] = __float_as_uint(__fmul_rn(__uint_as_float(r[j]), s[kUnitRows + c0 + j]));
+          }
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float4 v = *reinterpret_cast<const float4*>(s + c0 + j);
@@ -679,8 +715,8 @@ __global__ void __launch_bounds__(Large<PAIR>::kThreads, 1)
       for (int i = 0; i < 64; ++i) sum[i] = 0;
       for (int kb = 0; kb < kblocks; ++kb) {
         const float s = __fmul_rn(next_x, next_w);
-        uint64_t s2;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+        const bool two = __any_sync(0xFFFFFFFFu, !one_factor(s));
+        uint64_t s2 = twice(s);
         if (kb + 1 < kblocks) {  // the next block's, while this one's MMAs run
           next_w = __ldg(sw + (kb + 1) * w_step);
           next_x = __ldg(sx + kb + 1);
@@ -694,6 +730,21 @@ __global__ void __launch_bounds__(Large<PAIR>::kThreads, 1)
         tc_fence_after();
         __syncwarp();
         const uint32_t t = t_base + static_cast<uint32_t>(acc * C::kFeatures);
+        if (two) {  // (rare) the sums meet their first factor in TMEM, 16 at a time: registers for it here would spill
+          float second = __ldg(sx + kb), first = __ldg(sw + kb * w_step);
+          two_factors(second, first);
+          s2 = twice(second);
+#pragma unroll 1
+          for (uint32_t c = 0; c < 128; c += 16) {
+            uint32_t d[16];
+            tmem_ld_32x32b_x16(t + c, d);
+            tmem_ld_wait(d);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) d[i] = __float_as_uint(__fmul_rn(__uint_as_float(d[i]), first));
+            tmem_st_32x32b(t + c, d);
+          }
+          tmem_st_wait();
+        }
         uint32_t r[2][16];
         tmem_ld_32x32b_x16(t, r[0]);
 #pragma unroll
