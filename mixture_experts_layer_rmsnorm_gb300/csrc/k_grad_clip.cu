@@ -286,8 +286,29 @@ __global__ void __launch_bounds__(32) grad_norm_kernel(const double* partials, i
 
 // ------------------------------------------------------------------ clipping
 
+// The factor f < 1 in two: below fp32's normal numbers, where f would lose bits (all below 2^-149, although f times a large
+// element is an ordinary number), it is `first`, 1 at most, times a power of two.
+struct Factor {
+  float first, last;
+
+  __device__ explicit Factor(double f) : first(1.0f), last(1.0f) {
+    if (!(f < 1.0)) return;
+    if (f >= 0x1p-126 || f == 0.0) {
+      first = static_cast<float>(f);
+      return;
+    }
+    int e;
+    const double m = frexp(f, &e);  // m in [0.5, 1)
+    const int last_e = e > -149 ? e : -149;
+    first = static_cast<float>(ldexp(m, e - last_e));
+    last = static_cast<float>(ldexp(1.0, last_e));
+  }
+  __device__ Factor(float first_, float last_) : first(first_), last(last_) {}
+  __device__ __forceinline__ float times(float x) const { return __fmul_rn(__fmul_rn(x, first), last); }
+};
+
 template <int TYPE, bool WHOLE>
-__device__ __forceinline__ void clip_vectors(const void* src, void* dst, int dst_type, int n, float factor) {
+__device__ __forceinline__ void clip_vectors(const void* src, void* dst, int dst_type, int n, Factor factor) {
 #pragma unroll 1
   for (int b = 0; b < kVecs<TYPE>; b += kLoads) {
     if (!WHOLE && b * kThreads * kWidth<TYPE> >= n) break;
@@ -299,14 +320,14 @@ __device__ __forceinline__ void clip_vectors(const void* src, void* dst, int dst
       float f[kWidth<TYPE>];
       values<TYPE>(raw[i], f);
 #pragma unroll
-      for (int j = 0; j < kWidth<TYPE>; ++j) f[j] = __fmul_rn(f[j], factor);
+      for (int j = 0; j < kWidth<TYPE>; ++j) f[j] = factor.times(f[j]);
       if (WHOLE || at + kWidth<TYPE> <= n) put(dst, dst_type, at, f);
     }
   }
 }
 
 template <int TYPE>
-__device__ __forceinline__ void clip_chunk(const GradTensor& t, int64_t from, float factor) {
+__device__ __forceinline__ void clip_chunk(const GradTensor& t, int64_t from, Factor factor) {
   const void* src = static_cast<const char*>(t.src) + from * (TYPE == 2 ? 4 : 2);
   void* dst = static_cast<char*>(t.dst) + from * (t.dst_type == 2 ? 4 : 2);
   const int n = static_cast<int>(min(t.n - from, kGradChunk));
@@ -316,7 +337,7 @@ __device__ __forceinline__ void clip_chunk(const GradTensor& t, int64_t from, fl
   } else if (vec) {
     clip_vectors<TYPE, false>(src, dst, t.dst_type, n, factor);
     const int at = n / kWidth<TYPE> * kWidth<TYPE> + threadIdx.x;
-    if (at < n) put_at(dst, t.dst_type, at, __fmul_rn(value_at<TYPE>(src, at), factor));
+    if (at < n) put_at(dst, t.dst_type, at, factor.times(value_at<TYPE>(src, at)));
   } else {
 #pragma unroll 1
     for (int at = threadIdx.x; at < n; at += 8 * kThreads) {
@@ -325,7 +346,7 @@ __device__ __forceinline__ void clip_chunk(const GradTensor& t, int64_t from, fl
       for (int j = 0; j < 8; ++j) f[j] = at + j * kThreads < n ? value_at<TYPE>(src, at + j * kThreads) : 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (at + j * kThreads < n) put_at(dst, t.dst_type, at + j * kThreads, __fmul_rn(f[j], factor));
+        if (at + j * kThreads < n) put_at(dst, t.dst_type, at + j * kThreads, factor.times(f[j]));
     }
   }
 }
@@ -339,27 +360,25 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     pdl_wait();
     pdl_launch_dependents();
   }
-  __shared__ float clipping;
+  __shared__ float clipping[2];
   if (threadIdx.x < 32) {
     const float total = sums > 0 ? norm_of_sums(partials, sums) : __ldcg(norm);
     if (threadIdx.x == 0) {
       if (sums > 0 && first && blockIdx.x == 0) *norm = total;
-      float f = 1.0f;
-      if (total < __int_as_float(0x7F800000)) {  // (a norm that is no number clips nothing)
-        const double exact = max_norm / (static_cast<double>(total) + eps);
-        if (exact < 1.0) f = static_cast<float>(exact);
-      }
-      clipping = f;
+      // (a norm that is no number clips nothing)
+      const Factor f(total < __int_as_float(0x7F800000) ? max_norm / (static_cast<double>(total) + eps) : 1.0);
+      clipping[0] = f.first, clipping[1] = f.last;
     }
   }
   __syncthreads();
-  const float factor = clipping;
-  const bool nothing = factor == 1.0f && table.in_place;
+  const Factor factor(clipping[0], clipping[1]);
+  const bool one = factor.first == 1.0f && factor.last == 1.0f;
+  const bool nothing = one && table.in_place;
   for (int i = nothing ? table.chunks : blockIdx.x; i < table.chunks; i += gridDim.x) {
     const int c = table.chunks - 1 - i;
     const int at = tensor_of(table, c);
     const GradTensor t = table.get(at);
-    if (factor == 1.0f && t.dst == t.src) continue;
+    if (one && t.dst == t.src) continue;
     const int64_t from = static_cast<int64_t>(c - table.first[at]) * kGradChunk;
     if (t.type == 2)
       clip_chunk<2>(t, from, factor);
