@@ -771,7 +771,10 @@ MOE_API moe_status moe_norm_grad(const moe_norm_shape* shape, const void* dy, in
  *   out    of out_type; may be data itself (with the same type), else apart from
  *          every tensor, and each apart from the others: a tensor given twice would
  *          be clipped twice, or in part.  Unused by moe_grad_norm.
- * Where the norm is a NaN or infinite, nothing is clipped (the factor is 1).  A
+ * Where an element is a NaN or infinite, nothing is clipped (the factor is 1).  Finite
+ * elements whose norm passes fp32's range (`norm` is infinity) are clipped by its fp64
+ * value in moe_grad_norm_clip; moe_grad_clip, which reads the fp32 number, clips
+ * nothing by an infinite or NaN one.  A
  * factor of 1 leaves a tensor in place untouched.  max_norm >= 0 (infinity: never
  * clip), eps >= 0 and finite.  No tensors: the norm is 0.
  *   workspace  moe_grad_norm_workspace_size() bytes for as many tensors, 256-byte aligned,

@@ -1223,7 +1223,8 @@ class Gradients(_Buffers):
 
     def clip(self, max_norm, eps=1e-6, norm=None):
         """out = tensor * min(1, max_norm / (norm + eps)); returns the norm (before clipping).  norm: one already known,
-        such as that of these gradients and others."""
+        such as that of these gradients and others.  An element that is a NaN or infinite leaves all tensors as they are (the
+        norm says so), as does a norm passed that is."""
         if norm is None:
             norm = _empty((), self.fp32, self.device)
             _enqueue("moe_grad_norm_clip", self.device, self._table, len(self.tensors), float(max_norm), float(eps),

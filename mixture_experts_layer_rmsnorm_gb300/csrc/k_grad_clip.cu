@@ -237,13 +237,13 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 // The norm from n partial sums, by one warp, alike in every CTA.
-__device__ __forceinline__ float norm_of_sums(const double* partials, int n) {
+__device__ __forceinline__ double norm_of_sums(const double* partials, int n) {
   double sum = 0.0;
 #pragma unroll 8
   for (int i = threadIdx.x; i < n; i += 32) sum += __ldcg(partials + i);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  return static_cast<float>(sqrt(sum));
+  return sqrt(sum);
 }
 
 // norm: written where this CTA is the only one
@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 __global__ void __launch_bounds__(32) grad_norm_kernel(const double* partials, int n, float* norm) {
   pdl_wait();
   pdl_launch_dependents();
-  const float total = norm_of_sums(partials, n);
-  if (threadIdx.x == 0) *norm = total;
+  const double total = norm_of_sums(partials, n);
+  if (threadIdx.x == 0) *norm = static_cast<float>(total);
 }
 
 // ------------------------------------------------------------------ clipping
@@ -362,11 +362,14 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   }
   __shared__ float clipping[2];
   if (threadIdx.x < 32) {
-    const float total = sums > 0 ? norm_of_sums(partials, sums) : __ldcg(norm);
+    const double root = sums > 0 ? norm_of_sums(partials, sums) : __ldcg(norm);
     if (threadIdx.x == 0) {
+      const float total = static_cast<float>(root);
       if (sums > 0 && first && blockIdx.x == 0) *norm = total;
-      // (a norm that is no number clips nothing)
-      const Factor f(total < __int_as_float(0x7F800000) ? max_norm / (static_cast<double>(total) + eps) : 1.0);
+      // The norm as the caller gets it, or, where finite elements have one beyond fp32, in 64 bits.  (One that is no number clips
+      // nothing: an infinite or NaN gradient is for the caller to see in the norm, before or after.)
+      const double by = total < __int_as_float(0x7F800000) ? total : root;
+      const Factor f(by < __longlong_as_double(0x7FF0000000000000ll) ? max_norm / (by + eps) : 1.0);
       clipping[0] = f.first, clipping[1] = f.last;
     }
   }
