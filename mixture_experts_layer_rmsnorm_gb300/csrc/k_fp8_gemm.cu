@@ -78,15 +78,14 @@ __device__ __forceinline__ uint16_t to16(float v, bool fp16) {
   return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// A block's sum times sx sw.  Where the product of the scales is a normal fp32 number (or a NaN), that is one factor.
-// Elsewhere the sum meets the larger scale, then the smaller one: it is 0 or lies in [2^-18, 2^25), so if it overflows with the
+// A block's sum times sx sw.  Where the product of the scales is a normal fp32 number, that is one factor.  Elsewhere the
+// sum meets the larger scale, then the smaller one: it is 0 or lies in [2^-18, 2^25), so if it overflows with the
 // larger scale the result does too (beyond fp32's largest product the smaller scale is above 1), and if it falls below the normal
 // range with it the result vanishes (the scales are then below 2^-108).
 __device__ __forceinline__ bool one_factor(float product) {
-  const float m = fabsf(product);
-  return !(m < 0x1p-126f || m > 0x1.fffffep127f);
+  return (__float_as_uint(product) << 1) - 0x01000000u < 0xFE000000u;  // (neither the lowest exponent nor the highest)
 }
-// The first factor and s, the second, from two scales; 1 and their product where one factor does.
+// The second factor (s) and the first from two scales; their product and 1 where one factor does.
 __device__ __forceinline__ void two_factors(float& s, float& first) {
   const float product = __fmul_rn(s, first), a = s, b = first;
   const bool one = one_factor(product), a_larger = fabsf(a) > fabsf(b);
@@ -302,39 +301,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* s = s_buf + (kb & 1) * 2 * kUnitRows;  // (the other one may still be read by slower lanes)
         const float product = __fmul_rn(next[0], next_w[0]);
         s[lane] = product;
-        const bool two = __any_sync(0xFFFFFFFFu, valid && !one_factor(product));
-        if (two) {  // (rare: some row's scales; the other rows' first factor is 1)
-          float second = next[0], first = next_w[0];
-          two_factors(second, first);
-          s[lane] = second;
-          s[kUnitRows + lane] = first;
-        }
 #pragma unroll
         for (int k = 0; k + 1 < kAhead; ++k) {
           next[k] = next[k + 1];
           next_w[k] = next_w[k + 1];
         }
         scales_of(kb + kAhead, next[kAhead - 1], next_w[kAhead - 1]);
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kUnitRows);
         // warp-uniform outcome: tcgen05.ld below is executed by all 32 lanes
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_phase, kWaitTimeoutNs, abort_flag))) {
-          ok = false;
-          where = kWaitAccFull;
-          break;
+        const bool got = mbar_wait(&tfull[acc], acc_phase, kWaitTimeoutNs, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, got && (one_factor(product) || !valid))) {
+          if (!__all_sync(0xFFFFFFFFu, got)) {
+            ok = false;
+            where = kWaitAccFull;
+            break;
+          }
+          // (rare) some row's scales are two factors: the sums meet the first one in TMEM
+          tc_fence_after();
+          float first = __ldg(sw + kb * w_step), second = valid ? __ldg(sx + kb) : 0.0f;
+          two_factors(second, first);
+          s[lane] = second;
+          s[kUnitRows + lane] = first;
+          __syncwarp();
+#pragma unroll 1
+          for (int c0 = 0; c0 < un.n; c0 += 16) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(t_row + c0, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              r[j] = __float_as_uint(__fmul_rn(__uint_as_float(r[j]), s[kUnitRows + c0 + j]));
+            tmem_st_32x32b(t_row + c0, r);
+          }
+          tmem_st_wait();
         }
         tc_fence_after();
         __syncwarp();
-        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kUnitRows);
 #pragma unroll
         for (int c0 = 0; c0 < kUnitRows; c0 += 16) {
           if (c0 >= un.n) break;
           uint32_t r[16];
           tmem_ld_32x32b_x16(t_row + c0, r);
           tmem_ld_wait();
-          if (two) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              r[j] = __float_as_uint(__fmul_rn(__uint_as_float(r[j]), s[kUnitRows + c0 + j]));
-          }
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float4 v = *reinterpret_cast<const float4*>(s + c0 + j);
@@ -710,12 +718,14 @@ __global__ void __launch_bounds__(Large<PAIR>::kThreads, 1)
         sx = args.x_scales + (un.tok0 + min(z.from + q * 32 + lane, un.n - 1)) * args.ldxs;
       }
       float next_w = __ldg(sw), next_x = __ldg(sx);
+      // a block's factor, and whether some lane's are two: asked for once the block before is summed (before the wait
+      // for its own MMAs: 64 x 300 rows, N = K = 4096, input gradient 385 -> 401 us)
+      float s = __fmul_rn(next_x, next_w);
+      bool two = __any_sync(0xFFFFFFFFu, !one_factor(s));
       uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
       for (int kb = 0; kb < kblocks; ++kb) {
-        const float s = __fmul_rn(next_x, next_w);
-        const bool two = __any_sync(0xFFFFFFFFu, !one_factor(s));
         uint64_t s2 = twice(s);
         if (kb + 1 < kblocks) {  // the next block's, while this one's MMAs run
           next_w = __ldg(sw + (kb + 1) * w_step);
@@ -765,6 +775,8 @@ __global__ void __launch_bounds__(Large<PAIR>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; i += 2) fma2(sum[8 * c + i / 2], r[c & 1][i], r[c & 1][i + 1], s2);
         }
+        s = __fmul_rn(next_x, next_w);
+        two = __any_sync(0xFFFFFFFFu, !one_factor(s));
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
