@@ -956,7 +956,8 @@ class Fp8Rows(_Buffers):
     ``max_rows`` rows of K elements, filled by :meth:`quantize`.  Calls go to the
     current stream of the device.  More rows than ``max_rows`` get larger buffers; the
     outgrown ones live as long as the object, for graphs that were captured with them and
-    work still queued on other streams."""
+    work still queued on other streams.  On several streams, :meth:`quantize` must not overlap
+    with calls that read the rows before."""
 
     def __init__(self, K, max_rows=0, device=None):
         import torch
@@ -1018,8 +1019,10 @@ class Fp8Rows(_Buffers):
 
 class Fp8Weights(_Workspace):
     """Weights of ``groups`` matrices [N, K] in 8 bits (one scale for each 128 x 128) and their
-    products with 8-bit rows (moe_fp8_gemm, moe_fp8_gemm_dgrad).  codes: uint8 [groups, N, K];
-    scales: fp32 [groups, ceil(N / 128), ceil(K / 128)]."""
+    products with 8-bit rows (moe_fp8_gemm, moe_fp8_gemm_dgrad), with a workspace of their own.
+    codes: uint8 [groups, N, K]; scales: fp32 [groups, ceil(N / 128), ceil(K / 128)].  Calls go to
+    the current stream of the device; products of one object, forward and dgrad alike, on several
+    streams share its workspace and must not overlap, nor with :meth:`update`."""
 
     def __init__(self, codes, scales):
         import torch
