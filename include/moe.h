@@ -690,7 +690,10 @@ MOE_API moe_status moe_fp8_dequantize(const moe_fp8_shape* shape, const uint8_t*
  * input gradient (lists, workspace of moe_grouped_workspace_size(), errors; GEMM
  * kernel id 12), with x [rows, K] (dy [rows, N]) quantized per row and w
  * [groups, N, K] quantized per block, once for both products.  N and K multiples
- * of 16 (else MOE_ERR_UNSUPPORTED).  shape->type: the type of y (dx).  (The weight
+ * of 16 (else MOE_ERR_UNSUPPORTED).  shape->type: the type of y (dx).  The host does
+ * not see the lists, so the tile plan follows the mean, rows / groups (rows of no group
+ * count): where a few of many groups hold nearly all rows, a mean of up to 16 costs
+ * these groups three to four times what they need.  (The weight
  * gradient sums over rows, whose scales differ: moe_grouped_gemm_wgrad takes 16 bits.) */
 MOE_API moe_status moe_fp8_gemm(const moe_grouped_shape* shape, const uint8_t* x_codes, const float* x_scales,
                                 int64_t ldxs, const uint8_t* w_codes, const float* w_scales, const int32_t* offsets,
@@ -721,7 +724,9 @@ MOE_API moe_status moe_swiglu_grad(int32_t type, int64_t rows, int32_t I, const 
  *   dweight = sum over the rows of dy n,  dbias = sum over the rows of dy
  * fp32 inside, one rounding per output; a row's results depend on the row alone,
  * and calls repeat bit for bit.  Squares and sums are fp32 numbers: rows whose
- * squares do not fit them (|x| above some 1e18) get r = 0.
+ * squares do not fit them (|x| above some 1e17) get r = 0, rows of the layer norm whose
+ * sum does not (|x| above some 1e34) a NaN; with eps = 0, rows whose squares vanish (|x|
+ * below some 1e-23) r = infinity.
  *   type         of x, y, dy, dx: MOE_TYPE_*
  *   weight_type  of weight and bias: type, or MOE_TYPE_FP32
  *   weight, bias [H], NULL for ones and zeros

@@ -344,7 +344,10 @@ moe_status fp8_rows(const moe_fp8_shape* s, int32_t type, const void* rows, int6
 // The plan follows the mean of the rows, as for 16 bits.  A pair takes 12/7 of a single CTA's time for a unit of
 // twice the rows, whether they are all there or not.
 //   us on pairs / single CTAs, 64 groups, N = K = 4096     160 rows    256        300        384        512
-//                                                          237 / 258   249 / 275  437 / 379  441 / 396  463 / 507
+//                                                          242 / 260   250 / 276  425 / 383  432 / 389  450 / 510
+// Measured with 64 groups alone: units are not counted, so few groups leave SMs without one (one group of 256 rows,
+// N = K = 4096: 16 pairs work, 22.6 us), and groups far from the mean take the plan of the others (960 of 960 rows in one of 64
+// groups, N = K = 4096: 82 us in units of 32 rows, 25 to 27 in the others).
 moe::Fp8Plan choose_fp8_plan(const moe_grouped_shape* s) {
   const int64_t per_group = (s->rows + s->groups - 1) / s->groups;
   if (per_group <= 16) return moe::Fp8Plan::kSmall;

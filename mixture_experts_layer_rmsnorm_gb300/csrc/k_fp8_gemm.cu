@@ -23,12 +23,13 @@
 // are rows with a scale each, and reading them from shared memory took half of the time: one
 // group of 8192 rows, N = K = 8192: 772 us.)  MMAs of M = 128 (256 for pairs) take the same time for
 // any number of rows.
-//   up to 128 rows a group: single CTAs, units of 128 rows, bound by HBM
-//   more: CTA pairs, units of 256 rows handed out on demand
+//   single CTAs: units of 128 rows, bound by HBM where a group has no more
+//   CTA pairs: units of 256 rows handed out on demand, where the mean group's units of 256 rows take less time
+//   than its units of 128 (choose_fp8_plan: 129 to 256, 385 to 512 and above 640 rows a group)
 //                                         pairs   single CTAs
-//   64 x 100 rows, N = 8192, K = 4096      441    354 us
-//   64 x 512 rows, N = K = 4096            453    507
-//   8192 rows, N = K = 8192                421    483
+//   64 x 100 rows, N = 8192, K = 4096      435    354 us
+//   64 x 512 rows, N = K = 4096            450    510
+//   8192 rows, N = K = 8192                422    480
 //   - A block's MMAs (128 x 256 x 128 an SM) take 512 cycles at the FP8 rate.  The
 //     eight epilogue warps read 128 x 256 accumulators for it and issue as many
 //     multiply-adds, paired (fma.f32x2), 64 a thread; a load is under way while the one before it is summed.
@@ -36,7 +37,7 @@
 //     What leads from one unit to the next is worked out anew for each, since registers kept for it
 //     would spill, and any spill costs a quarter of the rate.
 //   - TMEM holds two blocks of 256 columns: one is read while the next is computed.
-// Bound: reading TMEM beside the MMAs that write it.  One group of 8192 rows, N = K = 8192, pairs: 421 us (2.6 PFLOP/s,
+// Bound: reading TMEM beside the MMAs that write it.  One group of 8192 rows, N = K = 8192, pairs: 421 us (412 to 438 over boxes; 2.6 PFLOP/s,
 // 870 cycles a block); with a quarter of the multiply-adds 417, without reading TMEM 333.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
